@@ -77,8 +77,12 @@ typedef enum {
     MOE_ERR_TIMEOUT = 6,        /* a bounded device-side wait expired */
     MOE_ERR_CUDA = 7,           /* the CUDA runtime reported an error */
     MOE_ERR_INTERNAL = 8,       /* a device-side consistency check failed (a library fault) */
-    MOE_ERR_SCRATCH_LIMIT = 9   /* the shape needs more than moe_layer_noalloc's fixed scratch */
+    MOE_ERR_SCRATCH_LIMIT = 9,  /* the shape needs more than moe_layer_noalloc's fixed scratch */
+    MOE_ERR_CACHE_RANGE = 10    /* device saw a page, length or offset outside the paged cache */
 } moe_status;
+
+/* Element types of the entry points that take more than fp32. */
+typedef enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2 } moe_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
 MOE_API const char *moe_status_str(moe_status s);
@@ -291,6 +295,17 @@ MOE_API moe_status moe_layer_q8k(const float *x_dev, const float *Wr_dev, const 
                          int32_t *idx_dev, float *w_dev, float *y_dev,
                          void *ws_dev, size_t ws_bytes, void *stream);
 
+/*
+ * moe_ffn_q8k on activations that are Q8_K already (moe_quantize_q8k,
+ * moe_add_rmsnorm): q_dev int8 [T, H], d_dev fp32 [T, H/256], sums_dev int32
+ * [T, H/32] in place of x.  Everything else as moe_ffn_q8k, whose y it gives
+ * bit for bit on the codes of the same x.  Three launches.
+ */
+MOE_API moe_status moe_ffn_q8k_codes(const int8_t *q_dev, const float *d_dev, const int32_t *sums_dev,
+                       const int32_t *idx_dev, const float *w_dev, const void *gate_dev,
+                       const void *up_dev, const void *down_dev, int T, int H, int E, int k, int I,
+                       float *y_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
 /* Number of kernel launches one moe_layer_q8k call enqueues (0: invalid shape). */
 MOE_API int moe_layer_q8k_launch_count(int T, int H, int E, int k, int I);
 
@@ -318,6 +333,103 @@ MOE_API moe_status moe_layer_noalloc(const float *x_dev, const float *Wr_dev, co
                                      const void *gate_dev, const void *up_dev, const void *down_dev,
                                      int T, int H, int E, int k, int I,
                                      int32_t *idx_dev, float *w_dev, float *y_dev, void *stream);
+
+/*
+ * The attention half of a decoder block: residual addition with RMSNorm,
+ * rotary positions with the append to a paged cache, and attention over that
+ * cache.  The projections between them are the caller's.
+ *
+ * moe_add_rmsnorm, per row of H values:
+ *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * gamma
+ *  x_dev [T,H] of x_dtype (the branch output that joins the residual stream);
+ *  residual_dev [T,H] fp32 or NULL (s = x); gamma_dev [H] fp32; eps >= 0 and
+ *  finite.  Outputs, at least one of them: sum_dev [T,H] fp32 or NULL receives
+ *  s (it may be residual_dev itself, or x_dev when that is fp32); y_dev [T,H]
+ *  of y_dtype or NULL; q_dev int8 [T,H], d_dev fp32 [T,H/256], sums_dev int32
+ *  [T,H/32] (all three or none) receive the Q8_K blocks of y, the codes that
+ *  moe_quantize_q8k gives for the fp32 y.  The sum, the statistics and y are
+ *  fp32; a 16-bit y is rounded once, at the store.  Limits: 1 <= T <= 2^22, H
+ *  a multiple of 8 (of 256 with Q8_K), H <= 16384.  One launch.
+ */
+MOE_API moe_status moe_add_rmsnorm(const void *x_dev, moe_dtype x_dtype, const float *residual_dev,
+                       const float *gamma_dev, float eps, int T, int H, float *sum_dev, void *y_dev,
+                       moe_dtype y_dtype, int8_t *q_dev, float *d_dev, int32_t *sums_dev,
+                       void *stream);
+
+/*
+ * The paged cache and the batch, for the next two calls:
+ *  k_pages_dev, v_pages_dev [num_pages, Hkv, page, D] of dtype (MOE_F16 or
+ *  MOE_BF16); page 16, 32, 64, 128 or 256 tokens; D 64 or 128.
+ *  page_table_dev int32 [B, max_pages]: sequence b's cached token j is row
+ *  j % page of page page_table[b][j / page]; entries past its last page are
+ *  not read.  kv_lens_dev int32 [B]: cached tokens of each sequence, the new
+ *  ones of this step included.  q_offs_dev int32 [B+1]: the new tokens of
+ *  sequence b are rows q_offs[b] .. q_offs[b+1]-1 of the N rows (n = 0 is
+ *  legal), and their cache indexes are the last n below kv_lens[b]; rows at or
+ *  past q_offs[B] belong to no sequence and are left alone (padded batches).
+ *  Tokens at a negative index (kv_lens[b] < n) are not cached and see nothing.
+ *  The table, lengths and offsets are read on the device, so a captured graph
+ *  serves a growing batch.  One of them out of range (a page outside
+ *  [0, num_pages), a length outside [0, max_pages * page], offsets that
+ *  decrease or leave [0, N]) never leads out of the buffers: the sticky status
+ *  records MOE_ERR_CACHE_RANGE (detail: the value), and the rows of that
+ *  sequence are not valid output.
+ *  Limits: 1 <= N <= 2^22, 1 <= B <= 4096, Hkv >= 1, Hq a multiple of Hkv,
+ *  Hq <= 256, Hq / Hkv <= 128, num_pages * Hkv <= 2^30.
+ *
+ * moe_rope_append: rows of projected queries, keys and values -> rotated
+ * queries, and keys and values in the cache.
+ *  qkv_dev [N, Hq + 2 Hkv, D] of dtype: a row's query heads, key heads, value
+ *  heads.  q_norm_w_dev / k_norm_w_dev [D] fp32 or NULL: per-head RMSNorm of
+ *  the queries / keys before the rotation (norm_eps as above).
+ *  Rotation of the first rot_dim channels (a multiple of 16, 16 <= rot_dim <=
+ *  D) of every query and key head: pair j < rot_dim/2, of channels (j,
+ *  j + rot_dim/2) or, with interleaved != 0, (2j, 2j+1), turns by the angle
+ *  pos[axis[j]][row] * inv_freq[j]:  (a cos - b sin, b cos + a sin).
+ *  pos_dev int32 [axes, N], 1 <= axes <= 8 (text: one axis; images and video:
+ *  time, height, width), any value; inv_freq_dev fp64 [rot_dim/2] radians per
+ *  position, finite; axis_dev int32 [rot_dim/2], each in [0, axes), or NULL
+ *  (axis 0; an entry out of range takes axis 0 and is recorded as
+ *  MOE_ERR_CACHE_RANGE).  Angles are reduced exactly (64-bit fixed-point
+ *  turns), so far positions lose nothing; the rest is fp32, rounded once.
+ *  q_out_dev [N, Hq, D] of dtype; keys and values go to their cache rows.
+ *  ws_dev: at least 256 bytes, initialised (status word only).  One launch.
+ */
+MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
+                       const double *inv_freq_dev, const int32_t *axis_dev, int axes, int rot_dim,
+                       int interleaved, const float *q_norm_w_dev, const float *k_norm_w_dev,
+                       float norm_eps, void *q_out_dev, void *k_pages_dev, void *v_pages_dev,
+                       const int32_t *page_table_dev, const int32_t *q_offs_dev,
+                       const int32_t *kv_lens_dev, int N, int B, int max_pages, int num_pages,
+                       int page, int Hq, int Hkv, int D, moe_dtype dtype, void *ws_dev,
+                       size_t ws_bytes, void *stream);
+
+/*
+ * moe_attention_paged: attention of every sequence's new tokens over its
+ * cached ones (a single token, a few drafted ones, a chunk of a prompt).
+ *  The row at cache index t sees the keys j <= t and, with window > 0,
+ *  j > t - window.  z_j = scale * (q . k_j), with softcap > 0 then
+ *  softcap * tanh(z_j / softcap);  out = sum_j softmax(z)_j v_j, and lse_dev
+ *  [N, Hq] fp32 (or NULL) receives log sum_j exp(z_j).  Query head h reads
+ *  key/value head h / (Hq / Hkv).  A row that sees nothing gives out 0 and
+ *  lse -inf.  q_dev, out_dev [N, Hq, D] of dtype; scale finite.
+ *  max_new >= 1: the most new tokens of any sequence, as far as the caller
+ *  knows; it picks the kernel and may be wrong (only speed depends on it).
+ *  Scores, softmax statistics and sums are fp32; the weights are rounded to
+ *  dtype for their product with V, as the scores' operands are.  The cached
+ *  rows below kv_lens must be finite (a non-finite V row reaches the rows of
+ *  the same tile that do not see it); rows at or past it may hold anything.
+ *  The workspace needs moe_attention_workspace_bytes (0: invalid shape; never
+ *  above 48 MiB), initialised once with moe_workspace_init; one call at a time
+ *  may use it.  Results are bitwise repeatable.
+ */
+MOE_API size_t moe_attention_workspace_bytes(int Hq, int Hkv, int D);
+MOE_API moe_status moe_attention_paged(const void *q_dev, const void *k_pages_dev,
+                       const void *v_pages_dev, const int32_t *page_table_dev,
+                       const int32_t *q_offs_dev, const int32_t *kv_lens_dev, int N, int B,
+                       int max_new, int max_pages, int num_pages, int page, int Hq, int Hkv, int D,
+                       moe_dtype dtype, float scale, float softcap, int window, void *out_dev,
+                       float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream);
 
 /*
  * Test hooks for the bounded device-side waits (not for production use).

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "abi_checks.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -52,8 +53,6 @@ moe_status moeq4k::device_info(int *sms, int *dev_out) {
 
 namespace {
 
-inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 moe_status check_shape(int T, int H, int E, int k, int I) {
     if (T < 1 || H < 1 || E < 1 || k < 1 || I < 1) return MOE_ERR_INVALID_SHAPE;
     if (k > E || E > kMaxE || k > kMaxK) return MOE_ERR_INVALID_SHAPE;
@@ -61,18 +60,6 @@ moe_status check_shape(int T, int H, int E, int k, int I) {
     if (int64_t(T) * k > (int64_t(1) << 22)) return MOE_ERR_INVALID_SHAPE;
     return MOE_OK;
 }
-
-moe_status check_ptr(const void *p, size_t align) {
-    if (p == nullptr) return MOE_ERR_NULL;
-    if (!aligned(p, align)) return MOE_ERR_MISALIGNED;
-    return MOE_OK;
-}
-
-#define MOE_TRY(expr)                        \
-    do {                                     \
-        moe_status _s = (expr);              \
-        if (_s != MOE_OK) return _s;         \
-    } while (0)
 
 struct Ws {
     uint8_t *base;
@@ -104,8 +91,6 @@ moe_status check_ws(void *ws, size_t ws_bytes, const WsLayout &L) {
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     return MOE_OK;
 }
-
-inline moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 moe_status ffn_enqueue(const float *x, const int32_t *idx, const float *w, const void *gate,
                        const void *up, const void *down, int T, int H, int E, int k, int I,
@@ -193,17 +178,34 @@ Q8Scratch q8_scratch(const Ws &W, int T, int H, int k, int I) {
     return q;
 }
 
-moe_status q8k_ffn_enqueue(const float *x, const int32_t *idx, const float *w, const void *gate,
+// `codes` (q, d, sums of x already quantised) replaces x when its q is set.
+struct Q8Codes {
+    const int8_t *q = nullptr;
+    const float *d = nullptr;
+    const int32_t *sums = nullptr;
+};
+
+moe_status q8k_ffn_enqueue(const float *x, const Q8Codes &codes, const int32_t *idx, const float *w, const void *gate,
                            const void *up, const void *down, int T, int H, int E, int k, int I,
                            float *y, const Ws &W, int sms, cudaStream_t s) {
     const Q8Scratch q = q8_scratch(W, T, H, k, I);
-    return cuda_status(launch_q8k_ffn(x, idx, w, static_cast<const uint8_t *>(gate),
+    Q8Codes in = codes;
+    if (in.q == nullptr) {
+        MOE_TRY(cuda_status(launch_q8k_quantize(x, T, H, q.xq, q.xd, q.xs, sms, s)));
+        in.q = q.xq;
+        in.d = q.xd;
+        in.sums = q.xs;
+    }
+    return cuda_status(launch_q8k_ffn(in.q, in.d, in.sums, idx, w,
+                                      static_cast<const uint8_t *>(gate),
                                       static_cast<const uint8_t *>(up),
-                                      static_cast<const uint8_t *>(down), T, H, E, k, I, y, q.xq,
-                                      q.xd, q.xs, W.f32(W.L.h), q.hq, q.hd, q.hs, W.hdr(), sms, s));
+                                      static_cast<const uint8_t *>(down), T, H, E, k, I, y,
+                                      W.f32(W.L.h), q.hq, q.hd, q.hs, W.hdr(), sms, s));
 }
 
 }  // namespace
+
+unsigned long long moeq4k::device_wait_ns() { return g_wait_ns; }
 
 moe_status moeq4k::validate_shape(int T, int H, int E, int k, int I) {
     return check_shape(T, H, E, k, I);
@@ -223,6 +225,7 @@ const char *moe_status_str(moe_status s) {
         case MOE_ERR_CUDA: return "MOE_ERR_CUDA";
         case MOE_ERR_INTERNAL: return "MOE_ERR_INTERNAL";
         case MOE_ERR_SCRATCH_LIMIT: return "MOE_ERR_SCRATCH_LIMIT";
+        case MOE_ERR_CACHE_RANGE: return "MOE_ERR_CACHE_RANGE";
     }
     return "MOE_ERR_UNKNOWN";
 }
@@ -497,8 +500,31 @@ moe_status moe_ffn_q8k(const float *x, const int32_t *idx, const float *w, const
     int sms = 0;
     MOE_TRY(device_info(&sms, nullptr));
     Ws W{static_cast<uint8_t *>(ws), L};
-    return q8k_ffn_enqueue(x, idx, w, gate, up, down, T, H, E, k, I, y, W, sms,
+    return q8k_ffn_enqueue(x, Q8Codes{}, idx, w, gate, up, down, T, H, E, k, I, y, W, sms,
                            static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_ffn_q8k_codes(const int8_t *q, const float *d, const int32_t *sums,
+                             const int32_t *idx, const float *w, const void *gate, const void *up,
+                             const void *down, int T, int H, int E, int k, int I, float *y,
+                             void *ws, size_t ws_bytes, void *stream) {
+    MOE_TRY(check_shape(T, H, E, k, I));
+    MOE_TRY(check_ptr(q, 16));
+    MOE_TRY(check_ptr(d, 4));
+    MOE_TRY(check_ptr(sums, 4));
+    MOE_TRY(check_ptr(idx, 16));
+    MOE_TRY(check_ptr(w, 16));
+    MOE_TRY(check_ptr(gate, 16));
+    MOE_TRY(check_ptr(up, 16));
+    MOE_TRY(check_ptr(down, 16));
+    MOE_TRY(check_ptr(y, 16));
+    WsLayout L = ws_layout(T, H, E, k, I, false);
+    MOE_TRY(check_ws(ws, ws_bytes, L));
+    int sms = 0;
+    MOE_TRY(device_info(&sms, nullptr));
+    Ws W{static_cast<uint8_t *>(ws), L};
+    return q8k_ffn_enqueue(nullptr, Q8Codes{q, d, sums}, idx, w, gate, up, down, T, H, E, k, I, y,
+                           W, sms, static_cast<cudaStream_t>(stream));
 }
 
 moe_status moe_layer_q8k(const float *x, const float *Wr, const float *bias, const void *gate,
@@ -522,7 +548,7 @@ moe_status moe_layer_q8k(const float *x, const float *Wr, const float *bias, con
     Ws W{static_cast<uint8_t *>(ws), L};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     MOE_TRY(cuda_status(launch_router(x, Wr, bias, T, H, E, k, idx, w, W.f32(L.logits), W.hdr(), sms, g_wait_ns, s)));
-    return q8k_ffn_enqueue(x, idx, w, gate, up, down, T, H, E, k, I, y, W, sms, s);
+    return q8k_ffn_enqueue(x, Q8Codes{}, idx, w, gate, up, down, T, H, E, k, I, y, W, sms, s);
 }
 
 moe_status moe_read_device_status(const void *ws, void *stream, int32_t *detail) {

@@ -105,14 +105,75 @@ cudaError_t launch_decode_stream(const float *x, const int32_t *idx, const float
 
 // Q8_K activations: `rows` fp32 rows of n values (n a multiple of 256) ->
 // codes [rows, n], block scales [rows, n/256], sub-block code sums
-// [rows, n/32]; and the expert FFN on them (x and h quantised; `hbuf`
-// T*k*I floats of scratch; xq/xd/xs and hq/hd/hs the quantised x and h).
+// [rows, n/32]; and the expert FFN on such codes of x (h quantised the same
+// way; `hbuf` T*k*I floats of scratch; hq/hd/hs the quantised h).
 cudaError_t launch_q8k_quantize(const float *v, long rows, int n, int8_t *q, float *d,
                                 int32_t *sums, int num_sms, cudaStream_t s);
-cudaError_t launch_q8k_ffn(const float *x, const int32_t *idx, const float *w, const uint8_t *gate,
-                           const uint8_t *up, const uint8_t *down, int T, int H, int E, int k,
-                           int I, float *y, int8_t *xq, float *xd, int32_t *xs, float *hbuf,
-                           int8_t *hq, float *hd, int32_t *hs, WsHeader *hdr, int num_sms,
-                           cudaStream_t s);
+cudaError_t launch_q8k_ffn(const int8_t *xq, const float *xd, const int32_t *xs, const int32_t *idx,
+                           const float *w, const uint8_t *gate, const uint8_t *up,
+                           const uint8_t *down, int T, int H, int E, int k, int I, float *y,
+                           float *hbuf, int8_t *hq, float *hd, int32_t *hs, WsHeader *hdr,
+                           int num_sms, cudaStream_t s);
+
+// The device-side wait limit of later launches, in ns (moe_debug_set_wait_limit).
+unsigned long long device_wait_ns();
+
+// Residual addition + RMSNorm (moe_add_rmsnorm); null outputs are skipped.
+struct AddNormArgs {
+    const void *x;          // [T, H] of x_type
+    const float *residual;  // [T, H] or null
+    const float *gamma;     // [H]
+    float *sum_out;         // [T, H] or null
+    void *y;                // [T, H] of y_type, or null
+    int8_t *q;              // Q8_K codes, scales, sub-block sums (all or none)
+    float *d;
+    int32_t *sums;
+    float eps;
+    int T, H;
+    moe_dtype x_type, y_type;
+};
+cudaError_t launch_add_rmsnorm(const AddNormArgs &a, int num_sms, cudaStream_t s);
+
+// A paged K/V cache and the batch of sequences that a call works on.
+struct PagedBatch {
+    const int32_t *table;   // [B, max_pages]
+    const int32_t *offs;    // [B + 1]
+    const int32_t *lens;    // [B]
+    int N, B, max_pages, num_pages, page, Hq, Hkv, D;
+};
+
+struct RopeArgs {
+    const void *qkv;          // [N, Hq + 2 Hkv, D]
+    const int32_t *pos;       // [axes, N]
+    const double *inv_freq;   // [rot / 2]
+    const int32_t *axis;      // [rot / 2] or null
+    const float *qw, *kw;     // [D] or null
+    void *q_out;              // [N, Hq, D]
+    void *k, *v;              // pages
+    PagedBatch b;
+    int axes, rot;
+    float eps;
+    int interleaved;
+    moe_dtype type;
+    WsHeader *hdr;
+};
+cudaError_t launch_rope_append(const RopeArgs &a, int num_sms, cudaStream_t s);
+
+struct AttnArgs {
+    const void *q;            // [N, Hq, D]
+    const void *k, *v;        // pages
+    void *out;                // [N, Hq, D]
+    float *lse;               // [N, Hq] or null
+    PagedBatch b;
+    float scale, softcap;     // softcap 0: none
+    int window;               // 0: none
+    moe_dtype type;
+    WsHeader *hdr;
+    float *part;              // partial results (attention_part_bytes)
+    unsigned long long wait_ns;
+};
+// Scratch for partial results of split key ranges.
+size_t attention_part_bytes(int D);
+cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s);
 
 }  // namespace moeq4k

@@ -214,19 +214,17 @@ cudaError_t launch_q8k_quantize(const float *v, long rows, int n, int8_t *q, flo
     return cudaGetLastError();
 }
 
-cudaError_t launch_q8k_ffn(const float *x, const int32_t *idx, const float *w, const uint8_t *gate,
-                           const uint8_t *up, const uint8_t *down, int T, int H, int E, int k,
-                           int I, float *y, int8_t *xq, float *xd, int32_t *xs, float *hbuf,
-                           int8_t *hq, float *hd, int32_t *hs, WsHeader *hdr, int num_sms,
-                           cudaStream_t s) {
+cudaError_t launch_q8k_ffn(const int8_t *xq, const float *xd, const int32_t *xs, const int32_t *idx,
+                           const float *w, const uint8_t *gate, const uint8_t *up,
+                           const uint8_t *down, int T, int H, int E, int k, int I, float *y,
+                           float *hbuf, int8_t *hq, float *hd, int32_t *hs, WsHeader *hdr,
+                           int num_sms, cudaStream_t s) {
     const long pairs = long(T) * k;
-    cudaError_t err = launch_q8k_quantize(x, T, H, xq, xd, xs, num_sms, s);
-    if (err != cudaSuccess) return err;
     const long gu_items = pairs * I;
     const long gu_grid = std::min<long>((gu_items + q8::kWarps - 1) / q8::kWarps, long(num_sms) * 64);
     launch_pdl(q8::q8k_gateup_kernel, dim3(unsigned(gu_grid)), dim3(q8::kThreads), size_t(0), s,
                xq, xd, xs, idx, gate, up, T, H, E, k, I, hbuf, hdr);
-    err = launch_q8k_quantize(hbuf, pairs, I, hq, hd, hs, num_sms, s);
+    cudaError_t err = launch_q8k_quantize(hbuf, pairs, I, hq, hd, hs, num_sms, s);
     if (err != cudaSuccess) return err;
     const long dn_items = long(T) * H;
     const long dn_grid = std::min<long>((dn_items + q8::kWarps - 1) / q8::kWarps, long(num_sms) * 64);

@@ -48,6 +48,15 @@ _SIGS = {
     "moe_layer_q8k": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _S, _P],
                       ctypes.c_int),
     "moe_layer_q8k_launch_count": ([_I, _I, _I, _I, _I], ctypes.c_int),
+    "moe_ffn_q8k_codes": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _S, _P],
+                          ctypes.c_int),
+    "moe_add_rmsnorm": ([_P, _I, _P, _P, ctypes.c_float, _I, _I, _P, _P, _I, _P, _P, _P, _P],
+                        ctypes.c_int),
+    "moe_rope_append": ([_P, _P, _P, _P, _I, _I, _I, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P,
+                         _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _S, _P], ctypes.c_int),
+    "moe_attention_workspace_bytes": ([_I, _I, _I], _S),
+    "moe_attention_paged": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                             ctypes.c_float, ctypes.c_float, _I, _P, _P, _P, _S, _P], ctypes.c_int),
     "moe_read_device_status": ([_P, _P, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "moe_layer_noalloc": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P],
                           ctypes.c_int),
@@ -62,7 +71,10 @@ for _name, (_args, _res) in _SIGS.items():
 EXPORTS = tuple(_SIGS)
 
 MOE_OK = 0
-STATUS_NAMES = {i: _lib.moe_status_str(i).decode() for i in range(10)}
+STATUS_NAMES = {i: _lib.moe_status_str(i).decode() for i in range(11)}
+
+
+MOE_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
 class MoeError(RuntimeError):
@@ -215,6 +227,114 @@ def moe_layer_q8k(x, Wr, bias, gate, up, down, k, I, idx, w, y, ws, stream=None)
     _check(_lib.moe_layer_q8k(_ptr(x), _ptr(Wr), _ptr(bias), _ptr(gate), _ptr(up), _ptr(down),
                               T, H, E, k, I, _ptr(idx), _ptr(w), _ptr(y), _ptr(ws), ws.numel(),
                               _stream(stream)), "moe_layer_q8k")
+
+
+def moe_ffn_q8k_codes(q, d, sums, idx, w, gate, up, down, E, I, y, ws, stream=None) -> None:
+    """``moe_ffn_q8k`` on Q8_K rows: codes ``q`` [T, H], scales ``d``, sub-block sums ``sums``."""
+    T, H = q.shape
+    k = idx.shape[1]
+    _check(_lib.moe_ffn_q8k_codes(_ptr(q), _ptr(d), _ptr(sums), _ptr(idx), _ptr(w), _ptr(gate),
+                                  _ptr(up), _ptr(down), T, H, E, k, I, _ptr(y), _ptr(ws),
+                                  ws.numel(), _stream(stream)), "moe_ffn_q8k_codes")
+
+
+def _tensor(t, shape, dtype, name):
+    """The device pointer of a contiguous tensor of this shape and type (None: NULL).  The
+    attention half takes many buffers whose sizes follow from one another, so the
+    binding checks them before the library, which sees only pointers."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return t.data_ptr()
+
+
+def _dtype(t, name) -> int:
+    code = MOE_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: {t.dtype} is not one of float32, float16, bfloat16")
+    return code
+
+
+def moe_add_rmsnorm(x, residual, gamma, eps, sum_out=None, y=None, q8k=None, stream=None) -> None:
+    """s = x + residual (None: s = x), y = RMSNorm(s) * gamma.  ``sum_out`` receives s, ``y`` the
+    normed rows (fp32, fp16 or bf16), ``q8k`` = (q, d, sums) their Q8_K blocks."""
+    T, H = x.shape
+    f32 = torch.float32
+    q = d = sums = None
+    if q8k is not None:
+        q = _tensor(q8k[0], (T, H), torch.int8, "q")
+        d = _tensor(q8k[1], (T, H // 256), f32, "d")
+        sums = _tensor(q8k[2], (T, H // 32), torch.int32, "sums")
+    _check(_lib.moe_add_rmsnorm(_tensor(x, (T, H), x.dtype, "x"), _dtype(x, "x"),
+                                _tensor(residual, (T, H), f32, "residual"),
+                                _tensor(gamma, (H,), f32, "gamma"), eps, T, H,
+                                _tensor(sum_out, (T, H), f32, "sum_out"),
+                                None if y is None else _tensor(y, (T, H), y.dtype, "y"),
+                                0 if y is None else _dtype(y, "y"), q, d, sums, _stream(stream)),
+           "moe_add_rmsnorm")
+
+
+def _batch(k_pages, v_pages, page_table, q_offs, kv_lens):
+    """(pointers of the pages, table, offsets and lengths; B, max_pages, num_pages, page, Hkv, D)."""
+    P, Hkv, page, D = k_pages.shape
+    B, max_pages = page_table.shape
+    i32 = torch.int32
+    return ((_tensor(k_pages, (P, Hkv, page, D), k_pages.dtype, "k_pages"),
+             _tensor(v_pages, (P, Hkv, page, D), k_pages.dtype, "v_pages"),
+             _tensor(page_table, (B, max_pages), i32, "page_table"),
+             _tensor(q_offs, (B + 1,), i32, "q_offs"), _tensor(kv_lens, (B,), i32, "kv_lens")),
+            (B, max_pages, P, page, Hkv, D))
+
+
+def moe_rope_append(qkv, pos, inv_freq, q_out, k_pages, v_pages, page_table, q_offs, kv_lens, ws,
+                    axis=None, q_norm_w=None, k_norm_w=None, eps=1e-6, interleaved=False,
+                    stream=None) -> None:
+    """Rows ``qkv`` [N, (Hq + 2 Hkv) D] -> normed and rotated queries ``q_out`` [N, Hq, D], keys
+    (normed, rotated) and values into the cache.  ``pos`` int32 [axes, N], ``inv_freq`` float64
+    [rot / 2] radians per position, ``axis`` int32 [rot / 2]: the axis of each pair."""
+    ptrs, (B, max_pages, P, page, Hkv, D) = _batch(k_pages, v_pages, page_table, q_offs, kv_lens)
+    N, Hq, _ = q_out.shape
+    axes, half = pos.shape[0], inv_freq.shape[0]
+    f32, i32 = torch.float32, torch.int32
+    _check(_lib.moe_rope_append(
+        _tensor(qkv, (N, (Hq + 2 * Hkv) * D), k_pages.dtype, "qkv"), _tensor(pos, (axes, N), i32, "pos"),
+        _tensor(inv_freq, (half,), torch.float64, "inv_freq"), _tensor(axis, (half,), i32, "axis"),
+        axes, 2 * half, 1 if interleaved else 0, _tensor(q_norm_w, (D,), f32, "q_norm_w"),
+        _tensor(k_norm_w, (D,), f32, "k_norm_w"), eps,
+        _tensor(q_out, (N, Hq, D), k_pages.dtype, "q_out"), *ptrs, N, B, max_pages, P, page, Hq, Hkv,
+        D, _dtype(k_pages, "k_pages"), _ptr(ws), ws.numel(), _stream(stream)), "moe_rope_append")
+
+
+def moe_attention_workspace_bytes(Hq, Hkv, D) -> int:
+    return _lib.moe_attention_workspace_bytes(Hq, Hkv, D)
+
+
+def alloc_attention_workspace(Hq, Hkv, D, device="cuda") -> torch.Tensor:
+    """A uint8 device workspace for moe_attention_paged (and moe_rope_append), initialised."""
+    n = moe_attention_workspace_bytes(Hq, Hkv, D)
+    if n == 0:
+        raise MoeError(1, "moe_attention_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    moe_workspace_init(ws)
+    return ws
+
+
+def moe_attention_paged(q, k_pages, v_pages, page_table, q_offs, kv_lens, max_new, scale, out, ws,
+                        lse=None, window=0, softcap=0.0, stream=None) -> None:
+    """Attention of the new rows ``q`` [N, Hq, D] over each sequence's cached tokens -> ``out``
+    [N, Hq, D], ``lse`` [N, Hq] (optional).  ``max_new``: the most new tokens of a sequence."""
+    ptrs, (B, max_pages, P, page, Hkv, D) = _batch(k_pages, v_pages, page_table, q_offs, kv_lens)
+    N, Hq, _ = q.shape
+    _check(_lib.moe_attention_paged(
+        _tensor(q, (N, Hq, D), k_pages.dtype, "q"), *ptrs, N, B, max_new, max_pages, P, page, Hq, Hkv,
+        D, _dtype(k_pages, "k_pages"), scale, softcap, window,
+        _tensor(out, (N, Hq, D), k_pages.dtype, "out"), _tensor(lse, (N, Hq), torch.float32, "lse"),
+        _ptr(ws), ws.numel(), _stream(stream)), "moe_attention_paged")
 
 
 def moe_read_device_status(ws, stream=None):
