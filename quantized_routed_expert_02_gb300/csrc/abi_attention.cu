@@ -134,7 +134,7 @@ moe_status moe_attention_paged(const void *q, const void *k_pages, const void *v
     a.q = q, a.k = k_pages, a.v = v_pages, a.out = out, a.lse = lse, a.b = p;
     a.scale = scale, a.softcap = softcap, a.window = window, a.type = dtype;
     a.hdr = static_cast<WsHeader *>(ws);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + sizeof(WsHeader));
+    a.scratch = static_cast<uint8_t *>(ws) + sizeof(WsHeader);
     a.wait_ns = device_wait_ns();
     return cuda_status(launch_attention(a, max_new, sms, static_cast<cudaStream_t>(stream)));
 }

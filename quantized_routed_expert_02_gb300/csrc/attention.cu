@@ -1,109 +1,452 @@
-// Attention of new tokens over a paged cache (moe_attention_paged), the plain
-// kernel: one warp per (row, query head), lanes over the channels, one pass
-// over the keys with the running maximum and sum of the softmax.
+// Attention of few query rows per key/value head over a paged cache: single
+// tokens, drafted tokens (moe_attention_paged up to kMaxRows rows a tile).
+//
+// Bytes bound: every cached key and value is read once, 4 D bytes for 4 D
+// flops per row.  So the keys stream through the SM and everything else stays
+// in registers: each of a CTA's four warps owns a ring of its own, filled by
+// TMA boxes of 16 keys (a box never crosses a page), and walks its pieces
+// with no barrier but its ring's: S = Q K^T and O += P V by mma.sync m16n8k16 on
+// 16-bit operands with fp32 sums, the running maximum and sum of the softmax in
+// between.  The instruction's 16 rows are one tile of query rows (the G heads of a
+// group times the tokens); a tcgen05 tile would be 128 rows, seven eighths of
+// it padding, for work that the memory bounds anyway.  The four warps'
+// results meet at the end of a segment.
 #include <algorithm>
 
-#include <math_constants.h>
+#include <cuda.h>
 
-#include "common.cuh"
-#include "kernels.cuh"
-#include "paged.cuh"
+#include "attention.cuh"
 
 namespace moeq4k {
 namespace attn {
 
 constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kPiece = 16;                // keys of a piece
+constexpr int kTile = kWarps * kPiece;    // keys of a tile: a piece for every warp
+constexpr int kRing = 24 * 1024;          // bytes of a warp's ring
+constexpr int kMaxRows = 32;
+constexpr int kLeastTiles = 4;
+
+struct StreamParams {
+    CUtensorMap mk, mv;
+    Params p;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                 uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4],
+                                                        uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Box of 64 channels x 16 cache rows of page-head z; out-of-range z reads as zeros.
+__device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int ch, int row, int z,
+                                        uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(ch), "r"(row), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Wait for a phase; the limit counts from the first miss.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity, global_timer_ns() + limit_ns);
+}
+
+template <typename T, int D, int MT, bool kCap>
+__global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __grid_constant__ StreamParams sp) {
+    constexpr int kHalves = D / 64;                      // boxes of a row
+    constexpr int kBox = kPiece * 128;                   // bytes of a box
+    constexpr int kStage = 2 * kHalves * kBox;           // K and V of a piece
+    constexpr int kStages = kRing / kStage;
+    constexpr int kRows = 16 * MT;
+    constexpr int kOS = D + 8;                           // floats of a row of the warps' meeting buffer
+    static_assert(kRows * kOS * 4 <= kRing, "a warp's sums fit its ring");
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ uint64_t full[kWarps][kStages];
+    __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
+    __shared__ unsigned flag, failed;
+    const Params &p = sp.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gid = lane >> 2, tig = lane & 3;
+    const int G = p.b.Hq / p.b.Hkv;
+    uint8_t *ring = smem + warp * kRing;
+    if (tid == 0) failed = 0;
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
+    fence_mbar_init();
+    pdl_enter();
+    Run run;
+    const bool work = run_begin<kTile>(p, kLeastTiles, reinterpret_cast<long *>(smem), run);
+    if (!work) return;
+    fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
+    __syncthreads();
+
+    uint32_t done = 0, issued = 0;  // pieces of this warp, over all segments
+    while (run.u < run.end) {
+        const Item it = run.item;
+        const int s0 = int(run.u - run.item_u);
+        const int s1 = int(min(long(it.tiles), s0 + (run.end - run.u)));
+        const int key_first = (it.t0 + s0) * kTile + warp * kPiece;  // this warp's first piece
+        const int last = it.pos0 + it.nt - 1;                       // the last key any row sees
+        int n = s1 - s0;  // pieces of this warp that hold such keys
+        n = max(0, min(n, last >= key_first ? (last - key_first) / kTile + 1 : 0));
+        // the pages of 32 pieces at a time, and of the 32 after them
+        auto page_at = [&](int i) {
+            if (i >= n) return 0;
+            const int pg = page_of(p.b, it.b, key_first + i * kTile, p.hdr);
+            return pg < 0 ? p.b.num_pages : pg;  // a bad page: past the tensor, read as zeros
+        };
+        int pages = page_at(lane), pages_next = page_at(32 + lane);
+        int sent = 0;  // pieces of this segment issued
+        auto issue = [&]() {
+            if (sent > 0 && (sent & 31) == 0) {
+                pages = pages_next;
+                pages_next = page_at(sent + 32 + lane);
+            }
+            const int z = __shfl_sync(0xffffffffu, pages, sent & 31) * p.b.Hkv + it.kh;
+            if (lane == 0) {
+                const uint32_t st = issued % kStages;
+                uint8_t *dst = ring + st * kStage;
+                uint64_t *bar = &full[warp][st];
+                const int row = (key_first + sent * kTile) & (p.b.page - 1);
+                mbar_arrive_expect_tx(bar, kStage);
+#pragma unroll
+                for (int c = 0; c < kHalves; ++c) tma_box(dst + c * kBox, &sp.mk, c * 64, row, z, bar);
+#pragma unroll
+                for (int c = 0; c < kHalves; ++c)
+                    tma_box(dst + (kHalves + c) * kBox, &sp.mv, c * 64, row, z, bar);
+            }
+            ++sent;
+            ++issued;
+        };
+        for (int i = 0; i < kStages && i < n; ++i) issue();
+
+        // this thread's rows: gid, gid + 8 of each 16; their position, -1 for rows past the tile
+        int pos[MT][2];
+        uint32_t qa[MT][D / 16][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 16 * m + 8 * h + gid;
+                const int tok = r / G;
+                const bool live = tok < it.nt;
+                pos[m][h] = live ? it.pos0 + tok : -1;
+                const T *row = static_cast<const T *>(p.q) +
+                               (size_t(it.row0 + (live ? tok : 0)) * p.b.Hq + it.kh * G + r % G) * D;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row + 16 * k + 2 * tig);
+                    qa[m][k][h] = live ? w[0] : 0u;
+                    qa[m][k][2 + h] = live ? w[4] : 0u;
+                }
+            }
+        float o[MT][D / 8][4], mx[MT][2], l[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            mx[m][0] = mx[m][1] = -CUDART_INF_F;
+            l[m][0] = l[m][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) o[m][j][0] = o[m][j][1] = o[m][j][2] = o[m][j][3] = 0.f;
+        }
+
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const uint32_t st = done % kStages;
+            if (!__all_sync(0xffffffffu, wait_phase(&full[warp][st], (done / kStages) & 1u, p.wait_ns))) {
+                ok = false;
+                break;
+            }
+            const int key0 = key_first + i * kTile;
+            const uint32_t kb = smem_addr(ring + st * kStage), vb = kb + kHalves * kBox;
+            float s[MT][2][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) s[m][j][0] = s[m][j][1] = s[m][j][2] = s[m][j][3] = 0.f;
+            // S: matrices (keys 0-7, channels lo/hi), (keys 8-15, lo/hi) of each 16 channels
+            const int krow = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[4];
+                const int ch = (2 * k + kc) & 7;
+                ldsm4(b, kb + (k / 4) * kBox + krow * 128 + ((ch ^ (krow & 7)) << 4));
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    mma16816<T>(s[m][0], qa[m][k], b[0], b[1]);
+                    mma16816<T>(s[m][1], qa[m][k], b[2], b[3]);
+                }
+            }
+            const bool edge = key0 + kPiece - 1 > it.pos0 || (p.window > 0 && key0 <= last - p.window);
+            uint32_t pa[MT][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        s[m][j][c] = score<kCap>(s[m][j][c], p);
+                        if (edge) {
+                            const int key = key0 + 8 * j + 2 * tig + (c & 1), at = pos[m][c >> 1];
+                            if (key > at || (p.window > 0 && at - key >= p.window))
+                                s[m][j][c] = -CUDART_INF_F;
+                        }
+                    }
+                float cor[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v = fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]),
+                                    fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                    v = fmaxf(v, mx[m][h]);
+                    const float base = v == -CUDART_INF_F ? 0.f : v;  // nothing seen yet
+                    cor[h] = exp2_approx(mx[m][h] - base);
+                    mx[m][h] = v;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            s[m][j][2 * h + c] = exp2_approx(s[m][j][2 * h + c] - base);
+                    l[m][h] = l[m][h] * cor[h] + ((s[m][0][2 * h] + s[m][0][2 * h + 1]) +
+                                                  (s[m][1][2 * h] + s[m][1][2 * h + 1]));
+                }
+                // the weights rounded to the 16-bit type for the product; the sum l keeps them whole
+                pa[m][0] = Pair<T>::make(s[m][0][0], s[m][0][1]);
+                pa[m][1] = Pair<T>::make(s[m][0][2], s[m][0][3]);
+                pa[m][2] = Pair<T>::make(s[m][1][0], s[m][1][1]);
+                pa[m][3] = Pair<T>::make(s[m][1][2], s[m][1][3]);
+                if (__any_sync(0xffffffffu, cor[0] != 1.f || cor[1] != 1.f)) {
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        o[m][j][0] *= cor[0], o[m][j][1] *= cor[0];
+                        o[m][j][2] *= cor[1], o[m][j][3] *= cor[1];
+                    }
+                }
+            }
+            // O: matrices (keys 0-7, channel chunk c), (keys 8-15, c), then c + 1, transposed;
+            // rows past the sequence's end hold anything: their weights are 0, and so must they be
+            const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
+            const bool tail = key0 + kPiece > it.len;
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+            if (tail)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int key = key0 + 8 * h + 2 * tig;
+                    keep[h] = (key < it.len ? 0xffffu : 0u) | (key + 1 < it.len ? 0xffff0000u : 0u);
+                }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t b[4];
+                const int ch = (2 * j + vc) & 7;
+                ldsm4_trans(b, vb + (j / 4) * kBox + vrow * 128 + ((ch ^ (vrow & 7)) << 4));
+                if (tail) {
+                    b[0] &= keep[0], b[1] &= keep[1];
+                    b[2] &= keep[0], b[3] &= keep[1];
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    mma16816<T>(o[m][2 * j], pa[m], b[0], b[1]);
+                    mma16816<T>(o[m][2 * j + 1], pa[m], b[2], b[3]);
+                }
+            }
+            ++done;
+            __syncwarp();  // every lane has read the stage
+            if (sent < n) issue();
+        }
+        if (!ok) {
+            record_status(p.hdr, MOE_ERR_TIMEOUT, 40 + warp);
+            failed = 1;
+        }
+        // copies still in flight after a time-out land before the ring is written
+        for (; done < issued; ++done)
+            wait_phase(&full[warp][done % kStages], (done / kStages) & 1u, p.wait_ns);
+
+        // the warps' sums into their rings, the rows' statistics beside them
+        float *so = reinterpret_cast<float *>(ring);
+        __syncwarp();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v = l[m][h];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                const int r = 16 * m + 8 * h + gid;
+                if (tig == 0) {
+                    sm_m[warp][r] = mx[m][h];
+                    sm_l[warp][r] = v;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j)
+                    *reinterpret_cast<float2 *>(so + r * kOS + 8 * j + 2 * tig) =
+                        make_float2(o[m][j][2 * h], o[m][j][2 * h + 1]);
+            }
+        __syncthreads();
+        if (failed != 0) return;
+        const bool whole = s0 == 0 && s1 == it.tiles;
+        const int rows = it.nt * G;
+        constexpr int kPer = D / 32;  // channels a lane joins
+        auto store = [&](int r, float top, float sum, const float (&v)[kPer]) {
+            const int tok = r / G;
+            const size_t at = size_t(it.row0 + tok) * p.b.Hq + it.kh * G + r % G;
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at * D + lane * kPer);
+#pragma unroll
+            for (int c = 0; c < kPer / 2; ++c) dst[c] = Pair<T>::make(v[2 * c] * inv, v[2 * c + 1] * inv);
+            if (p.lse != nullptr && lane == 0)
+                p.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
+        };
+        float *mine = p.part + size_t(part_slot(run)) * part_floats(kRows, D);
+        for (int r = warp; r < rows; r += kWarps) {
+            float top = sm_m[0][r];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][r]);
+            const float base = top == -CUDART_INF_F ? 0.f : top;
+            float sum = 0.f, v[kPer];
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) v[c] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = exp2_approx(sm_m[w][r] - base);
+                sum = fmaf(sm_l[w][r], f, sum);
+                const float *src = reinterpret_cast<const float *>(smem + w * kRing) + r * kOS + lane * kPer;
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) v[c] = fmaf(src[c], f, v[c]);
+            }
+            if (whole) {
+                store(r, top, sum, v);
+            } else {
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) mine[size_t(r) * D + lane * kPer + c] = v[c];
+                if (lane == 0) {
+                    mine[kRows * D + r] = top;
+                    mine[kRows * (D + 1) + r] = sum;
+                }
+            }
+        }
+        if (!whole) {
+            const Join j = join_of(run);
+            if (join_arrive(p, j, &flag)) {
+                for (int r = warp; r < rows; r += kWarps) {
+                    auto part = [&](int i) { return p.part + size_t(j.slot_of(i)) * part_floats(kRows, D); };
+                    float top = -CUDART_INF_F;
+                    for (int i = lane; i < j.parts; i += 32) top = fmaxf(top, __ldcg(part(i) + kRows * D + r));
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+                    const float base = top == -CUDART_INF_F ? 0.f : top;
+                    float sum = 0.f, v[kPer];
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) v[c] = 0.f;
+#pragma unroll 8
+                    for (int i = 0; i < j.parts; ++i) {
+                        const float *src = part(i);
+                        const float f = exp2_approx(__ldcg(src + kRows * D + r) - base);
+                        sum = fmaf(__ldcg(src + kRows * (D + 1) + r), f, sum);
+#pragma unroll
+                        for (int c = 0; c < kPer; ++c)
+                            v[c] = fmaf(__ldcg(src + size_t(r) * D + lane * kPer + c), f, v[c]);
+                    }
+                    store(r, top, sum, v);
+                }
+            }
+        }
+        run.u += s1 - s0;
+        if (run.u < run.end) {
+            run_next<kTile>(p, run);
+            fence_proxy_async_smem();  // the sums in the rings (generic) before the next copies
+            __syncthreads();
+        }
+    }
+}
+
+template <typename T, int D, int MT>
+cudaError_t launch_stream_cap(const StreamParams &sp, int grid, cudaStream_t s) {
+    const size_t smem = size_t(kWarps) * kRing;
+    auto go = [&](auto kernel) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, sp);
+    };
+    return sp.p.cap_in != 0.f ? go(attention_stream_kernel<T, D, MT, true>)
+                              : go(attention_stream_kernel<T, D, MT, false>);
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) attention_rows_kernel(const AttnArgs a) {
-    pdl_enter();
-    constexpr int kPer = D / 32;  // channels a lane holds: 2 or 4
-    const int lane = threadIdx.x & 31;
-    for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < a.b.B; b += gridDim.x * blockDim.x)
-        seq_view(a.b, b, a.hdr, true);
-    const int end = a.b.offs[a.b.B];
-    const long items = long(a.b.N) * a.b.Hq;
-    for (long it = long(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < items;
-         it += long(gridDim.x) * kWarps) {
-        const int row = int(it / a.b.Hq), h = int(it % a.b.Hq);
-        if (row >= end) break;
-        int lo = 0, hi = a.b.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.b.offs[mid] <= row) lo = mid;
-            else hi = mid - 1;
-        }
-        const SeqView sv = seq_view(a.b, lo, a.hdr, false);
-        if (!sv.ok || row < sv.first || row >= sv.first + sv.n) continue;
-        const int t = sv.len - sv.n + (row - sv.first);
-        const int first = a.window > 0 ? max(0, t - a.window + 1) : 0;
-        const int kh = h / (a.b.Hq / a.b.Hkv);
-        float q[kPer], o[kPer];
-        const uint32_t *qp = reinterpret_cast<const uint32_t *>(
-            static_cast<const T *>(a.q) + (size_t(row) * a.b.Hq + h) * D + lane * kPer);
-#pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) {
-            const float2 f = Pair<T>::load(qp[i]);
-            q[2 * i] = f.x * a.scale, q[2 * i + 1] = f.y * a.scale;
-            o[2 * i] = o[2 * i + 1] = 0.f;
-        }
-        float m = -CUDART_INF_F, l = 0.f;
-        int pg = -1;
-        for (int j = first; j <= t; ++j) {
-            if (j == first || j % a.b.page == 0) pg = page_of(a.b, lo, j, a.hdr);
-            if (pg < 0) continue;
-            const size_t at = ((size_t(pg) * a.b.Hkv + kh) * a.b.page + j % a.b.page) * D + lane * kPer;
-            const uint32_t *kp = reinterpret_cast<const uint32_t *>(static_cast<const T *>(a.k) + at);
-            const uint32_t *vp = reinterpret_cast<const uint32_t *>(static_cast<const T *>(a.v) + at);
-            float z = 0.f;
-#pragma unroll
-            for (int i = 0; i < kPer / 2; ++i) {
-                const float2 f = Pair<T>::load(kp[i]);
-                z = fmaf(q[2 * i], f.x, z);
-                z = fmaf(q[2 * i + 1], f.y, z);
-            }
-            z = warp_sum(z);
-            if (a.softcap > 0.f) z = a.softcap * tanhf(z / a.softcap);
-            const float mn = fmaxf(m, z), c = expf(m - mn), e = expf(z - mn);
-            m = mn;
-            l = l * c + e;
-#pragma unroll
-            for (int i = 0; i < kPer / 2; ++i) {
-                const float2 f = Pair<T>::load(vp[i]);
-                o[2 * i] = fmaf(o[2 * i], c, e * f.x);
-                o[2 * i + 1] = fmaf(o[2 * i + 1], c, e * f.y);
-            }
-        }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        uint32_t *op = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) +
-                                                    (size_t(row) * a.b.Hq + h) * D + lane * kPer);
-#pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) op[i] = Pair<T>::make(o[2 * i] * inv, o[2 * i + 1] * inv);
-        if (a.lse != nullptr && lane == 0)
-            a.lse[size_t(row) * a.b.Hq + h] = l > 0.f ? m + logf(l) : -CUDART_INF_F;
-    }
+cudaError_t launch_stream_rows(const StreamParams &sp, int rows, int grid, cudaStream_t s) {
+    return rows <= 16 ? launch_stream_cap<T, D, 1>(sp, grid, s) : launch_stream_cap<T, D, 2>(sp, grid, s);
+}
+
+Params make_params(const AttnArgs &a) {
+    Params p = {};
+    constexpr float kLog2e = 1.4426950408889634f;
+    p.b = a.b;
+    p.q = a.q;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.scale_log2 = a.scale * kLog2e;
+    p.cap_in = a.softcap > 0.f ? 2.f * kLog2e * a.scale / a.softcap : 0.f;
+    p.cap_log2 = a.softcap * kLog2e;
+    p.window = a.window;
+    p.hdr = a.hdr;
+    p.count = reinterpret_cast<unsigned *>(a.scratch);
+    p.part = reinterpret_cast<float *>(a.scratch + kCounterBytes);
+    p.wait_ns = a.wait_ns;
+    return p;
 }
 
 }  // namespace attn
 
 size_t attention_part_bytes(int D) {
-    (void)D;
-    return 0;
+    return attn::kCounterBytes + size_t(2) * attn::kMaxCtas * attn::part_floats(attn::kMaxRows, D) * 4;
 }
 
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s) {
     using namespace attn;
-    (void)max_new;
-    const long items = long(a.b.N) * a.b.Hq;
-    const dim3 grid(unsigned(std::min<long>((items + kWarps - 1) / kWarps, long(num_sms) * 64)));
-    const dim3 block(kWarps * 32);
+    const int G = a.b.Hq / a.b.Hkv;
+    if (G > kMaxRows) return launch_attention_rows(a, num_sms, s);
+    StreamParams sp = {};
+    sp.p = make_params(a);
+    const int rows = int(std::min<long>(kMaxRows, long(max_new) * G)) <= 16 ? 16 : kMaxRows;
+    sp.p.tt = std::max(1, rows / G);
+    if (!encode_pages_map(&sp.mk, a.k, a.b, a.type, kPiece) || !encode_pages_map(&sp.mv, a.v, a.b, a.type, kPiece))
+        return cudaErrorInvalidValue;
+    const int grid = std::min(2 * num_sms, kMaxCtas);
     if (a.type == MOE_F16)
-        return a.b.D == 64
-                   ? launch_pdl(attention_rows_kernel<__half, 64>, grid, block, size_t(0), s, a)
-                   : launch_pdl(attention_rows_kernel<__half, 128>, grid, block, size_t(0), s, a);
-    return a.b.D == 64
-               ? launch_pdl(attention_rows_kernel<__nv_bfloat16, 64>, grid, block, size_t(0), s, a)
-               : launch_pdl(attention_rows_kernel<__nv_bfloat16, 128>, grid, block, size_t(0), s, a);
+        return a.b.D == 64 ? launch_stream_rows<__half, 64>(sp, rows, grid, s)
+                           : launch_stream_rows<__half, 128>(sp, rows, grid, s);
+    return a.b.D == 64 ? launch_stream_rows<__nv_bfloat16, 64>(sp, rows, grid, s)
+                       : launch_stream_rows<__nv_bfloat16, 128>(sp, rows, grid, s);
 }
 
 }  // namespace moeq4k

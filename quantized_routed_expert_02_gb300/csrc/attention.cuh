@@ -1,0 +1,238 @@
+// What the two attention kernels share: the split of the work over the CTAs
+// and the joining of split key ranges.
+//
+// An item is a tile of query rows of one sequence and one key/value head: tt
+// tokens times the G query heads that read the head.  Its work is the run of
+// key tiles (KT keys) that any of its rows sees, at least one.  All items'
+// tiles, laid end to end, are cut into equal runs, one per CTA, whatever the
+// sequences' lengths: a CTA's run is a few segments, each a range of key tiles
+// of one item.  An item inside one run is finished there; one that crosses a
+// cut leaves a partial result (unnormalised sums, running maximum and sum)
+// per segment, and the CTA that arrives last joins them in key order.  So the
+// order of every sum depends on the shapes alone and results repeat bit for bit.
+#pragma once
+
+#include <math_constants.h>
+
+#include "async_copy.cuh"
+#include "common.cuh"
+#include "kernels.cuh"
+#include "paged.cuh"
+
+namespace moeq4k {
+namespace attn {
+
+constexpr int kMaxCtas = 304;                  // 2 per SM
+constexpr int kMaxParts = kMaxCtas;            // of one item
+constexpr size_t kCounterBytes = 2048;         // one counter per CTA, zeroed by moe_workspace_init
+static_assert(kMaxCtas * sizeof(unsigned) <= kCounterBytes, "a counter per CTA");
+static_assert(kCounterBytes <= sizeof(unsigned long long) * kSyncWords, "moe_workspace_init zeroes them");
+
+struct Params {
+    PagedBatch b;
+    const void *q;
+    void *out;
+    float *lse;
+    float scale_log2;   // scale * log2(e), or without softcap's scale: see score()
+    float cap_in;       // softcap: 2 log2(e) scale / cap; 0: none
+    float cap_log2;     // softcap * log2(e)
+    int window;
+    int tt;             // tokens of a query tile
+    WsHeader *hdr;
+    unsigned *count;    // [kMaxCtas]
+    float *part;
+    unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The score in units of log2: scale q.k log2(e), or cap tanh(scale q.k / cap)
+// log2(e) with tanh(x) = 1 - 2 / (1 + e^2x).  Its error is about 2^-22 of the
+// cap, whatever the score: the absolute error is what the softmax feels.
+template <bool kCap>
+__device__ __forceinline__ float score(float s, const Params &p) {
+    if (!kCap) return s * p.scale_log2;
+    return fmaf(__fdividef(-2.f, 1.f + exp2_approx(s * p.cap_in)), p.cap_log2, p.cap_log2);
+}
+
+struct Item {
+    int b, qt, kh;
+    int row0;    // first row (token) of the tile
+    int nt;      // tokens in it
+    int pos0;    // cache index of the first
+    int len;     // cached tokens
+    int t0;      // first key tile
+    int tiles;   // key tiles, at least 1 (a tile whose rows see nothing has one, all masked)
+};
+
+template <int KT>
+__device__ __forceinline__ void item_tiles(int window, int tt, const SeqView &s, int qt, int &nt,
+                                           int &pos0, int &t0, int &tiles) {
+    nt = min(tt, s.n - qt * tt);
+    pos0 = s.len - s.n + qt * tt;
+    const int last = pos0 + nt - 1;
+    const int kb = window > 0 && pos0 >= window ? pos0 - window + 1 : 0;
+    t0 = kb / KT;
+    tiles = last >= kb ? last / KT + 1 - t0 : 1;
+}
+
+// The CTA's run: `left` tiles from tile `skip` of `item` on.
+struct Run {
+    long per;         // tiles of a full run
+    long u;           // position of the next tile among all
+    long end;
+    long item_u;      // position of the item's first tile
+    Item item;
+};
+
+// Every thread of the CTA calls it; `scratch`: (B + 2) longs of shared memory
+// (free again at the next barrier).  Runs have at least `least` tiles.  False:
+// nothing to do.
+template <int KT>
+__device__ inline bool run_begin(const Params &p, int least, long *scratch, Run &r) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int B = p.b.B, Hkv = p.b.Hkv;
+    for (int b = warp; b < B; b += nw) {
+        const SeqView s = seq_view(p.b, b, p.hdr, blockIdx.x == 0 && lane == 0);
+        const int nq = (s.n + p.tt - 1) / p.tt;
+        long total = 0;
+        for (int qt = lane; qt < nq; qt += 32) {
+            int nt, pos0, t0, tiles;
+            item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, t0, tiles);
+            total += tiles;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (lane == 0) scratch[b + 1] = total * Hkv;
+    }
+    __syncthreads();
+    if (warp == 0) {  // inclusive prefix sums, in place
+        long carry = 0;
+        for (int base = 0; base < B; base += 32) {
+            long v = base + lane < B ? scratch[base + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long w = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += w;
+            }
+            v += carry;
+            if (base + lane < B) scratch[base + lane + 1] = v;
+            carry = __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) scratch[0] = 0;
+    }
+    __syncthreads();
+    const long U = scratch[B];
+    r.per = max(long(least), (U + gridDim.x - 1) / gridDim.x);
+    r.u = r.per * blockIdx.x;
+    r.end = min(U, r.u + r.per);
+    if (r.u >= r.end) return false;
+    int lo = 0, hi = B - 1;  // the last sequence that starts at or before u and has work
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (scratch[mid] <= r.u) lo = mid;
+        else hi = mid - 1;
+    }
+    // lo may be followed by empty sequences only at equal positions: the
+    // search takes the last one, which then holds u
+    const SeqView s = seq_view(p.b, lo, p.hdr, false);
+    const int nq = (s.n + p.tt - 1) / p.tt;
+    long at = scratch[lo];
+    Item &it = r.item;
+    it.b = lo;
+    it.len = s.len;
+    for (int base = 0; base < nq; base += 32) {
+        const int qt = base + lane;
+        int nt = 0, pos0 = 0, t0 = 0, tiles = 0;
+        if (qt < nq) item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, t0, tiles);
+        long v = long(tiles) * Hkv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long w = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += w;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, qt < nq && at + v > r.u);
+        if (past != 0u) {
+            const int src = __ffs(past) - 1;
+            it.qt = base + src;
+            it.nt = __shfl_sync(0xffffffffu, nt, src);
+            it.pos0 = __shfl_sync(0xffffffffu, pos0, src);
+            it.t0 = __shfl_sync(0xffffffffu, t0, src);
+            it.tiles = __shfl_sync(0xffffffffu, tiles, src);
+            const long first = at + __shfl_sync(0xffffffffu, v, src) - long(it.tiles) * Hkv;
+            it.kh = int((r.u - first) / it.tiles);
+            r.item_u = first + long(it.kh) * it.tiles;
+            break;
+        }
+        at += __shfl_sync(0xffffffffu, v, 31);
+    }
+    it.row0 = s.first + it.qt * p.tt;
+    return true;
+}
+
+// On to the item after r.item (r.u is its first tile).
+template <int KT>
+__device__ inline void run_next(const Params &p, Run &r) {
+    Item &it = r.item;
+    r.item_u = r.u;
+    if (++it.kh < p.b.Hkv) return;
+    it.kh = 0;
+    ++it.qt;
+    SeqView s = seq_view(p.b, it.b, p.hdr, false);
+    while (it.qt * p.tt >= s.n && it.b + 1 < p.b.B) {
+        ++it.b;
+        it.qt = 0;
+        s = seq_view(p.b, it.b, p.hdr, false);
+    }
+    it.len = s.len;
+    it.row0 = s.first + it.qt * p.tt;
+    item_tiles<KT>(p.window, p.tt, s, it.qt, it.nt, it.pos0, it.t0, it.tiles);
+}
+
+// A partial result: `rows` rows of D sums, then their maxima, then their sums.
+__host__ __device__ constexpr size_t part_floats(int rows, int D) { return size_t(rows) * (D + 2); }
+
+// Segment [s0, s1) of r.item's tiles is done and, where it is not the whole
+// item, its partial result stored by all threads.  Returns true in every
+// thread of the CTA that has to join the item's parts: part i is at
+// slot_of(i).  `flag`: one word of shared memory.
+struct Join {
+    int first_cta, parts, first_slot;
+    __device__ int slot_of(int i) const { return i == 0 ? first_slot : 2 * (first_cta + i); }
+};
+
+// The slot of this CTA's partial result for the segment that starts at r.u.
+__device__ __forceinline__ int part_slot(const Run &r) {
+    return 2 * int(blockIdx.x) + (r.u == r.per * long(blockIdx.x) ? 0 : 1);
+}
+
+__device__ inline Join join_of(const Run &r) {
+    Join j;
+    j.first_cta = int(r.item_u / r.per);
+    j.parts = int((r.item_u + r.item.tiles - 1) / r.per) - j.first_cta + 1;
+    j.first_slot = 2 * j.first_cta + (r.item_u == r.per * j.first_cta ? 0 : 1);
+    return j;
+}
+
+// All threads have stored their share of the partial result: the last CTA to
+// arrive gets true (in all its threads) and sees the others' stores.
+__device__ inline bool join_arrive(const Params &p, const Join &j, unsigned *flag) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const unsigned before = atomicAdd(p.count + j.first_cta, 1u);
+        *flag = before + 1 == unsigned(j.parts) ? 1u : 0u;
+        if (*flag != 0u) p.count[j.first_cta] = 0u;  // for the next call
+    }
+    __syncthreads();
+    const bool last = *flag != 0u;
+    if (last) __threadfence();
+    return last;
+}
+
+}  // namespace attn
+}  // namespace moeq4k

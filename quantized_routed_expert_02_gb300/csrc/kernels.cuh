@@ -169,11 +169,17 @@ struct AttnArgs {
     int window;               // 0: none
     moe_dtype type;
     WsHeader *hdr;
-    float *part;              // partial results (attention_part_bytes)
+    uint8_t *scratch;         // counters, then partial results (attention_part_bytes)
     unsigned long long wait_ns;
 };
-// Scratch for partial results of split key ranges.
+// The pages [num_pages * Hkv][page][D] as a 3-D TMA map of a 16-bit type:
+// boxes of 64 channels x box_rows cache rows of one page and head, 128-byte
+// swizzle; page-heads out of range read as zeros.  Needs init_prefill_tc.
+bool encode_pages_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
+                      int box_rows);
+// Counters and scratch for partial results of split key ranges.
 size_t attention_part_bytes(int D);
+cudaError_t launch_attention_rows(const AttnArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s);
 
 }  // namespace moeq4k

@@ -839,6 +839,21 @@ bool encode_fp32_box_map(CUtensorMap *map, const float *base, int rows, int cols
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_pages_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
+                      int box_rows) {
+    if (g_encode == nullptr) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(b.D), cuuint64_t(b.page), cuuint64_t(b.num_pages) * b.Hkv};
+    const cuuint64_t strides[2] = {cuuint64_t(b.D) * 2, cuuint64_t(b.page) * b.D * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(map,
+                    type == MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    3, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t init_prefill_tc(int dev) {
     int optin = 0;
     cudaError_t err = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
