@@ -428,16 +428,19 @@ Params make_params(const AttnArgs &a) {
 }  // namespace attn
 
 size_t attention_part_bytes(int D) {
-    return attn::kCounterBytes + size_t(2) * attn::kMaxCtas * attn::part_floats(attn::kMaxRows, D) * 4;
+    using namespace attn;
+    return kCounterBytes +
+           std::max(size_t(2) * kMaxCtas * part_floats(kMaxRows, D) * sizeof(float), tc_part_bytes(D));
 }
 
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s) {
     using namespace attn;
     const int G = a.b.Hq / a.b.Hkv;
-    if (G > kMaxRows) return launch_attention_rows(a, num_sms, s);
+    const Params base = make_params(a);
+    if (long(max_new) * G > kMaxRows) return launch_tc(a, base, num_sms, s);
     StreamParams sp = {};
-    sp.p = make_params(a);
-    const int rows = int(std::min<long>(kMaxRows, long(max_new) * G)) <= 16 ? 16 : kMaxRows;
+    sp.p = base;
+    const int rows = max_new * G <= 16 ? 16 : kMaxRows;
     sp.p.tt = std::max(1, rows / G);
     if (!encode_pages_map(&sp.mk, a.k, a.b, a.type, kPiece) || !encode_pages_map(&sp.mv, a.v, a.b, a.type, kPiece))
         return cudaErrorInvalidValue;

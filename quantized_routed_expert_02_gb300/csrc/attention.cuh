@@ -234,5 +234,9 @@ __device__ inline bool join_arrive(const Params &p, const Join &j, unsigned *fla
     return last;
 }
 
+// The tensor-core kernel (many rows per key/value head).
+size_t tc_part_bytes(int D);
+cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s);
+
 }  // namespace attn
 }  // namespace moeq4k

@@ -1,0 +1,559 @@
+// Attention of many query rows per key/value head (chunks of prompts) on the
+// tensor cores: S = Q K^T and O += P V by tcgen05 with Q, K, V in shared
+// memory and S, P, O in tensor memory.
+//
+// An item is two halves of 128 query rows (tokens x the group's heads) that
+// share every key tile of 128 keys.  Ten warps: two groups of four softmax
+// warps, one per half (a thread per row), a copying warp (TMA boxes of one page
+// each into a ring of K and V tiles) and a warp that issues the MMAs.  The two
+// halves take turns on the tensor pipe: while one half's P V and next Q K^T
+// run, the other half's softmax does.  P overwrites S in tensor memory and is
+// the A operand from there.  O is rescaled only when a row's maximum has grown
+// by more than 2^8 since the last rescale (weights up to 2^8 are as exact in
+// 16 bits as those up to 1, and sums are fp32), so most tiles leave O alone.
+// Tensor memory: S/P of half h at column 128 h, O of half h at 256 + 128 h.
+#include <algorithm>
+
+#include <cuda.h>
+
+#include "attention.cuh"
+#include "tcgen05.cuh"
+
+namespace moeq4k {
+namespace attn {
+namespace tc5 {
+
+constexpr int kHalf = 128;                 // rows of a half
+constexpr int kKeys = 128;                 // keys of a tile
+constexpr int kSoftmax = 256;              // threads of the softmax warps
+constexpr int kThreads = kSoftmax + 64;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
+constexpr int kLeastTiles = 2;
+constexpr float kGrowth = 8.f;             // log2 growth of the maximum that forces a rescale
+
+struct TcParams {
+    CUtensorMap mq, mk, mv;
+    Params p;          // p.tt: tokens of an item (both halves)
+    int tth;           // tokens of a half
+    int box_rows;      // rows of a K/V box
+    uint32_t idesc_qk, idesc_pv;
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kCh = D / 64;                 // 64-channel slabs of a row
+    static constexpr int kSlab = 128 * 128;            // bytes of a 128-row slab
+    static constexpr int kTileB = kCh * kSlab;         // a tile of K, of V, or of a half's Q
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kSmem = kStages * kTileB + 2 * kTileB;
+};
+
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                         uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A holds two 16-bit values of a row per column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(acc ? 1u : 0u)
+        : "memory");
+}
+
+// Descriptor of an operand whose rows of 64 values are its K (here: V's keys)
+// and whose columns, contiguous, are its N: 128-byte swizzle, 8-row groups
+// 1024 B apart, the next 64 columns `slab` bytes on.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t slab) {
+    uint64_t d = 0;
+    d |= uint64_t((saddr >> 4) & 0x3FFF);
+    d |= uint64_t((slab >> 4) & 0x3FFF) << 16;
+    d |= uint64_t(1024 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+
+#define R4(a, i) "=f"(a[i]), "=f"(a[i + 1]), "=f"(a[i + 2]), "=f"(a[i + 3])
+#define W4(a, i) "+f"(a[i]), "+f"(a[i + 1]), "+f"(a[i + 2]), "+f"(a[i + 3])
+#define S4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
+// 32 consecutive columns of this thread's lane; the values are there after wait_ld32.
+__device__ __forceinline__ void tmem_ld32(uint32_t t, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : R4(v, 0), R4(v, 4), R4(v, 8), R4(v, 12), R4(v, 16), R4(v, 20), R4(v, 24), R4(v, 28)
+        : "r"(t));
+}
+__device__ __forceinline__ void wait_ld32(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : W4(v, 0), W4(v, 4), W4(v, 8), W4(v, 12), W4(v, 16), W4(v, 20), W4(v, 24), W4(v, 28)
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16};" ::"r"(t),
+        S4(v, 0), S4(v, 4), S4(v, 8), S4(v, 12)
+        : "memory");
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld16(uint32_t t, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+        "[%16];"
+        : R4(v, 0), R4(v, 4), R4(v, 8), R4(v, 12)
+        : "r"(t));
+}
+__device__ __forceinline__ void wait_ld16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : W4(v, 0), W4(v, 4), W4(v, 8), W4(v, 12) : : "memory");
+}
+#undef R4
+#undef W4
+#undef S4
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is = 0;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(is));
+    return is != 0u;
+}
+
+// The whole warp waits for a phase (limit from the first miss); recorded when it runs out.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Params &p, int who) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = mbar_wait(bar, parity, global_timer_ns() + p.wait_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) record_status(p.hdr, MOE_ERR_TIMEOUT, who);
+    return ok;
+}
+
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+template <typename T, int D, bool kGeneral>
+__global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_constant__ TcParams tp) {
+    using C = Cfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2],
+        o_full[2], drain;
+    __shared__ uint32_t tmem_base, flag[2];
+    const Params &p = tp.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = p.b.Hq / p.b.Hkv;
+    uint8_t *q_smem = smem + C::kStages * C::kTileB;
+    if (tid == 0) {
+        for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+        mbar_init(&q_full, 1);
+        mbar_init(&q_empty, 1);
+        for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h], 4), mbar_init(&o_full[h], 1);
+        mbar_init(&drain, 1);
+    }
+    fence_mbar_init();
+    pdl_enter();
+    Run run;
+    if (!run_begin<kKeys>(p, kLeastTiles, reinterpret_cast<long *>(smem), run)) return;
+    if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);
+    fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_base;
+
+    if (warp == kCopyWarp) {
+        // ---- Q of each segment, then its K and V tiles in turn
+        const int nbox = kKeys / tp.box_rows;  // boxes of a tile, one lane each
+        uint32_t g = 0, seg = 0;               // tiles copied, segments
+        bool ok = true;
+        while (ok && run.u < run.end) {
+            const Item it = run.item;
+            const int s0 = int(run.u - run.item_u), s1 = int(min(long(it.tiles), s0 + (run.end - run.u)));
+            const int halves = it.nt > tp.tth ? 2 : 1;
+            if (seg > 0 && !(ok = warp_wait(&q_empty, (seg - 1) & 1u, p, 50))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&q_full, uint32_t(halves) * C::kCh * G * tp.tth * 128);
+                for (int h = 0; h < halves; ++h)
+                    for (int c = 0; c < C::kCh; ++c)
+                        tma_box3(smem_addr(q_smem) + h * C::kTileB + c * C::kSlab, &tp.mq, c * 64, it.kh * G,
+                                 it.row0 + h * tp.tth, &q_full);
+            }
+            ++seg;
+            auto page_z = [&](int j) {  // page-head of this lane's box of tile j
+                const int key = (it.t0 + s0 + j) * kKeys + lane * tp.box_rows;
+                if (j >= s1 - s0 || lane >= nbox || key >= it.len) return 0;
+                const int pg = page_of(p.b, it.b, key, p.hdr);
+                return (pg < 0 ? p.b.num_pages : pg) * p.b.Hkv + it.kh;  // a bad page reads as zeros
+            };
+            int z_next = page_z(0);
+            for (int j = 0; ok && j < s1 - s0; ++j) {
+                const int z = z_next;
+                z_next = page_z(j + 1);
+                const int key0 = (it.t0 + s0 + j) * kKeys;
+                const int key = key0 + lane * tp.box_rows, row = key & (p.b.page - 1);
+                const bool mine = lane < nbox && key < it.len;
+                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
+                for (int kv = 0; kv < 2; ++kv, ++g) {
+                    const uint32_t st = g % C::kStages;
+                    if (g >= uint32_t(C::kStages) &&
+                        !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 51 + kv)))
+                        break;
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * C::kCh * tp.box_rows * 128);
+                    __syncwarp();
+                    if (mine) {
+                        const uint32_t dst = smem_addr(smem) + st * C::kTileB + lane * tp.box_rows * 128;
+#pragma unroll
+                        for (int c = 0; c < C::kCh; ++c)
+                            tma_box3(dst + c * C::kSlab, kv == 0 ? &tp.mk : &tp.mv, c * 64, row, z, &full[st]);
+                    }
+                }
+            }
+            run.u += s1 - s0;
+            if (run.u < run.end) run_next<kKeys>(p, run);
+        }
+        // copies that a time-out left unawaited land before the CTA exits
+        if (!ok) {
+            for (uint32_t i = 0; i < uint32_t(C::kStages) && i < g; ++i) {
+                const uint32_t gg = g - 1 - i;
+                warp_wait(&full[gg % C::kStages], (gg / C::kStages) & 1u, p, 53);
+            }
+        }
+        if (seg > 0) warp_wait(&q_full, (seg - 1) & 1u, p, 54);
+    } else if (warp == kMmaWarp) {
+        // ---- the MMAs; the whole warp walks the loop, one lane issues
+        const bool leader = elect_one();
+        uint32_t g = 0, seg = 0, np[2] = {0, 0};  // ring tiles, segments, P tiles of each half
+        const uint32_t ring = smem_addr(smem), qs = smem_addr(q_smem);
+        bool ok = true;
+        auto qk = [&](int h, uint32_t st) {
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc::mma_f16(tmem + 128u * h,
+                                tc::smem_desc_sw128(qs + h * C::kTileB + (k / 4) * C::kSlab) + uint64_t(2 * (k % 4)),
+                                tc::smem_desc_sw128(ring + st * C::kTileB + (k / 4) * C::kSlab) + uint64_t(2 * (k % 4)),
+                                tp.idesc_qk, k > 0);
+                tc::commit_arrive(&s_full[h]);
+            }
+        };
+        auto pv = [&](int h, uint32_t st, bool acc) {
+            if (leader) {
+                const uint64_t dv = desc_mn_sw128(ring + st * C::kTileB, C::kSlab);
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 2048 bytes on
+                    mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * k, dv + uint64_t(128 * k), tp.idesc_pv,
+                           acc || k > 0);
+            }
+        };
+        while (ok && run.u < run.end) {
+            const Item it = run.item;
+            const int s0 = int(run.u - run.item_u), s1 = int(min(long(it.tiles), s0 + (run.end - run.u)));
+            const int n = s1 - s0, halves = it.nt > tp.tth ? 2 : 1;
+            uint32_t ks = g % C::kStages;
+            if (!(ok = warp_wait(&q_full, seg & 1u, p, 55)) ||
+                !(ok = warp_wait(&full[ks], (g / C::kStages) & 1u, p, 56)))
+                break;
+            tc::fence_after_sync();
+            for (int h = 0; h < halves; ++h) qk(h, ks);
+            if (leader) {
+                tc::commit_arrive(&empty[ks]);
+                if (n == 1) tc::commit_arrive(&q_empty);
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                const uint32_t vs = (g + 2 * j + 1) % C::kStages, vph = ((g + 2 * j + 1) / C::kStages) & 1u;
+                if (!(ok = warp_wait(&full[vs], vph, p, 57))) break;
+                const int key0 = (it.t0 + s0 + j) * kKeys;
+                if (key0 + kKeys > it.len) {
+                    // rows at or past the sequence's end hold anything (or an earlier tile's
+                    // values): their weights are 0, and so must they be
+                    const int first = max(0, it.len - key0);
+                    for (int i = first * 8 + lane; i < kKeys * 8; i += 32)
+#pragma unroll
+                        for (int c = 0; c < C::kCh; ++c)
+                            *reinterpret_cast<uint4 *>(smem + vs * C::kTileB + c * C::kSlab + i * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (j + 1 < n) {
+                    ks = (g + 2 * j + 2) % C::kStages;
+                    if (!(ok = warp_wait(&full[ks], ((g + 2 * j + 2) / C::kStages) & 1u, p, 58))) break;
+                }
+                for (int h = 0; ok && h < halves; ++h) {
+                    if (!(ok = warp_wait(&p_ready[h], np[h] & 1u, p, 59))) break;
+                    ++np[h];
+                    tc::fence_after_sync();
+                    pv(h, vs, j > 0);
+                    if (j + 1 < n) qk(h, ks);
+                    else if (leader) tc::commit_arrive(&o_full[h]);
+                }
+                if (leader) {
+                    tc::commit_arrive(&empty[vs]);
+                    if (j + 1 < n) tc::commit_arrive(&empty[ks]);
+                    if (j + 2 == n) tc::commit_arrive(&q_empty);
+                }
+                __syncwarp();
+            }
+            g += 2 * n;
+            ++seg;
+            run.u += n;
+            if (run.u < run.end) run_next<kKeys>(p, run);
+        }
+        // every MMA complete before the tensor memory is released
+        if (leader) tc::commit_arrive(&drain);
+        __syncwarp();
+        warp_wait(&drain, 0, p, 60);
+    } else {
+        // ---- softmax of half h, a thread per row
+        const int h = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + 128u * h + lanes, to = tmem + 256u + 128u * h + lanes;
+        const int tok_h = row / G, head = row % G;
+        const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
+        auto value = [&](float x) {  // the score in log2 units
+            return kGeneral && p.cap_in != 0.f ? score<true>(x, p) : score<false>(x, p);
+        };
+        uint32_t ns = 0, no = 0;  // S tiles and O results taken
+        bool ok = true;           // after a time-out: no more waits, every barrier still met
+        while (run.u < run.end) {
+            const Item it = run.item;
+            const int s0 = int(run.u - run.item_u), s1 = int(min(long(it.tiles), s0 + (run.end - run.u)));
+            const int nth = min(tp.tth, it.nt - h * tp.tth);  // this half's tokens
+            if (nth > 0) {
+                const int first = it.pos0 + h * tp.tth;  // position of the half's first token
+                const bool live = tok_h < nth;
+                const int at = live ? first + tok_h : -1;
+                float top = -CUDART_INF_F, sum = 0.f;  // reference maximum (log2), sum of weights
+                for (int j = 0; j < s1 - s0; ++j) {
+                    ok = ok && warp_wait(&s_full[h], ns & 1u, p, 61 + h);
+                    ++ns;
+                    if (!ok) continue;
+                    tc::fence_after_sync();
+                    const int key0 = (it.t0 + s0 + j) * kKeys;
+                    const bool edge =
+                        key0 + kKeys - 1 > first || (p.window > 0 && key0 <= first + nth - 1 - p.window);
+                    const int hi = at - key0, lo = p.window > 0 ? hi - p.window : -1;  // sees lo < i <= hi
+                    // first pass over the row: its maximum (the score grows with sign * q.k,
+                    // so the maximum of those gives the maximum of the scores)
+                    float mt = -CUDART_INF_F;
+                    float v[2][32];
+                    tmem_ld32(ts, v[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        wait_ld32(v[c & 1]);
+                        if (c < 3) tmem_ld32(ts + 32 * (c + 1), v[(c + 1) & 1]);
+                        float m2[2] = {-CUDART_INF_F, -CUDART_INF_F};
+                        if (edge) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float x = kGeneral ? v[c & 1][i] * sign : v[c & 1][i];
+                                if (32 * c + i <= hi && 32 * c + i > lo) m2[i & 1] = fmaxf(m2[i & 1], x);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                m2[i & 1] = fmaxf(m2[i & 1], kGeneral ? v[c & 1][i] * sign : v[c & 1][i]);
+                        }
+                        mt = fmaxf(mt, fmaxf(m2[0], m2[1]));
+                    }
+                    tmem_ld32(ts, v[0]);
+                    if (mt != -CUDART_INF_F) mt = value(kGeneral ? mt * sign : mt);
+                    if (j == 0) {
+                        top = mt;
+                    } else if (__any_sync(0xffffffffu, mt - top > kGrowth)) {
+                        // this half's P V of the tile before is complete: its S came after it
+                        const float up = fmaxf(top, mt);
+                        const float f = exp2_approx(top - (up == -CUDART_INF_F ? 0.f : up));
+                        sum *= f;
+                        top = up;
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            float o[16];
+                            tmem_ld16(to + 16 * c, o);
+                            wait_ld16(o);
+                            uint32_t w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * f);
+                            tmem_st16(to + 16 * c, w);
+                        }
+                    }
+                    // second pass: the weights, over the scores that are read already
+                    const float base = top == -CUDART_INF_F ? 0.f : top;
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        wait_ld32(v[c & 1]);
+                        if (c < 3) tmem_ld32(ts + 32 * (c + 1), v[(c + 1) & 1]);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float e[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float x = v[c & 1][i + k];
+                                e[k] = exp2_approx(kGeneral ? value(x) - base : fmaf(x, p.scale_log2, -base));
+                                if (edge && !(32 * c + i + k <= hi && 32 * c + i + k > lo)) e[k] = 0.f;
+                            }
+                            s4[(i >> 1) & 3] += e[0] + e[1];
+                            // rounded for the product; the sum keeps the weight whole
+                            w[i / 2] = Pair<T>::make(e[0], e[1]);
+                        }
+                        tmem_st16(ts + 16 * c, w);
+                    }
+                    sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_ready[h]);
+                }
+                // ---- the half's result
+                ok = ok && warp_wait(&o_full[h], no & 1u, p, 63 + h);
+                ++no;
+                tc::fence_after_sync();
+                const size_t q_row = size_t(it.row0 + h * tp.tth + (live ? tok_h : 0)) * p.b.Hq + it.kh * G + head;
+                auto put = [&](int c, const float (&o)[32], float inv) {
+                    T *dst = static_cast<T *>(p.out) + q_row * D + 32 * c;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            w[i] = Pair<T>::make(o[16 * k + 2 * i] * inv, o[16 * k + 2 * i + 1] * inv);
+                        store32(dst + 16 * k, w);
+                    }
+                };
+                auto put_lse = [&](float m, float l) {
+                    if (p.lse != nullptr)
+                        p.lse[q_row] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -CUDART_INF_F;
+                };
+                const bool whole = s0 == 0 && s1 == it.tiles;
+                // a partial result: row r's channels 4 c .. 4 c + 3 at float4 c * 128 + r
+                constexpr size_t kPart = part_floats(kHalf, D);
+                float *mine = p.part + size_t(2 * part_slot(run) + h) * kPart;
+                if (ok) {
+                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        tmem_ld32(to + 32 * c, o);
+                        wait_ld32(o);
+                        if (!live) continue;
+                        if (whole) {
+                            put(c, o, inv);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                reinterpret_cast<float4 *>(mine)[(8 * c + i / 4) * kHalf + row] =
+                                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        }
+                    }
+                    if (live && whole) put_lse(top, sum);
+                    if (live && !whole) {
+                        mine[size_t(D) * kHalf + row] = top;
+                        mine[size_t(D + 1) * kHalf + row] = sum;
+                    }
+                }
+                tc::fence_before_sync();
+                if (!whole) {
+                    const Join jn = join_of(run);
+                    __threadfence();
+                    named_bar_sync(1 + h, 128);
+                    if ((tid & 127) == 0) {
+                        flag[h] = 0;
+                        if (ok) {
+                            unsigned *cnt = p.count + 2 * jn.first_cta + h;
+                            flag[h] = atomicAdd(cnt, 1u) + 1 == unsigned(jn.parts) ? 1u : 0u;
+                            if (flag[h] != 0u) *cnt = 0u;  // for the next call
+                        }
+                    }
+                    named_bar_sync(1 + h, 128);
+                    if (flag[h] != 0u && live) {
+                        __threadfence();
+                        auto part = [&](int i) { return p.part + size_t(2 * jn.slot_of(i) + h) * kPart; };
+                        float m = -CUDART_INF_F, l = 0.f;
+                        for (int i = 0; i < jn.parts; ++i) m = fmaxf(m, __ldcg(part(i) + size_t(D) * kHalf + row));
+                        const float base = m == -CUDART_INF_F ? 0.f : m;
+                        for (int i = 0; i < jn.parts; ++i)
+                            l = fmaf(__ldcg(part(i) + size_t(D + 1) * kHalf + row),
+                                     exp2_approx(__ldcg(part(i) + size_t(D) * kHalf + row) - base), l);
+                        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                            for (int i = 0; i < jn.parts; ++i) {
+                                const float f = exp2_approx(__ldcg(part(i) + size_t(D) * kHalf + row) - base);
+                                const float4 *src = reinterpret_cast<const float4 *>(part(i)) + 8 * c * kHalf + row;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    const float4 x = __ldcg(src + k * kHalf);
+                                    o[4 * k] = fmaf(x.x, f, o[4 * k]);
+                                    o[4 * k + 1] = fmaf(x.y, f, o[4 * k + 1]);
+                                    o[4 * k + 2] = fmaf(x.z, f, o[4 * k + 2]);
+                                    o[4 * k + 3] = fmaf(x.w, f, o[4 * k + 3]);
+                                }
+                            }
+                            put(c, o, inv);
+                        }
+                        put_lse(m, l);
+                    }
+                }
+            }
+            run.u += s1 - s0;
+            if (run.u < run.end) run_next<kKeys>(p, run);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+template <typename T, int D>
+cudaError_t launch(const TcParams &tp, int grid, cudaStream_t s) {
+    auto go = [&](auto kernel) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(Cfg<D>::kSmem), s, tp);
+    };
+    // the general form: capped scores, or a scale that does not keep the order of q.k
+    return tp.p.cap_in != 0.f || !(tp.p.scale_log2 > 0.f) ? go(attention_tc_kernel<T, D, true>)
+                                                          : go(attention_tc_kernel<T, D, false>);
+}
+
+}  // namespace tc5
+
+size_t tc_part_bytes(int D) { return size_t(4) * tc5::kMaxGrid * part_floats(tc5::kHalf, D) * 4; }
+
+cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s) {
+    using namespace tc5;
+    const int G = a.b.Hq / a.b.Hkv;
+    TcParams tp = {};
+    tp.p = p;
+    tp.tth = kHalf / G;
+    tp.p.tt = 2 * tp.tth;
+    tp.box_rows = std::min(a.b.page, kKeys);
+    const uint32_t fmt = a.type == MOE_BF16 ? (1u << 7) | (1u << 10) : 0u;  // A and B bf16
+    tp.idesc_qk = tc::idesc_f16_f32(kHalf, kKeys) | fmt;
+    tp.idesc_pv = tc::idesc_f16_f32(kHalf, a.b.D) | fmt | (1u << 16);       // B: N contiguous
+    if (!encode_pages_map(&tp.mk, a.k, a.b, a.type, tp.box_rows) ||
+        !encode_pages_map(&tp.mv, a.v, a.b, a.type, tp.box_rows) ||
+        !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
+        return cudaErrorInvalidValue;
+    const int grid = std::min(num_sms, kMaxGrid);
+    if (a.type == MOE_F16)
+        return a.b.D == 64 ? launch<__half, 64>(tp, grid, s) : launch<__half, 128>(tp, grid, s);
+    return a.b.D == 64 ? launch<__nv_bfloat16, 64>(tp, grid, s) : launch<__nv_bfloat16, 128>(tp, grid, s);
+}
+
+}  // namespace attn
+}  // namespace moeq4k

@@ -177,9 +177,12 @@ struct AttnArgs {
 // swizzle; page-heads out of range read as zeros.  Needs init_prefill_tc.
 bool encode_pages_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
                       int box_rows);
+// Query rows [N][Hq][D] as a 3-D map: boxes of 64 channels x one group's heads
+// x `tokens` rows.
+bool encode_rows_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
+                     int tokens);
 // Counters and scratch for partial results of split key ranges.
 size_t attention_part_bytes(int D);
-cudaError_t launch_attention_rows(const AttnArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s);
 
 }  // namespace moeq4k

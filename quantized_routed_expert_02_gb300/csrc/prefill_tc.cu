@@ -839,12 +839,14 @@ bool encode_fp32_box_map(CUtensorMap *map, const float *base, int rows, int cols
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_pages_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
-                      int box_rows) {
+// A 3-D tensor of a 16-bit type with contiguous rows of D values, boxes of
+// 64 values x b1 x b2, 128-byte swizzle, zeros out of range.
+static bool encode_16bit_3d(CUtensorMap *map, const void *base, moe_dtype type, uint64_t D, uint64_t d1,
+                            uint64_t d2, int b1, int b2) {
     if (g_encode == nullptr) return false;
-    const cuuint64_t dims[3] = {cuuint64_t(b.D), cuuint64_t(b.page), cuuint64_t(b.num_pages) * b.Hkv};
-    const cuuint64_t strides[2] = {cuuint64_t(b.D) * 2, cuuint64_t(b.page) * b.D * 2};
-    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1};
+    const cuuint64_t dims[3] = {D, d1, d2};
+    const cuuint64_t strides[2] = {D * 2, d1 * D * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(b1), cuuint32_t(b2)};
     const cuuint32_t estr[3] = {1, 1, 1};
     return g_encode(map,
                     type == MOE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -852,6 +854,14 @@ bool encode_pages_map(CUtensorMap *map, const void *base, const PagedBatch &b, m
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_pages_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
+                      int box_rows) {
+    return encode_16bit_3d(map, base, type, b.D, b.page, uint64_t(b.num_pages) * b.Hkv, box_rows, 1);
+}
+bool encode_rows_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
+                     int tokens) {
+    return encode_16bit_3d(map, base, type, b.D, b.Hq, b.N, b.Hq / b.Hkv, tokens);
 }
 
 cudaError_t init_prefill_tc(int dev) {
