@@ -420,8 +420,8 @@ MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
  *  rows below kv_lens must be finite (a non-finite V row reaches the rows of
  *  the same tile that do not see it); rows at or past it may hold anything.
  *  The workspace needs moe_attention_workspace_bytes (0: invalid shape; never
- *  above 48 MiB), initialised once with moe_workspace_init; one call at a time
- *  may use it.  Results are bitwise repeatable.
+ *  above 48 MiB), initialised once with moe_workspace_init (status word); one
+ *  call at a time may use it.  Results are bitwise repeatable.
  */
 MOE_API size_t moe_attention_workspace_bytes(int Hq, int Hkv, int D);
 MOE_API moe_status moe_attention_paged(const void *q_dev, const void *k_pages_dev,

@@ -26,7 +26,8 @@ constexpr int kPiece = 16;                // keys of a piece
 constexpr int kTile = kWarps * kPiece;    // keys of a tile: a piece for every warp
 constexpr int kRing = 24 * 1024;          // bytes of a warp's ring
 constexpr int kMaxRows = 32;
-constexpr int kLeastTiles = 4;
+constexpr int kLeast = 5;
+constexpr int kExtra = 1;
 
 struct StreamParams {
     CUtensorMap mk, mv;
@@ -76,10 +77,35 @@ __device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int c
         : "memory");
 }
 
-// Wait for a phase; the limit counts from the first miss.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity, global_timer_ns() + limit_ns);
+__device__ __forceinline__ void put_vec(float *p, const float (&v)[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void put_vec(float *p, const float (&v)[2]) {
+    *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+}
+__device__ __forceinline__ void get_vec(const float *p, float (&v)[4]) {
+    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+}
+__device__ __forceinline__ void get_vec(const float *p, float (&v)[2]) {
+    const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
+    v[0] = x.x, v[1] = x.y;
+}
+
+// A finished row: sums v (this lane's kPer channels) over the weights' sum; a
+// row that saw nothing is 0, its logarithm -inf.
+template <typename T, int kPer>
+__device__ __forceinline__ void store_row(const Params &p, size_t row, int lane, float top, float sum,
+                                          const float (&v)[kPer]) {
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int c = 0; c < kPer / 2; ++c) w[c] = Pair<T>::make(v[2 * c] * inv, v[2 * c + 1] * inv);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + (row * 32 + lane) * kPer);
+    if (kPer == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[kPer / 2 - 1]);
+    else dst[0] = w[0];
+    if (p.lse != nullptr && lane == 0)
+        p.lse[row] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
 }
 
 template <typename T, int D, int MT, bool kCap>
@@ -94,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-    __shared__ unsigned flag, failed;
+    __shared__ unsigned failed;
     const Params &p = sp.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tig = lane & 3;
@@ -105,17 +131,17 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
     pdl_enter();
+    if (tid == 0) p.desc[blockIdx.x].parts = 0;
     Run run;
-    const bool work = run_begin<kTile>(p, kLeastTiles, reinterpret_cast<long *>(smem), run);
-    if (!work) return;
+    if (!run_begin<kTile>(p, kLeast, reinterpret_cast<long *>(smem), run)) return;
     fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
     __syncthreads();
 
     uint32_t done = 0, issued = 0;  // pieces of this warp, over all segments
     while (run.u < run.end) {
+        int s0, s1;
+        if (!run_segment(p, run, s0, s1)) break;
         const Item it = run.item;
-        const int s0 = int(run.u - run.item_u);
-        const int s1 = int(min(long(it.tiles), s0 + (run.end - run.u)));
         const int key_first = (it.t0 + s0) * kTile + warp * kPiece;  // this warp's first piece
         const int last = it.pos0 + it.nt - 1;                       // the last key any row sees
         int n = s1 - s0;  // pieces of this warp that hold such keys
@@ -317,17 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         const bool whole = s0 == 0 && s1 == it.tiles;
         const int rows = it.nt * G;
         constexpr int kPer = D / 32;  // channels a lane joins
-        auto store = [&](int r, float top, float sum, const float (&v)[kPer]) {
-            const int tok = r / G;
-            const size_t at = size_t(it.row0 + tok) * p.b.Hq + it.kh * G + r % G;
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at * D + lane * kPer);
-#pragma unroll
-            for (int c = 0; c < kPer / 2; ++c) dst[c] = Pair<T>::make(v[2 * c] * inv, v[2 * c + 1] * inv);
-            if (p.lse != nullptr && lane == 0)
-                p.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
-        };
-        float *mine = p.part + size_t(part_slot(run)) * part_floats(kRows, D);
+        float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(kRows, D);
         for (int r = warp; r < rows; r += kWarps) {
             float top = sm_m[0][r];
 #pragma unroll
@@ -345,48 +361,68 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 for (int c = 0; c < kPer; ++c) v[c] = fmaf(src[c], f, v[c]);
             }
             if (whole) {
-                store(r, top, sum, v);
+                store_row<T, kPer>(p, size_t(it.row0 + r / G) * p.b.Hq + it.kh * G + r % G, lane, top, sum, v);
             } else {
-#pragma unroll
-                for (int c = 0; c < kPer; ++c) mine[size_t(r) * D + lane * kPer + c] = v[c];
+                put_vec(mine + size_t(r) * D + lane * kPer, v);
                 if (lane == 0) {
                     mine[kRows * D + r] = top;
                     mine[kRows * (D + 1) + r] = sum;
                 }
             }
         }
-        if (!whole) {
-            const Join j = join_of(run);
-            if (join_arrive(p, j, &flag)) {
-                for (int r = warp; r < rows; r += kWarps) {
-                    auto part = [&](int i) { return p.part + size_t(j.slot_of(i)) * part_floats(kRows, D); };
-                    float top = -CUDART_INF_F;
-                    for (int i = lane; i < j.parts; i += 32) top = fmaxf(top, __ldcg(part(i) + kRows * D + r));
-#pragma unroll
-                    for (int o2 = 16; o2 > 0; o2 >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
-                    const float base = top == -CUDART_INF_F ? 0.f : top;
-                    float sum = 0.f, v[kPer];
-#pragma unroll
-                    for (int c = 0; c < kPer; ++c) v[c] = 0.f;
-#pragma unroll 8
-                    for (int i = 0; i < j.parts; ++i) {
-                        const float *src = part(i);
-                        const float f = exp2_approx(__ldcg(src + kRows * D + r) - base);
-                        sum = fmaf(__ldcg(src + kRows * (D + 1) + r), f, sum);
-#pragma unroll
-                        for (int c = 0; c < kPer; ++c)
-                            v[c] = fmaf(__ldcg(src + size_t(r) * D + lane * kPer + c), f, v[c]);
-                    }
-                    store(r, top, sum, v);
-                }
-            }
-        }
-        run.u += s1 - s0;
+        if (tid == 0 && s0 == 0 && !whole) p.desc[blockIdx.x] = join_desc(p, run);
+        run_next<kTile>(p, run);
         if (run.u < run.end) {
-            run_next<kTile>(p, run);
             fence_proxy_async_smem();  // the sums in the rings (generic) before the next copies
             __syncthreads();
         }
+    }
+}
+
+// ---- joining: a warp per row of a split item, lanes over the channels
+constexpr int kJoinThreads = 128;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Params p, int rows, int half, int tth) {
+    pdl_enter();
+    constexpr int kPer = D / 32;
+    const JoinDesc d = p.desc[blockIdx.x];
+    if (d.parts == 0) return;
+    const int lane = threadIdx.x & 31, G = p.b.Hq / p.b.Hkv;
+    const size_t stride = part_floats(rows, D);
+    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
+         r += gridDim.y * (kJoinThreads / 32)) {
+        const int tok_h = r % half / G, tok = r / half * tth + tok_h;
+        if (tok_h >= tth || tok >= d.nt) continue;
+        // part 0 is the item's start, the others go on in the CTAs after it
+        auto part = [&](int i) { return p.part + size_t(part_slot(blockIdx.x + i, i == 0)) * stride; };
+        float top = -CUDART_INF_F;
+        for (int i = lane; i < d.parts; i += 32) top = fmaxf(top, part(i)[size_t(rows) * D + r]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float base = top == -CUDART_INF_F ? 0.f : top;
+        float sum = 0.f, v[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) v[c] = 0.f;
+        for (int i0 = 0; i0 < d.parts; i0 += 32) {
+            float f = 0.f, l = 0.f;
+            if (i0 + lane < d.parts) {
+                const float *q = part(i0 + lane) + size_t(rows) * D + r;
+                f = exp2_approx(q[0] - base);
+                l = q[rows] * f;
+            }
+            sum += warp_sum(l);
+            const int n = min(32, d.parts - i0);
+#pragma unroll 16
+            for (int i = 0; i < n; ++i) {
+                const float w = __shfl_sync(0xffffffffu, f, i);
+                float x[kPer];
+                get_vec(part(i0 + i) + size_t(r) * D + lane * kPer, x);
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) v[c] = fmaf(x[c], w, v[c]);
+            }
+        }
+        store_row<T, kPer>(p, size_t(d.row0 + tok) * p.b.Hq + d.kh * G + r % half % G, lane, top, sum, v);
     }
 }
 
@@ -419,17 +455,26 @@ Params make_params(const AttnArgs &a) {
     p.cap_log2 = a.softcap * kLog2e;
     p.window = a.window;
     p.hdr = a.hdr;
-    p.count = reinterpret_cast<unsigned *>(a.scratch);
-    p.part = reinterpret_cast<float *>(a.scratch + kCounterBytes);
+    p.desc = reinterpret_cast<JoinDesc *>(a.scratch);
+    p.part = reinterpret_cast<float *>(a.scratch + kDescBytes);
     p.wait_ns = a.wait_ns;
     return p;
+}
+
+cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int half, int tth, cudaStream_t s) {
+    const dim3 blocks(grid, std::min(16, (rows + 3) / 4)), threads(kJoinThreads);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, blocks, threads, size_t(0), s, p, rows, half, tth); };
+    if (type == MOE_F16)
+        return p.b.D == 64 ? go(attention_join_kernel<__half, 64>) : go(attention_join_kernel<__half, 128>);
+    return p.b.D == 64 ? go(attention_join_kernel<__nv_bfloat16, 64>)
+                       : go(attention_join_kernel<__nv_bfloat16, 128>);
 }
 
 }  // namespace attn
 
 size_t attention_part_bytes(int D) {
     using namespace attn;
-    return kCounterBytes +
+    return kDescBytes +
            std::max(size_t(2) * kMaxCtas * part_floats(kMaxRows, D) * sizeof(float), tc_part_bytes(D));
 }
 
@@ -442,14 +487,19 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     sp.p = base;
     const int rows = max_new * G <= 16 ? 16 : kMaxRows;
     sp.p.tt = std::max(1, rows / G);
+    sp.p.extra = kExtra;
     if (!encode_pages_map(&sp.mk, a.k, a.b, a.type, kPiece) || !encode_pages_map(&sp.mv, a.v, a.b, a.type, kPiece))
         return cudaErrorInvalidValue;
     const int grid = std::min(2 * num_sms, kMaxCtas);
+    cudaError_t e;
     if (a.type == MOE_F16)
-        return a.b.D == 64 ? launch_stream_rows<__half, 64>(sp, rows, grid, s)
-                           : launch_stream_rows<__half, 128>(sp, rows, grid, s);
-    return a.b.D == 64 ? launch_stream_rows<__nv_bfloat16, 64>(sp, rows, grid, s)
-                       : launch_stream_rows<__nv_bfloat16, 128>(sp, rows, grid, s);
+        e = a.b.D == 64 ? launch_stream_rows<__half, 64>(sp, rows, grid, s)
+                        : launch_stream_rows<__half, 128>(sp, rows, grid, s);
+    else
+        e = a.b.D == 64 ? launch_stream_rows<__nv_bfloat16, 64>(sp, rows, grid, s)
+                        : launch_stream_rows<__nv_bfloat16, 128>(sp, rows, grid, s);
+    if (e != cudaSuccess) return e;
+    return launch_join(sp.p, a.type, grid, rows, rows, sp.p.tt, s);
 }
 
 }  // namespace moeq4k

@@ -1,15 +1,16 @@
-// What the two attention kernels share: the split of the work over the CTAs
-// and the joining of split key ranges.
+// What the attention kernels share: the split of the work over the CTAs and
+// the joining of split key ranges.
 //
 // An item is a tile of query rows of one sequence and one key/value head: tt
 // tokens times the G query heads that read the head.  Its work is the run of
-// key tiles (KT keys) that any of its rows sees, at least one.  All items'
-// tiles, laid end to end, are cut into equal runs, one per CTA, whatever the
-// sequences' lengths: a CTA's run is a few segments, each a range of key tiles
-// of one item.  An item inside one run is finished there; one that crosses a
-// cut leaves a partial result (unnormalised sums, running maximum and sum)
-// per segment, and the CTA that arrives last joins them in key order.  So the
-// order of every sum depends on the shapes alone and results repeat bit for bit.
+// key tiles (KT keys) that any of its rows sees, at least one, and a fixed cost
+// of `extra` tiles (queries in, results out).  All items' work, laid end to end,
+// is cut into equal runs, one per CTA, whatever the sequences' lengths: a CTA's
+// run is a few segments, each a range of key tiles of one item.  An item
+// inside one run is finished there; one that crosses a cut leaves a partial
+// result (unnormalised sums, running maximum and sum) per segment, and a
+// second launch joins them in key order over the whole GPU.  So the order of
+// every sum depends on the shapes alone and results repeat bit for bit.
 #pragma once
 
 #include <math_constants.h>
@@ -22,11 +23,14 @@
 namespace moeq4k {
 namespace attn {
 
-constexpr int kMaxCtas = 304;                  // 2 per SM
-constexpr int kMaxParts = kMaxCtas;            // of one item
-constexpr size_t kCounterBytes = 2048;         // one counter per CTA, zeroed by moe_workspace_init
-static_assert(kMaxCtas * sizeof(unsigned) <= kCounterBytes, "a counter per CTA");
-static_assert(kCounterBytes <= sizeof(unsigned long long) * kSyncWords, "moe_workspace_init zeroes them");
+constexpr int kMaxCtas = 304;  // 2 per SM
+
+// An item that starts in a CTA's run and does not end there (parts > 1), or
+// none (parts = 0).  One per CTA, written by every call.
+struct JoinDesc {
+    int parts, row0, nt, kh;
+};
+constexpr size_t kDescBytes = (kMaxCtas * sizeof(JoinDesc) + 255) / 256 * 256;
 
 struct Params {
     PagedBatch b;
@@ -38,11 +42,28 @@ struct Params {
     float cap_log2;     // softcap * log2(e)
     int window;
     int tt;             // tokens of a query tile
+    int extra;          // fixed cost of an item, in key tiles
     WsHeader *hdr;
-    unsigned *count;    // [kMaxCtas]
+    JoinDesc *desc;     // [kMaxCtas]
     float *part;
     unsigned long long wait_ns;
 };
+
+// Wait for a phase, for at most limit_ns.  The global timer takes longer to
+// read than a short wait lasts (about half a microsecond), so it is looked at
+// once in 1024 polls only.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint64_t start = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 1023u) == 0) {
+            const uint64_t now = global_timer_ns();
+            if (start == 0) start = now;
+            else if (now - start > limit_ns) return false;
+        }
+    }
+}
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -80,17 +101,17 @@ __device__ __forceinline__ void item_tiles(int window, int tt, const SeqView &s,
     tiles = last >= kb ? last / KT + 1 - t0 : 1;
 }
 
-// The CTA's run: `left` tiles from tile `skip` of `item` on.
+// The CTA's run: positions [u, end) of the whole work; u is inside `item`,
+// which starts at item_u with `extra` positions before its first tile.
 struct Run {
-    long per;         // tiles of a full run
-    long u;           // position of the next tile among all
-    long end;
-    long item_u;      // position of the item's first tile
+    long per;  // positions of a run
+    long u, end, item_u;
     Item item;
 };
 
 // Every thread of the CTA calls it; `scratch`: (B + 2) longs of shared memory
-// (free again at the next barrier).  Runs have at least `least` tiles.  False:
+// (free again at the next barrier).  A run is at least
+// `least` long.  False:
 // nothing to do.
 template <int KT>
 __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run &r) {
@@ -103,7 +124,7 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
         for (int qt = lane; qt < nq; qt += 32) {
             int nt, pos0, t0, tiles;
             item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, t0, tiles);
-            total += tiles;
+            total += tiles + p.extra;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -149,7 +170,8 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
         const int qt = base + lane;
         int nt = 0, pos0 = 0, t0 = 0, tiles = 0;
         if (qt < nq) item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, t0, tiles);
-        long v = long(tiles) * Hkv;
+        const long cost = qt < nq ? tiles + p.extra : 0;
+        long v = cost * Hkv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long w = __shfl_up_sync(0xffffffffu, v, o);
@@ -163,9 +185,10 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
             it.pos0 = __shfl_sync(0xffffffffu, pos0, src);
             it.t0 = __shfl_sync(0xffffffffu, t0, src);
             it.tiles = __shfl_sync(0xffffffffu, tiles, src);
-            const long first = at + __shfl_sync(0xffffffffu, v, src) - long(it.tiles) * Hkv;
-            it.kh = int((r.u - first) / it.tiles);
-            r.item_u = first + long(it.kh) * it.tiles;
+            const long each = it.tiles + p.extra;
+            const long first = at + __shfl_sync(0xffffffffu, v, src) - each * Hkv;
+            it.kh = int((r.u - first) / each);
+            r.item_u = first + it.kh * each;
             break;
         }
         at += __shfl_sync(0xffffffffu, v, 31);
@@ -174,12 +197,20 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
     return true;
 }
 
-// On to the item after r.item (r.u is its first tile).
+// The CTA's segment of r.item: tiles [s0, s1); false when the run ends before them.
+__device__ __forceinline__ bool run_segment(const Params &p, const Run &r, int &s0, int &s1) {
+    const long first = r.item_u + p.extra;
+    s0 = int(max(0l, r.u - first));
+    s1 = int(min(long(r.item.tiles), r.end - first));
+    return s1 > s0;
+}
+
+// On to the item after r.item, if the run reaches it.
 template <int KT>
 __device__ inline void run_next(const Params &p, Run &r) {
     Item &it = r.item;
-    r.item_u = r.u;
-    if (++it.kh < p.b.Hkv) return;
+    r.u = r.item_u = r.item_u + p.extra + it.tiles;
+    if (r.u >= r.end || ++it.kh < p.b.Hkv) return;
     it.kh = 0;
     ++it.qt;
     SeqView s = seq_view(p.b, it.b, p.hdr, false);
@@ -196,43 +227,24 @@ __device__ inline void run_next(const Params &p, Run &r) {
 // A partial result: `rows` rows of D sums, then their maxima, then their sums.
 __host__ __device__ constexpr size_t part_floats(int rows, int D) { return size_t(rows) * (D + 2); }
 
-// Segment [s0, s1) of r.item's tiles is done and, where it is not the whole
-// item, its partial result stored by all threads.  Returns true in every
-// thread of the CTA that has to join the item's parts: part i is at
-// slot_of(i).  `flag`: one word of shared memory.
-struct Join {
-    int first_cta, parts, first_slot;
-    __device__ int slot_of(int i) const { return i == 0 ? first_slot : 2 * (first_cta + i); }
-};
+// Its slot: a CTA has at most one segment that goes on from the CTA before
+// (its first) and one that it leaves to the next (its last).
+__device__ __forceinline__ int part_slot(int cta, bool starts_here) { return 2 * cta + (starts_here ? 1 : 0); }
 
-// The slot of this CTA's partial result for the segment that starts at r.u.
-__device__ __forceinline__ int part_slot(const Run &r) {
-    return 2 * int(blockIdx.x) + (r.u == r.per * long(blockIdx.x) ? 0 : 1);
+// The parts of r.item: consecutive CTAs from the one with its first tile on.
+__device__ __forceinline__ JoinDesc join_desc(const Params &p, const Run &r) {
+    const long first = r.item_u + p.extra;
+    JoinDesc d;
+    d.parts = int((first + r.item.tiles - 1) / r.per) - int(first / r.per) + 1;
+    d.row0 = r.item.row0;
+    d.nt = r.item.nt;
+    d.kh = r.item.kh;
+    return d;
 }
 
-__device__ inline Join join_of(const Run &r) {
-    Join j;
-    j.first_cta = int(r.item_u / r.per);
-    j.parts = int((r.item_u + r.item.tiles - 1) / r.per) - j.first_cta + 1;
-    j.first_slot = 2 * j.first_cta + (r.item_u == r.per * j.first_cta ? 0 : 1);
-    return j;
-}
-
-// All threads have stored their share of the partial result: the last CTA to
-// arrive gets true (in all its threads) and sees the others' stores.
-__device__ inline bool join_arrive(const Params &p, const Join &j, unsigned *flag) {
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const unsigned before = atomicAdd(p.count + j.first_cta, 1u);
-        *flag = before + 1 == unsigned(j.parts) ? 1u : 0u;
-        if (*flag != 0u) p.count[j.first_cta] = 0u;  // for the next call
-    }
-    __syncthreads();
-    const bool last = *flag != 0u;
-    if (last) __threadfence();
-    return last;
-}
+// Joins the partial results of items of up to `rows` rows; query row r of an item
+// is token r / half * tth + r % half / G, head r % half % G.
+cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int half, int tth, cudaStream_t s);
 
 // The tensor-core kernel (many rows per key/value head).
 size_t tc_part_bytes(int D);

@@ -29,7 +29,8 @@ constexpr int kSoftmax = 256;              // threads of the softmax warps
 constexpr int kThreads = kSoftmax + 64;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
-constexpr int kLeastTiles = 2;
+constexpr int kLeast = 4;
+constexpr int kExtra = 2;
 constexpr float kGrowth = 8.f;             // log2 growth of the maximum that forces a rescale
 
 struct TcParams {
@@ -125,11 +126,9 @@ __device__ __forceinline__ bool elect_one() {
     return is != 0u;
 }
 
-// The whole warp waits for a phase (limit from the first miss); recorded when it runs out.
+// The whole warp waits for a phase; recorded when it runs out.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Params &p, int who) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!ok) ok = mbar_wait(bar, parity, global_timer_ns() + p.wait_ns);
-    ok = __all_sync(0xffffffffu, ok);
+    const bool ok = __all_sync(0xffffffffu, wait_phase(bar, parity, p.wait_ns));
     if (!ok) record_status(p.hdr, MOE_ERR_TIMEOUT, who);
     return ok;
 }
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2],
         o_full[2], drain;
-    __shared__ uint32_t tmem_base, flag[2];
+    __shared__ uint32_t tmem_base;
     const Params &p = tp.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = p.b.Hq / p.b.Hkv;
@@ -160,8 +159,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     }
     fence_mbar_init();
     pdl_enter();
+    if (tid == kCopyWarp * 32) p.desc[blockIdx.x].parts = 0;
     Run run;
-    if (!run_begin<kKeys>(p, kLeastTiles, reinterpret_cast<long *>(smem), run)) return;
+    if (!run_begin<kKeys>(p, kLeast, reinterpret_cast<long *>(smem), run)) return;
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);
     fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
     tc::fence_before_sync();
@@ -175,8 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         uint32_t g = 0, seg = 0;               // tiles copied, segments
         bool ok = true;
         while (ok && run.u < run.end) {
+            int s0, s1;
+            if (!run_segment(p, run, s0, s1)) break;
             const Item it = run.item;
-            const int s0 = int(run.u - run.item_u), s1 = int(min(long(it.tiles), s0 + (run.end - run.u)));
             const int halves = it.nt > tp.tth ? 2 : 1;
             if (seg > 0 && !(ok = warp_wait(&q_empty, (seg - 1) & 1u, p, 50))) break;
             if (lane == 0) {
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                  it.row0 + h * tp.tth, &q_full);
             }
             ++seg;
+            if (lane == 0 && s0 == 0 && s1 < it.tiles) p.desc[blockIdx.x] = join_desc(p, run);
             auto page_z = [&](int j) {  // page-head of this lane's box of tile j
                 const int key = (it.t0 + s0 + j) * kKeys + lane * tp.box_rows;
                 if (j >= s1 - s0 || lane >= nbox || key >= it.len) return 0;
@@ -216,8 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     }
                 }
             }
-            run.u += s1 - s0;
-            if (run.u < run.end) run_next<kKeys>(p, run);
+            run_next<kKeys>(p, run);
         }
         // copies that a time-out left unawaited land before the CTA exits
         if (!ok) {
@@ -254,8 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
             }
         };
         while (ok && run.u < run.end) {
+            int s0, s1;
+            if (!run_segment(p, run, s0, s1)) break;
             const Item it = run.item;
-            const int s0 = int(run.u - run.item_u), s1 = int(min(long(it.tiles), s0 + (run.end - run.u)));
             const int n = s1 - s0, halves = it.nt > tp.tth ? 2 : 1;
             uint32_t ks = g % C::kStages;
             if (!(ok = warp_wait(&q_full, seg & 1u, p, 55)) ||
@@ -304,8 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
             }
             g += 2 * n;
             ++seg;
-            run.u += n;
-            if (run.u < run.end) run_next<kKeys>(p, run);
+            run_next<kKeys>(p, run);
         }
         // every MMA complete before the tensor memory is released
         if (leader) tc::commit_arrive(&drain);
@@ -324,8 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         uint32_t ns = 0, no = 0;  // S tiles and O results taken
         bool ok = true;           // after a time-out: no more waits, every barrier still met
         while (run.u < run.end) {
+            int s0, s1;
+            if (!run_segment(p, run, s0, s1)) break;
             const Item it = run.item;
-            const int s0 = int(run.u - run.item_u), s1 = int(min(long(it.tiles), s0 + (run.end - run.u)));
             const int nth = min(tp.tth, it.nt - h * tp.tth);  // this half's tokens
             if (nth > 0) {
                 const int first = it.pos0 + h * tp.tth;  // position of the half's first token
@@ -435,9 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         p.lse[q_row] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -CUDART_INF_F;
                 };
                 const bool whole = s0 == 0 && s1 == it.tiles;
-                // a partial result: row r's channels 4 c .. 4 c + 3 at float4 c * 128 + r
-                constexpr size_t kPart = part_floats(kHalf, D);
-                float *mine = p.part + size_t(2 * part_slot(run) + h) * kPart;
+                float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(2 * kHalf, D);
+                const int prow = h * kHalf + row;
                 if (ok) {
                     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
@@ -450,66 +451,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                             put(c, o, inv);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                reinterpret_cast<float4 *>(mine)[(8 * c + i / 4) * kHalf + row] =
-                                    make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            for (int i = 0; i < 32; i += 8)
+                                tc::st_global_v8(mine + size_t(prow) * D + 32 * c + i,
+                                                 {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5],
+                                                  o[i + 6], o[i + 7]});
                         }
                     }
                     if (live && whole) put_lse(top, sum);
                     if (live && !whole) {
-                        mine[size_t(D) * kHalf + row] = top;
-                        mine[size_t(D + 1) * kHalf + row] = sum;
+                        mine[size_t(2 * kHalf) * D + prow] = top;
+                        mine[size_t(2 * kHalf) * (D + 1) + prow] = sum;
                     }
                 }
                 tc::fence_before_sync();
-                if (!whole) {
-                    const Join jn = join_of(run);
-                    __threadfence();
-                    named_bar_sync(1 + h, 128);
-                    if ((tid & 127) == 0) {
-                        flag[h] = 0;
-                        if (ok) {
-                            unsigned *cnt = p.count + 2 * jn.first_cta + h;
-                            flag[h] = atomicAdd(cnt, 1u) + 1 == unsigned(jn.parts) ? 1u : 0u;
-                            if (flag[h] != 0u) *cnt = 0u;  // for the next call
-                        }
-                    }
-                    named_bar_sync(1 + h, 128);
-                    if (flag[h] != 0u && live) {
-                        __threadfence();
-                        auto part = [&](int i) { return p.part + size_t(2 * jn.slot_of(i) + h) * kPart; };
-                        float m = -CUDART_INF_F, l = 0.f;
-                        for (int i = 0; i < jn.parts; ++i) m = fmaxf(m, __ldcg(part(i) + size_t(D) * kHalf + row));
-                        const float base = m == -CUDART_INF_F ? 0.f : m;
-                        for (int i = 0; i < jn.parts; ++i)
-                            l = fmaf(__ldcg(part(i) + size_t(D + 1) * kHalf + row),
-                                     exp2_approx(__ldcg(part(i) + size_t(D) * kHalf + row) - base), l);
-                        const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-                            for (int i = 0; i < jn.parts; ++i) {
-                                const float f = exp2_approx(__ldcg(part(i) + size_t(D) * kHalf + row) - base);
-                                const float4 *src = reinterpret_cast<const float4 *>(part(i)) + 8 * c * kHalf + row;
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    const float4 x = __ldcg(src + k * kHalf);
-                                    o[4 * k] = fmaf(x.x, f, o[4 * k]);
-                                    o[4 * k + 1] = fmaf(x.y, f, o[4 * k + 1]);
-                                    o[4 * k + 2] = fmaf(x.z, f, o[4 * k + 2]);
-                                    o[4 * k + 3] = fmaf(x.w, f, o[4 * k + 3]);
-                                }
-                            }
-                            put(c, o, inv);
-                        }
-                        put_lse(m, l);
-                    }
-                }
             }
-            run.u += s1 - s0;
-            if (run.u < run.end) run_next<kKeys>(p, run);
+            run_next<kKeys>(p, run);
         }
     }
     tc::fence_before_sync();
@@ -532,7 +488,7 @@ cudaError_t launch(const TcParams &tp, int grid, cudaStream_t s) {
 
 }  // namespace tc5
 
-size_t tc_part_bytes(int D) { return size_t(4) * tc5::kMaxGrid * part_floats(tc5::kHalf, D) * 4; }
+size_t tc_part_bytes(int D) { return size_t(2) * tc5::kMaxGrid * part_floats(2 * tc5::kHalf, D) * 4; }
 
 cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s) {
     using namespace tc5;
@@ -541,6 +497,7 @@ cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStrea
     tp.p = p;
     tp.tth = kHalf / G;
     tp.p.tt = 2 * tp.tth;
+    tp.p.extra = kExtra;
     tp.box_rows = std::min(a.b.page, kKeys);
     const uint32_t fmt = a.type == MOE_BF16 ? (1u << 7) | (1u << 10) : 0u;  // A and B bf16
     tp.idesc_qk = tc::idesc_f16_f32(kHalf, kKeys) | fmt;
@@ -550,9 +507,13 @@ cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStrea
         !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
         return cudaErrorInvalidValue;
     const int grid = std::min(num_sms, kMaxGrid);
+    cudaError_t e;
     if (a.type == MOE_F16)
-        return a.b.D == 64 ? launch<__half, 64>(tp, grid, s) : launch<__half, 128>(tp, grid, s);
-    return a.b.D == 64 ? launch<__nv_bfloat16, 64>(tp, grid, s) : launch<__nv_bfloat16, 128>(tp, grid, s);
+        e = a.b.D == 64 ? launch<__half, 64>(tp, grid, s) : launch<__half, 128>(tp, grid, s);
+    else
+        e = a.b.D == 64 ? launch<__nv_bfloat16, 64>(tp, grid, s) : launch<__nv_bfloat16, 128>(tp, grid, s);
+    if (e != cudaSuccess) return e;
+    return launch_join(tp.p, a.type, grid, 2 * kHalf, kHalf, tp.tth, s);
 }
 
 }  // namespace attn
