@@ -83,15 +83,6 @@ __device__ __forceinline__ void put_vec(float *p, const float (&v)[4]) {
 __device__ __forceinline__ void put_vec(float *p, const float (&v)[2]) {
     *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
 }
-__device__ __forceinline__ void get_vec(const float *p, float (&v)[4]) {
-    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-}
-__device__ __forceinline__ void get_vec(const float *p, float (&v)[2]) {
-    const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
-    v[0] = x.x, v[1] = x.y;
-}
-
 // A finished row: sums v (this lane's kPer channels) over the weights' sum; a
 // row that saw nothing is 0, its logarithm -inf.
 template <typename T, int kPer>
@@ -115,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     constexpr int kStage = 2 * kHalves * kBox;           // K and V of a piece
     constexpr int kStages = kRing / kStage;
     constexpr int kRows = 16 * MT;
+    constexpr int kPartRows = kMaxRows;
     constexpr int kOS = D + 8;                           // floats of a row of the warps' meeting buffer
     static_assert(kRows * kOS * 4 <= kRing, "a warp's sums fit its ring");
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -343,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         const bool whole = s0 == 0 && s1 == it.tiles;
         const int rows = it.nt * G;
         constexpr int kPer = D / 32;  // channels a lane joins
-        float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(kRows, D);
+        float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(kPartRows, D);
         for (int r = warp; r < rows; r += kWarps) {
             float top = sm_m[0][r];
 #pragma unroll
@@ -363,10 +355,10 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
             if (whole) {
                 store_row<T, kPer>(p, size_t(it.row0 + r / G) * p.b.Hq + it.kh * G + r % G, lane, top, sum, v);
             } else {
-                put_vec(mine + size_t(r) * D + lane * kPer, v);
+                put_vec(mine + part_at(r, lane * kPer, D), v);
                 if (lane == 0) {
-                    mine[kRows * D + r] = top;
-                    mine[kRows * (D + 1) + r] = sum;
+                    mine[kPartRows * D + r] = top;
+                    mine[kPartRows * (D + 1) + r] = sum;
                 }
             }
         }
@@ -379,50 +371,120 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     }
 }
 
-// ---- joining: a warp per row of a split item, lanes over the channels
-constexpr int kJoinThreads = 128;
+// ---- joining.  What bounds it is the latency of dependent loads, so their
+// chain is kept short: a group of S warps (S by the number of parts) takes four consecutive
+// rows, each warp every S-th part, four at a time with all their loads in
+// flight together; the warps' results meet in shared memory.  Lane l holds
+// row l / 2 % 4, of each 32 channels the four from 8 (l / 8) + 4 (l % 2).
+constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 4;
+constexpr int kJoinParts = 4;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Params p, int rows, int half, int tth) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) attention_join_kernel(const Params p, int rows, int half, int tth) {
     pdl_enter();
-    constexpr int kPer = D / 32;
+    constexpr int kVec = D / 32;
+    __shared__ float4 sv[kJoinWarps][kVec][32];
+    __shared__ float sm[kJoinWarps][kJoinRows], sl[kJoinWarps][kJoinRows];
     const JoinDesc d = p.desc[blockIdx.x];
     if (d.parts == 0) return;
-    const int lane = threadIdx.x & 31, G = p.b.Hq / p.b.Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.b.Hq / p.b.Hkv;
     const size_t stride = part_floats(rows, D);
-    for (int r = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += gridDim.y * (kJoinThreads / 32)) {
-        const int tok_h = r % half / G, tok = r / half * tth + tok_h;
-        if (tok_h >= tth || tok >= d.nt) continue;
-        // part 0 is the item's start, the others go on in the CTAs after it
-        auto part = [&](int i) { return p.part + size_t(part_slot(blockIdx.x + i, i == 0)) * stride; };
-        float top = -CUDART_INF_F;
-        for (int i = lane; i < d.parts; i += 32) top = fmaxf(top, part(i)[size_t(rows) * D + r]);
+    const int S = d.parts <= kJoinParts ? 1 : d.parts <= 4 * kJoinParts ? 4 : kJoinWarps;
+    const int group = warp / S, w0 = warp % S, groups = kJoinWarps / S;
+    const int sub = (lane >> 1) & 3, ch0 = 8 * (lane >> 3) + 4 * (lane & 1);
+    const int blocks = (rows + kJoinRows * groups - 1) / (kJoinRows * groups);
+    for (int blk = blockIdx.y; blk < blocks; blk += gridDim.y) {
+        const int row = (blk * groups + group) * kJoinRows + sub;
+        const int tok_h = row % half / G, tok = row / half * tth + tok_h;
+        const bool live = row < rows && tok_h < tth && tok < d.nt;  // rows of no token have no sums
+        float top = -CUDART_INF_F, sum = 0.f;
+        float4 v[kVec];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float base = top == -CUDART_INF_F ? 0.f : top;
-        float sum = 0.f, v[kPer];
+        for (int c = 0; c < kVec; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = w0; live && i0 < d.parts; i0 += S * kJoinParts) {
+            float m[kJoinParts], l[kJoinParts];
+            float4 x[kJoinParts][kVec];
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) v[c] = 0.f;
-        for (int i0 = 0; i0 < d.parts; i0 += 32) {
-            float f = 0.f, l = 0.f;
-            if (i0 + lane < d.parts) {
-                const float *q = part(i0 + lane) + size_t(rows) * D + r;
-                f = exp2_approx(q[0] - base);
-                l = q[rows] * f;
+            for (int u = 0; u < kJoinParts; ++u) {
+                const int i = i0 + S * u;
+                m[u] = -CUDART_INF_F;
+                l[u] = 0.f;
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) x[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < d.parts) {
+                    // part 0 is the item's start, the others go on in the CTAs after it
+                    const float *q = p.part + size_t(part_slot(blockIdx.x + i, i == 0)) * stride;
+                    m[u] = q[rows * D + row];
+                    l[u] = q[rows * (D + 1) + row];
+#pragma unroll
+                    for (int c = 0; c < kVec; ++c)
+                        x[u][c] = *reinterpret_cast<const float4 *>(q + part_at(row, 32 * c + ch0, D));
+                }
             }
-            sum += warp_sum(l);
-            const int n = min(32, d.parts - i0);
-#pragma unroll 16
-            for (int i = 0; i < n; ++i) {
-                const float w = __shfl_sync(0xffffffffu, f, i);
-                float x[kPer];
-                get_vec(part(i0 + i) + size_t(r) * D + lane * kPer, x);
+            float up = top;
 #pragma unroll
-                for (int c = 0; c < kPer; ++c) v[c] = fmaf(x[c], w, v[c]);
+            for (int u = 0; u < kJoinParts; ++u) up = fmaxf(up, m[u]);
+            const float base = up == -CUDART_INF_F ? 0.f : up, old = exp2_approx(top - base);
+            top = up;
+            sum *= old;
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) v[c].x *= old, v[c].y *= old, v[c].z *= old, v[c].w *= old;
+#pragma unroll
+            for (int u = 0; u < kJoinParts; ++u) {
+                const float f = exp2_approx(m[u] - base);
+                sum = fmaf(l[u], f, sum);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    v[c].x = fmaf(x[u][c].x, f, v[c].x);
+                    v[c].y = fmaf(x[u][c].y, f, v[c].y);
+                    v[c].z = fmaf(x[u][c].z, f, v[c].z);
+                    v[c].w = fmaf(x[u][c].w, f, v[c].w);
+                }
             }
         }
-        store_row<T, kPer>(p, size_t(d.row0 + tok) * p.b.Hq + d.kh * G + r % half % G, lane, top, sum, v);
+        bool mine[kVec];  // the vectors this warp finishes
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) mine[c] = S == 1 || c % S == w0;
+        if (S > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) sv[warp][c][lane] = v[c];
+            if (ch0 == 0) {
+                sm[warp][sub] = top;
+                sl[warp][sub] = sum;
+            }
+            __syncthreads();
+            const int first = group * S;
+            for (int w = 0; w < S; ++w) top = fmaxf(top, sm[first + w][sub]);
+            const float base = top == -CUDART_INF_F ? 0.f : top;
+            sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < S; ++w) {
+                const float f = exp2_approx(sm[first + w][sub] - base);
+                sum = fmaf(sl[first + w][sub], f, sum);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    if (!mine[c]) continue;
+                    const float4 y = sv[first + w][c][lane];
+                    v[c].x = fmaf(y.x, f, v[c].x);
+                    v[c].y = fmaf(y.y, f, v[c].y);
+                    v[c].z = fmaf(y.z, f, v[c].z);
+                    v[c].w = fmaf(y.w, f, v[c].w);
+                }
+            }
+        }
+        if (!live) continue;
+        const size_t at = size_t(d.row0 + tok) * p.b.Hq + d.kh * G + row % half % G;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c)
+            if (mine[c])
+                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + at * D + 32 * c + ch0) =
+                    make_uint2(Pair<T>::make(v[c].x * inv, v[c].y * inv), Pair<T>::make(v[c].z * inv, v[c].w * inv));
+        if (p.lse != nullptr && ch0 == 0 && w0 == 0)
+            p.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
     }
 }
 
@@ -462,7 +524,7 @@ Params make_params(const AttnArgs &a) {
 }
 
 cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int half, int tth, cudaStream_t s) {
-    const dim3 blocks(grid, std::min(16, (rows + 3) / 4)), threads(kJoinThreads);
+    const dim3 blocks(grid, std::min(rows / kJoinRows, 8)), threads(kJoinWarps * 32);
     auto go = [&](auto kernel) { return launch_pdl(kernel, blocks, threads, size_t(0), s, p, rows, half, tth); };
     if (type == MOE_F16)
         return p.b.D == 64 ? go(attention_join_kernel<__half, 64>) : go(attention_join_kernel<__half, 128>);
@@ -499,7 +561,7 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
         e = a.b.D == 64 ? launch_stream_rows<__nv_bfloat16, 64>(sp, rows, grid, s)
                         : launch_stream_rows<__nv_bfloat16, 128>(sp, rows, grid, s);
     if (e != cudaSuccess) return e;
-    return launch_join(sp.p, a.type, grid, rows, rows, sp.p.tt, s);
+    return launch_join(sp.p, a.type, grid, kMaxRows, kMaxRows, sp.p.tt, s);
 }
 
 }  // namespace moeq4k

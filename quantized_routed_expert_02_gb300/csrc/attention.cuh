@@ -106,6 +106,7 @@ __device__ __forceinline__ void item_tiles(int window, int tt, const SeqView &s,
 struct Run {
     long per;  // positions of a run
     long u, end, item_u;
+    SeqView seq;  // item's sequence
     Item item;
 };
 
@@ -164,6 +165,7 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
     const int nq = (s.n + p.tt - 1) / p.tt;
     long at = scratch[lo];
     Item &it = r.item;
+    r.seq = s;
     it.b = lo;
     it.len = s.len;
     for (int base = 0; base < nq; base += 32) {
@@ -213,19 +215,23 @@ __device__ inline void run_next(const Params &p, Run &r) {
     if (r.u >= r.end || ++it.kh < p.b.Hkv) return;
     it.kh = 0;
     ++it.qt;
-    SeqView s = seq_view(p.b, it.b, p.hdr, false);
-    while (it.qt * p.tt >= s.n && it.b + 1 < p.b.B) {
+    while (it.qt * p.tt >= r.seq.n && it.b + 1 < p.b.B) {
         ++it.b;
         it.qt = 0;
-        s = seq_view(p.b, it.b, p.hdr, false);
+        r.seq = seq_view(p.b, it.b, p.hdr, false);
     }
-    it.len = s.len;
-    it.row0 = s.first + it.qt * p.tt;
-    item_tiles<KT>(p.window, p.tt, s, it.qt, it.nt, it.pos0, it.t0, it.tiles);
+    it.len = r.seq.len;
+    it.row0 = r.seq.first + it.qt * p.tt;
+    item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.t0, it.tiles);
 }
 
-// A partial result: `rows` rows of D sums, then their maxima, then their sums.
+// A partial result: `rows` (a multiple of 32) rows of D sums, then their maxima,
+// then their sums of weights.  The sums of 32 rows x 8 channels are
+// together, so that a warp with a row per lane stores 1 KB runs.
 __host__ __device__ constexpr size_t part_floats(int rows, int D) { return size_t(rows) * (D + 2); }
+__device__ __forceinline__ int part_at(int row, int ch, int D) {
+    return ((row >> 5) * (D / 8) + (ch >> 3)) * 256 + (row & 31) * 8 + (ch & 7);
+}
 
 // Its slot: a CTA has at most one segment that goes on from the CTA before
 // (its first) and one that it leaves to the next (its last).

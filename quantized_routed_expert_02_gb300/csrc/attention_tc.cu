@@ -13,6 +13,7 @@
 // 16 bits as those up to 1, and sums are fp32), so most tiles leave O alone.
 // Tensor memory: S/P of half h at column 128 h, O of half h at 256 + 128 h.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -46,8 +47,9 @@ struct Cfg {
     static constexpr int kCh = D / 64;                 // 64-channel slabs of a row
     static constexpr int kSlab = 128 * 128;            // bytes of a 128-row slab
     static constexpr int kTileB = kCh * kSlab;         // a tile of K, of V, or of a half's Q
-    static constexpr int kStages = D == 128 ? 5 : 10;
-    static constexpr int kSmem = kStages * kTileB + 2 * kTileB;
+    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStageOut = 32 * 128;         // a softmax warp's 32 rows x 64 channels on their way out
+    static constexpr int kSmem = kStages * kTileB + 2 * kTileB + kSoftmax / 32 * kStageOut;
 };
 
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
@@ -133,10 +135,29 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
     return ok;
 }
 
-__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+// Two fp32 operations an instruction.
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(unsigned long long r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 template <typename T, int D, bool kGeneral>
@@ -344,29 +365,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         key0 + kKeys - 1 > first || (p.window > 0 && key0 <= first + nth - 1 - p.window);
                     const int hi = at - key0, lo = p.window > 0 ? hi - p.window : -1;  // sees lo < i <= hi
                     // first pass over the row: its maximum (the score grows with sign * q.k,
-                    // so the maximum of those gives the maximum of the scores)
-                    float mt = -CUDART_INF_F;
+                    // so the maximum of those gives the maximum of the scores); the masked form
+                    // is code of its own, or every tile would pay for the comparisons
                     float v[2][32];
-                    tmem_ld32(ts, v[0]);
+                    auto row_max = [&](auto masked) {
+                        float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                        tmem_ld32(ts, v[0]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        wait_ld32(v[c & 1]);
-                        if (c < 3) tmem_ld32(ts + 32 * (c + 1), v[(c + 1) & 1]);
-                        float m2[2] = {-CUDART_INF_F, -CUDART_INF_F};
-                        if (edge) {
+                        for (int c = 0; c < 4; ++c) {
+                            wait_ld32(v[c & 1]);
+                            if (c < 3) tmem_ld32(ts + 32 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float x = kGeneral ? v[c & 1][i] * sign : v[c & 1][i];
-                                if (32 * c + i <= hi && 32 * c + i > lo) m2[i & 1] = fmaxf(m2[i & 1], x);
+                            for (int i = 0; i < 32; i += 2) {
+                                float x[2];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    x[k] = kGeneral ? v[c & 1][i + k] * sign : v[c & 1][i + k];
+                                    if (masked && (32 * c + i + k > hi || 32 * c + i + k <= lo)) x[k] = -CUDART_INF_F;
+                                }
+                                m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], x[0], x[1]);
                             }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                m2[i & 1] = fmaxf(m2[i & 1], kGeneral ? v[c & 1][i] * sign : v[c & 1][i]);
                         }
-                        mt = fmaxf(mt, fmaxf(m2[0], m2[1]));
-                    }
-                    tmem_ld32(ts, v[0]);
+                        tmem_ld32(ts, v[0]);  // for the second pass
+                        return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    };
+                    float mt = edge ? row_max(std::true_type{}) : row_max(std::false_type{});
                     if (mt != -CUDART_INF_F) mt = value(kGeneral ? mt * sign : mt);
                     if (j == 0) {
                         top = mt;
@@ -387,30 +410,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                             tmem_st16(to + 16 * c, w);
                         }
                     }
-                    // second pass: the weights, over the scores that are read already
+                    // second pass: the weights
                     const float base = top == -CUDART_INF_F ? 0.f : top;
-                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+                    unsigned long long s2[2] = {0ull, 0ull};  // pairs of sums
+                    const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(-base, -base);
+                    auto weights = [&](auto masked) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        wait_ld32(v[c & 1]);
-                        if (c < 3) tmem_ld32(ts + 32 * (c + 1), v[(c + 1) & 1]);
-                        uint32_t w[16];
+                        for (int c = 0; c < 4; ++c) {
+                            wait_ld32(v[c & 1]);
+                            if (c < 3) tmem_ld32(ts + 32 * (c + 1), v[(c + 1) & 1]);
+                            uint32_t w[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float e[2];
+                            for (int i = 0; i < 32; i += 2) {
+                                float e[2] = {v[c & 1][i], v[c & 1][i + 1]};
+                                if (kGeneral) {
+                                    e[0] = value(e[0]) - base;
+                                    e[1] = value(e[1]) - base;
+                                } else {
+                                    unpack2(fma2(pack2(e[0], e[1]), scale2, base2), e[0], e[1]);
+                                }
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const float x = v[c & 1][i + k];
-                                e[k] = exp2_approx(kGeneral ? value(x) - base : fmaf(x, p.scale_log2, -base));
-                                if (edge && !(32 * c + i + k <= hi && 32 * c + i + k > lo)) e[k] = 0.f;
+                                for (int k = 0; k < 2; ++k) {
+                                    e[k] = exp2_approx(e[k]);
+                                    if (masked && (32 * c + i + k > hi || 32 * c + i + k <= lo)) e[k] = 0.f;
+                                }
+                                s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], pack2(e[0], e[1]));
+                                // rounded for the product; the sum keeps the weight whole
+                                w[i / 2] = Pair<T>::make(e[0], e[1]);
                             }
-                            s4[(i >> 1) & 3] += e[0] + e[1];
-                            // rounded for the product; the sum keeps the weight whole
-                            w[i / 2] = Pair<T>::make(e[0], e[1]);
+                            tmem_st16(ts + 16 * c, w);
                         }
-                        tmem_st16(ts + 16 * c, w);
-                    }
-                    sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+                    };
+                    if (edge) weights(std::true_type{});
+                    else weights(std::false_type{});
+                    float sa, sb;
+                    unpack2(add2(s2[0], s2[1]), sa, sb);
+                    sum += sa + sb;
                     wait_st();
                     tc::fence_before_sync();
                     __syncwarp();
@@ -420,45 +455,56 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 ok = ok && warp_wait(&o_full[h], no & 1u, p, 63 + h);
                 ++no;
                 tc::fence_after_sync();
-                const size_t q_row = size_t(it.row0 + h * tp.tth + (live ? tok_h : 0)) * p.b.Hq + it.kh * G + head;
-                auto put = [&](int c, const float (&o)[32], float inv) {
-                    T *dst = static_cast<T *>(p.out) + q_row * D + 32 * c;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            w[i] = Pair<T>::make(o[16 * k + 2 * i] * inv, o[16 * k + 2 * i + 1] * inv);
-                        store32(dst + 16 * k, w);
-                    }
-                };
-                auto put_lse = [&](float m, float l) {
-                    if (p.lse != nullptr)
-                        p.lse[q_row] = l > 0.f ? (m + log2f(l)) * 0.693147180559945f : -CUDART_INF_F;
-                };
                 const bool whole = s0 == 0 && s1 == it.tiles;
+                const int out_row = live ? (it.row0 + h * tp.tth + tok_h) * p.b.Hq + it.kh * G + head : -1;
                 float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(2 * kHalf, D);
                 const int prow = h * kHalf + row;
-                if (ok) {
-                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                if (ok && whole) {
+                    // through shared memory, 64 channels at a time: a row per lane in (swizzled
+                    // 16-byte chunks), full 128-byte lines out
+                    uint8_t *stage = smem + (C::kStages + 2) * C::kTileB + warp * C::kStageOut;
+#pragma unroll 1
+                    for (int c = 0; c < C::kCh; ++c) {
+                        float o[2][32];
+                        tmem_ld32(to + 64 * c, o[0]);
+                        tmem_ld32(to + 64 * c + 32, o[1]);
+                        wait_ld32(o[0]);
+                        wait_ld32(o[1]);
 #pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float *x = &o[k >> 2][8 * (k & 3)];
+                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                                make_uint4(Pair<T>::make(x[0] * inv, x[1] * inv), Pair<T>::make(x[2] * inv, x[3] * inv),
+                                           Pair<T>::make(x[4] * inv, x[5] * inv), Pair<T>::make(x[6] * inv, x[7] * inv));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3), k = lane & 7;
+                            const int dst = __shfl_sync(0xffffffffu, out_row, r);
+                            const uint4 w = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((k ^ (r & 7)) << 4));
+                            if (dst >= 0)
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + size_t(dst) * D + 64 * c + 8 * k) = w;
+                        }
+                        __syncwarp();
+                    }
+                    if (live && p.lse != nullptr)
+                        p.lse[out_row] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
+                } else if (ok) {
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         float o[32];
                         tmem_ld32(to + 32 * c, o);
                         wait_ld32(o);
                         if (!live) continue;
-                        if (whole) {
-                            put(c, o, inv);
-                        } else {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                tc::st_global_v8(mine + size_t(prow) * D + 32 * c + i,
-                                                 {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5],
-                                                  o[i + 6], o[i + 7]});
-                        }
+                        for (int i = 0; i < 32; i += 8)
+                            tc::st_global_v8(mine + part_at(prow, 32 * c + i, D),
+                                             {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6],
+                                              o[i + 7]});
                     }
-                    if (live && whole) put_lse(top, sum);
-                    if (live && !whole) {
+                    if (live) {
                         mine[size_t(2 * kHalf) * D + prow] = top;
                         mine[size_t(2 * kHalf) * (D + 1) + prow] = sum;
                     }
