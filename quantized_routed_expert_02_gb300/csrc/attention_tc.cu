@@ -3,10 +3,11 @@
 // memory and S, P, O in tensor memory.
 //
 // An item is two halves of 128 query rows (tokens x the group's heads) that
-// share every key tile of 128 keys.  Ten warps: two groups of four softmax
-// warps, one per half (a thread per row), a copying warp (TMA boxes of one page
-// each into a ring of K and V tiles) and a warp that issues the MMAs.  The two
-// halves take turns on the tensor pipe: while one half's P V and next Q K^T
+// share every key tile of 128 keys.  Twelve warps: two groups of four softmax
+// warps, one per half (a thread per row), three copying warps (TMA boxes of one
+// page each into a ring of K and V tiles; one warp cannot issue the 32 boxes that
+// pages of 16 make of a tile pair in the time of its MMAs) and a warp that issues
+// the MMAs.  The two halves take turns on the tensor pipe: while one half's P V and next Q K^T
 // run, the other half's softmax does.  P overwrites S in tensor memory and is
 // the A operand from there.  O is rescaled only when a row's maximum has grown
 // by more than 2^8 since the last rescale (weights up to 2^8 are as exact in
@@ -27,8 +28,9 @@ namespace tc5 {
 constexpr int kHalf = 128;                 // rows of a half
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kSoftmax = 256;              // threads of the softmax warps
-constexpr int kThreads = kSoftmax + 64;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kCopyWarps = 3;
+constexpr int kMmaWarp = kSoftmax / 32, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = kSoftmax + 32 * (1 + kCopyWarps);
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 constexpr int kLeast = 4;
 constexpr int kExtra = 2;
@@ -160,7 +162,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-template <typename T, int D, bool kGeneral>
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// How a score follows from q.k: by a positive scale, by any scale, or capped.
+enum Mode { kScaled, kSigned, kCapped };
+
+template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_constant__ TcParams tp) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -190,8 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     tc::fence_after_sync();
     const uint32_t tmem = tmem_base;
 
-    if (warp == kCopyWarp) {
-        // ---- Q of each segment, then its K and V tiles in turn
+    if (warp >= kCopyWarp) {
+        // ---- Q of each segment (the first copying warp), then its K and V tiles,
+        // the ring's tiles in turn to the copying warps
+        const int me = warp - kCopyWarp;
         const int nbox = kKeys / tp.box_rows;  // boxes of a tile, one lane each
         uint32_t g = 0, seg = 0;               // tiles copied, segments
         bool ok = true;
@@ -200,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
             if (!run_segment(p, run, s0, s1)) break;
             const Item it = run.item;
             const int halves = it.nt > tp.tth ? 2 : 1;
-            if (seg > 0 && !(ok = warp_wait(&q_empty, (seg - 1) & 1u, p, 50))) break;
-            if (lane == 0) {
+            if (me == 0 && seg > 0 && !(ok = warp_wait(&q_empty, (seg - 1) & 1u, p, 50))) break;
+            if (me == 0 && lane == 0) {
                 mbar_arrive_expect_tx(&q_full, uint32_t(halves) * C::kCh * G * tp.tth * 128);
                 for (int h = 0; h < halves; ++h)
                     for (int c = 0; c < C::kCh; ++c)
@@ -209,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                  it.row0 + h * tp.tth, &q_full);
             }
             ++seg;
-            if (lane == 0 && s0 == 0 && s1 < it.tiles) p.desc[blockIdx.x] = join_desc(p, run);
+            if (me == 0 && lane == 0 && s0 == 0 && s1 < it.tiles) p.desc[blockIdx.x] = join_desc(p, run);
             auto page_z = [&](int j) {  // page-head of this lane's box of tile j
                 const int key = (it.t0 + s0 + j) * kKeys + lane * tp.box_rows;
                 if (j >= s1 - s0 || lane >= nbox || key >= it.len) return 0;
@@ -225,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 const bool mine = lane < nbox && key < it.len;
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
                 for (int kv = 0; kv < 2; ++kv, ++g) {
+                    if (int(g % kCopyWarps) != me) continue;
                     const uint32_t st = g % C::kStages;
                     if (g >= uint32_t(C::kStages) &&
                         !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 51 + kv)))
@@ -245,10 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         if (!ok) {
             for (uint32_t i = 0; i < uint32_t(C::kStages) && i < g; ++i) {
                 const uint32_t gg = g - 1 - i;
-                warp_wait(&full[gg % C::kStages], (gg / C::kStages) & 1u, p, 53);
+                if (int(gg % kCopyWarps) == me) warp_wait(&full[gg % C::kStages], (gg / C::kStages) & 1u, p, 53);
             }
         }
-        if (seg > 0) warp_wait(&q_full, (seg - 1) & 1u, p, 54);
+        if (me == 0 && seg > 0) warp_wait(&q_full, (seg - 1) & 1u, p, 54);
     } else if (warp == kMmaWarp) {
         // ---- the MMAs; the whole warp walks the loop, one lane issues
         const bool leader = elect_one();
@@ -339,10 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 128u * h + lanes, to = tmem + 256u + 128u * h + lanes;
         const int tok_h = row / G, head = row % G;
-        const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
-        auto value = [&](float x) {  // the score in log2 units
-            return kGeneral && p.cap_in != 0.f ? score<true>(x, p) : score<false>(x, p);
-        };
+        const float sign = (kMode == kCapped ? p.cap_in : p.scale_log2) < 0.f ? -1.f : 1.f;
         uint32_t ns = 0, no = 0;  // S tiles and O results taken
         bool ok = true;           // after a time-out: no more waits, every barrier still met
         while (run.u < run.end) {
@@ -380,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                 float x[2];
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
-                                    x[k] = kGeneral ? v[c & 1][i + k] * sign : v[c & 1][i + k];
+                                    x[k] = kMode != kScaled ? v[c & 1][i + k] * sign : v[c & 1][i + k];
                                     if (masked && (32 * c + i + k > hi || 32 * c + i + k <= lo)) x[k] = -CUDART_INF_F;
                                 }
                                 m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], x[0], x[1]);
@@ -390,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     };
                     float mt = edge ? row_max(std::true_type{}) : row_max(std::false_type{});
-                    if (mt != -CUDART_INF_F) mt = value(kGeneral ? mt * sign : mt);
+                    if (mt != -CUDART_INF_F) mt = score<kMode == kCapped>(kMode != kScaled ? mt * sign : mt, p);
                     if (j == 0) {
                         top = mt;
                     } else if (__any_sync(0xffffffffu, mt - top > kGrowth)) {
@@ -413,7 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     // second pass: the weights
                     const float base = top == -CUDART_INF_F ? 0.f : top;
                     unsigned long long s2[2] = {0ull, 0ull};  // pairs of sums
-                    const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2), base2 = pack2(-base, -base);
+                    const float scale = kMode == kCapped ? p.cap_in : p.scale_log2;
+                    const float b = kMode == kCapped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
+                    const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
+                    const unsigned long long one2 = pack2(1.f, 1.f), cap2 = pack2(k2, k2);
                     auto weights = [&](auto masked) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -422,13 +441,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                             uint32_t w[16];
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
-                                float e[2] = {v[c & 1][i], v[c & 1][i + 1]};
-                                if (kGeneral) {
-                                    e[0] = value(e[0]) - base;
-                                    e[1] = value(e[1]) - base;
+                                unsigned long long e2 = pack2(v[c & 1][i], v[c & 1][i + 1]);
+                                float e[2];
+                                if (kMode == kCapped) {  // score() less the base, two at a time
+                                    unpack2(mul2(e2, scale2), e[0], e[1]);
+                                    unpack2(add2(pack2(exp2_approx(e[0]), exp2_approx(e[1])), one2), e[0], e[1]);
+                                    e2 = fma2(pack2(rcp_approx(e[0]), rcp_approx(e[1])), cap2, base2);
                                 } else {
-                                    unpack2(fma2(pack2(e[0], e[1]), scale2, base2), e[0], e[1]);
+                                    e2 = fma2(e2, scale2, base2);
                                 }
+                                unpack2(e2, e[0], e[1]);
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     e[k] = exp2_approx(e[k]);
@@ -527,9 +549,8 @@ cudaError_t launch(const TcParams &tp, int grid, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(Cfg<D>::kSmem), s, tp);
     };
-    // the general form: capped scores, or a scale that does not keep the order of q.k
-    return tp.p.cap_in != 0.f || !(tp.p.scale_log2 > 0.f) ? go(attention_tc_kernel<T, D, true>)
-                                                          : go(attention_tc_kernel<T, D, false>);
+    if (tp.p.cap_in != 0.f) return go(attention_tc_kernel<T, D, kCapped>);
+    return tp.p.scale_log2 > 0.f ? go(attention_tc_kernel<T, D, kScaled>) : go(attention_tc_kernel<T, D, kSigned>);
 }
 
 }  // namespace tc5
