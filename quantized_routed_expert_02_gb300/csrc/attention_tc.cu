@@ -14,7 +14,6 @@
 // 16 bits as those up to 1, and sums are fp32), so most tiles leave O alone.
 // Tensor memory: S/P of half h at column 128 h, O of half h at 256 + 128 h.
 #include <algorithm>
-#include <type_traits>
 
 #include <cuda.h>
 
@@ -87,6 +86,7 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t slab)
 
 #define R4(a, i) "=f"(a[i]), "=f"(a[i + 1]), "=f"(a[i + 2]), "=f"(a[i + 3])
 #define W4(a, i) "+f"(a[i]), "+f"(a[i + 1]), "+f"(a[i + 2]), "+f"(a[i + 3])
+#define F4(a, i) "f"(a[i]), "f"(a[i + 1]), "f"(a[i + 2]), "f"(a[i + 3])
 #define S4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
 // 32 consecutive columns of this thread's lane; the values are there after wait_ld32.
 __device__ __forceinline__ void tmem_ld32(uint32_t t, float (&v)[32]) {
@@ -109,6 +109,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&v)[16]) {
         S4(v, 0), S4(v, 4), S4(v, 8), S4(v, 12)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t t, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+        F4(v, 0), F4(v, 4), F4(v, 8), F4(v, 12), F4(v, 16), F4(v, 20), F4(v, 24), F4(v, 28)
+        : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld16(uint32_t t, float (&v)[16]) {
     asm volatile(
@@ -123,6 +130,7 @@ __device__ __forceinline__ void wait_ld16(float (&v)[16]) {
 #undef R4
 #undef W4
 #undef S4
+#undef F4
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t is = 0;
@@ -180,7 +188,7 @@ template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_constant__ TcParams tp) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2],
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2][2],
         o_full[2], drain;
     __shared__ uint32_t tmem_base;
     const Params &p = tp.p;
@@ -191,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
-        for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h], 4), mbar_init(&o_full[h], 1);
+        for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 4), mbar_init(&p_ready[h][1], 4), mbar_init(&o_full[h], 1);
         mbar_init(&drain, 1);
     }
     fence_mbar_init();
@@ -285,13 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 tc::commit_arrive(&s_full[h]);
             }
         };
-        auto pv = [&](int h, uint32_t st, bool acc) {
+        auto pv = [&](int h, uint32_t st, int chunk, bool acc) {  // 32 keys
             if (leader) {
                 const uint64_t dv = desc_mn_sw128(ring + st * C::kTileB, C::kSlab);
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 2048 bytes on
-                    mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 8u * k, dv + uint64_t(128 * k), tp.idesc_pv,
-                           acc || k > 0);
+                for (int k = 0; k < 2; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
+                    mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 32u * chunk + 8u * k,
+                           dv + uint64_t(128 * (2 * chunk + k)), tp.idesc_pv, acc || k > 0);
             }
         };
         while (ok && run.u < run.end) {
@@ -330,10 +338,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     if (!(ok = warp_wait(&full[ks], ((g + 2 * j + 2) / C::kStages) & 1u, p, 58))) break;
                 }
                 for (int h = 0; ok && h < halves; ++h) {
-                    if (!(ok = warp_wait(&p_ready[h], np[h] & 1u, p, 59))) break;
+                    if (!(ok = warp_wait(&p_ready[h][0], np[h] & 1u, p, 59))) break;
+                    tc::fence_after_sync();
+                    pv(h, vs, 1, j > 0);
+                    pv(h, vs, 2, true);
+                    __syncwarp();
+                    if (!(ok = warp_wait(&p_ready[h][1], np[h] & 1u, p, 59))) break;
                     ++np[h];
                     tc::fence_after_sync();
-                    pv(h, vs, j > 0);
+                    pv(h, vs, 3, true);
+                    pv(h, vs, 0, true);
                     if (j + 1 < n) qk(h, ks);
                     else if (leader) tc::commit_arrive(&o_full[h]);
                 }
@@ -359,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         const uint32_t ts = tmem + 128u * h + lanes, to = tmem + 256u + 128u * h + lanes;
         const int tok_h = row / G, head = row % G;
         const float sign = (kMode == kCapped ? p.cap_in : p.scale_log2) < 0.f ? -1.f : 1.f;
+        const float hidden = -CUDART_INF_F * sign;  // the q.k of a key that a row does not see
         uint32_t ns = 0, no = 0;  // S tiles and O results taken
         bool ok = true;           // after a time-out: no more waits, every barrier still met
         while (run.u < run.end) {
@@ -380,32 +395,51 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     const bool edge =
                         key0 + kKeys - 1 > first || (p.window > 0 && key0 <= first + nth - 1 - p.window);
                     const int hi = at - key0, lo = p.window > 0 ? hi - p.window : -1;  // sees lo < i <= hi
-                    // first pass over the row: its maximum (the score grows with sign * q.k,
-                    // so the maximum of those gives the maximum of the scores); the masked form
-                    // is code of its own, or every tile would pay for the comparisons
-                    float v[2][32];
-                    auto row_max = [&](auto masked) {
-                        float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                        tmem_ld32(ts, v[0]);
-#pragma unroll
+                    // a tile that some row does not see whole: what it does not see becomes the
+                    // score of weight 0, in place, so that the passes below (whose code is long)
+                    // exist once and pay for no comparisons
+                    if (edge) {
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            wait_ld32(v[c & 1]);
-                            if (c < 3) tmem_ld32(ts + 32 * (c + 1), v[(c + 1) & 1]);
+                            float u[32];
+                            tmem_ld32(ts + 32 * c, u);
+                            wait_ld32(u);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float x[2];
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    x[k] = kMode != kScaled ? v[c & 1][i + k] * sign : v[c & 1][i + k];
-                                    if (masked && (32 * c + i + k > hi || 32 * c + i + k <= lo)) x[k] = -CUDART_INF_F;
-                                }
-                                m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], x[0], x[1]);
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i > hi || 32 * c + i <= lo) u[i] = hidden;
+                            tmem_st32(ts + 32 * c, u);
                         }
-                        tmem_ld32(ts, v[0]);  // for the second pass
-                        return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                    };
-                    float mt = edge ? row_max(std::true_type{}) : row_max(std::false_type{});
+                        wait_st();
+                    }
+                    // first pass over the row: its maximum (the score grows with sign * q.k,
+                    // so the maximum of those gives the maximum of the scores).  Of the four
+                    // chunks of 32 keys three fit in registers: 1, 2 and 3 stay for the second
+                    // pass, chunk 0 is read again behind chunk 2's arithmetic.
+                    float v[3][32];
+                    float mt;
+                    {
+                        float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                        auto take = [&](const float (&u)[32]) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2)
+                                m4[(i >> 1) & 3] = kMode != kScaled
+                                                       ? max3(m4[(i >> 1) & 3], u[i] * sign, u[i + 1] * sign)
+                                                       : max3(m4[(i >> 1) & 3], u[i], u[i + 1]);
+                        };
+                        tmem_ld32(ts, v[0]);
+                        tmem_ld32(ts + 32, v[1]);
+                        tmem_ld32(ts + 64, v[2]);
+                        wait_ld32(v[0]);
+                        wait_ld32(v[1]);
+                        wait_ld32(v[2]);
+                        take(v[0]);
+                        tmem_ld32(ts + 96, v[0]);
+                        take(v[1]);
+                        take(v[2]);
+                        wait_ld32(v[0]);
+                        take(v[0]);
+                        mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    }
                     if (mt != -CUDART_INF_F) mt = score<kMode == kCapped>(kMode != kScaled ? mt * sign : mt, p);
                     if (j == 0) {
                         top = mt;
@@ -433,15 +467,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     const float b = kMode == kCapped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
                     const unsigned long long one2 = pack2(1.f, 1.f), cap2 = pack2(k2, k2);
-                    auto weights = [&](auto masked) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            wait_ld32(v[c & 1]);
-                            if (c < 3) tmem_ld32(ts + 32 * (c + 1), v[(c + 1) & 1]);
+                    {
+                        auto take = [&](int c, const float (&u)[32]) {
                             uint32_t w[16];
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
-                                unsigned long long e2 = pack2(v[c & 1][i], v[c & 1][i + 1]);
+                                unsigned long long e2 = pack2(u[i], u[i + 1]);
                                 float e[2];
                                 if (kMode == kCapped) {  // score() less the base, two at a time
                                     unpack2(mul2(e2, scale2), e[0], e[1]);
@@ -454,24 +485,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     e[k] = exp2_approx(e[k]);
-                                    if (masked && (32 * c + i + k > hi || 32 * c + i + k <= lo)) e[k] = 0.f;
+                                    // capped, or times 0, an infinity does not give weight 0 by itself
+                                    if (kMode != kScaled && u[i + k] == hidden) e[k] = 0.f;
                                 }
                                 s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], pack2(e[0], e[1]));
                                 // rounded for the product; the sum keeps the weight whole
                                 w[i / 2] = Pair<T>::make(e[0], e[1]);
                             }
-                            tmem_st16(ts + 16 * c, w);
-                        }
-                    };
-                    if (edge) weights(std::true_type{});
-                    else weights(std::false_type{});
+                            tmem_st16(ts + 32 * c, w);  // over the chunk's own scores
+                        };
+                        auto ready = [&](uint64_t *bar) {
+                            wait_st();
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar);
+                        };
+                        take(1, v[1]);
+                        tmem_ld32(ts, v[1]);
+                        take(2, v[2]);
+                        ready(&p_ready[h][0]);  // the product of chunks 1 and 2 can begin
+                        take(3, v[0]);
+                        wait_ld32(v[1]);
+                        take(0, v[1]);
+                        ready(&p_ready[h][1]);
+                    }
                     float sa, sb;
                     unpack2(add2(s2[0], s2[1]), sa, sb);
                     sum += sa + sb;
-                    wait_st();
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_ready[h]);
                 }
                 // ---- the half's result
                 ok = ok && warp_wait(&o_full[h], no & 1u, p, 63 + h);
