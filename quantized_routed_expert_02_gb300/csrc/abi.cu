@@ -42,6 +42,7 @@ moe_status moeq4k::device_info(int *sms, int *dev_out) {
         if (init_prefill_tc(dev) != cudaSuccess) return MOE_ERR_CUDA;
         if (init_router_tc() != cudaSuccess) return MOE_ERR_CUDA;
         if (init_decode_stream(dev) != cudaSuccess) return MOE_ERR_CUDA;
+        if (init_attention() != cudaSuccess) return MOE_ERR_CUDA;
         g_dev[dev].sms = n;
         g_dev[dev].id = dev;
         g_dev[dev].ready = true;

@@ -488,13 +488,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) attention_join_kernel(cons
     }
 }
 
+constexpr int kStreamSmem = kWarps * kRing;
+
+// f on every form of the kernel, until one fails.
+template <typename F>
+cudaError_t each_stream(F f) {
+    cudaError_t e = cudaSuccess;
+    auto of = [&](auto type) {
+        using T = decltype(type);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, 1, false>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, 1, true>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, 2, false>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, 2, true>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, 1, false>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, 1, true>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, 2, false>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, 2, true>);
+    };
+    of(__half());
+    of(__nv_bfloat16());
+    return e;
+}
+
 template <typename T, int D, int MT>
 cudaError_t launch_stream_cap(const StreamParams &sp, int grid, cudaStream_t s) {
-    const size_t smem = size_t(kWarps) * kRing;
     auto go = [&](auto kernel) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return e;
-        return launch_pdl(kernel, dim3(grid), dim3(kThreads), smem, s, sp);
+        return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(kStreamSmem), s, sp);
     };
     return sp.p.cap_in != 0.f ? go(attention_stream_kernel<T, D, MT, true>)
                               : go(attention_stream_kernel<T, D, MT, false>);
@@ -538,6 +557,14 @@ size_t attention_part_bytes(int D) {
     using namespace attn;
     return kDescBytes +
            std::max(size_t(2) * kMaxCtas * part_floats(kMaxRows, D) * sizeof(float), tc_part_bytes(D));
+}
+
+cudaError_t init_attention() {
+    using namespace attn;
+    const cudaError_t e = each_stream([](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+    });
+    return e != cudaSuccess ? e : init_tc();
 }
 
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s) {

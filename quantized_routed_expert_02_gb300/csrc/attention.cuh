@@ -49,22 +49,6 @@ struct Params {
     unsigned long long wait_ns;
 };
 
-// Wait for a phase, for at most limit_ns.  The global timer takes longer to
-// read than a short wait lasts (about half a microsecond), so it is looked at
-// once in 1024 polls only.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    uint64_t start = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 1023u) == 0) {
-            const uint64_t now = global_timer_ns();
-            if (start == 0) start = now;
-            else if (now - start > limit_ns) return false;
-        }
-    }
-}
-
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -254,6 +238,7 @@ cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int
 
 // The tensor-core kernel (many rows per key/value head).
 size_t tc_part_bytes(int D);
+cudaError_t init_tc();
 cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s);
 
 }  // namespace attn

@@ -562,17 +562,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
 template <typename T, int D>
 cudaError_t launch(const TcParams &tp, int grid, cudaStream_t s) {
     auto go = [&](auto kernel) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
-        if (e != cudaSuccess) return e;
         return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(Cfg<D>::kSmem), s, tp);
     };
     if (tp.p.cap_in != 0.f) return go(attention_tc_kernel<T, D, kCapped>);
     return tp.p.scale_log2 > 0.f ? go(attention_tc_kernel<T, D, kScaled>) : go(attention_tc_kernel<T, D, kSigned>);
 }
 
+template <typename T, int D>
+cudaError_t init() {
+    auto set = [](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    };
+    cudaError_t e = set(attention_tc_kernel<T, D, kScaled>);
+    if (e == cudaSuccess) e = set(attention_tc_kernel<T, D, kSigned>);
+    if (e == cudaSuccess) e = set(attention_tc_kernel<T, D, kCapped>);
+    return e;
+}
+
 }  // namespace tc5
 
 size_t tc_part_bytes(int D) { return size_t(2) * tc5::kMaxGrid * part_floats(2 * tc5::kHalf, D) * 4; }
+
+cudaError_t init_tc() {
+    using namespace tc5;
+    cudaError_t e = init<__half, 64>();
+    if (e == cudaSuccess) e = init<__half, 128>();
+    if (e == cudaSuccess) e = init<__nv_bfloat16, 64>();
+    if (e == cudaSuccess) e = init<__nv_bfloat16, 128>();
+    return e;
+}
 
 cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s) {
     using namespace tc5;

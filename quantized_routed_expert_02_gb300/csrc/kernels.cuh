@@ -183,6 +183,7 @@ bool encode_rows_map(CUtensorMap *map, const void *base, const PagedBatch &b, mo
                      int tokens);
 // Counters and scratch for partial results of split key ranges.
 size_t attention_part_bytes(int D);
+cudaError_t init_attention();
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s);
 
 }  // namespace moeq4k

@@ -8,10 +8,9 @@
 // pos, as in fp64, at a 64-bit integer product a pair.
 //
 // Bytes bound (every row read once and written once) as long as the arithmetic
-// stays small: a warp takes a row (or, with few rows, a share of its heads),
-// works out the row's sines once and keeps each lane's eight pairs in registers
-// for all the row's heads, so that a head costs its loads, packed fp32 arithmetic
-// and its stores, with no barrier.
+// stays small: a warp works out a row's sines once and keeps each lane's eight
+// pairs in registers for all the heads of the row that are its, so that a head
+// costs its loads, packed fp32 arithmetic and its stores, with no barrier.
 #include <algorithm>
 
 #include "common.cuh"
@@ -25,7 +24,7 @@ namespace rope {
 constexpr int kMaxPairs = 64;  // D / 2
 constexpr int kWarps = 4;
 constexpr int kCtas = 4;       // on an SM
-constexpr int kBatch = 4;      // heads' chunks that a lane has in flight
+constexpr int kBatch = 3;      // heads' chunks that a lane has in flight
 
 // 2^64 times the fraction of a turn per position.
 __device__ __forceinline__ unsigned long long turn_fraction(double f) {
@@ -35,28 +34,40 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
     return static_cast<unsigned long long>(__double2ll_rn(t * 4611686018427387904.0)) << 2;
 }
 
-// The last sequence that starts at or before `row`, found by a whole warp in
-// steps of 32 ways.
-__device__ __forceinline__ int find_seq(const PagedBatch &p, int row, int lane) {
+// The last sequence that starts at or before `row`: one thread alone, or a
+// whole warp for one row in steps of 32 ways.
+__device__ __forceinline__ int find_seq(const PagedBatch &p, int row) {
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.offs[mid] <= row) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int find_seq_warp(const PagedBatch &p, int row, int lane) {
     int lo = 0, n = p.B;  // among [lo, lo + n)
     while (n > 1) {
         const int step = (n + 31) / 32;
         const int b = lo + lane * step;
         const unsigned before = __ballot_sync(0xffffffffu, b < lo + n && p.offs[b] <= row);
-        const int last = before == 0u ? 0 : 31 - __clz(before);
-        const int at = lo + last * step;
+        const int at = lo + (before == 0u ? 0 : 31 - __clz(before)) * step;
         n = min(step, lo + n - at);
         lo = at;
     }
     return lo;
 }
 
-// A warp takes units of (row, share of its heads): `shares` of `share` heads
-// each.  Lane: chunk c = lane % (D / 16) of a head at a time, kBatch of them
-// loaded together: the channels 8 c .. 8 c + 7 and the 8 they pair with (rotated
-// halves), or 16 in a row.
+// The work is a run of steps, 512 / D heads each (what a warp turns at a time),
+// row after row; a warp takes `run` of them, whatever the number of rows.
+// Lane: chunk c = lane % (D / 16) of a head at a time: the channels
+// 8 c .. 8 c + 7 and the 8 they pair with (rotated halves), or 16 in a row.
+// kBatch of them are loaded ahead, over the ends of rows too, each slot again
+// as soon as it is used; the places in the cache of a warp's next 32 rows are looked
+// up together, a row per lane, so that no row waits for the chain of table loads.
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const RopeArgs a, int shares, int share) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const RopeArgs a, int run) {
     __shared__ __align__(16) float co_sh[kWarps][kMaxPairs], si_sh[kWarps][kMaxPairs];
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -80,44 +91,67 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
     const int c = lane % per, sub = lane / per, step = 32 / per;
     const bool in_rot = 16 * c < a.rot, norms = a.qw != nullptr || a.kw != nullptr;
     const bool split = in_rot && !kInterleaved;
+    const float mean = 1.f / float(D);  // exact: D is a power of two
     const int c0 = split ? 8 * c : 16 * c, c1 = split ? 8 * c + half : 16 * c + 8;
-    const long units = long(a.b.N) * shares;
-    for (long un = long(blockIdx.x) * kWarps + warp; un < units; un += long(gridDim.x) * kWarps) {
-        const int row = int(un / shares), h0 = int(un - long(row) * shares) * share, h1 = min(heads, h0 + share);
-        const T *src = static_cast<const T *>(a.qkv) + size_t(row) * heads * D;
-        uint4 in[kBatch][2];
-        auto load = [&](int h) {
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int u = h + k * step + sub;
-                in[k][0] = in[k][1] = make_uint4(0, 0, 0, 0);
-                if (u < h1) {
-                    in[k][0] = *reinterpret_cast<const uint4 *>(src + size_t(u) * D + c0);
-                    in[k][1] = *reinterpret_cast<const uint4 *>(src + size_t(u) * D + c1);
-                }
-            }
-        };
-        load(h0);  // under way while the row's place and sines are worked out
-        int pos[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) pos[k] = a.pos[size_t(axis[k]) * a.b.N + row];
-        const int b = find_seq(a.b, row, lane);
-        const SeqView sv = seq_view(a.b, b, a.hdr, false);
-        if (!sv.ok || row < sv.first || row >= sv.first + sv.n) continue;  // a row of no sequence
-        const int at = sv.len - sv.n + (row - sv.first);                    // cache index
-        long cache = -1;  // the first key/value head's cache row
-        if (at >= 0) {
-            const int pg = page_of(a.b, b, at, a.hdr);
-            if (pg >= 0) cache = long(pg) * Hkv * a.b.page + at % a.b.page;
+    // the warp's steps [at_step, end): rows from row on, heads [h0, h1) of it
+    const int row_steps = (heads + step - 1) / step, total = a.b.N * row_steps;
+    const int begin = (blockIdx.x * kWarps + warp) * run, end = min(total, begin + run);
+    if (begin >= end) return;
+    const int row_first = begin / row_steps, row_last = (end - 1) / row_steps;
+    auto heads_of = [&](int r, int &from, int &to) {  // an empty range past the last row
+        from = r == row_first ? (begin - r * row_steps) * step : 0;
+        to = r > row_last ? 0 : r == row_last ? min(heads, (end - r * row_steps) * step) : heads;
+    };
+    uint4 in[kBatch][2];
+    auto fetch = [&](int k, int row, int h0, int h1) {  // slot k of the batch that starts at head h0
+        const int u = h0 + k * step + sub;
+        in[k][0] = in[k][1] = make_uint4(0, 0, 0, 0);
+        if (u < h1) {
+            const T *p = static_cast<const T *>(a.qkv) + (size_t(row) * heads + u) * D;
+            in[k][0] = *reinterpret_cast<const uint4 *>(p + c0);
+            in[k][1] = *reinterpret_cast<const uint4 *>(p + c1);
         }
-        __syncwarp();  // the unit before has read its sines
+    };
+    int h0, h1;
+    heads_of(row_first, h0, h1);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) fetch(k, row_first, h0, h1);
+    int pos[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) pos[k] = a.pos[size_t(axis[k]) * a.b.N + row_first];
+    bool live32 = false;
+    long cache32 = -1;  // of this lane's row among the next 32: the first key/value head's cache row
+    for (int row = row_first; row <= row_last; ++row) {
+        const int turn = (row - row_first) & 31;
+        if (turn == 0) {
+            const int r = min(row + lane, row_last);
+            const int b = row == row_last ? find_seq_warp(a.b, row, lane) : find_seq(a.b, r);
+            const SeqView sv = seq_view(a.b, b, a.hdr, false);
+            live32 = sv.ok && r >= sv.first && r < sv.first + sv.n;
+            cache32 = -1;
+            const int at = sv.len - sv.n + (r - sv.first);  // cache index
+            if (live32 && at >= 0) {
+                const int pg = page_of(a.b, b, at, a.hdr);
+                if (pg >= 0) cache32 = long(pg) * Hkv * a.b.page + at % a.b.page;
+            }
+        }
+        const bool live = __shfl_sync(0xffffffffu, int(live32), turn) != 0;  // else a row of no sequence
+        const long cache = __shfl_sync(0xffffffffu, cache32, turn);
+        const int nrow = min(row + 1, row_last);
+        int nh0, nh1;  // the next row's
+        heads_of(row + 1, nh0, nh1);
+        T *q_row = static_cast<T *>(a.q_out) + size_t(row) * Hq * D;
+        T *k_row = static_cast<T *>(a.k) + max(cache, 0l) * D, *v_row = static_cast<T *>(a.v) + max(cache, 0l) * D;
+        __syncwarp();  // the row before has read its sines
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const long long turn = static_cast<long long>(static_cast<unsigned long long>(static_cast<long long>(pos[k])) * frac[k]);
+            const long long angle = static_cast<long long>(static_cast<unsigned long long>(static_cast<long long>(pos[k])) * frac[k]);
             // the top 32 bits (rounded): a signed fraction of a turn, in half turns for sincospi
-            const int top = static_cast<int>((turn + 0x80000000ll) >> 32);
+            const int top = static_cast<int>((angle + 0x80000000ll) >> 32);
             sincospif(float(top) * 4.6566128730773926e-10f, &si_sh[warp][lane + 32 * k], &co_sh[warp][lane + 32 * k]);  // * 2^-31
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) pos[k] = a.pos[size_t(axis[k]) * a.b.N + nrow];
         __syncwarp();
         // two pairs at a time: cosines, sines, negated sines
         unsigned long long co[4], si[4], ni[4];
@@ -131,10 +165,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
             ni[2 * i] = pack2(-y.x, -y.y), ni[2 * i + 1] = pack2(-y.z, -y.w);
         }
         for (int h = h0; h < h1; h += kBatch * step) {
-            if (h > h0) load(h);
+            const bool more = h + kBatch * step < h1;  // of this row
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                if (h + k * step >= h1) break;
                 const int head = min(h + k * step + sub, h1 - 1);  // no lane leaves before the sum of squares
                 const bool mine = h + k * step + sub < h1;
                 const uint32_t w[8] = {in[k][0].x, in[k][0].y, in[k][0].z, in[k][0].w,
@@ -145,6 +178,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
                     const float2 f = Pair<T>::load(w[i]);
                     v[i] = pack2(f.x, f.y);
                 }
+                fetch(k, more ? row : nrow, more ? h + kBatch * step : nh0, more ? h1 : nh1);
+                if (h + k * step >= h1) continue;
                 const bool query = head < Hq, value = head >= Hq + Hkv;
                 if (norms) {
                     unsigned long long s2[2] = {0ull, 0ull};
@@ -156,7 +191,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
                     for (int o = per >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                     const float *nw = query ? a.qw : value ? nullptr : a.kw;
                     if (nw != nullptr) {
-                        const float inv = 1.0f / sqrtf(ss / float(D) + a.eps);
+                        const float inv = rsqrtf(fmaf(ss, mean, a.eps));
                         const unsigned long long inv2 = pack2(inv, inv);
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) {
@@ -184,14 +219,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
                         }
                     }
                 }
-                T *dst = nullptr;
-                if (query) {
-                    dst = static_cast<T *>(a.q_out) + (size_t(row) * Hq + head) * D;
-                } else if (cache >= 0) {
-                    const int kh = value ? head - Hq - Hkv : head - Hq;
-                    dst = static_cast<T *>(value ? a.v : a.k) + (cache + long(kh) * a.b.page) * D;
-                }
-                if (mine && dst != nullptr) {
+                // heads are D apart in the queries, a page's rows apart in the cache
+                T *dst = query ? q_row + head * D : value ? v_row + (head - Hq - Hkv) * (a.b.page * D)
+                                                          : k_row + (head - Hq) * (a.b.page * D);
+                if (mine && live && (query || cache >= 0)) {
                     uint32_t o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -204,6 +235,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
                 }
             }
         }
+        h0 = nh0;
+        h1 = nh1;
     }
 }
 
@@ -211,16 +244,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
 
 cudaError_t launch_rope_append(const RopeArgs &a, int num_sms, cudaStream_t s) {
     using namespace rope;
-    // few rows: a row's heads are shared out until every SM has its warps; a
-    // share is whole steps of 512 / D heads (what a warp turns at a time)
     const int heads = a.b.Hq + 2 * a.b.Hkv, step = 512 / a.b.D, warps = num_sms * kCtas * kWarps;
-    const int most = (heads + step - 1) / step;
-    int shares = std::min(most, std::max(1, warps / a.b.N));
-    const int share = (most + shares - 1) / shares * step;
-    shares = (heads + share - 1) / share;
-    const long units = long(a.b.N) * shares;
-    const dim3 grid(unsigned(std::min<long>((units + kWarps - 1) / kWarps, long(num_sms) * kCtas))), block(kWarps * 32);
-    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, size_t(0), s, a, shares, share); };
+    const int total = a.b.N * ((heads + step - 1) / step);  // at most 2^22 * 192
+    const int run = (total + warps - 1) / warps;
+    const int used = (total + run - 1) / run;
+    const dim3 grid((used + kWarps - 1) / kWarps), block(kWarps * 32);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, size_t(0), s, a, run); };
     if (a.type == MOE_F16) return a.interleaved ? go(rope_append_kernel<__half, true>) : go(rope_append_kernel<__half, false>);
     return a.interleaved ? go(rope_append_kernel<__nv_bfloat16, true>) : go(rope_append_kernel<__nv_bfloat16, false>);
 }
