@@ -68,7 +68,10 @@ __global__ void add_rmsnorm_kernel(const AddNormArgs a) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const size_t row = size_t(blockIdx.x) * a.H;
     const TX *x = static_cast<const TX *>(a.x) + row;
-    float v[kBlocks][8];
+    // gamma with the rest, not after the reduction's barrier, where the registers do not cost
+    // occupancy (333 rows of 4096 with Q8_K 6.6 -> 5.7 us; rows of 16384 would lose a tenth)
+    constexpr bool kEarly = kBlocks == 1;
+    float v[kBlocks][8], g[kBlocks][8];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
@@ -77,6 +80,7 @@ __global__ void add_rmsnorm_kernel(const AddNormArgs a) {
         for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
         if (c < a.H) {
             load8(x + c, v[i]);
+            if (kEarly) load8(a.gamma + c, g[i]);
             if (a.residual != nullptr) {
                 float r[8];
                 load8(a.residual + row + c, r);
@@ -107,10 +111,9 @@ __global__ void add_rmsnorm_kernel(const AddNormArgs a) {
         const int c = b * kQK + lane * 8;
         if (b * kQK >= a.H) break;
         if (c < a.H) {
-            float g[8];
-            load8(a.gamma + c, g);
+            if (!kEarly) load8(a.gamma + c, g[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * g[j] * inv;
+            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * g[i][j] * inv;
             if (a.y != nullptr) store8(static_cast<TY *>(a.y) + row + c, v[i]);
         }
         if (a.q == nullptr) continue;
