@@ -27,7 +27,7 @@ constexpr int kTile = kWarps * kPiece;    // keys of a tile: a piece for every w
 constexpr int kRing = 24 * 1024;          // bytes of a warp's ring
 constexpr int kMaxRows = 32;
 constexpr int kLeast = 5;
-constexpr int kExtra = 1;
+constexpr int kExtra = 3;
 
 struct StreamParams {
     CUtensorMap mk, mv;

@@ -33,7 +33,7 @@ constexpr int kMmaWarp = kSoftmax / 32, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = kSoftmax + 32 * (1 + kCopyWarps);
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 constexpr int kLeast = 4;
-constexpr int kExtra = 2;
+constexpr int kExtra = 3;
 constexpr float kGrowth = 8.f;             // log2 growth of the maximum that forces a rescale
 
 struct TcParams {
