@@ -118,7 +118,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     const int gid = lane >> 2, tig = lane & 3;
     const int G = p.b.Hq / p.b.Hkv;
     uint8_t *ring = smem + warp * kRing;
-    if (tid == 0) failed = 0;
+    if (tid == 0) {
+        failed = 0;
+        prefetch_map(&sp.mk);
+        prefetch_map(&sp.mv);
+    }
     if (lane == 0)
         for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
@@ -144,7 +148,27 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
             const int pg = page_of(p.b, it.b, key_first + i * kTile, p.hdr);
             return pg < 0 ? p.b.num_pages : pg;  // a bad page: past the tensor, read as zeros
         };
-        int pages = page_at(lane), pages_next = page_at(32 + lane);
+        int pages = page_at(lane), pages_next = n > 32 ? page_at(32 + lane) : 0;
+        // this thread's rows: gid, gid + 8 of each 16; their position, -1 for rows past the tile
+        int pos[MT][2];
+        uint32_t qa[MT][D / 16][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = 16 * m + 8 * h + gid;
+                const int tok = r / G;
+                const bool live = tok < it.nt;
+                pos[m][h] = live ? it.pos0 + tok : -1;
+                const T *row = static_cast<const T *>(p.q) +
+                               (size_t(it.row0 + (live ? tok : 0)) * p.b.Hq + it.kh * G + r % G) * D;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row + 16 * k + 2 * tig);
+                    qa[m][k][h] = live ? w[0] : 0u;
+                    qa[m][k][2 + h] = live ? w[4] : 0u;
+                }
+            }
         int sent = 0;  // pieces of this segment issued
         auto issue = [&]() {
             if (sent > 0 && (sent & 31) == 0) {
@@ -169,26 +193,6 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         };
         for (int i = 0; i < kStages && i < n; ++i) issue();
 
-        // this thread's rows: gid, gid + 8 of each 16; their position, -1 for rows past the tile
-        int pos[MT][2];
-        uint32_t qa[MT][D / 16][4];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = 16 * m + 8 * h + gid;
-                const int tok = r / G;
-                const bool live = tok < it.nt;
-                pos[m][h] = live ? it.pos0 + tok : -1;
-                const T *row = static_cast<const T *>(p.q) +
-                               (size_t(it.row0 + (live ? tok : 0)) * p.b.Hq + it.kh * G + r % G) * D;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row + 16 * k + 2 * tig);
-                    qa[m][k][h] = live ? w[0] : 0u;
-                    qa[m][k][2 + h] = live ? w[4] : 0u;
-                }
-            }
         float o[MT][D / 8][4], mx[MT][2], l[MT][2];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {

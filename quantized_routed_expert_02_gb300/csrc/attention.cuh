@@ -49,6 +49,11 @@ struct Params {
     unsigned long long wait_ns;
 };
 
+// Bring a tensor map (a kernel parameter) into the cache of such descriptors.
+__device__ __forceinline__ void prefetch_map(const void *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -94,92 +99,99 @@ struct Run {
     Item item;
 };
 
-// Every thread of the CTA calls it; `scratch`: (B + 2) longs of shared memory
-// (free again at the next barrier).  A run is at least
-// `least` long.  False:
-// nothing to do.
+// The work of a sequence: its query tiles' key tiles and fixed costs, of one
+// key/value head.
+template <int KT>
+__device__ __forceinline__ long tile_cost(const Params &p, const SeqView &s, int qt) {
+    int nt, pos0, t0, tiles;
+    item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, t0, tiles);
+    return tiles + p.extra;
+}
+
+// a / b for a >= 0, b > 0: as 32 bits where they fit (64-bit division is long).
+__device__ __forceinline__ long div_pos(long a, long b) {
+    if (((a | b) >> 31) == 0) return long(unsigned(a) / unsigned(b));
+    return a / b;
+}
+
+// Every thread of the CTA calls it; `scratch`: B longs of shared memory (free
+// again at the next barrier).  A run is at least `least` long.  False: nothing
+// to do.  A thread per sequence where its tiles are few (decode), a warp where
+// they are many, then each warp sums and searches by itself: at 64 sequences this
+// takes 2 us of the kernel's start where a warp per sequence took 10.
 template <int KT>
 __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run &r) {
+    constexpr int kFew = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int B = p.b.B, Hkv = p.b.Hkv;
-    for (int b = warp; b < B; b += nw) {
-        const SeqView s = seq_view(p.b, b, p.hdr, blockIdx.x == 0 && lane == 0);
-        const int nq = (s.n + p.tt - 1) / p.tt;
+    for (int base = warp * 32; base < B; base += nw * 32) {
+        const int b = base + lane;
+        int nq = 0;
         long total = 0;
-        for (int qt = lane; qt < nq; qt += 32) {
-            int nt, pos0, t0, tiles;
-            item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, t0, tiles);
-            total += tiles + p.extra;
+        if (b < B) {
+            const SeqView s = seq_view(p.b, b, p.hdr, blockIdx.x == 0);
+            nq = (s.n + p.tt - 1) / p.tt;
+            if (nq <= kFew) {
+                for (int qt = 0; qt < nq; ++qt) total += tile_cost<KT>(p, s, qt);
+                scratch[b] = total * Hkv;
+            }
         }
+        for (unsigned many = __ballot_sync(0xffffffffu, nq > kFew); many != 0; many &= many - 1) {
+            const int src = __ffs(many) - 1, nqs = __shfl_sync(0xffffffffu, nq, src);
+            const SeqView s = seq_view(p.b, base + src, p.hdr, false);
+            total = 0;
+            for (int qt = lane; qt < nqs; qt += 32) total += tile_cost<KT>(p, s, qt);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (lane == 0) scratch[b + 1] = total * Hkv;
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            if (lane == 0) scratch[base + src] = total * Hkv;
+        }
     }
     __syncthreads();
-    if (warp == 0) {  // inclusive prefix sums, in place
-        long carry = 0;
-        for (int base = 0; base < B; base += 32) {
-            long v = base + lane < B ? scratch[base + lane + 1] : 0;
+    long U = 0;
+    for (int b = lane; b < B; b += 32) U += scratch[b];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
+    r.per = max(long(least), div_pos(U + gridDim.x - 1, gridDim.x));
+    r.u = r.per * blockIdx.x;
+    r.end = min(U, r.u + r.per);
+    if (r.u >= r.end) return false;
+    // the first position past which a prefix sum over steps of 32 goes
+    auto locate = [&](int n, long at, auto cost, int &which, long &start) {
+        for (int base = 0; base < n; base += 32) {
+            long v = base + lane < n ? cost(base + lane) : 0;
+            const long mine = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long w = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += w;
             }
-            v += carry;
-            if (base + lane < B) scratch[base + lane + 1] = v;
-            carry = __shfl_sync(0xffffffffu, v, 31);
+            const unsigned past = __ballot_sync(0xffffffffu, at + v > r.u);
+            if (past != 0u) {
+                const int src = __ffs(past) - 1;
+                which = base + src;
+                start = at + __shfl_sync(0xffffffffu, v - mine, src);
+                return;
+            }
+            at += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) scratch[0] = 0;
-    }
-    __syncthreads();
-    const long U = scratch[B];
-    r.per = max(long(least), (U + gridDim.x - 1) / gridDim.x);
-    r.u = r.per * blockIdx.x;
-    r.end = min(U, r.u + r.per);
-    if (r.u >= r.end) return false;
-    int lo = 0, hi = B - 1;  // the last sequence that starts at or before u and has work
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (scratch[mid] <= r.u) lo = mid;
-        else hi = mid - 1;
-    }
-    // lo may be followed by empty sequences only at equal positions: the
-    // search takes the last one, which then holds u
-    const SeqView s = seq_view(p.b, lo, p.hdr, false);
-    const int nq = (s.n + p.tt - 1) / p.tt;
-    long at = scratch[lo];
+    };
     Item &it = r.item;
-    r.seq = s;
-    it.b = lo;
-    it.len = s.len;
-    for (int base = 0; base < nq; base += 32) {
-        const int qt = base + lane;
-        int nt = 0, pos0 = 0, t0 = 0, tiles = 0;
-        if (qt < nq) item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, t0, tiles);
-        const long cost = qt < nq ? tiles + p.extra : 0;
-        long v = cost * Hkv;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long w = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += w;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, qt < nq && at + v > r.u);
-        if (past != 0u) {
-            const int src = __ffs(past) - 1;
-            it.qt = base + src;
-            it.nt = __shfl_sync(0xffffffffu, nt, src);
-            it.pos0 = __shfl_sync(0xffffffffu, pos0, src);
-            it.t0 = __shfl_sync(0xffffffffu, t0, src);
-            it.tiles = __shfl_sync(0xffffffffu, tiles, src);
-            const long each = it.tiles + p.extra;
-            const long first = at + __shfl_sync(0xffffffffu, v, src) - each * Hkv;
-            it.kh = int((r.u - first) / each);
-            r.item_u = first + it.kh * each;
-            break;
-        }
-        at += __shfl_sync(0xffffffffu, v, 31);
-    }
-    it.row0 = s.first + it.qt * p.tt;
+    it.b = 0;
+    it.qt = 0;
+    long at = 0, first = 0;
+    locate(B, 0, [&](int b) { return scratch[b]; }, it.b, at);
+    r.seq = seq_view(p.b, it.b, p.hdr, false);
+    const int nq = (r.seq.n + p.tt - 1) / p.tt;
+    if (nq > 1)
+        locate(nq, at, [&](int qt) { return tile_cost<KT>(p, r.seq, qt) * Hkv; }, it.qt, first);
+    else
+        first = at;
+    it.len = r.seq.len;
+    it.row0 = r.seq.first + it.qt * p.tt;
+    item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.t0, it.tiles);
+    const long each = it.tiles + p.extra;
+    it.kh = int(div_pos(r.u - first, each));
+    r.item_u = first + it.kh * each;
     return true;
 }
 
@@ -225,7 +237,7 @@ __device__ __forceinline__ int part_slot(int cta, bool starts_here) { return 2 *
 __device__ __forceinline__ JoinDesc join_desc(const Params &p, const Run &r) {
     const long first = r.item_u + p.extra;
     JoinDesc d;
-    d.parts = int((first + r.item.tiles - 1) / r.per) - int(first / r.per) + 1;
+    d.parts = int(div_pos(first + r.item.tiles - 1, r.per) - div_pos(first, r.per)) + 1;
     d.row0 = r.item.row0;
     d.nt = r.item.nt;
     d.kh = r.item.kh;

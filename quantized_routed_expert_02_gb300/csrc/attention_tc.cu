@@ -178,6 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         mbar_init(&q_empty, 1);
         for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 4), mbar_init(&p_ready[h][1], 4), mbar_init(&o_full[h], 1);
         mbar_init(&drain, 1);
+        prefetch_map(&tp.mq);
+        prefetch_map(&tp.mk);
+        prefetch_map(&tp.mv);
     }
     fence_mbar_init();
     pdl_enter();
