@@ -32,6 +32,7 @@ constexpr int kExtra = 3;
 struct StreamParams {
     CUtensorMap mk, mv;
     Params p;
+    bool join_launch;  // split items are joined by a second launch
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
     __shared__ unsigned failed;
+    __shared__ bool joins;
     const Params &p = sp.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tig = lane & 3;
@@ -127,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
     fence_mbar_init();
     pdl_enter();
-    if (tid == 0) p.desc[blockIdx.x].parts = 0;
+    if (sp.join_launch && tid == 0) p.desc[blockIdx.x].parts = 0;
     Run run;
     if (!run_begin<kTile>(p, kLeast, reinterpret_cast<long *>(smem), run)) return;
     fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
@@ -366,7 +368,25 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 }
             }
         }
-        if (tid == 0 && s0 == 0 && !whole) p.desc[blockIdx.x] = join_desc(p, run);
+        if (sp.join_launch) {
+            if (tid == 0 && s0 == 0 && !whole) p.desc[blockIdx.x] = join_desc(p, run);
+        } else if (!whole) {
+            // the CTA that arrives last joins the parts (all are stored and seen then)
+            const int first_cta = int(div_pos(run.item_u + p.extra, run.per));
+            const JoinDesc d = join_desc(p, run);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                joins = atomicAdd(p.count + first_cta, 1u) + 1 == unsigned(d.parts);
+                if (joins) p.count[first_cta] = 0u;  // for the next call
+            }
+            __syncthreads();
+            if (joins) {
+                __threadfence();
+                join_rows<T, D, kWarps>(p, d, first_cta, kPartRows, kPartRows, p.tt, 0, 1,
+                                        reinterpret_cast<float *>(smem), &sm_m[0][0], &sm_l[0][0]);
+            }
+        }
         run_next<kTile>(p, run);
         if (run.u < run.end) {
             fence_proxy_async_smem();  // the sums in the rings (generic) before the next copies
@@ -375,121 +395,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     }
 }
 
-// ---- joining.  What bounds it is the latency of dependent loads, so their
-// chain is kept short: a group of S warps (S by the number of parts) takes four consecutive
-// rows, each warp every S-th part, four at a time with all their loads in
-// flight together; the warps' results meet in shared memory.  Lane l holds
-// row l / 2 % 4, of each 32 channels the four from 8 (l / 8) + 4 (l % 2).
 constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 4;
-constexpr int kJoinParts = 4;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32, 2) attention_join_kernel(const Params p, int rows, int half, int tth) {
     pdl_enter();
-    constexpr int kVec = D / 32;
-    __shared__ float4 sv[kJoinWarps][kVec][32];
-    __shared__ float sm[kJoinWarps][kJoinRows], sl[kJoinWarps][kJoinRows];
+    __shared__ __align__(16) float sv[kJoinWarps * D * kJoinRows];
+    __shared__ float sm[kJoinWarps * kJoinRows], sl[kJoinWarps * kJoinRows];
     const JoinDesc d = p.desc[blockIdx.x];
     if (d.parts == 0) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.b.Hq / p.b.Hkv;
-    const size_t stride = part_floats(rows, D);
-    const int S = d.parts <= kJoinParts ? 1 : d.parts <= 4 * kJoinParts ? 4 : kJoinWarps;
-    const int group = warp / S, w0 = warp % S, groups = kJoinWarps / S;
-    const int sub = (lane >> 1) & 3, ch0 = 8 * (lane >> 3) + 4 * (lane & 1);
-    const int blocks = (rows + kJoinRows * groups - 1) / (kJoinRows * groups);
-    for (int blk = blockIdx.y; blk < blocks; blk += gridDim.y) {
-        const int row = (blk * groups + group) * kJoinRows + sub;
-        const int tok_h = row % half / G, tok = row / half * tth + tok_h;
-        const bool live = row < rows && tok_h < tth && tok < d.nt;  // rows of no token have no sums
-        float top = -CUDART_INF_F, sum = 0.f;
-        float4 v[kVec];
-#pragma unroll
-        for (int c = 0; c < kVec; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = w0; live && i0 < d.parts; i0 += S * kJoinParts) {
-            float m[kJoinParts], l[kJoinParts];
-            float4 x[kJoinParts][kVec];
-#pragma unroll
-            for (int u = 0; u < kJoinParts; ++u) {
-                const int i = i0 + S * u;
-                m[u] = -CUDART_INF_F;
-                l[u] = 0.f;
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) x[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < d.parts) {
-                    // part 0 is the item's start, the others go on in the CTAs after it
-                    const float *q = p.part + size_t(part_slot(blockIdx.x + i, i == 0)) * stride;
-                    m[u] = q[rows * D + row];
-                    l[u] = q[rows * (D + 1) + row];
-#pragma unroll
-                    for (int c = 0; c < kVec; ++c)
-                        x[u][c] = *reinterpret_cast<const float4 *>(q + part_at(row, 32 * c + ch0, D));
-                }
-            }
-            float up = top;
-#pragma unroll
-            for (int u = 0; u < kJoinParts; ++u) up = fmaxf(up, m[u]);
-            const float base = up == -CUDART_INF_F ? 0.f : up, old = exp2_approx(top - base);
-            top = up;
-            sum *= old;
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) v[c].x *= old, v[c].y *= old, v[c].z *= old, v[c].w *= old;
-#pragma unroll
-            for (int u = 0; u < kJoinParts; ++u) {
-                const float f = exp2_approx(m[u] - base);
-                sum = fmaf(l[u], f, sum);
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) {
-                    v[c].x = fmaf(x[u][c].x, f, v[c].x);
-                    v[c].y = fmaf(x[u][c].y, f, v[c].y);
-                    v[c].z = fmaf(x[u][c].z, f, v[c].z);
-                    v[c].w = fmaf(x[u][c].w, f, v[c].w);
-                }
-            }
-        }
-        bool mine[kVec];  // the vectors this warp finishes
-#pragma unroll
-        for (int c = 0; c < kVec; ++c) mine[c] = S == 1 || c % S == w0;
-        if (S > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) sv[warp][c][lane] = v[c];
-            if (ch0 == 0) {
-                sm[warp][sub] = top;
-                sl[warp][sub] = sum;
-            }
-            __syncthreads();
-            const int first = group * S;
-            for (int w = 0; w < S; ++w) top = fmaxf(top, sm[first + w][sub]);
-            const float base = top == -CUDART_INF_F ? 0.f : top;
-            sum = 0.f;
-#pragma unroll
-            for (int c = 0; c < kVec; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < S; ++w) {
-                const float f = exp2_approx(sm[first + w][sub] - base);
-                sum = fmaf(sl[first + w][sub], f, sum);
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) {
-                    if (!mine[c]) continue;
-                    const float4 y = sv[first + w][c][lane];
-                    v[c].x = fmaf(y.x, f, v[c].x);
-                    v[c].y = fmaf(y.y, f, v[c].y);
-                    v[c].z = fmaf(y.z, f, v[c].z);
-                    v[c].w = fmaf(y.w, f, v[c].w);
-                }
-            }
-        }
-        if (!live) continue;
-        const size_t at = size_t(d.row0 + tok) * p.b.Hq + d.kh * G + row % half % G;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-        for (int c = 0; c < kVec; ++c)
-            if (mine[c])
-                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + at * D + 32 * c + ch0) =
-                    make_uint2(Pair<T>::make(v[c].x * inv, v[c].y * inv), Pair<T>::make(v[c].z * inv, v[c].w * inv));
-        if (p.lse != nullptr && ch0 == 0 && w0 == 0)
-            p.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
-    }
+    join_rows<T, D, kJoinWarps>(p, d, blockIdx.x, rows, half, tth, blockIdx.y, gridDim.y, sv, sm, sl);
 }
 
 constexpr int kStreamSmem = kWarps * kRing;
@@ -540,8 +455,9 @@ Params make_params(const AttnArgs &a) {
     p.cap_log2 = a.softcap * kLog2e;
     p.window = a.window;
     p.hdr = a.hdr;
-    p.desc = reinterpret_cast<JoinDesc *>(a.scratch);
-    p.part = reinterpret_cast<float *>(a.scratch + kDescBytes);
+    p.count = reinterpret_cast<unsigned *>(a.scratch);
+    p.desc = reinterpret_cast<JoinDesc *>(a.scratch + kCountBytes);
+    p.part = reinterpret_cast<float *>(a.scratch + kCountBytes + kDescBytes);
     p.wait_ns = a.wait_ns;
     return p;
 }
@@ -559,7 +475,7 @@ cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int
 
 size_t attention_part_bytes(int D) {
     using namespace attn;
-    return kDescBytes +
+    return kCountBytes + kDescBytes +
            std::max(size_t(2) * kMaxCtas * part_floats(kMaxRows, D) * sizeof(float), tc_part_bytes(D));
 }
 
@@ -580,10 +496,19 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     sp.p = base;
     const int rows = max_new * G <= 16 ? 16 : kMaxRows;
     sp.p.tt = std::max(1, rows / G);
+    sp.p.tt_magic = 0xffffffffu / unsigned(sp.p.tt) + 1;
     sp.p.extra = kExtra;
     if (!encode_pages_map(&sp.mk, a.k, a.b, a.type, kPiece) || !encode_pages_map(&sp.mv, a.v, a.b, a.type, kPiece))
         return cudaErrorInvalidValue;
     const int grid = std::min(2 * num_sms, kMaxCtas);
+    // Few items over many CTAs make many parts of each.  Up to kJoinInside of them the last
+    // CTA joins them on its way out (one token over 93: 9.3 us with the launch, 5.2 without);
+    // more take it longer than a second launch that spreads them over the GPU (one token
+    // over 131071, 76 parts: 52.4 us with the launch, 55.2 without).
+    constexpr long kJoinInside = 16;
+    const long items = long(a.b.B) * a.b.Hkv;
+    const long tiles = (long(a.b.max_pages) * a.b.page + kTile - 1) / kTile + kExtra;  // of an item, at most
+    sp.join_launch = std::min(grid / items, tiles / kLeast) + 1 > kJoinInside;
     cudaError_t e;
     if (a.type == MOE_F16)
         e = a.b.D == 64 ? launch_stream_rows<__half, 64>(sp, rows, grid, s)
@@ -591,7 +516,7 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     else
         e = a.b.D == 64 ? launch_stream_rows<__nv_bfloat16, 64>(sp, rows, grid, s)
                         : launch_stream_rows<__nv_bfloat16, 128>(sp, rows, grid, s);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || !sp.join_launch) return e;
     return launch_join(sp.p, a.type, grid, kMaxRows, kMaxRows, sp.p.tt, s);
 }
 

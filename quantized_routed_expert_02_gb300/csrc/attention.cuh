@@ -8,9 +8,10 @@
 // is cut into equal runs, one per CTA, whatever the sequences' lengths: a CTA's
 // run is a few segments, each a range of key tiles of one item.  An item
 // inside one run is finished there; one that crosses a cut leaves a partial
-// result (unnormalised sums, running maximum and sum) per segment, and a
-// second launch joins them in key order over the whole GPU.  So the order of
-// every sum depends on the shapes alone and results repeat bit for bit.
+// result (unnormalised sums, running maximum and sum) per segment.  These are
+// joined in a fixed order, by the CTA that arrives last (few rows) or by a second
+// launch over the whole GPU (many rows), so that the order of every sum depends
+// on the shapes alone and results repeat bit for bit.
 #pragma once
 
 #include <math_constants.h>
@@ -31,6 +32,11 @@ struct JoinDesc {
     int parts, row0, nt, kh;
 };
 constexpr size_t kDescBytes = (kMaxCtas * sizeof(JoinDesc) + 255) / 256 * 256;
+// Arrivals at each CTA's item, ahead of the descriptors: zero before the first
+// call (moe_workspace_init) and after every call.
+constexpr size_t kCountBytes = 2048;
+static_assert(kMaxCtas * sizeof(unsigned) <= kCountBytes && kCountBytes <= sizeof(unsigned long long) * kSyncWords,
+              "one per CTA, zeroed by moe_workspace_init");
 
 struct Params {
     PagedBatch b;
@@ -42,8 +48,10 @@ struct Params {
     float cap_log2;     // softcap * log2(e)
     int window;
     int tt;             // tokens of a query tile
+    unsigned tt_magic;  // ceil(2^32 / tt), tt > 1: n / tt as a high product (n < 2^23)
     int extra;          // fixed cost of an item, in key tiles
     WsHeader *hdr;
+    unsigned *count;    // [kMaxCtas]
     JoinDesc *desc;     // [kMaxCtas]
     float *part;
     unsigned long long wait_ns;
@@ -78,6 +86,11 @@ struct Item {
     int t0;      // first key tile
     int tiles;   // key tiles, at least 1 (a tile whose rows see nothing has one, all masked)
 };
+
+// Query tiles of a sequence with n new rows.
+__device__ __forceinline__ int query_tiles(const Params &p, int n) {
+    return p.tt == 1 ? n : int(__umulhi(unsigned(n + p.tt - 1), p.tt_magic));
+}
 
 template <int KT>
 __device__ __forceinline__ void item_tiles(int window, int tt, const SeqView &s, int qt, int &nt,
@@ -130,7 +143,7 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
         long total = 0;
         if (b < B) {
             const SeqView s = seq_view(p.b, b, p.hdr, blockIdx.x == 0);
-            nq = (s.n + p.tt - 1) / p.tt;
+            nq = query_tiles(p, s.n);
             if (nq <= kFew) {
                 for (int qt = 0; qt < nq; ++qt) total += tile_cost<KT>(p, s, qt);
                 scratch[b] = total * Hkv;
@@ -147,20 +160,12 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
         }
     }
     __syncthreads();
-    long U = 0;
-    for (int b = lane; b < B; b += 32) U += scratch[b];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
-    r.per = max(long(least), div_pos(U + gridDim.x - 1, gridDim.x));
-    r.u = r.per * blockIdx.x;
-    r.end = min(U, r.u + r.per);
-    if (r.u >= r.end) return false;
-    // the first position past which a prefix sum over steps of 32 goes
+    // the first of n entries past which the prefix sum from `at` goes beyond u
     auto locate = [&](int n, long at, auto cost, int &which, long &start) {
         for (int base = 0; base < n; base += 32) {
             long v = base + lane < n ? cost(base + lane) : 0;
             const long mine = v;
-#pragma unroll
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
                 const long w = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += w;
@@ -175,13 +180,25 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
             at += __shfl_sync(0xffffffffu, v, 31);
         }
     };
+    long U = lane < B ? scratch[lane] : 0;
+    if (B > 1) {
+        for (int b = lane + 32; b < B; b += 32) U += scratch[b];
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
+    } else {
+        U = scratch[0];
+    }
+    r.per = max(long(least), div_pos(U + gridDim.x - 1, gridDim.x));
+    r.u = r.per * blockIdx.x;
+    r.end = min(U, r.u + r.per);
+    if (r.u >= r.end) return false;
     Item &it = r.item;
     it.b = 0;
     it.qt = 0;
     long at = 0, first = 0;
-    locate(B, 0, [&](int b) { return scratch[b]; }, it.b, at);
+    if (B > 1) locate(B, 0, [&](int b) { return scratch[b]; }, it.b, at);
     r.seq = seq_view(p.b, it.b, p.hdr, false);
-    const int nq = (r.seq.n + p.tt - 1) / p.tt;
+    const int nq = query_tiles(p, r.seq.n);
     if (nq > 1)
         locate(nq, at, [&](int qt) { return tile_cost<KT>(p, r.seq, qt) * Hkv; }, it.qt, first);
     else
@@ -190,7 +207,11 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
     it.row0 = r.seq.first + it.qt * p.tt;
     item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.t0, it.tiles);
     const long each = it.tiles + p.extra;
-    it.kh = int(div_pos(r.u - first, each));
+    // the head, of few: a quotient in fp32, put right
+    const long in = r.u - first;
+    it.kh = min(int(__fdividef(float(in), float(each))), Hkv - 1);
+    while (it.kh * each > in) --it.kh;
+    while ((it.kh + 1) * each <= in) ++it.kh;
     r.item_u = first + it.kh * each;
     return true;
 }
@@ -233,6 +254,19 @@ __device__ __forceinline__ int part_at(int row, int ch, int D) {
 // (its first) and one that it leaves to the next (its last).
 __device__ __forceinline__ int part_slot(int cta, bool starts_here) { return 2 * cta + (starts_here ? 1 : 0); }
 
+__device__ __forceinline__ float ld_l2(const float *p) {
+    float v;
+    asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float4 ld_l2_v4(const float *p) {
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // The parts of r.item: consecutive CTAs from the one with its first tile on.
 __device__ __forceinline__ JoinDesc join_desc(const Params &p, const Run &r) {
     const long first = r.item_u + p.extra;
@@ -244,8 +278,126 @@ __device__ __forceinline__ JoinDesc join_desc(const Params &p, const Run &r) {
     return d;
 }
 
-// Joins the partial results of items of up to `rows` rows; query row r of an item
-// is token r / half * tth + r % half / G, head r % half % G.
+// Joins parts first_cta .. of an item of `rows` rows: row r is token
+// r / half * tth + r % half / G of the item, head r % half % G.  All threads of a
+// CTA of W warps call it, for the blocks of rows blk, blk + step, ...; `sv`, `sm`,
+// `sl`: W * D * 4, W * 4 and W * 4 floats of shared memory.
+//
+// What bounds it is the latency of dependent loads, so their chain is kept
+// short: a group of S warps (S by the number of parts) takes four consecutive
+// rows, each warp every S-th part, four at a time with all their loads in
+// flight together; the warps' results meet in shared memory.  Lane l holds
+// row l / 2 % 4, of each 32 channels the four from 8 (l / 8) + 4 (l % 2).
+constexpr int kJoinRows = 4;
+constexpr int kJoinParts = 4;
+
+template <typename T, int D, int W>
+__device__ inline void join_rows(const Params &p, const JoinDesc &d, int first_cta, int rows, int half, int tth,
+                                 int blk0, int step, float *sv_mem, float *sm, float *sl) {
+    constexpr int kVec = D / 32;
+    float4 *sv = reinterpret_cast<float4 *>(sv_mem);  // [W][kVec][32]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.b.Hq / p.b.Hkv;
+    const size_t stride = part_floats(rows, D);
+    const int S = d.parts <= kJoinParts ? 1 : d.parts <= 4 * kJoinParts ? 4 : W;
+    const int group = warp / S, w0 = warp % S, groups = W / S;
+    const int sub = (lane >> 1) & 3, ch0 = 8 * (lane >> 3) + 4 * (lane & 1);
+    const int used = half == rows ? min(rows, d.nt * G) : rows;  // rows past the tokens' end
+    const int blocks = (used + kJoinRows * groups - 1) / (kJoinRows * groups);
+    for (int blk = blk0; blk < blocks; blk += step) {
+        const int row = (blk * groups + group) * kJoinRows + sub;
+        const int tok_h = row % half / G, tok = row / half * tth + tok_h;
+        const bool live = row < rows && tok_h < tth && tok < d.nt;  // rows of no token have no sums
+        float top = -CUDART_INF_F, sum = 0.f;
+        float4 v[kVec];
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = w0; live && i0 < d.parts; i0 += S * kJoinParts) {
+            float m[kJoinParts], l[kJoinParts];
+            float4 x[kJoinParts][kVec];
+#pragma unroll
+            for (int u = 0; u < kJoinParts; ++u) {
+                const int i = i0 + S * u;
+                m[u] = -CUDART_INF_F;
+                l[u] = 0.f;
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) x[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < d.parts) {
+                    // part 0 is the item's start, the others go on in the CTAs after it; read where
+                    // other CTAs' stores are (not in L1)
+                    const float *q = p.part + size_t(part_slot(first_cta + i, i == 0)) * stride;
+                    m[u] = ld_l2(q + rows * D + row);
+                    l[u] = ld_l2(q + rows * (D + 1) + row);
+#pragma unroll
+                    for (int c = 0; c < kVec; ++c) x[u][c] = ld_l2_v4(q + part_at(row, 32 * c + ch0, D));
+                }
+            }
+            float up = top;
+#pragma unroll
+            for (int u = 0; u < kJoinParts; ++u) up = fmaxf(up, m[u]);
+            const float base = up == -CUDART_INF_F ? 0.f : up, old = exp2_approx(top - base);
+            top = up;
+            sum *= old;
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) v[c].x *= old, v[c].y *= old, v[c].z *= old, v[c].w *= old;
+#pragma unroll
+            for (int u = 0; u < kJoinParts; ++u) {
+                const float f = exp2_approx(m[u] - base);
+                sum = fmaf(l[u], f, sum);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    v[c].x = fmaf(x[u][c].x, f, v[c].x);
+                    v[c].y = fmaf(x[u][c].y, f, v[c].y);
+                    v[c].z = fmaf(x[u][c].z, f, v[c].z);
+                    v[c].w = fmaf(x[u][c].w, f, v[c].w);
+                }
+            }
+        }
+        bool mine[kVec];  // the vectors this warp finishes
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) mine[c] = S == 1 || c % S == w0;
+        if (S > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) sv[(warp * kVec + c) * 32 + lane] = v[c];
+            if (ch0 == 0) {
+                sm[warp * kJoinRows + sub] = top;
+                sl[warp * kJoinRows + sub] = sum;
+            }
+            __syncthreads();
+            const int first = group * S;
+            for (int w = 0; w < S; ++w) top = fmaxf(top, sm[(first + w) * kJoinRows + sub]);
+            const float base = top == -CUDART_INF_F ? 0.f : top;
+            sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < S; ++w) {
+                const float f = exp2_approx(sm[(first + w) * kJoinRows + sub] - base);
+                sum = fmaf(sl[(first + w) * kJoinRows + sub], f, sum);
+#pragma unroll
+                for (int c = 0; c < kVec; ++c) {
+                    if (!mine[c]) continue;
+                    const float4 y = sv[((first + w) * kVec + c) * 32 + lane];
+                    v[c].x = fmaf(y.x, f, v[c].x);
+                    v[c].y = fmaf(y.y, f, v[c].y);
+                    v[c].z = fmaf(y.z, f, v[c].z);
+                    v[c].w = fmaf(y.w, f, v[c].w);
+                }
+            }
+        }
+        if (!live) continue;
+        const size_t at = size_t(d.row0 + tok) * p.b.Hq + d.kh * G + row % half % G;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c)
+            if (mine[c])
+                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + at * D + 32 * c + ch0) =
+                    make_uint2(Pair<T>::make(v[c].x * inv, v[c].y * inv), Pair<T>::make(v[c].z * inv, v[c].w * inv));
+        if (p.lse != nullptr && ch0 == 0 && w0 == 0)
+            p.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
+    }
+}
+
+// The second launch: joins the items that start in each CTA's run.
 cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int half, int tth, cudaStream_t s);
 
 // The tensor-core kernel (many rows per key/value head).

@@ -602,6 +602,7 @@ cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStrea
     tp.p = p;
     tp.tth = kHalf / G;
     tp.p.tt = 2 * tp.tth;
+    tp.p.tt_magic = 0xffffffffu / unsigned(tp.p.tt) + 1;
     tp.p.extra = kExtra;
     tp.box_rows = std::min(a.b.page, kKeys);
     const uint32_t fmt = a.type == MOE_BF16 ? (1u << 7) | (1u << 10) : 0u;  // A and B bf16
