@@ -394,8 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     // first pass over the row: its maximum (the score grows with sign * q.k,
                     // so the maximum of those gives the maximum of the scores).  Of the four
                     // chunks of 32 keys three fit in registers: 1, 2 and 3 stay for the second
-                    // pass, chunk 0 is read again behind chunk 2's arithmetic.
-                    float v[3][32];
+                    // pass, chunk 0 is read again behind chunk 2's arithmetic.  Capped scores, whose
+                    // arithmetic is long and wants the registers, are read again all.
+                    constexpr bool kHold = kMode != kCapped;
+                    float v[kHold ? 3 : 2][32];
                     float mt;
                     {
                         float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
@@ -406,18 +408,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                                        ? max3(m4[(i >> 1) & 3], u[i] * sign, u[i + 1] * sign)
                                                        : max3(m4[(i >> 1) & 3], u[i], u[i + 1]);
                         };
-                        tmem_ld32(ts, v[0]);
-                        tmem_ld32(ts + 32, v[1]);
-                        tmem_ld32(ts + 64, v[2]);
-                        wait_ld32(v[0]);
-                        wait_ld32(v[1]);
-                        wait_ld32(v[2]);
-                        take(v[0]);
-                        tmem_ld32(ts + 96, v[0]);
-                        take(v[1]);
-                        take(v[2]);
-                        wait_ld32(v[0]);
-                        take(v[0]);
+                        if constexpr (kHold) {
+                            tmem_ld32(ts, v[0]);
+                            tmem_ld32(ts + 32, v[1]);
+                            tmem_ld32(ts + 64, v[2]);
+                            wait_ld32(v[0]);
+                            wait_ld32(v[1]);
+                            wait_ld32(v[2]);
+                            take(v[0]);
+                            tmem_ld32(ts + 96, v[0]);
+                            take(v[1]);
+                            take(v[2]);
+                            wait_ld32(v[0]);
+                            take(v[0]);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 4; c += 2) {
+                                tmem_ld32(ts + 32 * c, v[0]);
+                                tmem_ld32(ts + 32 * c + 32, v[1]);
+                                wait_ld32(v[0]);
+                                wait_ld32(v[1]);
+                                take(v[0]);
+                                take(v[1]);
+                            }
+                            tmem_ld32(ts + 32, v[1]);  // for the second pass
+                        }
                         mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     }
                     if (mt != -CUDART_INF_F) mt = score<kMode == kCapped>(kMode != kScaled ? mt * sign : mt, p);
@@ -447,30 +462,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     const float b = kMode == kCapped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
                     const unsigned long long one2 = pack2(1.f, 1.f), cap2 = pack2(k2, k2);
+                    const unsigned long long hide2 = pack2(1e-30f * sign, 1e-30f * sign);
                     {
                         auto take = [&](int c, const float (&u)[32]) {
                             uint32_t w[16];
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                unsigned long long e2 = pack2(u[i], u[i + 1]);
-                                float e[2];
-                                if (kMode == kCapped) {  // score() less the base, two at a time
-                                    unpack2(mul2(e2, scale2), e[0], e[1]);
-                                    unpack2(add2(pack2(exp2_approx(e[0]), exp2_approx(e[1])), one2), e[0], e[1]);
-                                    e2 = fma2(pack2(rcp_approx(e[0]), rcp_approx(e[1])), cap2, base2);
+                            for (int i = 0; i < 32; i += 4) {
+                                unsigned long long e2[2] = {pack2(u[i], u[i + 1]), pack2(u[i + 2], u[i + 3])};
+                                if (kMode == kCapped) {
+                                    // score() less the base: d = 1 + e^2x, and both reciprocals of a pair of
+                                    // pairs from that of their product (d is kept below 2^60 for it: the
+                                    // tangent is 1 long before)
+                                    unsigned long long d2[2];
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) {
+                                        float x, y;
+                                        unpack2(mul2(e2[k], scale2), x, y);
+                                        d2[k] = add2(pack2(exp2_approx(fminf(x, 60.f)), exp2_approx(fminf(y, 60.f))), one2);
+                                    }
+                                    float x, y;
+                                    unpack2(mul2(d2[0], d2[1]), x, y);
+                                    const unsigned long long r2 = pack2(rcp_approx(x), rcp_approx(y));
+                                    // a hidden score (an infinity) is brought back by a product that is
+                                    // nothing beside any other score
+                                    e2[0] = fma2(e2[0], hide2, fma2(mul2(r2, d2[1]), cap2, base2));
+                                    e2[1] = fma2(e2[1], hide2, fma2(mul2(r2, d2[0]), cap2, base2));
                                 } else {
-                                    e2 = fma2(e2, scale2, base2);
+                                    e2[0] = fma2(e2[0], scale2, base2);
+                                    e2[1] = fma2(e2[1], scale2, base2);
                                 }
-                                unpack2(e2, e[0], e[1]);
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
-                                    e[k] = exp2_approx(e[k]);
-                                    // capped, or times 0, an infinity does not give weight 0 by itself
-                                    if (kMode != kScaled && u[i + k] == hidden) e[k] = 0.f;
+                                    float x, y;
+                                    unpack2(e2[k], x, y);
+                                    x = exp2_approx(x);
+                                    y = exp2_approx(y);
+                                    if (kMode == kSigned) {  // times 0 an infinity does not give weight 0 by itself
+                                        if (u[i + 2 * k] == hidden) x = 0.f;
+                                        if (u[i + 2 * k + 1] == hidden) y = 0.f;
+                                    }
+                                    s2[k] = add2(s2[k], pack2(x, y));
+                                    // rounded for the product; the sum keeps the weight whole
+                                    w[i / 2 + k] = Pair<T>::make(x, y);
                                 }
-                                s2[(i >> 1) & 1] = add2(s2[(i >> 1) & 1], pack2(e[0], e[1]));
-                                // rounded for the product; the sum keeps the weight whole
-                                w[i / 2] = Pair<T>::make(e[0], e[1]);
                             }
                             tmem_st16(ts + 32 * c, w);  // over the chunk's own scores
                         };
@@ -480,13 +514,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar);
                         };
-                        take(1, v[1]);
-                        tmem_ld32(ts, v[1]);
-                        take(2, v[2]);
-                        ready(&p_ready[h][0]);  // the product of chunks 1 and 2 can begin
-                        take(3, v[0]);
-                        wait_ld32(v[1]);
-                        take(0, v[1]);
+                        if constexpr (kHold) {
+                            take(1, v[1]);
+                            tmem_ld32(ts, v[1]);
+                            take(2, v[2]);
+                            ready(&p_ready[h][0]);  // the product of chunks 1 and 2 can begin
+                            take(3, v[0]);
+                            wait_ld32(v[1]);
+                            take(0, v[1]);
+                        } else {
+                            wait_ld32(v[1]);
+                            tmem_ld32(ts + 64, v[0]);
+                            take(1, v[1]);
+                            wait_ld32(v[0]);
+                            tmem_ld32(ts + 96, v[1]);
+                            take(2, v[0]);
+                            ready(&p_ready[h][0]);
+                            wait_ld32(v[1]);
+                            tmem_ld32(ts, v[0]);
+                            take(3, v[1]);
+                            wait_ld32(v[0]);
+                            take(0, v[0]);
+                        }
                         ready(&p_ready[h][1]);
                     }
                     float sa, sb;
