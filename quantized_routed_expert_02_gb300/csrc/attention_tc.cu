@@ -3,11 +3,11 @@
 // memory and S, P, O in tensor memory.
 //
 // An item is two halves of 128 query rows (tokens x the group's heads) that
-// share every key tile of 128 keys.  Twelve warps: two groups of four softmax
-// warps, one per half (a thread per row), three copying warps (TMA boxes of one
+// share every key tile of 128 keys.  Eleven warps: two groups of four softmax
+// warps, one per half (a thread per row), two copying warps (TMA boxes of one
 // page each into a ring of K and V tiles; one warp cannot issue the 32 boxes that
-// pages of 16 make of a tile pair in the time of its MMAs) and a warp that issues
-// the MMAs.  The two halves take turns on the tensor pipe: while one half's P V and next Q K^T
+// pages of 16 make of a K and a V tile in the time of their MMAs) and a warp that
+// issues the MMAs.  The two halves take turns on the tensor pipe: while one half's P V and next Q K^T
 // run, the other half's softmax does.  P overwrites S in tensor memory and is
 // the A operand from there.  O is rescaled only when a row's maximum has grown
 // by more than 2^8 since the last rescale (weights up to 2^8 are as exact in
@@ -28,7 +28,7 @@ namespace tc5 {
 constexpr int kHalf = 128;                 // rows of a half
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kSoftmax = 256;              // threads of the softmax warps
-constexpr int kCopyWarps = 3;
+constexpr int kCopyWarps = 2;               // K tiles, V tiles
 constexpr int kMmaWarp = kSoftmax / 32, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = kSoftmax + 32 * (1 + kCopyWarps);
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
@@ -195,8 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     const uint32_t tmem = tmem_base;
 
     if (warp >= kCopyWarp) {
-        // ---- Q of each segment (the first copying warp), then its K and V tiles,
-        // the ring's tiles in turn to the copying warps
+        // ---- Q of each segment and its K tiles, or its V tiles
         const int me = warp - kCopyWarp;
         const int nbox = kKeys / tp.box_rows;  // boxes of a tile, one lane each
         uint32_t g = 0, seg = 0;               // tiles copied, segments
@@ -231,7 +230,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 const bool mine = lane < nbox && key < it.len;
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, mine));
                 for (int kv = 0; kv < 2; ++kv, ++g) {
-                    if (int(g % kCopyWarps) != me) continue;
+                    // a ring slot has one copying warp (K tiles the first, V tiles the second): the
+                    // parity of its phases says something only to who waits for each of them
+                    if (kv != me) continue;
                     const uint32_t st = g % C::kStages;
                     if (g >= uint32_t(C::kStages) &&
                         !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 51 + kv)))
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         if (!ok) {
             for (uint32_t i = 0; i < uint32_t(C::kStages) && i < g; ++i) {
                 const uint32_t gg = g - 1 - i;
-                if (int(gg % kCopyWarps) == me) warp_wait(&full[gg % C::kStages], (gg / C::kStages) & 1u, p, 53);
+                if (int(gg % 2) == me) warp_wait(&full[gg % C::kStages], (gg / C::kStages) & 1u, p, 53);
             }
         }
         if (me == 0 && seg > 0) warp_wait(&q_full, (seg - 1) & 1u, p, 54);
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         for (int c = 0; c < C::kCh; ++c)
                             *reinterpret_cast<uint4 *>(smem + vs * C::kTileB + c * C::kSlab + i * 16) =
                                 make_uint4(0, 0, 0, 0);
+                    __syncwarp();
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -320,14 +322,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 for (int h = 0; ok && h < halves; ++h) {
                     if (!(ok = warp_wait(&p_ready[h][0], np[h] & 1u, p, 59))) break;
                     tc::fence_after_sync();
-                    pv(h, vs, 1, j > 0);
-                    pv(h, vs, 2, true);
+                    pv(h, vs, 0, j > 0);
+                    pv(h, vs, 1, true);
                     __syncwarp();
                     if (!(ok = warp_wait(&p_ready[h][1], np[h] & 1u, p, 59))) break;
                     ++np[h];
                     tc::fence_after_sync();
+                    pv(h, vs, 2, true);
                     pv(h, vs, 3, true);
-                    pv(h, vs, 0, true);
                     if (j + 1 < n) qk(h, ks);
                     else if (leader) tc::commit_arrive(&o_full[h]);
                 }
@@ -391,13 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         }
                         wait_st();
                     }
-                    // first pass over the row: its maximum (the score grows with sign * q.k,
-                    // so the maximum of those gives the maximum of the scores).  Of the four
-                    // chunks of 32 keys three fit in registers: 1, 2 and 3 stay for the second
-                    // pass, chunk 0 is read again behind chunk 2's arithmetic.  Capped scores, whose
-                    // arithmetic is long and wants the registers, are read again all.
-                    constexpr bool kHold = kMode != kCapped;
-                    float v[kHold ? 3 : 2][32];
+                    // first pass over the row: its maximum (the score grows with sign * q.k, so the
+                    // maximum of those gives the maximum of the scores).  The second pass reads
+                    // the scores again: kept between the passes, they leave too few registers for
+                    // the arithmetic to overlap with itself (prompt of 4096: 121 against 117 us).
+                    float v[2][32];
                     float mt;
                     {
                         float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
@@ -408,31 +408,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                                        ? max3(m4[(i >> 1) & 3], u[i] * sign, u[i + 1] * sign)
                                                        : max3(m4[(i >> 1) & 3], u[i], u[i + 1]);
                         };
-                        if constexpr (kHold) {
-                            tmem_ld32(ts, v[0]);
-                            tmem_ld32(ts + 32, v[1]);
-                            tmem_ld32(ts + 64, v[2]);
+#pragma unroll
+                        for (int c = 0; c < 4; c += 2) {
+                            tmem_ld32(ts + 32 * c, v[0]);
+                            tmem_ld32(ts + 32 * c + 32, v[1]);
                             wait_ld32(v[0]);
                             wait_ld32(v[1]);
-                            wait_ld32(v[2]);
                             take(v[0]);
-                            tmem_ld32(ts + 96, v[0]);
                             take(v[1]);
-                            take(v[2]);
-                            wait_ld32(v[0]);
-                            take(v[0]);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 4; c += 2) {
-                                tmem_ld32(ts + 32 * c, v[0]);
-                                tmem_ld32(ts + 32 * c + 32, v[1]);
-                                wait_ld32(v[0]);
-                                wait_ld32(v[1]);
-                                take(v[0]);
-                                take(v[1]);
-                            }
-                            tmem_ld32(ts + 32, v[1]);  // for the second pass
                         }
+                        tmem_ld32(ts, v[0]);  // for the second pass
                         mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     }
                     if (mt != -CUDART_INF_F) mt = score<kMode == kCapped>(kMode != kScaled ? mt * sign : mt, p);
@@ -514,28 +499,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar);
                         };
-                        if constexpr (kHold) {
-                            take(1, v[1]);
-                            tmem_ld32(ts, v[1]);
-                            take(2, v[2]);
-                            ready(&p_ready[h][0]);  // the product of chunks 1 and 2 can begin
-                            take(3, v[0]);
-                            wait_ld32(v[1]);
-                            take(0, v[1]);
-                        } else {
-                            wait_ld32(v[1]);
-                            tmem_ld32(ts + 64, v[0]);
-                            take(1, v[1]);
-                            wait_ld32(v[0]);
-                            tmem_ld32(ts + 96, v[1]);
-                            take(2, v[0]);
-                            ready(&p_ready[h][0]);
-                            wait_ld32(v[1]);
-                            tmem_ld32(ts, v[0]);
-                            take(3, v[1]);
-                            wait_ld32(v[0]);
-                            take(0, v[0]);
-                        }
+                        wait_ld32(v[0]);
+                        tmem_ld32(ts + 32, v[1]);
+                        take(0, v[0]);
+                        wait_ld32(v[1]);
+                        tmem_ld32(ts + 64, v[0]);
+                        take(1, v[1]);
+                        ready(&p_ready[h][0]);  // the product of the first 64 keys can begin
+                        wait_ld32(v[0]);
+                        tmem_ld32(ts + 96, v[1]);
+                        take(2, v[0]);
+                        wait_ld32(v[1]);
+                        take(3, v[1]);
                         ready(&p_ready[h][1]);
                     }
                     float sa, sb;
@@ -588,12 +563,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         float o[32];
                         tmem_ld32(to + 32 * c, o);
                         wait_ld32(o);
-                        if (!live) continue;
+                        if (live) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            tc::st_global_v8(mine + part_at(prow, 32 * c + i, D),
-                                             {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6],
-                                              o[i + 7]});
+                            for (int i = 0; i < 32; i += 8)
+                                tc::st_global_v8(mine + part_at(prow, 32 * c + i, D),
+                                                 {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5],
+                                                  o[i + 6], o[i + 7]});
+                        }
+                        __syncwarp();  // the next load of tensor memory wants the warp together
                     }
                     if (live) {
                         mine[size_t(2 * kHalf) * D + prow] = top;
