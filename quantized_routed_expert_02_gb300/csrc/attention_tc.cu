@@ -27,10 +27,10 @@ namespace tc5 {
 
 constexpr int kHalf = 128;                 // rows of a half
 constexpr int kKeys = 128;                 // keys of a tile
-constexpr int kSoftmax = 256;              // threads of the softmax warps
+constexpr int kSoftmaxWarps = 16;
 constexpr int kCopyWarps = 2;               // K tiles, V tiles
-constexpr int kMmaWarp = kSoftmax / 32, kCopyWarp = kMmaWarp + 1;
-constexpr int kThreads = kSoftmax + 32 * (1 + kCopyWarps);
+constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kCopyWarps);
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 constexpr int kLeast = 4;
 constexpr int kExtra = 3;
@@ -50,8 +50,8 @@ struct Cfg {
     static constexpr int kSlab = 128 * 128;            // bytes of a 128-row slab
     static constexpr int kTileB = kCh * kSlab;         // a tile of K, of V, or of a half's Q
     static constexpr int kStages = D == 128 ? 4 : 8;
-    static constexpr int kStageOut = 32 * 128;         // a softmax warp's 32 rows x 64 channels on their way out
-    static constexpr int kSmem = kStages * kTileB + 2 * kTileB + kSoftmax / 32 * kStageOut;
+    static constexpr int kStageOut = 32 * 64;          // a softmax warp's 32 rows x 32 channels on their way out
+    static constexpr int kSmem = kStages * kTileB + 2 * kTileB + kSoftmaxWarps * kStageOut;
 };
 
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
@@ -110,6 +110,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&v)[16]) {
         S4(v, 0), S4(v, 4), S4(v, 8), S4(v, 12)
         : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), S4(v, 0), S4(v, 4)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t t, const float (&v)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
@@ -158,8 +162,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-// How a score follows from q.k: by a positive scale, by any scale, or capped.
-enum Mode { kScaled, kSigned, kCapped };
+// How a score follows from q.k: by a positive scale, capped after a positive
+// scale, or in any other way (negative and zero scales).
+enum Mode { kScaled, kCapped, kAny };
 
 template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_constant__ TcParams tp) {
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
-        for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 4), mbar_init(&p_ready[h][1], 4), mbar_init(&o_full[h], 1);
+        for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 8), mbar_init(&p_ready[h][1], 8), mbar_init(&o_full[h], 1);
         mbar_init(&drain, 1);
         prefetch_map(&tp.mq);
         prefetch_map(&tp.mk);
@@ -323,12 +328,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     if (!(ok = warp_wait(&p_ready[h][0], np[h] & 1u, p, 59))) break;
                     tc::fence_after_sync();
                     pv(h, vs, 0, j > 0);
-                    pv(h, vs, 1, true);
+                    pv(h, vs, 2, true);
                     __syncwarp();
                     if (!(ok = warp_wait(&p_ready[h][1], np[h] & 1u, p, 59))) break;
                     ++np[h];
                     tc::fence_after_sync();
-                    pv(h, vs, 2, true);
+                    pv(h, vs, 1, true);
                     pv(h, vs, 3, true);
                     if (j + 1 < n) qk(h, ks);
                     else if (leader) tc::commit_arrive(&o_full[h]);
@@ -349,15 +354,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         __syncwarp();
         warp_wait(&drain, 0, p, 60);
     } else {
-        // ---- softmax of half h, a thread per row
-        const int h = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + 128u * h + lanes, to = tmem + 256u + 128u * h + lanes;
+        // ---- softmax: half h, rows 32 q4 + lane, keys 64 ch .. of each tile (and of the
+        // result the channels D/2 ch ..)
+        const int q4 = warp & 3, h = (warp >> 2) & 1, ch = warp >> 3, row = 32 * q4 + lane;
+        const uint32_t lanes = uint32_t(32 * q4) << 16;
+        const uint32_t ts = tmem + 128u * h + 64u * ch + lanes, to = tmem + 256u + 128u * h + uint32_t(D / 2) * ch + lanes;
         const int tok_h = row / G, head = row % G;
-        const float sign = (kMode == kCapped ? p.cap_in : p.scale_log2) < 0.f ? -1.f : 1.f;
+        const bool capped = kMode == kCapped || (kMode == kAny && p.cap_in != 0.f);
+        const float sign = kMode == kAny && (capped ? p.cap_in : p.scale_log2) < 0.f ? -1.f : 1.f;
         const float hidden = -CUDART_INF_F * sign;  // the q.k of a key that a row does not see
-        uint32_t ns = 0, no = 0;  // S tiles and O results taken
-        bool ok = true;           // after a time-out: no more waits, every barrier still met
+        uint32_t ns = 0, no = 0, nx = 0;  // S tiles and O results taken, exchanges
+        bool ok = true;  // after a time-out: no more waits, but every barrier still met
+        // a value of the row's other thread, through the space of the results on their way out
+        uint8_t *stage = smem + (C::kStages + 2) * C::kTileB + warp * C::kStageOut;
+        float *mine_x = reinterpret_cast<float *>(stage) + lane;  // in turns at 0 and 32
+        const float *other_x = reinterpret_cast<float *>(stage + ((warp ^ 8) - warp) * C::kStageOut) + lane;
+        auto meet = [&]() { named_bar_sync(1 + (warp & 7), 64); };
+        auto exchange = [&](float mine) {
+            const uint32_t o = (nx++ & 1) * 32;
+            mine_x[o] = mine;
+            meet();
+            return other_x[o];
+        };
         while (run.u < run.end) {
             int s0, s1;
             if (!run_segment(p, run, s0, s1)) break;
@@ -371,18 +389,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 for (int j = 0; j < s1 - s0; ++j) {
                     ok = ok && warp_wait(&s_full[h], ns & 1u, p, 61 + h);
                     ++ns;
-                    if (!ok) continue;
                     tc::fence_after_sync();
                     const int key0 = (it.t0 + s0 + j) * kKeys;
                     const bool edge =
                         key0 + kKeys - 1 > first || (p.window > 0 && key0 <= first + nth - 1 - p.window);
-                    const int hi = at - key0, lo = p.window > 0 ? hi - p.window : -1;  // sees lo < i <= hi
                     // a tile that some row does not see whole: what it does not see becomes the
                     // score of weight 0, in place, so that the passes below (whose code is long)
                     // exist once and pay for no comparisons
                     if (edge) {
+                        const int hi = at - key0 - 64 * ch, lo = p.window > 0 ? hi - p.window : -1;  // sees lo < i <= hi
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < 2; ++c) {
                             float u[32];
                             tmem_ld32(ts + 32 * c, u);
                             wait_ld32(u);
@@ -393,34 +410,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         }
                         wait_st();
                     }
-                    // first pass over the row: its maximum (the score grows with sign * q.k, so the
-                    // maximum of those gives the maximum of the scores).  The second pass reads
-                    // the scores again: kept between the passes, they leave too few registers for
-                    // the arithmetic to overlap with itself (prompt of 4096: 121 against 117 us).
-                    float v[2][32];
+                    // first pass: the row's maximum (the score grows with sign * q.k, so the maximum
+                    // of those gives the maximum of the scores)
+                    float v[2][16];
                     float mt;
                     {
                         float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                        auto take = [&](const float (&u)[32]) {
+                        float u[2][32];
+                        tmem_ld32(ts, u[0]);
+                        tmem_ld32(ts + 32, u[1]);
+                        wait_ld32(u[0]);
+                        wait_ld32(u[1]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; i += 2)
-                                m4[(i >> 1) & 3] = kMode != kScaled
-                                                       ? max3(m4[(i >> 1) & 3], u[i] * sign, u[i + 1] * sign)
-                                                       : max3(m4[(i >> 1) & 3], u[i], u[i + 1]);
-                        };
-#pragma unroll
-                        for (int c = 0; c < 4; c += 2) {
-                            tmem_ld32(ts + 32 * c, v[0]);
-                            tmem_ld32(ts + 32 * c + 32, v[1]);
-                            wait_ld32(v[0]);
-                            wait_ld32(v[1]);
-                            take(v[0]);
-                            take(v[1]);
-                        }
-                        tmem_ld32(ts, v[0]);  // for the second pass
-                        mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                                m4[(i >> 1) & 3] = kMode == kAny ? max3(m4[(i >> 1) & 3], u[c][i] * sign, u[c][i + 1] * sign)
+                                                                 : max3(m4[(i >> 1) & 3], u[c][i], u[c][i + 1]);
+                        mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
                     }
-                    if (mt != -CUDART_INF_F) mt = score<kMode == kCapped>(kMode != kScaled ? mt * sign : mt, p);
+                    tmem_ld16(ts, v[0]);  // for the second pass
+                    mt = fmaxf(mt, exchange(mt));
+                    if (mt != -CUDART_INF_F) mt = capped ? score<true>(mt * sign, p) : score<false>(mt * sign, p);
                     if (j == 0) {
                         top = mt;
                     } else if (__any_sync(0xffffffffu, mt - top > kGrowth)) {
@@ -429,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         const float f = exp2_approx(top - (up == -CUDART_INF_F ? 0.f : up));
                         sum *= f;
                         top = up;
-#pragma unroll
-                        for (int c = 0; c < D / 16; ++c) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
                             float o[16];
                             tmem_ld16(to + 16 * c, o);
                             wait_ld16(o);
@@ -443,81 +454,84 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     // second pass: the weights
                     const float base = top == -CUDART_INF_F ? 0.f : top;
                     unsigned long long s2[2] = {0ull, 0ull};  // pairs of sums
-                    const float scale = kMode == kCapped ? p.cap_in : p.scale_log2;
-                    const float b = kMode == kCapped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
+                    const float scale = capped ? p.cap_in : p.scale_log2;
+                    const float b = capped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
                     const unsigned long long one2 = pack2(1.f, 1.f), cap2 = pack2(k2, k2);
                     const unsigned long long hide2 = pack2(1e-30f * sign, 1e-30f * sign);
-                    {
-                        auto take = [&](int c, const float (&u)[32]) {
-                            uint32_t w[16];
+                    auto take = [&](int c, const float (&u)[16]) {
+                        uint32_t w[8];
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                unsigned long long e2[2] = {pack2(u[i], u[i + 1]), pack2(u[i + 2], u[i + 3])};
-                                if (kMode == kCapped) {
-                                    // score() less the base: d = 1 + e^2x, and both reciprocals of a pair of
-                                    // pairs from that of their product (d is kept below 2^60 for it: the
-                                    // tangent is 1 long before)
-                                    unsigned long long d2[2];
-#pragma unroll
-                                    for (int k = 0; k < 2; ++k) {
-                                        float x, y;
-                                        unpack2(mul2(e2[k], scale2), x, y);
-                                        d2[k] = add2(pack2(exp2_approx(fminf(x, 60.f)), exp2_approx(fminf(y, 60.f))), one2);
-                                    }
-                                    float x, y;
-                                    unpack2(mul2(d2[0], d2[1]), x, y);
-                                    const unsigned long long r2 = pack2(rcp_approx(x), rcp_approx(y));
-                                    // a hidden score (an infinity) is brought back by a product that is
-                                    // nothing beside any other score
-                                    e2[0] = fma2(e2[0], hide2, fma2(mul2(r2, d2[1]), cap2, base2));
-                                    e2[1] = fma2(e2[1], hide2, fma2(mul2(r2, d2[0]), cap2, base2));
-                                } else {
-                                    e2[0] = fma2(e2[0], scale2, base2);
-                                    e2[1] = fma2(e2[1], scale2, base2);
-                                }
+                        for (int i = 0; i < 16; i += 4) {
+                            unsigned long long e2[2] = {pack2(u[i], u[i + 1]), pack2(u[i + 2], u[i + 3])};
+                            if (capped) {
+                                // score() less the base: d = 1 + e^2x, and the four reciprocals from that
+                                // of their product (a reciprocal takes twice an exponential's time; d is
+                                // kept below 2^30 for it, where the tangent is 1 in fp32)
+                                unsigned long long d2[2];
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     float x, y;
-                                    unpack2(e2[k], x, y);
-                                    x = exp2_approx(x);
-                                    y = exp2_approx(y);
-                                    if (kMode == kSigned) {  // times 0 an infinity does not give weight 0 by itself
-                                        if (u[i + 2 * k] == hidden) x = 0.f;
-                                        if (u[i + 2 * k + 1] == hidden) y = 0.f;
-                                    }
-                                    s2[k] = add2(s2[k], pack2(x, y));
-                                    // rounded for the product; the sum keeps the weight whole
-                                    w[i / 2 + k] = Pair<T>::make(x, y);
+                                    unpack2(mul2(e2[k], scale2), x, y);
+                                    d2[k] = add2(pack2(exp2_approx(fminf(x, 30.f)), exp2_approx(fminf(y, 30.f))), one2);
                                 }
+                                float x, y;
+                                unpack2(mul2(d2[0], d2[1]), x, y);
+                                const float r = rcp_approx(x * y);
+                                const unsigned long long r2 = mul2(pack2(r, r), pack2(y, x));
+                                // a hidden score (an infinity) is brought back by a product that is
+                                // nothing beside any other score
+                                e2[0] = fma2(e2[0], hide2, fma2(mul2(r2, d2[1]), cap2, base2));
+                                e2[1] = fma2(e2[1], hide2, fma2(mul2(r2, d2[0]), cap2, base2));
+                            } else {
+                                e2[0] = fma2(e2[0], scale2, base2);
+                                e2[1] = fma2(e2[1], scale2, base2);
                             }
-                            tmem_st16(ts + 32 * c, w);  // over the chunk's own scores
-                        };
-                        auto ready = [&](uint64_t *bar) {
-                            wait_st();
-                            tc::fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar);
-                        };
-                        wait_ld32(v[0]);
-                        tmem_ld32(ts + 32, v[1]);
-                        take(0, v[0]);
-                        wait_ld32(v[1]);
-                        tmem_ld32(ts + 64, v[0]);
-                        take(1, v[1]);
-                        ready(&p_ready[h][0]);  // the product of the first 64 keys can begin
-                        wait_ld32(v[0]);
-                        tmem_ld32(ts + 96, v[1]);
-                        take(2, v[0]);
-                        wait_ld32(v[1]);
-                        take(3, v[1]);
-                        ready(&p_ready[h][1]);
-                    }
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float x, y;
+                                unpack2(e2[k], x, y);
+                                x = exp2_approx(x);
+                                y = exp2_approx(y);
+                                if (kMode == kAny) {  // times 0 an infinity does not give weight 0 by itself
+                                    if (u[i + 2 * k] == hidden) x = 0.f;
+                                    if (u[i + 2 * k + 1] == hidden) y = 0.f;
+                                }
+                                s2[k] = add2(s2[k], pack2(x, y));
+                                // rounded for the product; the sum keeps the weight whole
+                                w[i / 2 + k] = Pair<T>::make(x, y);
+                            }
+                        }
+                        // over the chunk's own scores: 32 keys' weights side by side
+                        tmem_st8(ts + 32 * (c >> 1) + 8 * (c & 1), w);
+                    };
+                    auto ready = [&](uint64_t *bar) {
+                        wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0 && ok) mbar_arrive(bar);
+                        __syncwarp();
+                    };
+                    wait_ld16(v[0]);
+                    tmem_ld16(ts + 16, v[1]);
+                    take(0, v[0]);
+                    wait_ld16(v[1]);
+                    tmem_ld16(ts + 32, v[0]);
+                    take(1, v[1]);
+                    ready(&p_ready[h][0]);  // the product of this thread's first 32 keys can begin
+                    wait_ld16(v[0]);
+                    tmem_ld16(ts + 48, v[1]);
+                    take(2, v[0]);
+                    wait_ld16(v[1]);
+                    take(3, v[1]);
+                    ready(&p_ready[h][1]);
                     float sa, sb;
                     unpack2(add2(s2[0], s2[1]), sa, sb);
                     sum += sa + sb;
                 }
-                // ---- the half's result
+                // ---- the half's result: this warp's channels
+                sum += exchange(sum);
+                meet();  // both have read: the space is free for the results
                 ok = ok && warp_wait(&o_full[h], no & 1u, p, 63 + h);
                 ++no;
                 tc::fence_after_sync();
@@ -526,57 +540,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(2 * kHalf, D);
                 const int prow = h * kHalf + row;
                 const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                if (ok && whole) {
-                    // through shared memory, 64 channels at a time: a row per lane in (swizzled
-                    // 16-byte chunks), full 128-byte lines out
-                    uint8_t *stage = smem + (C::kStages + 2) * C::kTileB + warp * C::kStageOut;
 #pragma unroll 1
-                    for (int c = 0; c < C::kCh; ++c) {
-                        float o[2][32];
-                        tmem_ld32(to + 64 * c, o[0]);
-                        tmem_ld32(to + 64 * c + 32, o[1]);
-                        wait_ld32(o[0]);
-                        wait_ld32(o[1]);
+                for (int c = 0; ok && c < D / 64; ++c) {
+                    const int ch0 = D / 2 * ch + 32 * c;  // first of 32 channels
+                    float o[32];
+                    tmem_ld32(to + 32 * c, o);
+                    wait_ld32(o);
+                    if (whole) {
+                        // through shared memory: a row per lane in (16-byte chunks, swizzled),
+                        // 64-byte runs of eight rows at a time out
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float *x = &o[k >> 2][8 * (k & 3)];
-                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                        for (int k = 0; k < 4; ++k) {
+                            const float *x = &o[8 * k];
+                            *reinterpret_cast<uint4 *>(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)) =
                                 make_uint4(Pair<T>::make(x[0] * inv, x[1] * inv), Pair<T>::make(x[2] * inv, x[3] * inv),
                                            Pair<T>::make(x[4] * inv, x[5] * inv), Pair<T>::make(x[6] * inv, x[7] * inv));
                         }
                         __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + (lane >> 3), k = lane & 7;
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 8 * i + (lane >> 2), k = lane & 3;
                             const int dst = __shfl_sync(0xffffffffu, out_row, r);
-                            const uint4 w = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((k ^ (r & 7)) << 4));
+                            const uint4 w = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((k ^ ((r >> 1) & 3)) << 4));
                             if (dst >= 0)
-                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + size_t(dst) * D + 64 * c + 8 * k) = w;
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + size_t(dst) * D + ch0 + 8 * k) = w;
                         }
-                        __syncwarp();
-                    }
-                    if (live && p.lse != nullptr)
-                        p.lse[out_row] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
-                } else if (ok) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        tmem_ld32(to + 32 * c, o);
-                        wait_ld32(o);
-                        if (live) {
+                    } else if (live) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                tc::st_global_v8(mine + part_at(prow, 32 * c + i, D),
-                                                 {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5],
-                                                  o[i + 6], o[i + 7]});
-                        }
-                        __syncwarp();  // the next load of tensor memory wants the warp together
+                        for (int i = 0; i < 32; i += 8)
+                            tc::st_global_v8(mine + part_at(prow, ch0 + i, D),
+                                             {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6],
+                                              o[i + 7]});
                     }
-                    if (live) {
+                    __syncwarp();  // the next load of tensor memory wants the warp together
+                }
+                if (ok && live && ch == 0) {
+                    if (!whole) {
                         mine[size_t(2 * kHalf) * D + prow] = top;
                         mine[size_t(2 * kHalf) * (D + 1) + prow] = sum;
+                    } else if (p.lse != nullptr) {
+                        p.lse[out_row] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
                     }
                 }
+                __syncwarp();
                 tc::fence_before_sync();
             }
             run_next<kKeys>(p, run);
@@ -593,8 +599,10 @@ cudaError_t launch(const TcParams &tp, int grid, cudaStream_t s) {
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(Cfg<D>::kSmem), s, tp);
     };
-    if (tp.p.cap_in != 0.f) return go(attention_tc_kernel<T, D, kCapped>);
-    return tp.p.scale_log2 > 0.f ? go(attention_tc_kernel<T, D, kScaled>) : go(attention_tc_kernel<T, D, kSigned>);
+    if (tp.p.cap_in > 0.f) return go(attention_tc_kernel<T, D, kCapped>);
+    if (tp.p.cap_in == 0.f && tp.p.scale_log2 > 0.f) return go(attention_tc_kernel<T, D, kScaled>);
+    return go(attention_tc_kernel<T, D, kAny>);
+
 }
 
 template <typename T, int D>
@@ -603,7 +611,7 @@ cudaError_t init() {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
     };
     cudaError_t e = set(attention_tc_kernel<T, D, kScaled>);
-    if (e == cudaSuccess) e = set(attention_tc_kernel<T, D, kSigned>);
+    if (e == cudaSuccess) e = set(attention_tc_kernel<T, D, kAny>);
     if (e == cudaSuccess) e = set(attention_tc_kernel<T, D, kCapped>);
     return e;
 }
