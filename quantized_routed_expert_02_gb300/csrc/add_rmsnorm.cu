@@ -102,6 +102,7 @@ __global__ void add_rmsnorm_kernel(const AddNormArgs a) {
     ss = warp_sum(ss);
     if (lane == 0) part[warp] = ss;
     __syncthreads();
+    __syncwarp();
     float total = 0.f;
     for (int w = 0; w < nw; ++w) total += part[w];
     const float inv = 1.0f / sqrtf(total / float(a.H) + a.eps);

@@ -98,6 +98,7 @@ __device__ __forceinline__ void store_row(const Params &p, size_t row, int lane,
     else dst[0] = w[0];
     if (p.lse != nullptr && lane == 0)
         p.lse[row] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
+    __syncwarp();
 }
 
 template <typename T, int D, int MT, bool kCap>
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
     __shared__ unsigned failed;
     __shared__ bool joins;
+    __shared__ Run run_sh;
     const Params &p = sp.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gid = lane >> 2, tig = lane & 3;
@@ -127,11 +129,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     }
     if (lane == 0)
         for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
+    __syncwarp();
     fence_mbar_init();
     pdl_enter();
     if (sp.join_launch && tid == 0) p.desc[blockIdx.x].parts = 0;
     Run run;
-    if (!run_begin<kTile>(p, kLeast, reinterpret_cast<long *>(smem), run)) return;
+    if (!run_begin<kTile>(p, kLeast, reinterpret_cast<long *>(smem), &run_sh, run)) return;
     fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
     __syncthreads();
 
@@ -171,11 +174,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                     qa[m][k][2 + h] = live ? w[4] : 0u;
                 }
             }
+        __syncwarp();
         int sent = 0;  // pieces of this segment issued
         auto issue = [&]() {
             if (sent > 0 && (sent & 31) == 0) {
                 pages = pages_next;
                 pages_next = page_at(sent + 32 + lane);
+                __syncwarp();
             }
             const int z = __shfl_sync(0xffffffffu, pages, sent & 31) * p.b.Hkv + it.kh;
             if (lane == 0) {
@@ -190,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 for (int c = 0; c < kHalves; ++c)
                     tma_box(dst + (kHalves + c) * kBox, &sp.mv, c * 64, row, z, bar);
             }
+            __syncwarp();
             ++sent;
             ++issued;
         };
@@ -331,12 +337,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                     sm_m[warp][r] = mx[m][h];
                     sm_l[warp][r] = v;
                 }
+                __syncwarp();
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j)
                     *reinterpret_cast<float2 *>(so + r * kOS + 8 * j + 2 * tig) =
                         make_float2(o[m][j][2 * h], o[m][j][2 * h + 1]);
             }
         __syncthreads();
+        __syncwarp();
         if (failed != 0) return;
         const bool whole = s0 == 0 && s1 == it.tiles;
         const int rows = it.nt * G;
@@ -366,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                     mine[kPartRows * D + r] = top;
                     mine[kPartRows * (D + 1) + r] = sum;
                 }
+                __syncwarp();
             }
         }
         if (sp.join_launch) {
@@ -381,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 if (joins) p.count[first_cta] = 0u;  // for the next call
             }
             __syncthreads();
+            __syncwarp();
             if (joins) {
                 __threadfence();
                 join_rows<T, D, kWarps>(p, d, first_cta, kPartRows, kPartRows, p.tt, 0, 1,

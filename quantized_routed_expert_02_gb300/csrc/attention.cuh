@@ -127,71 +127,49 @@ __device__ __forceinline__ long div_pos(long a, long b) {
     return a / b;
 }
 
-// Every thread of the CTA calls it; `scratch`: B longs of shared memory (free
-// again at the next barrier).  A run is at least `least` long.  False: nothing
-// to do.  A thread per sequence where its tiles are few (decode), a warp where
-// they are many, then each warp sums and searches by itself: at 64 sequences this
-// takes 2 us of the kernel's start where a warp per sequence took 10.
+// The run of this CTA from the sequences' costs, by one warp.
 template <int KT>
-__device__ inline bool run_begin(const Params &p, int least, long *scratch, Run &r) {
-    constexpr int kFew = 4;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    const int B = p.b.B, Hkv = p.b.Hkv;
-    for (int base = warp * 32; base < B; base += nw * 32) {
-        const int b = base + lane;
-        int nq = 0;
-        long total = 0;
-        if (b < B) {
-            const SeqView s = seq_view(p.b, b, p.hdr, blockIdx.x == 0);
-            nq = query_tiles(p, s.n);
-            if (nq <= kFew) {
-                for (int qt = 0; qt < nq; ++qt) total += tile_cost<KT>(p, s, qt);
-                scratch[b] = total * Hkv;
-            }
-        }
-        for (unsigned many = __ballot_sync(0xffffffffu, nq > kFew); many != 0; many &= many - 1) {
-            const int src = __ffs(many) - 1, nqs = __shfl_sync(0xffffffffu, nq, src);
-            const SeqView s = seq_view(p.b, base + src, p.hdr, false);
-            total = 0;
-            for (int qt = lane; qt < nqs; qt += 32) total += tile_cost<KT>(p, s, qt);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            if (lane == 0) scratch[base + src] = total * Hkv;
-        }
-    }
-    __syncthreads();
-    // the first of n entries past which the prefix sum from `at` goes beyond u
+__device__ inline void run_find(const Params &p, int least, const long *scratch, Run &r) {
+    const int lane = threadIdx.x & 31, B = p.b.B, Hkv = p.b.Hkv;
+    // the sum of the lanes' values, each below 2^58, by 32-bit reductions
+    auto total = [&](long v) {
+        const unsigned lo = __reduce_add_sync(0xffffffffu, unsigned(v) & 0x3ffffffu);
+        const unsigned mid = __reduce_add_sync(0xffffffffu, unsigned(v >> 26) & 0x3ffffffu);
+        const unsigned hi = __reduce_add_sync(0xffffffffu, unsigned(v >> 52));
+        return long(lo) + (long(mid) << 26) + (long(hi) << 52);
+    };
+    // the first of n entries past which the prefix sum from `at` goes beyond u: steps of 32
+    // by their totals, then within the step
     auto locate = [&](int n, long at, auto cost, int &which, long &start) {
         for (int base = 0; base < n; base += 32) {
-            long v = base + lane < n ? cost(base + lane) : 0;
-            const long mine = v;
-#pragma unroll 1
+            const long mine = base + lane < n ? cost(base + lane) : 0;
+            const long step = total(mine);
+            if (at + step <= r.u) {
+                at += step;
+                continue;
+            }
+            long v = mine;
+#pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long w = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += w;
             }
-            const unsigned past = __ballot_sync(0xffffffffu, at + v > r.u);
-            if (past != 0u) {
-                const int src = __ffs(past) - 1;
-                which = base + src;
-                start = at + __shfl_sync(0xffffffffu, v - mine, src);
-                return;
-            }
-            at += __shfl_sync(0xffffffffu, v, 31);
+            const int src = __ffs(__ballot_sync(0xffffffffu, at + v > r.u)) - 1;
+            which = base + src;
+            start = at + __shfl_sync(0xffffffffu, v - mine, src);
+            return;
         }
     };
-    long U = lane < B ? scratch[lane] : 0;
+    long U = scratch[0];
     if (B > 1) {
+        U = lane < B ? scratch[lane] : 0;
         for (int b = lane + 32; b < B; b += 32) U += scratch[b];
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1) U += __shfl_xor_sync(0xffffffffu, U, o);
-    } else {
-        U = scratch[0];
+        U = total(U);
     }
     r.per = max(long(least), div_pos(U + gridDim.x - 1, gridDim.x));
     r.u = r.per * blockIdx.x;
     r.end = min(U, r.u + r.per);
-    if (r.u >= r.end) return false;
+    if (r.u >= r.end) return;
     Item &it = r.item;
     it.b = 0;
     it.qt = 0;
@@ -213,7 +191,55 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
     while (it.kh * each > in) --it.kh;
     while ((it.kh + 1) * each <= in) ++it.kh;
     r.item_u = first + it.kh * each;
-    return true;
+}
+
+// Every thread of the CTA calls it; `scratch`: B longs of shared memory, `out`:
+// the run that the first warp finds.  A run is at least `least` long.  False:
+// nothing to do.  A thread per sequence where its tiles are few (decode), a warp
+// where they are many, then one warp sums and searches.
+template <int KT>
+__device__ inline bool run_begin(const Params &p, int least, long *scratch, Run *out, Run &run) {
+    constexpr int kFew = 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int B = p.b.B, Hkv = p.b.Hkv;
+    for (int base = warp * 32; base < B; base += nw * 32) {
+        const int b = base + lane;
+        int nq = 0;
+        long total = 0;
+        if (b < B) {
+            const SeqView s = seq_view(p.b, b, p.hdr, blockIdx.x == 0);
+            nq = query_tiles(p, s.n);
+            if (nq <= kFew) {
+                for (int qt = 0; qt < nq; ++qt) total += tile_cost<KT>(p, s, qt);
+                scratch[b] = total * Hkv;
+            }
+        }
+        __syncwarp();
+        for (unsigned many = __ballot_sync(0xffffffffu, nq > kFew); many != 0; many &= many - 1) {
+            const int src = __ffs(many) - 1, nqs = __shfl_sync(0xffffffffu, nq, src);
+            const SeqView s = seq_view(p.b, base + src, p.hdr, false);
+            total = 0;
+            for (int qt = lane; qt < nqs; qt += 32) total += tile_cost<KT>(p, s, qt);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+            if (lane == 0) scratch[base + src] = total * Hkv;
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // A warp that left a branch lane by lane stays apart, at a multiple of the time, until it is
+        // brought together (the search took 6000 cycles that way, 2000 so); so wherever
+        // single lanes have just worked, here and in the kernels.
+        __syncwarp();
+        Run r;
+        run_find<KT>(p, least, scratch, r);
+        if (lane == 0) *out = r;
+    }
+    __syncthreads();
+    __syncwarp();
+    run = *out;
+    return run.u < run.end;
 }
 
 // The CTA's segment of r.item: tiles [s0, s1); false when the run ends before them.
@@ -384,6 +410,7 @@ __device__ inline void join_rows(const Params &p, const JoinDesc &d, int first_c
                 }
             }
         }
+        __syncwarp();
         if (!live) continue;
         const size_t at = size_t(d.row0 + tok) * p.b.Hq + d.kh * G + row % half % G;
         const float inv = sum > 0.f ? 1.f / sum : 0.f;

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2][2],
         o_full[2], drain;
     __shared__ uint32_t tmem_base;
+    __shared__ Run run_sh;
     const Params &p = tp.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = p.b.Hq / p.b.Hkv;
@@ -187,17 +188,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         prefetch_map(&tp.mk);
         prefetch_map(&tp.mv);
     }
+    __syncwarp();
     fence_mbar_init();
     pdl_enter();
     if (tid == kCopyWarp * 32) p.desc[blockIdx.x].parts = 0;
+    __syncwarp();
     Run run;
-    if (!run_begin<kKeys>(p, kLeast, reinterpret_cast<long *>(smem), run)) return;
-    if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);
-    fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
+    if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);  // beside the search
     tc::fence_before_sync();
-    __syncthreads();
+    const bool work = run_begin<kKeys>(p, kLeast, reinterpret_cast<long *>(smem), &run_sh, run);
     tc::fence_after_sync();
     const uint32_t tmem = tmem_base;
+    if (!work) {
+        if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+        return;
+    }
+    fence_proxy_async_smem();  // the sequences' costs (generic) before the copies into the ring
+    __syncthreads();
 
     if (warp >= kCopyWarp) {
         // ---- Q of each segment and its K tiles, or its V tiles
@@ -220,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
             }
             ++seg;
             if (me == 0 && lane == 0 && s0 == 0 && s1 < it.tiles) p.desc[blockIdx.x] = join_desc(p, run);
+            __syncwarp();
             auto page_z = [&](int j) {  // page-head of this lane's box of tile j
                 const int key = (it.t0 + s0 + j) * kKeys + lane * tp.box_rows;
                 if (j >= s1 - s0 || lane >= nbox || key >= it.len) return 0;
@@ -250,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         for (int c = 0; c < C::kCh; ++c)
                             tma_box3(dst + c * C::kSlab, kv == 0 ? &tp.mk : &tp.mv, c * 64, row, z, &full[st]);
                     }
+                    __syncwarp();
                 }
             }
             run_next<kKeys>(p, run);

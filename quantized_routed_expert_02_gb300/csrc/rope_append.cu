@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
                 if (pg >= 0) cache32 = long(pg) * Hkv * a.b.page + at % a.b.page;
             }
         }
+        __syncwarp();
         const bool live = __shfl_sync(0xffffffffu, int(live32), turn) != 0;  // else a row of no sequence
         const long cache = __shfl_sync(0xffffffffu, cache32, turn);
         const int nrow = min(row + 1, row_last);
