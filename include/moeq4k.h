@@ -375,7 +375,7 @@ MOE_API moe_status moe_add_rmsnorm(const void *x_dev, moe_dtype x_dtype, const f
  *  records MOE_ERR_CACHE_RANGE (detail: the value), and the rows of that
  *  sequence are not valid output.
  *  Limits: 1 <= N <= 2^22, 1 <= B <= 4096, Hkv >= 1, Hq a multiple of Hkv,
- *  Hq <= 256, Hq / Hkv <= 128, num_pages * Hkv <= 2^30.
+ *  Hq <= 256, Hq / Hkv <= 128, num_pages * Hkv and max_pages * page <= 2^30.
  *
  * moe_rope_append: rows of projected queries, keys and values -> rotated
  * queries, and keys and values in the cache.
@@ -412,16 +412,19 @@ MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
  *  softcap * tanh(z_j / softcap);  out = sum_j softmax(z)_j v_j, and lse_dev
  *  [N, Hq] fp32 (or NULL) receives log sum_j exp(z_j).  Query head h reads
  *  key/value head h / (Hq / Hkv).  A row that sees nothing gives out 0 and
- *  lse -inf.  q_dev, out_dev [N, Hq, D] of dtype; scale finite.
+ *  lse -inf.  q_dev, out_dev [N, Hq, D] of dtype; scale finite, and
+ *  scale / softcap.
  *  max_new >= 1: the most new tokens of any sequence, as far as the caller
  *  knows; it picks the kernel and may be wrong (only speed depends on it).
  *  Scores, softmax statistics and sums are fp32; the weights are rounded to
  *  dtype for their product with V, as the scores' operands are.  The cached
  *  rows below kv_lens must be finite (a non-finite V row reaches the rows of
  *  the same tile that do not see it); rows at or past it may hold anything.
- *  The workspace needs moe_attention_workspace_bytes (0: invalid shape; never
- *  above 48 MiB), initialised once with moe_workspace_init (status word); one
- *  call at a time may use it.  Results are bitwise repeatable.
+ *  One or two launches.  ws_dev: moe_attention_workspace_bytes (0: invalid
+ *  shape; never above 48 MiB), a workspace of its own, not one that the FFN
+ *  calls use (both keep values behind the header), initialised with
+ *  moe_workspace_init before its first use and after MOE_ERR_TIMEOUT; one call
+ *  at a time may use it.  Results are bitwise repeatable.
  */
 MOE_API size_t moe_attention_workspace_bytes(int Hq, int Hkv, int D);
 MOE_API moe_status moe_attention_paged(const void *q_dev, const void *k_pages_dev,

@@ -14,6 +14,7 @@ constexpr int kMaxSeqs = 4096;
 constexpr int kMaxHeads = 256;
 constexpr int kMaxGroup = 128;
 constexpr int kMaxAxes = 8;
+constexpr int64_t kMaxIndex = int64_t(1) << 30;  // page-heads of a cache, tokens of a sequence
 
 bool known_type(moe_dtype t) { return t == MOE_F32 || t == MOE_F16 || t == MOE_BF16; }
 bool type16(moe_dtype t) { return t == MOE_F16 || t == MOE_BF16; }
@@ -31,7 +32,8 @@ moe_status check_batch(const PagedBatch &p, moe_dtype type) {
     if (p.page != 16 && p.page != 32 && p.page != 64 && p.page != 128 && p.page != 256)
         return MOE_ERR_INVALID_SHAPE;
     MOE_TRY(check_heads(p.Hq, p.Hkv, p.D));
-    if (int64_t(p.num_pages) * p.Hkv > (int64_t(1) << 30)) return MOE_ERR_INVALID_SHAPE;
+    if (int64_t(p.num_pages) * p.Hkv > kMaxIndex || int64_t(p.max_pages) * p.page > kMaxIndex)
+        return MOE_ERR_INVALID_SHAPE;
     if (!type16(type)) return MOE_ERR_INVALID_SHAPE;
     return MOE_OK;
 }
@@ -123,6 +125,7 @@ moe_status moe_attention_paged(const void *q, const void *k_pages, const void *v
     MOE_TRY(check_batch(p, dtype));
     if (max_new < 1 || window < 0 || !finite_f(scale) || !(softcap >= 0.f) || !finite_f(softcap))
         return MOE_ERR_INVALID_SHAPE;
+    if (softcap > 0.f && !finite_f(4.f * scale / softcap)) return MOE_ERR_INVALID_SHAPE;
     MOE_TRY(check_ptr(q, 16));
     MOE_TRY(check_ptr(out, 16));
     MOE_TRY(check_opt(lse, 4));

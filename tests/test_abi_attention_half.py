@@ -35,7 +35,7 @@ BATCH = dict(N=5, B=2, max_pages=4, num_pages=9, page=16, Hq=8, Hkv=2, D=128, dt
 BAD_BATCH = [dict(N=0), dict(N=(1 << 22) + 1), dict(B=0), dict(B=4097), dict(max_pages=0), dict(num_pages=0),
              dict(page=0), dict(page=8), dict(page=24), dict(page=512), dict(Hkv=0), dict(Hq=0), dict(Hq=9),
              dict(Hq=264), dict(Hq=129, Hkv=1), dict(D=96), dict(D=256), dict(D=0), dict(dtype=0), dict(dtype=3),
-             dict(num_pages=1 << 30)]
+             dict(num_pages=1 << 30), dict(max_pages=1 << 27)]
 
 
 def rope(lib, qkv=ALIGNED, pos=ALIGNED, freq=ALIGNED, axis=None, axes=1, rot=64, qw=None, kw=None, eps=1e-6,
@@ -79,7 +79,8 @@ def attn(lib, q=ALIGNED, k=ALIGNED, v=ALIGNED, table=ALIGNED, offs=ALIGNED, lens
 
 
 @pytest.mark.parametrize("bad", BAD_BATCH + [dict(max_new=0), dict(window=-1), dict(scale=NAN), dict(scale=INF),
-                                             dict(softcap=-1.0), dict(softcap=INF), dict(softcap=NAN)])
+                                             dict(softcap=-1.0), dict(softcap=INF), dict(softcap=NAN),
+                                             dict(softcap=1e-38, scale=1e5)])
 def test_attention_shapes(lib, bad):
     assert attn(lib, **bad) == SHAPE
 

@@ -345,6 +345,62 @@ def test_attention_repeat_is_bitwise(m):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("seed", range(40))
+def test_attention_drawn(m, seed):
+    """Ragged batches, head layouts, pages, masks and scales drawn at random."""
+    r = np.random.default_rng([7, seed])
+    Hkv = int(r.choice([1, 2, 3, 4]))
+    G = int(r.choice([1, 2, 3, 5, 7, 8, 16, 24, 40]))
+    D, page = int(r.choice([64, 128])), int(r.choice([16, 32, 64, 128, 256]))
+    B = int(r.integers(1, 7))
+    most = int(r.choice([1, 1, 3, 20, 150]))
+    new = [int(r.integers(0, most + 1)) for _ in range(B)]
+    new[0] = max(1, new[0])
+    lens = [int(max(0, n + r.integers(-3, 1) if r.random() < 0.2 else n + r.integers(0, 900))) for n in new]
+    dtype = torch.float16 if r.random() < 0.5 else torch.bfloat16
+    case = Batch(new, lens, Hkv * G, Hkv, D, page, dtype, seed=seed, spare_rows=int(r.integers(0, 3)))
+    check_attn(m, case, window=int(r.choice([0, 0, 1, 17, 128, 300])), softcap=float(r.choice([0, 0, 3.0, 40.0])),
+               scale=float(r.choice([D ** -0.5, D ** -0.5, -0.1, 0.3])))
+
+
+@pytest.mark.parametrize("B,most", [(700, 1), (4096, 1), (300, 12)])
+def test_attention_many_sequences(m, B, most):
+    """More sequences than CTAs, most of them short, some empty."""
+    r = np.random.default_rng(B)
+    new = [int(x) for x in r.integers(0, most + 1, B)]
+    lens = [n + int(x) for n, x in zip(new, r.integers(0, 40, B))]
+    check_attn(m, Batch(new, lens, 8, 2, 64, 16, torch.bfloat16, seed=B))
+
+
+def test_cache_past_32_bits(m):
+    """A cache of over 2^31 values (and 2^32 bytes) per tensor: rows at its far end are written and read."""
+    Hq, Hkv, D, page = 16, 4, 128, 64
+    case = Batch([3, 40], [700, 130], Hq, Hkv, D, page, torch.bfloat16, seed=9)
+    P = (1 << 31) // (Hkv * page * D) + case.P + 5
+    far = {}
+    for n in ("k", "v"):
+        far[n] = torch.empty(P, Hkv, page, D, dtype=case.dtype, device=DEV)
+        far[n][P - case.P:] = getattr(case, n).to(DEV)
+    table = torch.where(case.table < case.P, case.table + (P - case.P), 1 << 30).to(DEV)
+    ws = m.alloc_attention_workspace(Hq, Hkv, D, device=DEV)
+    out = torch.full((case.N, Hq, D), float("nan"), dtype=case.dtype, device=DEV)
+    for most in (1, 40):  # both kernels
+        m.moe_attention_paged(case.q.to(DEV), far["k"], far["v"], table, case.offs.to(DEV), case.lens.to(DEV), most,
+                              D ** -0.5, out, ws)
+        o, _, tol, _ = attention_ref(case, D ** -0.5)
+        within(out, o, tol, "out")
+    g = torch.Generator().manual_seed(1)
+    qkv = torch.randn(case.N, (Hq + 2 * Hkv) * D, generator=g).to(case.dtype)
+    pos = torch.cat([torch.arange(L - n, L) for n, L in zip(case.new, case.lens_list)])[None].to(torch.int32)
+    m.moe_rope_append(qkv.to(DEV), pos.to(DEV), inv_freq(D).to(DEV), out, far["k"], far["v"], table,
+                      case.offs.to(DEV), case.lens.to(DEV), ws)
+    assert m.moe_read_device_status(ws)[0] == 0
+    q, k, v, qe, ke = rope_ref(qkv, pos, inv_freq(D), None, Hq, Hkv, D, None, None, EPS, False)
+    r = dict(q_out=out.cpu(), k=far["k"][P - case.P:].cpu(), v=far["v"][P - case.P:].cpu(), q=q, k_ref=k, v_ref=v,
+             qe=qe, ke=ke, code=0)
+    check_rope(case, r)
+
+
 def test_attention_in_a_graph_on_a_side_stream(m):
     """Captured once, replayed while the lengths and the table grow on the device."""
     case = Batch([1, 1], [64, 30], 16, 2, 128, 16, torch.bfloat16, seed=6)
