@@ -408,7 +408,8 @@ MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
  * moe_attention_paged: attention of every sequence's new tokens over its
  * cached ones (a single token, a few drafted ones, a chunk of a prompt).
  *  The row at cache index t sees the keys j <= t and, with window > 0,
- *  j > t - window.  z_j = scale * (q . k_j), with softcap > 0 then
+ *  j > t - window (table entries of pages that no new token sees are then
+ *  not read).  z_j = scale * (q . k_j), with softcap > 0 then
  *  softcap * tanh(z_j / softcap);  out = sum_j softmax(z)_j v_j, and lse_dev
  *  [N, Hq] fp32 (or NULL) receives log sum_j exp(z_j).  Query head h reads
  *  key/value head h / (Hq / Hkv).  A row that sees nothing gives out 0 and

@@ -89,7 +89,7 @@ __device__ __forceinline__ void put_vec(float *p, const float (&v)[2]) {
 template <typename T, int kPer>
 __device__ __forceinline__ void store_row(const Params &p, size_t row, int lane, float top, float sum,
                                           const float (&v)[kPer]) {
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = over_sum(sum);
     uint32_t w[kPer / 2];
 #pragma unroll
     for (int c = 0; c < kPer / 2; ++c) w[c] = Pair<T>::make(v[2 * c] * inv, v[2 * c + 1] * inv);
@@ -97,7 +97,7 @@ __device__ __forceinline__ void store_row(const Params &p, size_t row, int lane,
     if (kPer == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[kPer / 2 - 1]);
     else dst[0] = w[0];
     if (p.lse != nullptr && lane == 0)
-        p.lse[row] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
+        p.lse[row] = log_sum(top, sum);
     __syncwarp();
 }
 
@@ -150,8 +150,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         // the pages of 32 pieces at a time, and of the 32 after them
         auto page_at = [&](int i) {
             if (i >= n) return 0;
-            const int pg = page_of(p.b, it.b, key_first + i * kTile, p.hdr);
-            return pg < 0 ? p.b.num_pages : pg;  // a bad page: past the tensor, read as zeros
+            // past the tensor, read as zeros: a piece before every row's window (its page may be
+            // gone already) and a bad page
+            const int key = key_first + i * kTile;
+            const int pg = key + kPiece <= it.seen ? -1 : page_of(p.b, it.b, key, p.hdr);
+            return pg < 0 ? p.b.num_pages : pg;
         };
         int pages = page_at(lane), pages_next = n > 32 ? page_at(32 + lane) : 0;
         // this thread's rows: gid, gid + 8 of each 16; their position, -1 for rows past the tile

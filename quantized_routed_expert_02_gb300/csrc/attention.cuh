@@ -77,12 +77,20 @@ __device__ __forceinline__ float score(float s, const Params &p) {
     return fmaf(__fdividef(-2.f, 1.f + exp2_approx(s * p.cap_in)), p.cap_log2, p.cap_log2);
 }
 
+// 1 / the weights' sum, 0 for a row that saw nothing, and the natural logarithm
+// of the sum over the scores themselves (a NaN stays one in both).
+__device__ __forceinline__ float over_sum(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+__device__ __forceinline__ float log_sum(float top, float sum) {
+    return sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.693147180559945f;
+}
+
 struct Item {
     int b, qt, kh;
     int row0;    // first row (token) of the tile
     int nt;      // tokens in it
     int pos0;    // cache index of the first
     int len;     // cached tokens
+    int seen;    // first key that a row sees
     int t0;      // first key tile
     int tiles;   // key tiles, at least 1 (a tile whose rows see nothing has one, all masked)
 };
@@ -94,13 +102,13 @@ __device__ __forceinline__ int query_tiles(const Params &p, int n) {
 
 template <int KT>
 __device__ __forceinline__ void item_tiles(int window, int tt, const SeqView &s, int qt, int &nt,
-                                           int &pos0, int &t0, int &tiles) {
+                                           int &pos0, int &seen, int &t0, int &tiles) {
     nt = min(tt, s.n - qt * tt);
     pos0 = s.len - s.n + qt * tt;
     const int last = pos0 + nt - 1;
-    const int kb = window > 0 && pos0 >= window ? pos0 - window + 1 : 0;
-    t0 = kb / KT;
-    tiles = last >= kb ? last / KT + 1 - t0 : 1;
+    seen = window > 0 && pos0 >= window ? pos0 - window + 1 : 0;
+    t0 = seen / KT;
+    tiles = last >= seen ? last / KT + 1 - t0 : 1;
 }
 
 // The CTA's run: positions [u, end) of the whole work; u is inside `item`,
@@ -116,8 +124,8 @@ struct Run {
 // key/value head.
 template <int KT>
 __device__ __forceinline__ long tile_cost(const Params &p, const SeqView &s, int qt) {
-    int nt, pos0, t0, tiles;
-    item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, t0, tiles);
+    int nt, pos0, seen, t0, tiles;
+    item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, seen, t0, tiles);
     return tiles + p.extra;
 }
 
@@ -183,7 +191,7 @@ __device__ inline void run_find(const Params &p, int least, const long *scratch,
         first = at;
     it.len = r.seq.len;
     it.row0 = r.seq.first + it.qt * p.tt;
-    item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.t0, it.tiles);
+    item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.seen, it.t0, it.tiles);
     const long each = it.tiles + p.extra;
     // the head, of few: a quotient in fp32, put right
     const long in = r.u - first;
@@ -265,7 +273,7 @@ __device__ inline void run_next(const Params &p, Run &r) {
     }
     it.len = r.seq.len;
     it.row0 = r.seq.first + it.qt * p.tt;
-    item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.t0, it.tiles);
+    item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.seen, it.t0, it.tiles);
 }
 
 // A partial result: `rows` (a multiple of 32) rows of D sums, then their maxima,
@@ -413,14 +421,14 @@ __device__ inline void join_rows(const Params &p, const JoinDesc &d, int first_c
         __syncwarp();
         if (!live) continue;
         const size_t at = size_t(d.row0 + tok) * p.b.Hq + d.kh * G + row % half % G;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = over_sum(sum);
 #pragma unroll
         for (int c = 0; c < kVec; ++c)
             if (mine[c])
                 *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + at * D + 32 * c + ch0) =
                     make_uint2(Pair<T>::make(v[c].x * inv, v[c].y * inv), Pair<T>::make(v[c].z * inv, v[c].w * inv));
         if (p.lse != nullptr && ch0 == 0 && w0 == 0)
-            p.lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
+            p.lse[at] = log_sum(top, sum);
     }
 }
 

@@ -231,8 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
             auto page_z = [&](int j) {  // page-head of this lane's box of tile j
                 const int key = (it.t0 + s0 + j) * kKeys + lane * tp.box_rows;
                 if (j >= s1 - s0 || lane >= nbox || key >= it.len) return 0;
-                const int pg = page_of(p.b, it.b, key, p.hdr);
-                return (pg < 0 ? p.b.num_pages : pg) * p.b.Hkv + it.kh;  // a bad page reads as zeros
+                // past the tensor, read as zeros: a box before every row's window (its page may be
+                // gone already) and a bad page
+                const int pg = key + tp.box_rows <= it.seen ? -1 : page_of(p.b, it.b, key, p.hdr);
+                return (pg < 0 ? p.b.num_pages : pg) * p.b.Hkv + it.kh;
             };
             int z_next = page_z(0);
             for (int j = 0; ok && j < s1 - s0; ++j) {
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     const float b = capped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
                     const unsigned long long one2 = pack2(1.f, 1.f), cap2 = pack2(k2, k2);
-                    const unsigned long long hide2 = pack2(1e-30f * sign, 1e-30f * sign);
+                    const unsigned long long hide2 = pack2(1.2e-38f * sign, 1.2e-38f * sign);
                     auto take = [&](int c, const float (&u)[16]) {
                         uint32_t w[8];
 #pragma unroll
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 const int out_row = live ? (it.row0 + h * tp.tth + tok_h) * p.b.Hq + it.kh * G + head : -1;
                 float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(2 * kHalf, D);
                 const int prow = h * kHalf + row;
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const float inv = over_sum(sum);
 #pragma unroll 1
                 for (int c = 0; ok && c < D / 64; ++c) {
                     const int ch0 = D / 2 * ch + 32 * c;  // first of 32 channels
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         mine[size_t(2 * kHalf) * D + prow] = top;
                         mine[size_t(2 * kHalf) * (D + 1) + prow] = sum;
                     } else if (p.lse != nullptr) {
-                        p.lse[out_row] = sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -CUDART_INF_F;
+                        p.lse[out_row] = log_sum(top, sum);
                     }
                 }
                 __syncwarp();

@@ -315,6 +315,42 @@ def test_attention_rows_past_the_end(m):
         check_attn(m, case)
 
 
+@pytest.mark.parametrize("new,lens,page,D,cap", [
+    ([1, 1, 1, 1], [900, 90, 129, 4000], 16, 128, 0.0), ([1, 5, 2], [700, 230, 64], 32, 64, 20.0),
+    ([150, 1, 40], [900, 800, 45], 16, 128, 0.0), ([300, 33], [301, 2000], 64, 64, 20.0),
+    ([20, 200], [1500, 700], 128, 128, 0.0), ([9, 130], [1500, 700], 256, 64, 0.0)])
+def test_attention_pages_before_the_window(m, new, lens, page, D, cap):
+    """Pages that no new token sees may be gone: their entries name nothing, their rows are NaN."""
+    for window in (1, 70, 128):
+        case = Batch(new, lens, 12, 3, D, page, torch.bfloat16, seed=window)
+        o, e, tol, lse_tol = attention_ref(case, 1 / math.sqrt(D), window, cap)
+        for b, (n, L) in enumerate(zip(new, lens)):
+            gone = max(0, L - n - window + 1) // page
+            for t in (case.k, case.v):
+                t[case.table[b, :gone].long()] = float("nan")
+            case.table[b, :gone] = -1
+        out, lse, code, detail = run_attn(m, case, window=window, softcap=cap)
+        assert code == 0, (m.status_str(code), detail)
+        within(out, o, tol, "out")
+        within(lse, e, lse_tol, "lse")
+
+
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("softcap", [0.0, 10.0])
+def test_attention_nan_query(m, new, softcap):
+    """A NaN in a query head reaches that row's output and lse, and no other."""
+    case = Batch([new, new], [500, 900], 8, 2, 128, 16, torch.float16)
+    o, e, tol, lse_tol = attention_ref(case, 1 / math.sqrt(128), 0, softcap)
+    case.q[new // 2, 3, 5] = float("nan")
+    out, lse, code, _ = run_attn(m, case, softcap=softcap)
+    assert code == 0
+    assert bool(out[new // 2, 3].isnan().all()) and bool(lse[new // 2, 3].isnan())
+    for t in (out, lse, o, e):
+        t[new // 2, 3] = 0.0
+    within(out, o, tol, "out")
+    within(lse, e, lse_tol, "lse")
+
+
 def test_attention_bad_descriptions(m):
     """A page, length or offset out of range is recorded; the other sequences stay right."""
     for what, bad in (("table", -3), ("table", 1 << 30), ("lens", 1 << 30), ("lens", -1), ("lens", 49)):
