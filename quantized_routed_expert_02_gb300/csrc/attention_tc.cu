@@ -14,6 +14,7 @@
 // 16 bits as those up to 1, and sums are fp32), so most tiles leave O alone.
 // Tensor memory: S/P of half h at column 128 h, O of half h at 256 + 128 h.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -35,6 +36,7 @@ constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 constexpr int kLeast = 4;
 constexpr int kExtra = 3;
 constexpr float kGrowth = 8.f;             // log2 growth of the maximum that forces a rescale
+constexpr float kTanhOne = 30.f;           // 2^-30 from 1 is 1 in fp32
 
 struct TcParams {
     CUtensorMap mq, mk, mv;
@@ -442,6 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     }
                     tmem_ld16(ts, v[0]);  // for the second pass
                     mt = fmaxf(mt, exchange(mt));
+                    // a capped tile that every row sees whole and whose tangents stay off 1
+                    const bool plain = kMode == kCapped && !edge && !__any_sync(0xffffffffu, mt * p.cap_in > kTanhOne);
                     if (mt != -CUDART_INF_F) mt = capped ? score<true>(mt * sign, p) : score<false>(mt * sign, p);
                     if (j == 0) {
                         top = mt;
@@ -468,9 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     const float scale = capped ? p.cap_in : p.scale_log2;
                     const float b = capped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
-                    const unsigned long long one2 = pack2(1.f, 1.f), cap2 = pack2(k2, k2);
+                    const unsigned long long one2 = pack2(1.f, 1.f);
                     const unsigned long long hide2 = pack2(1.2e-38f * sign, 1.2e-38f * sign);
-                    auto take = [&](int c, const float (&u)[16]) {
+                    auto take = [&](auto is_plain, int c, const float (&u)[16]) {
+                        constexpr bool kPlain = decltype(is_plain)::value;
                         uint32_t w[8];
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
@@ -478,22 +483,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                             if (capped) {
                                 // score() less the base: d = 1 + e^2x, and the four reciprocals from that
                                 // of their product (a reciprocal takes twice an exponential's time; d is
-                                // kept below 2^30 for it, where the tangent is 1 in fp32)
+                                // kept below 2^30 for it, where the tangent is 1 in fp32: by the tile's
+                                // maxima where it is plain)
                                 unsigned long long d2[2];
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     float x, y;
                                     unpack2(mul2(e2[k], scale2), x, y);
-                                    d2[k] = add2(pack2(exp2_approx(fminf(x, 30.f)), exp2_approx(fminf(y, 30.f))), one2);
+                                    if (!kPlain) x = fminf(x, kTanhOne), y = fminf(y, kTanhOne);
+                                    d2[k] = add2(pack2(exp2_approx(x), exp2_approx(y)), one2);
                                 }
                                 float x, y;
                                 unpack2(mul2(d2[0], d2[1]), x, y);
-                                const float r = rcp_approx(x * y);
+                                const float r = rcp_approx(x * y) * k2;
                                 const unsigned long long r2 = mul2(pack2(r, r), pack2(y, x));
                                 // a hidden score (an infinity) is brought back by a product that is
                                 // nothing beside any other score
-                                e2[0] = fma2(e2[0], hide2, fma2(mul2(r2, d2[1]), cap2, base2));
-                                e2[1] = fma2(e2[1], hide2, fma2(mul2(r2, d2[0]), cap2, base2));
+                                e2[0] = fma2(r2, d2[1], kPlain ? base2 : fma2(e2[0], hide2, base2));
+                                e2[1] = fma2(r2, d2[0], kPlain ? base2 : fma2(e2[1], hide2, base2));
                             } else {
                                 e2[0] = fma2(e2[0], scale2, base2);
                                 e2[1] = fma2(e2[1], scale2, base2);
@@ -523,19 +530,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         if (lane == 0 && ok) mbar_arrive(bar);
                         __syncwarp();
                     };
-                    wait_ld16(v[0]);
-                    tmem_ld16(ts + 16, v[1]);
-                    take(0, v[0]);
-                    wait_ld16(v[1]);
-                    tmem_ld16(ts + 32, v[0]);
-                    take(1, v[1]);
-                    ready(&p_ready[h][0]);  // the product of this thread's first 32 keys can begin
-                    wait_ld16(v[0]);
-                    tmem_ld16(ts + 48, v[1]);
-                    take(2, v[0]);
-                    wait_ld16(v[1]);
-                    take(3, v[1]);
-                    ready(&p_ready[h][1]);
+                    auto weights = [&](auto is_plain) {
+                        wait_ld16(v[0]);
+                        tmem_ld16(ts + 16, v[1]);
+                        take(is_plain, 0, v[0]);
+                        wait_ld16(v[1]);
+                        tmem_ld16(ts + 32, v[0]);
+                        take(is_plain, 1, v[1]);
+                        ready(&p_ready[h][0]);  // the product of this thread's first 32 keys can begin
+                        wait_ld16(v[0]);
+                        tmem_ld16(ts + 48, v[1]);
+                        take(is_plain, 2, v[0]);
+                        wait_ld16(v[1]);
+                        take(is_plain, 3, v[1]);
+                        ready(&p_ready[h][1]);
+                    };
+                    if (plain) weights(std::true_type());
+                    else weights(std::false_type());
                     float sa, sb;
                     unpack2(add2(s2[0], s2[1]), sa, sb);
                     sum += sa + sb;
