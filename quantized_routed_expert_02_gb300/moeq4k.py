@@ -23,6 +23,8 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+from . import _binding  # noqa: E402  (native entry points; needs the library above)
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _S = ctypes.c_size_t
@@ -72,10 +74,6 @@ EXPORTS = tuple(_SIGS)
 
 MOE_OK = 0
 STATUS_NAMES = {i: _lib.moe_status_str(i).decode() for i in range(11)}
-
-
-_F32, _F64, _I32, _I8 = torch.float32, torch.float64, torch.int32, torch.int8
-MOE_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
 class MoeError(RuntimeError):
@@ -246,83 +244,12 @@ def moe_ffn_q8k_codes(q, d, sums, idx, w, gate, up, down, E, I, y, ws, stream=No
                                   ws.numel(), _stream(stream)), "moe_ffn_q8k_codes")
 
 
-def _refuse(t, shape, dtype, name):
-    """What is wrong with a tensor that is not a contiguous one of this shape and type."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: {t.dtype}, not {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    raise ValueError(f"{name}: not contiguous")
-
-
-def _tensor(t, shape, dtype, name):
-    """The device pointer of a contiguous tensor of this shape and type.  The attention half
-    takes many buffers whose sizes follow from one another, so the binding checks them before
-    the library, which sees only pointers."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, shape, dtype, name)
-
-
-def _dtype(t, name) -> int:
-    code = MOE_DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: {t.dtype} is not one of float32, float16, bfloat16")
-    return code
-
-
-def moe_add_rmsnorm(x, residual, gamma, eps, sum_out=None, y=None, q8k=None, stream=None) -> None:
-    """s = x + residual (None: s = x), y = RMSNorm(s) * gamma.  ``sum_out`` receives s, ``y`` the
-    normed rows (fp32, fp16 or bf16), ``q8k`` = (q, d, sums) their Q8_K blocks."""
-    rows = T, H = x.shape
-    q = d = sums = None
-    if q8k is not None:
-        q = _tensor(q8k[0], rows, _I8, "q")
-        d = _tensor(q8k[1], (T, H // 256), _F32, "d")
-        sums = _tensor(q8k[2], (T, H // 32), _I32, "sums")
-    code = _lib.moe_add_rmsnorm(
-        _tensor(x, rows, x.dtype, "x"), _dtype(x, "x"),
-        None if residual is None else _tensor(residual, rows, _F32, "residual"),
-        _tensor(gamma, (H,), _F32, "gamma"), eps, T, H,
-        None if sum_out is None else _tensor(sum_out, rows, _F32, "sum_out"),
-        None if y is None else _tensor(y, rows, y.dtype, "y"), 0 if y is None else _dtype(y, "y"),
-        q, d, sums, _stream(stream))
-    if code:
-        raise MoeError(code, "moe_add_rmsnorm")
-
-
-def _batch(k_pages, v_pages, page_table, q_offs, kv_lens):
-    """(pages, table, offsets, lengths) pointers, then B, max_pages, num_pages, page, Hkv, D."""
-    cache = P, Hkv, page, D = k_pages.shape
-    table = B, max_pages = page_table.shape
-    t = k_pages.dtype
-    return (_tensor(k_pages, cache, t, "k_pages"), _tensor(v_pages, cache, t, "v_pages"),
-            _tensor(page_table, table, _I32, "page_table"), _tensor(q_offs, (B + 1,), _I32, "q_offs"),
-            _tensor(kv_lens, (B,), _I32, "kv_lens"), B, max_pages, P, page, Hkv, D)
-
-
-def moe_rope_append(qkv, pos, inv_freq, q_out, k_pages, v_pages, page_table, q_offs, kv_lens, ws,
-                    axis=None, q_norm_w=None, k_norm_w=None, eps=1e-6, interleaved=False,
-                    stream=None) -> None:
-    """Rows ``qkv`` [N, (Hq + 2 Hkv) D] -> normed and rotated queries ``q_out`` [N, Hq, D], keys
-    (normed, rotated) and values into the cache.  ``pos`` int32 [axes, N], ``inv_freq`` float64
-    [rot / 2] radians per position, ``axis`` int32 [rot / 2]: the axis of each pair."""
-    k, v, table, offs, lens, B, max_pages, P, page, Hkv, D = _batch(k_pages, v_pages, page_table,
-                                                                    q_offs, kv_lens)
-    out = N, Hq, _ = q_out.shape
-    axes, half = pos.shape[0], inv_freq.shape[0]
-    t = k_pages.dtype
-    code = _lib.moe_rope_append(
-        _tensor(qkv, (N, (Hq + 2 * Hkv) * D), t, "qkv"), _tensor(pos, (axes, N), _I32, "pos"),
-        _tensor(inv_freq, (half,), _F64, "inv_freq"),
-        None if axis is None else _tensor(axis, (half,), _I32, "axis"), axes, 2 * half,
-        1 if interleaved else 0, None if q_norm_w is None else _tensor(q_norm_w, (D,), _F32, "q_norm_w"),
-        None if k_norm_w is None else _tensor(k_norm_w, (D,), _F32, "k_norm_w"), eps,
-        _tensor(q_out, out if out[2] == D else (N, Hq, D), t, "q_out"), k, v, table, offs, lens, N, B,
-        max_pages, P, page, Hq, Hkv, D, _dtype(k_pages, "k_pages"), ws.data_ptr(), ws.numel(),
-        _stream(stream))
-    if code:
-        raise MoeError(code, "moe_rope_append")
+# moe_add_rmsnorm, moe_rope_append and moe_attention_paged check many tensors against one another;
+# they are native (csrc/binding.cpp), for the calls of single tokens.
+_binding.set_error(MoeError)
+moe_add_rmsnorm = _binding.moe_add_rmsnorm
+moe_rope_append = _binding.moe_rope_append
+moe_attention_paged = _binding.moe_attention_paged
 
 
 def moe_attention_workspace_bytes(Hq, Hkv, D) -> int:
@@ -337,23 +264,6 @@ def alloc_attention_workspace(Hq, Hkv, D, device="cuda") -> torch.Tensor:
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     moe_workspace_init(ws)
     return ws
-
-
-def moe_attention_paged(q, k_pages, v_pages, page_table, q_offs, kv_lens, max_new, scale, out, ws,
-                        lse=None, window=0, softcap=0.0, stream=None) -> None:
-    """Attention of the new rows ``q`` [N, Hq, D] over each sequence's cached tokens -> ``out``
-    [N, Hq, D], ``lse`` [N, Hq] (optional).  ``max_new``: the most new tokens of a sequence."""
-    k, v, table, offs, lens, B, max_pages, P, page, Hkv, D = _batch(k_pages, v_pages, page_table,
-                                                                    q_offs, kv_lens)
-    N, Hq, _ = q.shape
-    rows, t = (N, Hq, D), k_pages.dtype
-    code = _lib.moe_attention_paged(
-        _tensor(q, rows, t, "q"), k, v, table, offs, lens, N, B, max_new, max_pages, P, page, Hq, Hkv, D,
-        _dtype(k_pages, "k_pages"), scale, softcap, window, _tensor(out, rows, t, "out"),
-        None if lse is None else _tensor(lse, (N, Hq), _F32, "lse"), ws.data_ptr(), ws.numel(),
-        _stream(stream))
-    if code:
-        raise MoeError(code, "moe_attention_paged")
 
 
 def moe_read_device_status(ws, stream=None):
