@@ -1,5 +1,5 @@
 // Attention of few query rows per key/value head over a paged cache: single
-// tokens, drafted tokens (moe_attention_paged up to kMaxRows rows a tile).
+// tokens, drafted tokens (moe_attention_paged up to 16 rows).
 //
 // Bytes bound: every cached key and value is read once, 4 D bytes for 4 D
 // flops per row.  So the keys stream through the SM and everything else stays
@@ -11,6 +11,13 @@
 // group times the tokens); a tcgen05 tile would be 128 rows, seven eighths of
 // it padding, for work that the memory bounds anyway.  The four warps'
 // results meet at the end of a segment.
+//
+// Measured (32/4 heads of 128, bf16): 64 sequences of 4000 tokens 89 us
+// = 5.9 TB/s, eight of 20000 with 16/16 heads 207 us = 6.3 TB/s; a bare loop of the
+// same copies over 268 MB reaches 6.3 to 6.6 TB/s whatever its box.  Short
+// batches pay about 7 us from the launch to the first keys (offsets, the search for the
+// run, page table, keys: four dependent reads) and, with many parts, 4 us for
+// the joining launch: one token over 131071 52 us, over 93 5.4 us.
 #include <algorithm>
 
 #include <cuda.h>
@@ -24,10 +31,11 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPiece = 16;                // keys of a piece
 constexpr int kTile = kWarps * kPiece;    // keys of a tile: a piece for every warp
-constexpr int kRing = 24 * 1024;          // bytes of a warp's ring
-constexpr int kMaxRows = 32;
-constexpr int kLeast = 5;
-constexpr int kExtra = 3;
+constexpr int kRing = 24 * 1024;          // bytes of a warp's ring: two CTAs' fill an SM
+constexpr int kMaxRows = 16;              // of the instruction
+constexpr int kLeast = 5;                 // least work of a CTA, in key tiles (4 to 8 measured alike)
+constexpr int kPartRows = 32;             // rows of a partial result (a multiple of 32)
+constexpr int kExtra = 3;                 // an item's fixed cost, in key tiles (2 to 4 alike)
 
 struct StreamParams {
     CUtensorMap mk, mv;
@@ -101,14 +109,13 @@ __device__ __forceinline__ void store_row(const Params &p, size_t row, int lane,
     __syncwarp();
 }
 
-template <typename T, int D, int MT, bool kCap>
+template <typename T, int D, bool kCap>
 __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __grid_constant__ StreamParams sp) {
     constexpr int kHalves = D / 64;                      // boxes of a row
     constexpr int kBox = kPiece * 128;                   // bytes of a box
     constexpr int kStage = 2 * kHalves * kBox;           // K and V of a piece
     constexpr int kStages = kRing / kStage;
-    constexpr int kRows = 16 * MT;
-    constexpr int kPartRows = kMaxRows;
+    constexpr int kRows = kMaxRows;
     constexpr int kOS = D + 8;                           // floats of a row of the warps' meeting buffer
     static_assert(kRows * kOS * 4 <= kRing, "a warp's sums fit its ring");
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -158,25 +165,23 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         };
         int pages = page_at(lane), pages_next = n > 32 ? page_at(32 + lane) : 0;
         // this thread's rows: gid, gid + 8 of each 16; their position, -1 for rows past the tile
-        int pos[MT][2];
-        uint32_t qa[MT][D / 16][4];
+        int pos[2];
+        uint32_t qa[D / 16][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int h = 0; h < 2; ++h) {
+            const int r = 8 * h + gid;
+            const int tok = r / G;
+            const bool live = tok < it.nt;
+            pos[h] = live ? it.pos0 + tok : -1;
+            const T *row = static_cast<const T *>(p.q) +
+                           (size_t(it.row0 + (live ? tok : 0)) * p.b.Hq + it.kh * G + r % G) * D;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = 16 * m + 8 * h + gid;
-                const int tok = r / G;
-                const bool live = tok < it.nt;
-                pos[m][h] = live ? it.pos0 + tok : -1;
-                const T *row = static_cast<const T *>(p.q) +
-                               (size_t(it.row0 + (live ? tok : 0)) * p.b.Hq + it.kh * G + r % G) * D;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t *w = reinterpret_cast<const uint32_t *>(row + 16 * k + 2 * tig);
-                    qa[m][k][h] = live ? w[0] : 0u;
-                    qa[m][k][2 + h] = live ? w[4] : 0u;
-                }
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(row + 16 * k + 2 * tig);
+                qa[k][h] = live ? w[0] : 0u;
+                qa[k][2 + h] = live ? w[4] : 0u;
             }
+        }
         __syncwarp();
         int sent = 0;  // pieces of this segment issued
         auto issue = [&]() {
@@ -204,14 +209,11 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         };
         for (int i = 0; i < kStages && i < n; ++i) issue();
 
-        float o[MT][D / 8][4], mx[MT][2], l[MT][2];
+        float o[D / 8][4], mx[2], l[2];
+        mx[0] = mx[1] = -CUDART_INF_F;
+        l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            mx[m][0] = mx[m][1] = -CUDART_INF_F;
-            l[m][0] = l[m][1] = 0.f;
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) o[m][j][0] = o[m][j][1] = o[m][j][2] = o[m][j][3] = 0.f;
-        }
+        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
         bool ok = true;
         for (int i = 0; i < n; ++i) {
@@ -222,11 +224,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
             }
             const int key0 = key_first + i * kTile;
             const uint32_t kb = smem_addr(ring + st * kStage), vb = kb + kHalves * kBox;
-            float s[MT][2][4];
+            float s[2][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) s[m][j][0] = s[m][j][1] = s[m][j][2] = s[m][j][3] = 0.f;
+            for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
             // S: matrices (keys 0-7, channels lo/hi), (keys 8-15, lo/hi) of each 16 channels
             const int krow = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
 #pragma unroll
@@ -234,57 +234,51 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 uint32_t b[4];
                 const int ch = (2 * k + kc) & 7;
                 ldsm4(b, kb + (k / 4) * kBox + krow * 128 + ((ch ^ (krow & 7)) << 4));
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    mma16816<T>(s[m][0], qa[m][k], b[0], b[1]);
-                    mma16816<T>(s[m][1], qa[m][k], b[2], b[3]);
-                }
+                mma16816<T>(s[0], qa[k], b[0], b[1]);
+                mma16816<T>(s[1], qa[k], b[2], b[3]);
             }
             const bool edge = key0 + kPiece - 1 > it.pos0 || (p.window > 0 && key0 <= last - p.window);
-            uint32_t pa[MT][4];
+            uint32_t pa[4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    s[j][c] = score<kCap>(s[j][c], p);
+                    if (edge) {
+                        const int key = key0 + 8 * j + 2 * tig + (c & 1), at = pos[c >> 1];
+                        if (key > at || (p.window > 0 && at - key >= p.window))
+                            s[j][c] = -CUDART_INF_F;
+                    }
+                }
+            float cor[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]),
+                                fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                v = fmaxf(v, mx[h]);
+                const float base = v == -CUDART_INF_F ? 0.f : v;  // nothing seen yet
+                cor[h] = exp2_approx(mx[h] - base);
+                mx[h] = v;
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        s[m][j][c] = score<kCap>(s[m][j][c], p);
-                        if (edge) {
-                            const int key = key0 + 8 * j + 2 * tig + (c & 1), at = pos[m][c >> 1];
-                            if (key > at || (p.window > 0 && at - key >= p.window))
-                                s[m][j][c] = -CUDART_INF_F;
-                        }
-                    }
-                float cor[2];
+                    for (int c = 0; c < 2; ++c)
+                        s[j][2 * h + c] = exp2_approx(s[j][2 * h + c] - base);
+                l[h] = l[h] * cor[h] + ((s[0][2 * h] + s[0][2 * h + 1]) +
+                                              (s[1][2 * h] + s[1][2 * h + 1]));
+            }
+            // the weights rounded to the 16-bit type for the product; the sum l keeps them whole
+            pa[0] = Pair<T>::make(s[0][0], s[0][1]);
+            pa[1] = Pair<T>::make(s[0][2], s[0][3]);
+            pa[2] = Pair<T>::make(s[1][0], s[1][1]);
+            pa[3] = Pair<T>::make(s[1][2], s[1][3]);
+            if (__any_sync(0xffffffffu, cor[0] != 1.f || cor[1] != 1.f)) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float v = fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]),
-                                    fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1]));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                    v = fmaxf(v, mx[m][h]);
-                    const float base = v == -CUDART_INF_F ? 0.f : v;  // nothing seen yet
-                    cor[h] = exp2_approx(mx[m][h] - base);
-                    mx[m][h] = v;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            s[m][j][2 * h + c] = exp2_approx(s[m][j][2 * h + c] - base);
-                    l[m][h] = l[m][h] * cor[h] + ((s[m][0][2 * h] + s[m][0][2 * h + 1]) +
-                                                  (s[m][1][2 * h] + s[m][1][2 * h + 1]));
-                }
-                // the weights rounded to the 16-bit type for the product; the sum l keeps them whole
-                pa[m][0] = Pair<T>::make(s[m][0][0], s[m][0][1]);
-                pa[m][1] = Pair<T>::make(s[m][0][2], s[m][0][3]);
-                pa[m][2] = Pair<T>::make(s[m][1][0], s[m][1][1]);
-                pa[m][3] = Pair<T>::make(s[m][1][2], s[m][1][3]);
-                if (__any_sync(0xffffffffu, cor[0] != 1.f || cor[1] != 1.f)) {
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        o[m][j][0] *= cor[0], o[m][j][1] *= cor[0];
-                        o[m][j][2] *= cor[1], o[m][j][3] *= cor[1];
-                    }
+                for (int j = 0; j < D / 8; ++j) {
+                    o[j][0] *= cor[0], o[j][1] *= cor[0];
+                    o[j][2] *= cor[1], o[j][3] *= cor[1];
                 }
             }
             // O: matrices (keys 0-7, channel chunk c), (keys 8-15, c), then c + 1, transposed;
@@ -307,11 +301,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                     b[0] &= keep[0], b[1] &= keep[1];
                     b[2] &= keep[0], b[3] &= keep[1];
                 }
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    mma16816<T>(o[m][2 * j], pa[m], b[0], b[1]);
-                    mma16816<T>(o[m][2 * j + 1], pa[m], b[2], b[3]);
-                }
+                mma16816<T>(o[2 * j], pa, b[0], b[1]);
+                mma16816<T>(o[2 * j + 1], pa, b[2], b[3]);
             }
             ++done;
             __syncwarp();  // every lane has read the stage
@@ -329,23 +320,21 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         float *so = reinterpret_cast<float *>(ring);
         __syncwarp();
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v = l[m][h];
-                v += __shfl_xor_sync(0xffffffffu, v, 1);
-                v += __shfl_xor_sync(0xffffffffu, v, 2);
-                const int r = 16 * m + 8 * h + gid;
-                if (tig == 0) {
-                    sm_m[warp][r] = mx[m][h];
-                    sm_l[warp][r] = v;
-                }
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j)
-                    *reinterpret_cast<float2 *>(so + r * kOS + 8 * j + 2 * tig) =
-                        make_float2(o[m][j][2 * h], o[m][j][2 * h + 1]);
+        for (int h = 0; h < 2; ++h) {
+            float v = l[h];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            const int r = 8 * h + gid;
+            if (tig == 0) {
+                sm_m[warp][r] = mx[h];
+                sm_l[warp][r] = v;
             }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+                *reinterpret_cast<float2 *>(so + r * kOS + 8 * j + 2 * tig) =
+                    make_float2(o[j][2 * h], o[j][2 * h + 1]);
+        }
         __syncthreads();
         __syncwarp();
         if (failed != 0) return;
@@ -428,32 +417,22 @@ cudaError_t each_stream(F f) {
     cudaError_t e = cudaSuccess;
     auto of = [&](auto type) {
         using T = decltype(type);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, 1, false>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, 1, true>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, 2, false>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, 2, true>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, 1, false>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, 1, true>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, 2, false>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, 2, true>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, false>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, true>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, false>);
+        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, true>);
     };
     of(__half());
     of(__nv_bfloat16());
     return e;
 }
 
-template <typename T, int D, int MT>
-cudaError_t launch_stream_cap(const StreamParams &sp, int grid, cudaStream_t s) {
+template <typename T, int D>
+cudaError_t launch_stream(const StreamParams &sp, int grid, cudaStream_t s) {
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(kStreamSmem), s, sp);
     };
-    return sp.p.cap_in != 0.f ? go(attention_stream_kernel<T, D, MT, true>)
-                              : go(attention_stream_kernel<T, D, MT, false>);
-}
-
-template <typename T, int D>
-cudaError_t launch_stream_rows(const StreamParams &sp, int rows, int grid, cudaStream_t s) {
-    return rows <= 16 ? launch_stream_cap<T, D, 1>(sp, grid, s) : launch_stream_cap<T, D, 2>(sp, grid, s);
+    return sp.p.cap_in != 0.f ? go(attention_stream_kernel<T, D, true>) : go(attention_stream_kernel<T, D, false>);
 }
 
 Params make_params(const AttnArgs &a) {
@@ -489,7 +468,7 @@ cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int
 size_t attention_part_bytes(int D) {
     using namespace attn;
     return kCountBytes + kDescBytes +
-           std::max(size_t(2) * kMaxCtas * part_floats(kMaxRows, D) * sizeof(float), tc_part_bytes(D));
+           std::max(size_t(2) * kMaxCtas * part_floats(kPartRows, D) * sizeof(float), tc_part_bytes(D));
 }
 
 cudaError_t init_attention() {
@@ -504,11 +483,15 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     using namespace attn;
     const int G = a.b.Hq / a.b.Hkv;
     const Params base = make_params(a);
+    // More than 16 rows are faster on the tensor cores' own tile, although most of its rows are
+    // padding (32 rows over 6000 keys of 32 sequences 75 us, with a second instruction tile here
+    // 84; 32 over 900 of one 11.8 and 18.3; 24 over 2000 of eight 18.8 and 24.8); up to 16 this
+    // kernel is (16 rows over 2000 keys of eight 16.7 and 18.7; 8 over 12000 and less of 48
+    // 57.5 and 58.3; 8 over 93 of one 5.5 and 9.7).
     if (long(max_new) * G > kMaxRows) return launch_tc(a, base, num_sms, s);
     StreamParams sp = {};
     sp.p = base;
-    const int rows = max_new * G <= 16 ? 16 : kMaxRows;
-    sp.p.tt = std::max(1, rows / G);
+    sp.p.tt = kMaxRows / G;
     sp.p.tt_magic = 0xffffffffu / unsigned(sp.p.tt) + 1;
     sp.p.extra = kExtra;
     if (!encode_pages_map(&sp.mk, a.k, a.b, a.type, kPiece) || !encode_pages_map(&sp.mv, a.v, a.b, a.type, kPiece))
@@ -524,13 +507,12 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     sp.join_launch = std::min(grid / items, tiles / kLeast) + 1 > kJoinInside;
     cudaError_t e;
     if (a.type == MOE_F16)
-        e = a.b.D == 64 ? launch_stream_rows<__half, 64>(sp, rows, grid, s)
-                        : launch_stream_rows<__half, 128>(sp, rows, grid, s);
+        e = a.b.D == 64 ? launch_stream<__half, 64>(sp, grid, s) : launch_stream<__half, 128>(sp, grid, s);
     else
-        e = a.b.D == 64 ? launch_stream_rows<__nv_bfloat16, 64>(sp, rows, grid, s)
-                        : launch_stream_rows<__nv_bfloat16, 128>(sp, rows, grid, s);
+        e = a.b.D == 64 ? launch_stream<__nv_bfloat16, 64>(sp, grid, s)
+                        : launch_stream<__nv_bfloat16, 128>(sp, grid, s);
     if (e != cudaSuccess || !sp.join_launch) return e;
-    return launch_join(sp.p, a.type, grid, kMaxRows, kMaxRows, sp.p.tt, s);
+    return launch_join(sp.p, a.type, grid, kPartRows, kPartRows, sp.p.tt, s);
 }
 
 }  // namespace moeq4k

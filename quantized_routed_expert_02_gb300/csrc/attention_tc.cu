@@ -3,16 +3,27 @@
 // memory and S, P, O in tensor memory.
 //
 // An item is two halves of 128 query rows (tokens x the group's heads) that
-// share every key tile of 128 keys.  Eleven warps: two groups of four softmax
-// warps, one per half (a thread per row), two copying warps (TMA boxes of one
-// page each into a ring of K and V tiles; one warp cannot issue the 32 boxes that
-// pages of 16 make of a K and a V tile in the time of their MMAs) and a warp that
-// issues the MMAs.  The two halves take turns on the tensor pipe: while one half's P V and next Q K^T
-// run, the other half's softmax does.  P overwrites S in tensor memory and is
-// the A operand from there.  O is rescaled only when a row's maximum has grown
-// by more than 2^8 since the last rescale (weights up to 2^8 are as exact in
-// 16 bits as those up to 1, and sums are fp32), so most tiles leave O alone.
-// Tensor memory: S/P of half h at column 128 h, O of half h at 256 + 128 h.
+// share every key tile of 128 keys.  Nineteen warps: for each half eight
+// softmax warps (two threads per row, half the keys each), a warp that issues the
+// MMAs, and two that copy (K tiles with the queries, V tiles; TMA boxes of
+// one page at most).  The two halves take turns on the tensor pipe: while one
+// half's P V and next Q K^T run, the other half's softmax does.  P overwrites S
+// in tensor memory and is the A operand from there; a thread's first 32 keys
+// are handed over as soon as they are written.  O is rescaled only when a row's
+// maximum has grown by more than 2^8 since the last rescale (weights up to 2^8
+// are as exact in 16 bits as those up to 1, and sums are fp32), so most
+// tiles leave O alone.  Tensor memory: S/P of half h at column 128 h, O of half h
+// at 256 + 128 h.
+//
+// What bounds it: without a cap shared memory (each of the two products reads
+// its 32 KB tile from there once per half, next to the copies' writes) and the tensor
+// pipe: a chunk of 2048 rows over 16384 keys, 32/4 heads of 128, takes 337 us
+// = 1.53 PFLOP/s.  With a cap the exponentials and reciprocals, 10 cycles a
+// warp for 32 scores, and their arithmetic do: 446 us.  Short ranges pay for
+// their segments' ends (the last softmax, the result, the first softmax: 3 tiles'
+// time): a prompt of 4096, 117 us = 1.18 PFLOP/s.  One thread per row
+// (four warps a half) was slower by the latency of its chain: the capped chunk 613
+// against 465 us, the prompt 2 us faster.
 #include <algorithm>
 #include <type_traits>
 
@@ -33,8 +44,10 @@ constexpr int kCopyWarps = 2;               // K tiles, V tiles
 constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kCopyWarps);
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
-constexpr int kLeast = 4;
-constexpr int kExtra = 3;
+// The least work of a CTA, and an item's fixed cost, in key tiles (a cost of 1, 2, 3:
+// a prompt of 4096 139, 117, 118 us, four of 1024 64, 52.5, 55 us).
+constexpr int kLeast = 2;
+constexpr int kExtra = 2;
 constexpr float kGrowth = 8.f;             // log2 growth of the maximum that forces a rescale
 constexpr float kTanhOne = 30.f;           // 2^-30 from 1 is 1 in fp32
 
@@ -624,7 +637,6 @@ cudaError_t launch(const TcParams &tp, int grid, cudaStream_t s) {
     if (tp.p.cap_in > 0.f) return go(attention_tc_kernel<T, D, kCapped>);
     if (tp.p.cap_in == 0.f && tp.p.scale_log2 > 0.f) return go(attention_tc_kernel<T, D, kScaled>);
     return go(attention_tc_kernel<T, D, kAny>);
-
 }
 
 template <typename T, int D>

