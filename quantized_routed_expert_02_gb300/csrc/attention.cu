@@ -34,6 +34,9 @@ constexpr int kTile = kWarps * kPiece;    // keys of a tile: a piece for every w
 constexpr int kRing = 24 * 1024;          // bytes of a warp's ring: two CTAs' fill an SM
 constexpr int kMaxRows = 16;              // of the instruction
 constexpr int kLeast = 5;                 // least work of a CTA, in key tiles (4 to 8 measured alike)
+// What parting items costs, in key tiles: of one sequence, 300 tokens take 8.1 us whole
+// and 10.7 in parts, 400 9.5 and 10.4, 600 12.1 and 10.8; of 64 sequences, 1000 27 and 31.
+constexpr int kSplit = 12;
 constexpr int kPartRows = 32;             // rows of a partial result (a multiple of 32)
 constexpr int kExtra = 3;                 // an item's fixed cost, in key tiles (2 to 4 alike)
 
@@ -141,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     pdl_enter();
     if (sp.join_launch && tid == 0) p.desc[blockIdx.x].parts = 0;
     Run run;
-    if (!run_begin<kTile>(p, kLeast, reinterpret_cast<long *>(smem), &run_sh, run)) return;
+    if (!run_begin<kTile>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, run)) return;
     fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
     __syncthreads();
 

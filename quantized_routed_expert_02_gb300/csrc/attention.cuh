@@ -5,7 +5,8 @@
 // tokens times the G query heads that read the head.  Its work is the run of
 // key tiles (KT keys) that any of its rows sees, at least one, and a fixed cost
 // of `extra` tiles (queries in, results out).  All items' work, laid end to end,
-// is cut into equal runs, one per CTA, whatever the sequences' lengths: a CTA's
+// is cut into equal runs, one per CTA, whatever the sequences' lengths (but a CTA
+// takes an item whole where that is as fast): a CTA's
 // run is a few segments, each a range of key tiles of one item.  An item
 // inside one run is finished there; one that crosses a cut leaves a partial
 // result (unnormalised sums, running maximum and sum) per segment.  These are
@@ -115,6 +116,7 @@ __device__ __forceinline__ void item_tiles(int window, int tt, const SeqView &s,
 // which starts at item_u with `extra` positions before its first tile.
 struct Run {
     long per;  // positions of a run
+    int pad;   // every item's cost where each CTA takes one whole, else 0
     long u, end, item_u;
     SeqView seq;  // item's sequence
     Item item;
@@ -135,9 +137,15 @@ __device__ __forceinline__ long div_pos(long a, long b) {
     return a / b;
 }
 
-// The run of this CTA from the sequences' costs, by one warp.
+// Beside a sequence's cost: its items (of all key/value heads) and their largest cost.
+struct Items {
+    int n, top;
+};
+
+// The run of this CTA from the sequences' costs and items, by one warp.
 template <int KT>
-__device__ inline void run_find(const Params &p, int least, const long *scratch, Run &r) {
+__device__ inline void run_find(const Params &p, int least, int split, const long *scratch, const Items *items,
+                                Run &r) {
     const int lane = threadIdx.x & 31, B = p.b.B, Hkv = p.b.Hkv;
     // the sum of the lanes' values, each below 2^58, by 32-bit reductions
     auto total = [&](long v) {
@@ -168,13 +176,24 @@ __device__ inline void run_find(const Params &p, int least, const long *scratch,
             return;
         }
     };
-    long U = scratch[0];
-    if (B > 1) {
-        U = lane < B ? scratch[lane] : 0;
-        for (int b = lane + 32; b < B; b += 32) U += scratch[b];
-        U = total(U);
+    long U = 0;
+    unsigned n = 0, top = 0;
+    for (int b = lane; b < B; b += 32) {
+        U += scratch[b];
+        n = min(n + unsigned(items[b].n), 1u << 26);
+        top = max(top, unsigned(items[b].top));
     }
-    r.per = max(long(least), div_pos(U + gridDim.x - 1, gridDim.x));
+    U = total(U);
+    n = __reduce_add_sync(0xffffffffu, n);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const long even = div_pos(U, gridDim.x);
+    r.pad = n <= gridDim.x && long(top) <= even + split ? int(top) : 0;
+    if (r.pad != 0) {
+        U = long(n) * r.pad;
+        r.per = r.pad;
+    } else {
+        r.per = max(long(least), even * gridDim.x == U ? even : even + 1);
+    }
     r.u = r.per * blockIdx.x;
     r.end = min(U, r.u + r.per);
     if (r.u >= r.end) return;
@@ -182,17 +201,18 @@ __device__ inline void run_find(const Params &p, int least, const long *scratch,
     it.b = 0;
     it.qt = 0;
     long at = 0, first = 0;
-    if (B > 1) locate(B, 0, [&](int b) { return scratch[b]; }, it.b, at);
+    if (B > 1) locate(B, 0, [&](int b) { return r.pad != 0 ? long(items[b].n) * r.pad : scratch[b]; }, it.b, at);
     r.seq = seq_view(p.b, it.b, p.hdr, false);
     const int nq = query_tiles(p, r.seq.n);
     if (nq > 1)
-        locate(nq, at, [&](int qt) { return tile_cost<KT>(p, r.seq, qt) * Hkv; }, it.qt, first);
+        locate(nq, at, [&](int qt) { return (r.pad != 0 ? long(r.pad) : tile_cost<KT>(p, r.seq, qt)) * Hkv; }, it.qt,
+               first);
     else
         first = at;
     it.len = r.seq.len;
     it.row0 = r.seq.first + it.qt * p.tt;
     item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.seen, it.t0, it.tiles);
-    const long each = it.tiles + p.extra;
+    const long each = r.pad != 0 ? r.pad : it.tiles + p.extra;
     // the head, of few: a quotient in fp32, put right
     const long in = r.u - first;
     it.kh = min(int(__fdividef(float(in), float(each))), Hkv - 1);
@@ -201,25 +221,33 @@ __device__ inline void run_find(const Params &p, int least, const long *scratch,
     r.item_u = first + it.kh * each;
 }
 
-// Every thread of the CTA calls it; `scratch`: B longs of shared memory, `out`:
-// the run that the first warp finds.  A run is at least `least` long.  False:
-// nothing to do.  A thread per sequence where its tiles are few (decode), a warp
-// where they are many, then one warp sums and searches.
+// Every thread of the CTA calls it; `scratch`: 16 B bytes of shared memory, `out`:
+// the run that the first warp finds.  A run is at least `least` long.  It is one
+// item where there are no more of them than CTAs and the longest takes no longer
+// than an even share and `split`, the time (in key tiles) of leaving parts and
+// joining them.  False: nothing to do.  A thread per sequence where its tiles are
+// few (decode), a warp where they are many, then one warp sums and searches.
 template <int KT>
-__device__ inline bool run_begin(const Params &p, int least, long *scratch, Run *out, Run &run) {
+__device__ inline bool run_begin(const Params &p, int least, int split, long *scratch, Run *out, Run &run) {
     constexpr int kFew = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int B = p.b.B, Hkv = p.b.Hkv;
+    Items *items = reinterpret_cast<Items *>(scratch + B);
     for (int base = warp * 32; base < B; base += nw * 32) {
         const int b = base + lane;
         int nq = 0;
-        long total = 0;
+        long total = 0, top = 0;
         if (b < B) {
             const SeqView s = seq_view(p.b, b, p.hdr, blockIdx.x == 0);
             nq = query_tiles(p, s.n);
             if (nq <= kFew) {
-                for (int qt = 0; qt < nq; ++qt) total += tile_cost<KT>(p, s, qt);
+                for (int qt = 0; qt < nq; ++qt) {
+                    const long c = tile_cost<KT>(p, s, qt);
+                    total += c;
+                    top = max(top, c);
+                }
                 scratch[b] = total * Hkv;
+                items[b] = {nq * Hkv, int(top)};
             }
         }
         __syncwarp();
@@ -227,10 +255,19 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
             const int src = __ffs(many) - 1, nqs = __shfl_sync(0xffffffffu, nq, src);
             const SeqView s = seq_view(p.b, base + src, p.hdr, false);
             total = 0;
-            for (int qt = lane; qt < nqs; qt += 32) total += tile_cost<KT>(p, s, qt);
+            unsigned most = 0;
+            for (int qt = lane; qt < nqs; qt += 32) {
+                const long c = tile_cost<KT>(p, s, qt);
+                total += c;
+                most = max(most, unsigned(c));
+            }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            if (lane == 0) scratch[base + src] = total * Hkv;
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) {
+                scratch[base + src] = total * Hkv;
+                items[base + src] = {nqs * Hkv, int(most)};
+            }
             __syncwarp();
         }
     }
@@ -241,7 +278,7 @@ __device__ inline bool run_begin(const Params &p, int least, long *scratch, Run 
         // single lanes have just worked, here and in the kernels.
         __syncwarp();
         Run r;
-        run_find<KT>(p, least, scratch, r);
+        run_find<KT>(p, least, split, scratch, items, r);
         if (lane == 0) *out = r;
     }
     __syncthreads();
@@ -262,7 +299,7 @@ __device__ __forceinline__ bool run_segment(const Params &p, const Run &r, int &
 template <int KT>
 __device__ inline void run_next(const Params &p, Run &r) {
     Item &it = r.item;
-    r.u = r.item_u = r.item_u + p.extra + it.tiles;
+    r.u = r.item_u = r.item_u + (r.pad != 0 ? r.pad : p.extra + it.tiles);
     if (r.u >= r.end || ++it.kh < p.b.Hkv) return;
     it.kh = 0;
     ++it.qt;

@@ -48,6 +48,9 @@ constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 // a prompt of 4096 139, 117, 118 us, four of 1024 64, 52.5, 55 us).
 constexpr int kLeast = 2;
 constexpr int kExtra = 2;
+// What parting items costs, in key tiles: 64 tokens over 500 of eight sequences take 17.1 us
+// whole and 20.6 in parts, a prompt of 300 15.1 and 15.7, 8 tokens over 500 of eight 14.4 and 13.0.
+constexpr int kSplit = 4;
 constexpr float kGrowth = 8.f;             // log2 growth of the maximum that forces a rescale
 constexpr float kTanhOne = 30.f;           // 2^-30 from 1 is 1 in fp32
 
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     Run run;
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);  // beside the search
     tc::fence_before_sync();
-    const bool work = run_begin<kKeys>(p, kLeast, reinterpret_cast<long *>(smem), &run_sh, run);
+    const bool work = run_begin<kKeys>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, run);
     tc::fence_after_sync();
     const uint32_t tmem = tmem_base;
     if (!work) {
@@ -687,6 +690,11 @@ cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStrea
     else
         e = a.b.D == 64 ? launch<__nv_bfloat16, 64>(tp, grid, s) : launch<__nv_bfloat16, 128>(tp, grid, s);
     if (e != cudaSuccess) return e;
+    // nothing is parted where even the most and longest items that the arguments allow are taken
+    // whole (a prompt of 100 in a table of its length: 9.5 us, with the joining launch 12.0)
+    const long items = long(a.b.B) * a.b.Hkv * ((a.b.N + tp.p.tt - 1) / tp.p.tt);
+    const long tiles = (long(a.b.max_pages) * a.b.page + kKeys - 1) / kKeys;
+    if (items <= grid && tiles + kExtra <= kSplit) return cudaSuccess;
     return launch_join(tp.p, a.type, grid, 2 * kHalf, kHalf, tp.tth, s);
 }
 

@@ -315,6 +315,15 @@ def test_attention_rows_past_the_end(m):
         check_attn(m, case)
 
 
+@pytest.mark.parametrize("B,new,tile", [(1, 1, 64), (19, 1, 64), (40, 1, 64), (1, 70, 128), (9, 40, 128), (30, 90, 128)])
+def test_attention_whole_and_parted(m, B, new, tile):
+    """Lengths around those from which items are parted, one long sequence among short ones."""
+    for tiles in (2, 3, 9, 10, 17):
+        lens = [tiles * tile + d for d in (-1, 0, 1)] * B
+        check_attn(m, Batch([new] * B, lens[:B], 8, 2, 64, 16, torch.bfloat16, seed=tiles))
+    check_attn(m, Batch([new] * B, [new + 5] * (B - 1) + [40 * tile], 8, 2, 64, 16, torch.bfloat16))
+
+
 @pytest.mark.parametrize("new,lens,page,D,cap", [
     ([1, 1, 1, 1], [900, 90, 129, 4000], 16, 128, 0.0), ([1, 5, 2], [700, 230, 64], 32, 64, 20.0),
     ([150, 1, 40], [900, 800, 45], 16, 128, 0.0), ([300, 33], [301, 2000], 64, 64, 20.0),
