@@ -392,7 +392,8 @@ MOE_API moe_status moe_add_rmsnorm(const void *x_dev, moe_dtype x_dtype, const f
  *  (axis 0; an entry out of range takes axis 0 and is recorded as
  *  MOE_ERR_CACHE_RANGE).  Angles are reduced exactly (64-bit fixed-point
  *  turns), so far positions lose nothing; the rest is fp32, rounded once.
- *  q_out_dev [N, Hq, D] of dtype; keys and values go to their cache rows.
+ *  q_out_dev [N, Hq, D] of dtype; keys and values go to their cache rows.  No
+ *  output overlaps an input.
  *  ws_dev: at least 256 bytes, initialised (status word only).  One launch.
  */
 MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
@@ -413,8 +414,8 @@ MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
  *  softcap * tanh(z_j / softcap);  out = sum_j softmax(z)_j v_j, and lse_dev
  *  [N, Hq] fp32 (or NULL) receives log sum_j exp(z_j).  Query head h reads
  *  key/value head h / (Hq / Hkv).  A row that sees nothing gives out 0 and
- *  lse -inf.  q_dev, out_dev [N, Hq, D] of dtype; scale finite, and
- *  scale / softcap.
+ *  lse -inf.  q_dev, out_dev [N, Hq, D] of dtype, not overlapping; scale
+ *  finite, and scale / softcap.
  *  max_new >= 1: the most new tokens of any sequence, as far as the caller
  *  knows; it picks the kernel and may be wrong (only speed depends on it).
  *  Scores, softmax statistics and sums are fp32; the weights are rounded to

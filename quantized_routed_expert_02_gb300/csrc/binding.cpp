@@ -59,26 +59,42 @@ at::IntArrayRef sizes(const at::Tensor &t, size_t n, const char *name) {
     return t.sizes();
 }
 
-// The pointer of a contiguous tensor of this shape and type.
-template <typename P = void>
-P *pointer(const at::Tensor &t, at::IntArrayRef shape, at::ScalarType type, const char *name) {
+// The device of a call's first tensor, where all the others have to be too.
+struct Place {
+    c10::Device device;
+
+    explicit Place(const at::Tensor &first) : device(first.device()) {}
+    void check(const at::Tensor &t, const char *name) const {
+        if (t.device() != device)
+            refuse(PyExc_ValueError, std::string(name) + ": on " + t.device().str() + ", not " + device.str());
+    }
+    // The pointer of a contiguous tensor of this shape and type.
+    template <typename P = void>
+    P *pointer(const at::Tensor &t, at::IntArrayRef shape, at::ScalarType type, const char *name) const;
+    template <typename P = void>
+    P *pointer(PyObject *o, at::IntArrayRef shape, at::ScalarType type, const char *name) const {
+        return pointer<P>(tensor(o, name), shape, type, name);
+    }
+    template <typename P = void>
+    P *optional(PyObject *o, at::IntArrayRef shape, at::ScalarType type, const char *name) const {
+        return o == Py_None ? nullptr : pointer<P>(o, shape, type, name);
+    }
+    void *workspace(const at::Tensor &t) const {
+        check(t, "ws");
+        return t.data_ptr();
+    }
+};
+
+template <typename P>
+P *Place::pointer(const at::Tensor &t, at::IntArrayRef shape, at::ScalarType type, const char *name) const {
     if (t.scalar_type() != type)
         refuse(PyExc_TypeError, std::string(name) + ": " + dtype_name(t.scalar_type()) + ", not " + dtype_name(type));
     if (t.sizes() != shape)
         refuse(PyExc_ValueError,
               std::string(name) + ": shape " + shape_text(t.sizes()) + ", not " + shape_text(shape));
     if (!t.is_contiguous()) refuse(PyExc_ValueError, std::string(name) + ": not contiguous");
+    check(t, name);
     return static_cast<P *>(t.data_ptr());
-}
-
-template <typename P = void>
-P *pointer(PyObject *o, at::IntArrayRef shape, at::ScalarType type, const char *name) {
-    return pointer<P>(tensor(o, name), shape, type, name);
-}
-
-template <typename P = void>
-P *optional(PyObject *o, at::IntArrayRef shape, at::ScalarType type, const char *name) {
-    return o == Py_None ? nullptr : pointer<P>(o, shape, type, name);
 }
 
 moe_dtype dtype_of(const at::Tensor &t, const char *name) {
@@ -190,6 +206,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         static const char *const names[] = {"x", "residual", "gamma", "eps", "sum_out", "y", "q8k", "stream"};
         const Args<8> a("moe_add_rmsnorm", names, 4, args, n, kwnames);
         const at::Tensor &x = tensor(a[0], "x");
+        const Place at_x(x);
         const at::IntArrayRef rows = sizes(x, 2, "x");
         const int T = extent(rows[0], "x"), H = extent(rows[1], "x");
         int8_t *q = nullptr;
@@ -198,22 +215,22 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         if (a[6] != Py_None) {
             if (!(PyTuple_Check(a[6]) || PyList_Check(a[6])) || PySequence_Fast_GET_SIZE(a[6]) != 3)
                 refuse(PyExc_TypeError, "q8k: not a tuple (q, d, sums)");
-            q = pointer<int8_t>(PySequence_Fast_GET_ITEM(a[6], 0), rows, at::kChar, "q");
-            d = pointer<float>(PySequence_Fast_GET_ITEM(a[6], 1), {T, H / 256}, at::kFloat, "d");
-            sums = pointer<int32_t>(PySequence_Fast_GET_ITEM(a[6], 2), {T, H / 32}, at::kInt, "sums");
+            q = at_x.pointer<int8_t>(PySequence_Fast_GET_ITEM(a[6], 0), rows, at::kChar, "q");
+            d = at_x.pointer<float>(PySequence_Fast_GET_ITEM(a[6], 1), {T, H / 256}, at::kFloat, "d");
+            sums = at_x.pointer<int32_t>(PySequence_Fast_GET_ITEM(a[6], 2), {T, H / 32}, at::kInt, "sums");
         }
         const moe_dtype xt = dtype_of(x, "x");
-        const void *xp = pointer(x, rows, x.scalar_type(), "x");
-        const float *residual = optional<float>(a[1], rows, at::kFloat, "residual");
-        const float *gamma = pointer<float>(a[2], {H}, at::kFloat, "gamma");
+        const void *xp = at_x.pointer(x, rows, x.scalar_type(), "x");
+        const float *residual = at_x.optional<float>(a[1], rows, at::kFloat, "residual");
+        const float *gamma = at_x.pointer<float>(a[2], {H}, at::kFloat, "gamma");
         const float eps = as_float(a[3]);
-        float *sum_out = optional<float>(a[4], rows, at::kFloat, "sum_out");
+        float *sum_out = at_x.optional<float>(a[4], rows, at::kFloat, "sum_out");
         void *y = nullptr;
         moe_dtype yt = MOE_F32;
         if (a[5] != Py_None) {
             const at::Tensor &t = tensor(a[5], "y");
             yt = dtype_of(t, "y");
-            y = pointer(t, rows, t.scalar_type(), "y");
+            y = at_x.pointer(t, rows, t.scalar_type(), "y");
         }
         void *s = as_stream(a[7]);
         run("moe_add_rmsnorm", [&] {
@@ -223,14 +240,15 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
 }
 
 // The paged cache and the batch of the next two.
-struct Cache {
+struct Cache : Place {
     void *k, *v;
     const int32_t *table, *offs, *lens;
     int B, max_pages, pages, page, Hkv, D;
     at::ScalarType type;
     moe_dtype dtype;
 
-    Cache(PyObject *kp, PyObject *vp, PyObject *table_, PyObject *offs_, PyObject *lens_) {
+    Cache(PyObject *kp, PyObject *vp, PyObject *table_, PyObject *offs_, PyObject *lens_)
+        : Place(tensor(kp, "k_pages")) {
         const at::Tensor &kt = tensor(kp, "k_pages"), &tt = tensor(table_, "page_table");
         const at::IntArrayRef c = sizes(kt, 4, "k_pages"), t = sizes(tt, 2, "page_table");
         pages = extent(c[0], "k_pages"), Hkv = extent(c[1], "k_pages");
@@ -258,18 +276,18 @@ PyObject *rope_append(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         const int N = extent(o[0], "q_out"), Hq = extent(o[1], "q_out");
         const int axes = extent(sizes(pos, 2, "pos")[0], "pos");
         const int half = extent(sizes(freq, 1, "inv_freq")[0], "inv_freq");
-        const void *qkv = pointer(a[0], {N, int64_t(Hq + 2 * int64_t(c.Hkv)) * c.D}, c.type, "qkv");
-        const int32_t *at_pos = pointer<int32_t>(pos, {axes, N}, at::kInt, "pos");
-        const double *f = pointer<double>(freq, {half}, at::kDouble, "inv_freq");
-        const int32_t *axis = optional<int32_t>(a[10], {half}, at::kInt, "axis");
-        const float *qw = optional<float>(a[11], {c.D}, at::kFloat, "q_norm_w");
-        const float *kw = optional<float>(a[12], {c.D}, at::kFloat, "k_norm_w");
+        const void *qkv = c.pointer(a[0], {N, int64_t(Hq + 2 * int64_t(c.Hkv)) * c.D}, c.type, "qkv");
+        const int32_t *at_pos = c.pointer<int32_t>(pos, {axes, N}, at::kInt, "pos");
+        const double *f = c.pointer<double>(freq, {half}, at::kDouble, "inv_freq");
+        const int32_t *axis = c.optional<int32_t>(a[10], {half}, at::kInt, "axis");
+        const float *qw = c.optional<float>(a[11], {c.D}, at::kFloat, "q_norm_w");
+        const float *kw = c.optional<float>(a[12], {c.D}, at::kFloat, "k_norm_w");
         const float eps = a[13] == Py_None ? 1e-6f : as_float(a[13]);
         const int turned = a[14] == Py_None ? 0 : PyObject_IsTrue(a[14]);
         if (turned < 0) throw Raised();
-        void *q_out = pointer(out, {N, Hq, c.D}, c.type, "q_out");
+        void *q_out = c.pointer(out, {N, Hq, c.D}, c.type, "q_out");
         const at::Tensor &ws = tensor(a[9], "ws");
-        void *w = ws.data_ptr(), *s = as_stream(a[15]);
+        void *w = c.workspace(ws), *s = as_stream(a[15]);
         run("moe_rope_append", [&] {
             return moe_rope_append(qkv, at_pos, f, axis, axes, 2 * half, turned, qw, kw, eps, q_out, c.k, c.v,
                                    c.table, c.offs, c.lens, N, c.B, c.max_pages, c.pages, c.page, Hq, c.Hkv, c.D,
@@ -287,13 +305,13 @@ PyObject *attention_paged(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
         const at::Tensor &qt = tensor(a[0], "q");
         const at::IntArrayRef r = sizes(qt, 3, "q");
         const int N = extent(r[0], "q"), Hq = extent(r[1], "q");
-        const void *q = pointer(qt, {N, Hq, c.D}, c.type, "q");
+        const void *q = c.pointer(qt, {N, Hq, c.D}, c.type, "q");
         const int most = as_int(a[6]), window = a[11] == Py_None ? 0 : as_int(a[11]);
         const float scale = as_float(a[7]), softcap = a[12] == Py_None ? 0.f : as_float(a[12]);
-        void *out = pointer(a[8], {N, Hq, c.D}, c.type, "out");
-        float *lse = optional<float>(a[10], {N, Hq}, at::kFloat, "lse");
+        void *out = c.pointer(a[8], {N, Hq, c.D}, c.type, "out");
+        float *lse = c.optional<float>(a[10], {N, Hq}, at::kFloat, "lse");
         const at::Tensor &ws = tensor(a[9], "ws");
-        void *w = ws.data_ptr(), *s = as_stream(a[13]);
+        void *w = c.workspace(ws), *s = as_stream(a[13]);
         run("moe_attention_paged", [&] {
             return moe_attention_paged(q, c.k, c.v, c.table, c.offs, c.lens, N, c.B, most, c.max_pages, c.pages,
                                        c.page, Hq, c.Hkv, c.D, c.dtype, scale, softcap, window, out, lse, w,

@@ -103,3 +103,18 @@ def test_the_library_refuses(call, change, status):
 def test_integers_past_32_bits():
     with pytest.raises(OverflowError):
         m.moe_attention_paged(**dict(attn_args(), max_new=1 << 40))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", CALLS)
+def test_a_tensor_left_on_the_host(call):
+    """Every tensor in turn: refused before a kernel could see its address."""
+    def to(v, dev):
+        return tuple(to(t, dev) for t in v) if isinstance(v, tuple) else v.to(dev) if isinstance(v, torch.Tensor) else v
+
+    args = {k: to(v, "cuda") for k, v in CALLS[call]().items()}
+    del args["stream"]
+    for name, v in CALLS[call]().items():
+        if isinstance(v, (torch.Tensor, tuple)):
+            with pytest.raises(ValueError, match="on c"):
+                getattr(m, call)(**dict(args, **{name: v}))
