@@ -17,7 +17,7 @@
 // same copies over 268 MB reaches 6.3 to 6.6 TB/s whatever its box.  Short
 // batches pay about 7 us from the launch to the first keys (offsets, the search for the
 // run, page table, keys: four dependent reads) and, with many parts, 4 us for
-// the joining launch: one token over 131071 52 us, over 93 5.4 us.
+// the joining launch: one token over 131071 52 us, over 2000 9.1, over 93 5.9 us.
 #include <algorithm>
 
 #include <cuda.h>
@@ -33,12 +33,14 @@ constexpr int kPiece = 16;                // keys of a piece
 constexpr int kTile = kWarps * kPiece;    // keys of a tile: a piece for every warp
 constexpr int kRing = 24 * 1024;          // bytes of a warp's ring: two CTAs' fill an SM
 constexpr int kMaxRows = 16;              // of the instruction
-constexpr int kLeast = 5;                 // least work of a CTA, in key tiles (4 to 8 measured alike)
-// What parting items costs, in key tiles: of one sequence, 300 tokens take 8.1 us whole
-// and 10.7 in parts, 400 9.5 and 10.4, 600 12.1 and 10.8; of 64 sequences, 1000 27 and 31.
-constexpr int kSplit = 12;
+// The least work of a CTA, in key tiles (1, 3, 5, 8: one token over 2000 9.1, 11.1, 12.7,
+// 15.2 us), and an item's fixed cost (2, 3, 4: 48 tokens over 1500 34.0, 33.1, 34.1 us).
+constexpr int kLeast = 1;
+constexpr int kExtra = 3;
+// What parting items costs, in key tiles: of one sequence, 300 tokens take 8.2 us whole
+// and 8.9 in parts, 400 9.6 and 8.8; of 64 sequences, 300 10.0 and 14.9, 1000 27 and 31.
+constexpr int kSplit = 9;
 constexpr int kPartRows = 32;             // rows of a partial result (a multiple of 32)
-constexpr int kExtra = 3;                 // an item's fixed cost, in key tiles (2 to 4 alike)
 
 struct StreamParams {
     CUtensorMap mk, mv;
@@ -501,10 +503,11 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
         return cudaErrorInvalidValue;
     const int grid = std::min(2 * num_sms, kMaxCtas);
     // Few items over many CTAs make many parts of each.  Up to kJoinInside of them the last
-    // CTA joins them on its way out (one token over 93: 9.3 us with the launch, 5.2 without);
+    // CTA joins them on its way out (one token over 93: 9.6 us with the launch, 5.9 without);
     // more take it longer than a second launch that spreads them over the GPU (one token
-    // over 131071, 76 parts: 52.4 us with the launch, 55.2 without).
-    constexpr long kJoinInside = 16;
+    // over 600, 10 parts and more: 8.8 us with the launch, 9.4 without; over 131071, 76
+    // parts: 52 and 56).
+    constexpr long kJoinInside = 10;
     const long items = long(a.b.B) * a.b.Hkv;
     const long tiles = (long(a.b.max_pages) * a.b.page + kTile - 1) / kTile + kExtra;  // of an item, at most
     sp.join_launch = std::min(grid / items, tiles / kLeast) + 1 > kJoinInside;
