@@ -48,9 +48,10 @@ constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 // a prompt of 4096 139, 117, 118 us, four of 1024 64, 52.5, 55 us).
 constexpr int kLeast = 2;
 constexpr int kExtra = 2;
-// What parting items costs, in key tiles: 64 tokens over 500 of eight sequences take 17.1 us
-// whole and 20.6 in parts, a prompt of 300 15.1 and 15.7, 8 tokens over 500 of eight 14.4 and 13.0.
-constexpr int kSplit = 4;
+// What parting items costs, in key tiles: 64 tokens over 500 of eight sequences take 17.3 us
+// whole and 20.7 in parts, a prompt of 300 12.8 and 15.2, of 1200 26.2 and 28.1; 8 tokens over
+// 500 of eight 14.5 and 13.2.
+constexpr int kSplit = 5;
 constexpr float kGrowth = 8.f;             // log2 growth of the maximum that forces a rescale
 constexpr float kTanhOne = 30.f;           // 2^-30 from 1 is 1 in fp32
 
