@@ -445,7 +445,9 @@ MOE_API moe_status moe_attention_paged(const void *q_dev, const void *k_pages_de
  * call records MOE_ERR_TIMEOUT in the workspace status and writes no output.
  * On the tensor-core batch path, CTA 0 of the gate/up GEMM then counts none
  * of its finished h rows, so the down GEMM's waits for those experts run
- * out: MOE_ERR_TIMEOUT again, and y holds no valid output.
+ * out: MOE_ERR_TIMEOUT again, and y holds no valid output.  CTA 0 of
+ * moe_attention_paged's kernels then waits for an arrival that nobody makes:
+ * MOE_ERR_TIMEOUT, no valid output.
  * Re-initialise the workspace (moe_workspace_init) afterwards to clear the
  * sticky status.
  */

@@ -207,6 +207,7 @@ moe_status q8k_ffn_enqueue(const float *x, const Q8Codes &codes, const int32_t *
 }  // namespace
 
 unsigned long long moeq4k::device_wait_ns() { return g_wait_ns; }
+int moeq4k::device_withhold() { return g_withhold; }
 
 moe_status moeq4k::validate_shape(int T, int H, int E, int k, int I) {
     return check_shape(T, H, E, k, I);

@@ -139,6 +139,7 @@ moe_status moe_attention_paged(const void *q, const void *k_pages, const void *v
     a.hdr = static_cast<WsHeader *>(ws);
     a.scratch = static_cast<uint8_t *>(ws) + sizeof(WsHeader);
     a.wait_ns = device_wait_ns();
+    a.withhold = device_withhold();
     return cuda_status(launch_attention(a, max_new, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -99,6 +99,12 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint6
     }
 }
 
+// The limit, in ns, of waits for work that a warp has in flight itself and that
+// must end before its CTA does (copies into shared memory, products into tensor
+// memory).  Not the limit of the other waits: where that one has run out, these
+// still have to be seen to end, and they hang on no other warp or CTA.
+constexpr uint64_t kDrainNs = 1000000000ull;
+
 // Order this thread's earlier generic-proxy accesses to shared memory before
 // later async-proxy (bulk copy) writes to it.
 __device__ __forceinline__ void fence_proxy_async_smem() {

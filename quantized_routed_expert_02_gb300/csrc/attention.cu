@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         prefetch_map(&sp.mv);
     }
     if (lane == 0)
-        for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1 + withheld(p));
     __syncwarp();
     fence_mbar_init();
     pdl_enter();
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         }
         // copies still in flight after a time-out land before the ring is written
         for (; done < issued; ++done)
-            wait_phase(&full[warp][done % kStages], (done / kStages) & 1u, p.wait_ns);
+            wait_phase(&full[warp][done % kStages], (done / kStages) & 1u, kDrainNs);
 
         // the warps' sums into their rings, the rows' statistics beside them
         float *so = reinterpret_cast<float *>(ring);
@@ -456,6 +456,7 @@ Params make_params(const AttnArgs &a) {
     p.desc = reinterpret_cast<JoinDesc *>(a.scratch + kCountBytes);
     p.part = reinterpret_cast<float *>(a.scratch + kCountBytes + kDescBytes);
     p.wait_ns = a.wait_ns;
+    p.withhold = a.withhold;
     return p;
 }
 

@@ -56,7 +56,11 @@ struct Params {
     JoinDesc *desc;     // [kMaxCtas]
     float *part;
     unsigned long long wait_ns;
+    int withhold;       // test hook: CTA 0's waits run out
 };
+
+// The arrivals that CTA 0's barriers expect and never get (moe_debug_withhold_arrivals).
+__device__ __forceinline__ int withheld(const Params &p) { return p.withhold != 0 && blockIdx.x == 0 ? 1 : 0; }
 
 // Bring a tensor map (a kernel parameter) into the cache of such descriptors.
 __device__ __forceinline__ void prefetch_map(const void *map) {

@@ -163,10 +163,14 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The whole warp waits for a phase; recorded when it runs out.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Params &p, int who) {
-    const bool ok = __all_sync(0xffffffffu, wait_phase(bar, parity, p.wait_ns));
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Params &p, int who,
+                                          uint64_t limit_ns) {
+    const bool ok = __all_sync(0xffffffffu, wait_phase(bar, parity, limit_ns));
     if (!ok) record_status(p.hdr, MOE_ERR_TIMEOUT, who);
     return ok;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const Params &p, int who) {
+    return warp_wait(bar, parity, p, who, p.wait_ns);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
-        for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 8), mbar_init(&p_ready[h][1], 8), mbar_init(&o_full[h], 1);
+        for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 8 + withheld(p)), mbar_init(&p_ready[h][1], 8), mbar_init(&o_full[h], 1);
         mbar_init(&drain, 1);
         prefetch_map(&tp.mq);
         prefetch_map(&tp.mk);
@@ -284,14 +288,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
             }
             run_next<kKeys>(p, run);
         }
-        // copies that a time-out left unawaited land before the CTA exits
-        if (!ok) {
-            for (uint32_t i = 0; i < uint32_t(C::kStages) && i < g; ++i) {
-                const uint32_t gg = g - 1 - i;
-                if (int(gg % 2) == me) warp_wait(&full[gg % C::kStages], (gg / C::kStages) & 1u, p, 53);
-            }
+        // this warp's last copies land before the CTA exits, whoever else gave up on what: the MMA
+        // warp may have left by a time-out of its own and not waited for them
+        for (uint32_t i = 0; i < uint32_t(C::kStages) && i < g; ++i) {
+            const uint32_t gg = g - 1 - i;
+            if (int(gg % 2) == me) warp_wait(&full[gg % C::kStages], (gg / C::kStages) & 1u, p, 53, kDrainNs);
         }
-        if (me == 0 && seg > 0) warp_wait(&q_full, (seg - 1) & 1u, p, 54);
+        if (me == 0 && seg > 0) warp_wait(&q_full, (seg - 1) & 1u, p, 54, kDrainNs);
     } else if (warp == kMmaWarp) {
         // ---- the MMAs; the whole warp walks the loop, one lane issues
         const bool leader = elect_one();
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         // every MMA complete before the tensor memory is released
         if (leader) tc::commit_arrive(&drain);
         __syncwarp();
-        warp_wait(&drain, 0, p, 60);
+        warp_wait(&drain, 0, p, 60, kDrainNs);
     } else {
         // ---- softmax: half h, rows 32 q4 + lane, keys 64 ch .. of each tile (and of the
         // result the channels D/2 ch ..)

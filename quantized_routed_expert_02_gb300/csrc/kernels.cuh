@@ -117,6 +117,8 @@ cudaError_t launch_q8k_ffn(const int8_t *xq, const float *xd, const int32_t *xs,
 
 // The device-side wait limit of later launches, in ns (moe_debug_set_wait_limit).
 unsigned long long device_wait_ns();
+// Whether later launches withhold arrivals (moe_debug_withhold_arrivals).
+int device_withhold();
 
 // Residual addition + RMSNorm (moe_add_rmsnorm); null outputs are skipped.
 struct AddNormArgs {
@@ -171,6 +173,7 @@ struct AttnArgs {
     WsHeader *hdr;
     uint8_t *scratch;         // counters, then partial results (attention_part_bytes)
     unsigned long long wait_ns;
+    int withhold;             // moe_debug_withhold_arrivals
 };
 // The pages [num_pages * Hkv][page][D] as a 3-D TMA map of a 16-bit type:
 // boxes of 64 channels x box_rows cache rows of one page and head, 128-byte
