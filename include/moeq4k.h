@@ -84,6 +84,9 @@ typedef enum {
 /* Element types of the entry points that take more than fp32. */
 typedef enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2 } moe_dtype;
 
+/* In place of a stream, where a call says so: check the arguments only. */
+#define MOE_CHECK_ONLY ((void *)-1)
+
 /* Human-readable name of a status code (static string, never NULL). */
 MOE_API const char *moe_status_str(moe_status s);
 
@@ -337,7 +340,9 @@ MOE_API moe_status moe_layer_noalloc(const float *x_dev, const float *Wr_dev, co
 /*
  * The attention half of a decoder block: residual addition with RMSNorm,
  * rotary positions with the append to a paged cache, and attention over that
- * cache.  The projections between them are the caller's.
+ * cache.  The projections between them are the caller's.  With
+ * MOE_CHECK_ONLY in place of a stream the three calls check their arguments and
+ * enqueue nothing (MOE_OK: a call with a stream would be enqueued).
  *
  * moe_add_rmsnorm, per row of H values:
  *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * gamma

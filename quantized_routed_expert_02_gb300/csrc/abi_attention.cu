@@ -70,6 +70,7 @@ moe_status moe_add_rmsnorm(const void *x, moe_dtype x_type, const float *residua
         MOE_TRY(check_ptr(sums, 4));
     }
     if (sum_out == nullptr && y == nullptr && !any_q) return MOE_ERR_NULL;
+    if (stream == MOE_CHECK_ONLY) return MOE_OK;
     int sms = 0;
     MOE_TRY(device_info(&sms, nullptr));
     AddNormArgs a = {};
@@ -100,6 +101,7 @@ moe_status moe_rope_append(const void *qkv, const int32_t *pos, const double *in
     MOE_TRY(check_ptr(q_out, 16));
     MOE_TRY(check_batch_ptrs(p, k_pages, v_pages, ws));
     if (ws_bytes < sizeof(WsHeader)) return MOE_ERR_WORKSPACE;
+    if (stream == MOE_CHECK_ONLY) return MOE_OK;
     int sms = 0;
     MOE_TRY(device_info(&sms, nullptr));
     RopeArgs a = {};
@@ -131,6 +133,7 @@ moe_status moe_attention_paged(const void *q, const void *k_pages, const void *v
     MOE_TRY(check_opt(lse, 4));
     MOE_TRY(check_batch_ptrs(p, k_pages, v_pages, ws));
     if (ws_bytes < moe_attention_workspace_bytes(Hq, Hkv, D)) return MOE_ERR_WORKSPACE;
+    if (stream == MOE_CHECK_ONLY) return MOE_OK;
     int sms = 0;
     MOE_TRY(device_info(&sms, nullptr));
     AttnArgs a = {};

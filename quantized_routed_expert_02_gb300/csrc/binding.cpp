@@ -62,8 +62,11 @@ at::IntArrayRef sizes(const at::Tensor &t, size_t n, const char *name) {
 // The device of a call's first tensor, where all the others have to be too.
 struct Place {
     c10::Device device;
+    bool current;  // the CUDA device that a call is launched on
 
-    explicit Place(const at::Tensor &first) : device(first.device()) {}
+    explicit Place(const at::Tensor &first)
+        : device(first.device()),
+          current(device.is_cuda() && device.index() == c10::cuda::current_device()) {}
     void check(const at::Tensor &t, const char *name) const {
         if (t.device() != device)
             refuse(PyExc_ValueError, std::string(name) + ": on " + t.device().str() + ", not " + device.str());
@@ -126,14 +129,17 @@ float as_float(PyObject *o) {
     return float(v);
 }
 
-// None: the current stream; a torch.cuda.Stream; or a handle.
-void *as_stream(PyObject *o) {
+// None: the current stream; a torch.cuda.Stream; or a handle.  Tensors that the
+// current device does not hold: their call is checked only (run() refuses it then).
+void *as_stream(PyObject *o, const Place &place) {
+    if (!place.current) return MOE_CHECK_ONLY;
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
     PyObject *h = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
     if (h == nullptr) throw Raised();
     void *s = PyLong_AsVoidPtr(h);
     Py_DECREF(h);
     if (s == nullptr && PyErr_Occurred()) throw Raised();
+    if (s == MOE_CHECK_ONLY) refuse(PyExc_ValueError, "stream: not a stream's handle: -1");
     return s;
 }
 
@@ -173,14 +179,18 @@ struct Args {
 };
 
 // Runs `call` without the interpreter's lock (a launch may wait for room in the
-// queue) and raises what it refuses.
+// queue) and raises what it refuses; then, what the library cannot see, tensors that
+// are not where it would be launched.
 template <typename F>
-void run(const char *where, F call) {
+void run(const char *where, const Place &place, F call) {
     moe_status code;
     Py_BEGIN_ALLOW_THREADS;
     code = call();
     Py_END_ALLOW_THREADS;
-    if (code == MOE_OK) return;
+    if (code == MOE_OK && place.current) return;
+    if (code == MOE_OK)
+        refuse(PyExc_ValueError, std::string(where) + ": tensors on " + place.device.str() +
+                                     ", which is not the current CUDA device");
     PyObject *e = PyObject_CallFunction(moe_error, "is", int(code), where);
     if (e != nullptr) {
         PyErr_SetObject(moe_error, e);
@@ -232,8 +242,8 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
             yt = dtype_of(t, "y");
             y = at_x.pointer(t, rows, t.scalar_type(), "y");
         }
-        void *s = as_stream(a[7]);
-        run("moe_add_rmsnorm", [&] {
+        void *s = as_stream(a[7], at_x);
+        run("moe_add_rmsnorm", at_x, [&] {
             return moe_add_rmsnorm(xp, xt, residual, gamma, eps, T, H, sum_out, y, yt, q, d, sums, s);
         });
     });
@@ -287,8 +297,8 @@ PyObject *rope_append(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         if (turned < 0) throw Raised();
         void *q_out = c.pointer(out, {N, Hq, c.D}, c.type, "q_out");
         const at::Tensor &ws = tensor(a[9], "ws");
-        void *w = c.workspace(ws), *s = as_stream(a[15]);
-        run("moe_rope_append", [&] {
+        void *w = c.workspace(ws), *s = as_stream(a[15], c);
+        run("moe_rope_append", c, [&] {
             return moe_rope_append(qkv, at_pos, f, axis, axes, 2 * half, turned, qw, kw, eps, q_out, c.k, c.v,
                                    c.table, c.offs, c.lens, N, c.B, c.max_pages, c.pages, c.page, Hq, c.Hkv, c.D,
                                    c.dtype, w, ws.nbytes(), s);
@@ -311,8 +321,8 @@ PyObject *attention_paged(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
         void *out = c.pointer(a[8], {N, Hq, c.D}, c.type, "out");
         float *lse = c.optional<float>(a[10], {N, Hq}, at::kFloat, "lse");
         const at::Tensor &ws = tensor(a[9], "ws");
-        void *w = c.workspace(ws), *s = as_stream(a[13]);
-        run("moe_attention_paged", [&] {
+        void *w = c.workspace(ws), *s = as_stream(a[13], c);
+        run("moe_attention_paged", c, [&] {
             return moe_attention_paged(q, c.k, c.v, c.table, c.offs, c.lens, N, c.B, most, c.max_pages, c.pages,
                                        c.page, Hq, c.Hkv, c.D, c.dtype, scale, softcap, window, out, lse, w,
                                        ws.nbytes(), s);

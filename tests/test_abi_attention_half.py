@@ -116,3 +116,27 @@ def test_codes_refusals(lib):
 
 def test_status_name(m):
     assert m.status_str(10) == "MOE_ERR_CACHE_RANGE" and m.STATUS_NAMES[10] == "MOE_ERR_CACHE_RANGE"
+
+
+class Recorder:
+    """Stands for the library: keeps the call that it gets."""
+
+    def __getattr__(self, name):
+        def take(*args):
+            self.call = name, args
+            return 0
+        return take
+
+
+@pytest.mark.parametrize("make,bad,code", [
+    (norm, dict(eps=-1.0), SHAPE), (norm, dict(x=ALIGNED + 8), MISALIGNED), (rope, dict(rot=8), SHAPE),
+    (rope, dict(q_out=0), NULL), (attn, dict(max_new=0), SHAPE), (attn, dict(ws_bytes=1 << 10), WORKSPACE)])
+def test_checks_alone(lib, make, bad, code):
+    """MOE_CHECK_ONLY in place of a stream: the checks' answer, with nothing enqueued (nor a GPU needed)."""
+    def check(**args):
+        call = Recorder()
+        make(call, **args)
+        name, a = call.call
+        return getattr(lib, name)(*a[:-1], P(-1))
+    assert check() == 0
+    assert check(**bad) == code

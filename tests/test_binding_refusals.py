@@ -118,3 +118,37 @@ def test_a_tensor_left_on_the_host(call):
         if isinstance(v, (torch.Tensor, tuple)):
             with pytest.raises(ValueError, match="on c"):
                 getattr(m, call)(**dict(args, **{name: v}))
+
+
+def on_aligned_storage(args):
+    """The same arguments on storage aligned as a device's would be."""
+    def align(t):
+        big = torch.zeros(t.nbytes + 256, dtype=torch.uint8)
+        at = -big.data_ptr() % 256
+        return big[at:at + t.nbytes].view(t.dtype).view(t.shape).copy_(t)
+
+    def to(v):
+        return tuple(map(to, v)) if isinstance(v, tuple) else align(v) if isinstance(v, torch.Tensor) else v
+
+    args = {k: to(v) for k, v in args.items()}
+    if "ws" in args:
+        args["ws"] = align(torch.zeros(48 << 20, dtype=torch.uint8))
+    return args
+
+
+@pytest.mark.parametrize("stream", [0, None, 1 << 20])
+@pytest.mark.parametrize("call", CALLS)
+def test_all_tensors_on_the_host(call, stream):
+    """Right in all but their place: refused, whatever the stream, before a kernel could see an address."""
+    args = dict(on_aligned_storage(CALLS[call]()), stream=stream)
+    with pytest.raises(ValueError, match="cpu, which is not the current CUDA device"):
+        getattr(m, call)(**args)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", CALLS)
+def test_a_stream_that_is_none(call):
+    """The handle that stands for checking alone is no stream of a caller's."""
+    args = {k: v.to("cuda") if isinstance(v, torch.Tensor) else v for k, v in CALLS[call]().items() if k != "q8k"}
+    with pytest.raises(ValueError, match="stream"):
+        getattr(m, call)(**dict(args, stream=-1))
