@@ -82,7 +82,9 @@ struct Place {
     P *optional(PyObject *o, at::IntArrayRef shape, at::ScalarType type, const char *name) const {
         return o == Py_None ? nullptr : pointer<P>(o, shape, type, name);
     }
+    // A workspace's size is that of its bytes in a row: an expanded view has more elements than bytes.
     void *workspace(const at::Tensor &t) const {
+        if (!t.is_contiguous()) refuse(PyExc_ValueError, "ws: not contiguous");
         check(t, "ws");
         return t.data_ptr();
     }

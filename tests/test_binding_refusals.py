@@ -145,6 +145,14 @@ def test_all_tensors_on_the_host(call, stream):
         getattr(m, call)(**args)
 
 
+@pytest.mark.parametrize("call", ["moe_rope_append", "moe_attention_paged"])
+@pytest.mark.parametrize("ws", [torch.zeros(1, dtype=torch.uint8).expand(48 << 20),
+                                torch.zeros(2 << 20, dtype=torch.uint8)[::2]], ids=["expanded", "strided"])
+def test_a_workspace_that_is_no_run_of_bytes(call, ws):
+    with pytest.raises(ValueError, match="ws: not contiguous"):
+        getattr(m, call)(**dict(CALLS[call](), ws=ws))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("call", CALLS)
 def test_a_stream_that_is_none(call):
