@@ -464,6 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     }
                     tmem_ld16(ts, v[0]);  // for the second pass
                     mt = fmaxf(mt, exchange(mt));
+                    // a row of no token holds what was in shared memory, or another sequence's query:
+                    // it has no say in the warp's choices below, which show in the live rows' roundings
+                    if (!live) mt = -CUDART_INF_F;
                     // a capped tile that every row sees whole and whose tangents stay off 1
                     const bool plain = kMode == kCapped && !edge && !__any_sync(0xffffffffu, mt * p.cap_in > kTanhOne);
                     if (mt != -CUDART_INF_F) mt = capped ? score<true>(mt * sign, p) : score<false>(mt * sign, p);

@@ -32,3 +32,27 @@ def test_waits_that_run_out(m, new, lens):
     o, e, tol, lse_tol = attention_ref(case, 1 / math.sqrt(128))
     within(out, o, tol, "out")
     within(lse, e, lse_tol, "lse")
+
+
+@pytest.mark.parametrize("G,D", [(3, 128), (7, 64), (12, 128)])
+def test_what_ran_before_leaves_no_trace(m, G, D):
+    """A group that does not fill the tensor cores' 128 rows: the rows left over hold what the call
+    before left in shared memory, and the result is the same bit for bit whatever that was."""
+    Hkv = 2
+    case = Batch([700, 1200], [2000, 1500], Hkv * G, Hkv, D, 16, torch.bfloat16, seed=G)
+    other = Batch([2000, 2000], [2100, 2000], 4 * Hkv, Hkv, D, 16, torch.bfloat16, seed=1)  # fills all 128
+    d, e = case.dev(DEV), other.dev(DEV)
+    ws = m.alloc_attention_workspace(case.Hq, Hkv, D, device=DEV)
+    out, out2 = torch.empty_like(d["q"]), torch.empty_like(e["q"])
+    lse = torch.empty(case.N, case.Hq, device=DEV)
+    got = []
+    for size in (0.0, 30.0, 100.0, 1000.0):
+        big = e["q"] * size
+        torch.cuda.synchronize()
+        m.moe_attention_paged(big, e["k"], e["v"], e["table"], e["offs"], e["lens"], 2000, 0.1, out2, ws)
+        m.moe_attention_paged(d["q"], d["k"], d["v"], d["table"], d["offs"], d["lens"], 1200, D ** -0.5, out, ws,
+                              lse=lse)
+        assert m.moe_read_device_status(ws)[0] == 0
+        got.append((out.clone(), lse.clone()))
+    for o, s in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(s, got[0][1])
