@@ -449,6 +449,7 @@ Params make_params(const AttnArgs &a) {
     p.lse = a.lse;
     p.scale_log2 = a.scale * kLog2e;
     p.cap_in = a.softcap > 0.f ? 2.f * kLog2e * a.scale / a.softcap : 0.f;
+    p.cap_y = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
     p.cap_log2 = a.softcap * kLog2e;
     p.window = a.window;
     p.hdr = a.hdr;

@@ -186,8 +186,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // How a score follows from q.k: by a positive scale, capped after a positive
-// scale, or in any other way (negative and zero scales).
+// scale, or in any other way (negative and zero scales, caps past kCapNear).
 enum Mode { kScaled, kCapped, kAny };
+
+// kCapped takes the tangent from 1 - 2 / (1 + e^2y) alone: its error is some 2^-22
+// of the cap, up to this cap no more than 2^-16, a few fp32 steps of the scores that
+// the cap lets through.  Caps beyond go to kAny, whose scores are score()'s.
+constexpr float kCapNear = 64.f;
 
 template <typename T, int D, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_constant__ TcParams tp) {
@@ -503,7 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
                             unsigned long long e2[2] = {pack2(u[i], u[i + 1]), pack2(u[i + 2], u[i + 3])};
-                            if (capped) {
+                            if (kMode == kAny && capped) {
+                                float z[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) z[k] = score<true>(u[i + k], p) - base;
+                                e2[0] = pack2(z[0], z[1]);
+                                e2[1] = pack2(z[2], z[3]);
+                            } else if (capped) {
                                 // score() less the base: d = 1 + e^2x, and the four reciprocals from that
                                 // of their product (a reciprocal takes twice an exponential's time; d is
                                 // kept below 2^30 for it, where the tangent is 1 in fp32: by the tile's
@@ -640,11 +651,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
 }
 
 template <typename T, int D>
-cudaError_t launch(const TcParams &tp, int grid, cudaStream_t s) {
+cudaError_t launch(const TcParams &tp, bool near_cap, int grid, cudaStream_t s) {
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(Cfg<D>::kSmem), s, tp);
     };
-    if (tp.p.cap_in > 0.f) return go(attention_tc_kernel<T, D, kCapped>);
+    if (tp.p.cap_in > 0.f && near_cap) return go(attention_tc_kernel<T, D, kCapped>);
     if (tp.p.cap_in == 0.f && tp.p.scale_log2 > 0.f) return go(attention_tc_kernel<T, D, kScaled>);
     return go(attention_tc_kernel<T, D, kAny>);
 }
@@ -691,11 +702,12 @@ cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStrea
         !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
         return cudaErrorInvalidValue;
     const int grid = std::min(num_sms, kMaxGrid);
+    const bool near_cap = a.softcap <= kCapNear;
     cudaError_t e;
     if (a.type == MOE_F16)
-        e = a.b.D == 64 ? launch<__half, 64>(tp, grid, s) : launch<__half, 128>(tp, grid, s);
+        e = a.b.D == 64 ? launch<__half, 64>(tp, near_cap, grid, s) : launch<__half, 128>(tp, near_cap, grid, s);
     else
-        e = a.b.D == 64 ? launch<__nv_bfloat16, 64>(tp, grid, s) : launch<__nv_bfloat16, 128>(tp, grid, s);
+        e = a.b.D == 64 ? launch<__nv_bfloat16, 64>(tp, near_cap, grid, s) : launch<__nv_bfloat16, 128>(tp, near_cap, grid, s);
     if (e != cudaSuccess) return e;
     // nothing is parted where even the most and longest items that the arguments allow are taken
     // whole (a prompt of 100 in a table of its length: 9.5 us, with the joining launch 12.0)

@@ -1,9 +1,10 @@
-"""The attention half at the edges of what its entry points promise: waits that run out."""
+"""The attention half at the edges of what its entry points promise: waits that run out, contents of
+rows that are nobody's, caps far from the scores."""
 import math
 
 import pytest
 
-from tests.block_cases import Batch, attention_ref
+from tests.block_cases import U32, Batch, attention_ref, half_step
 from tests.test_gpu_attention_half import run_attn, within
 from tests.test_gpu_parity import DEV, m  # noqa: F401
 
@@ -56,3 +57,59 @@ def test_what_ran_before_leaves_no_trace(m, G, D):
         got.append((out.clone(), lse.clone()))
     for o, s in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(s, got[0][1])
+
+
+def capped_ref(case, scale, cap):
+    """out, lse and their bounds of a batch of one sequence, in fp64.  A score's error: that of its fp32
+    products and sum, and 2^-20 of the score itself for the tangent (an exponential and a quotient
+    of 2^-22 each, doubled by 1 - 2 / (1 + e^2y) where y is least, or ten roundings of a polynomial).
+    Nothing grows with the cap."""
+    n, L, G = case.new[0], case.lens_list[0], case.Hq // case.Hkv
+    k, v = case.cached(0, case.k), case.cached(0, case.v)
+    q = case.q[:n].double().view(n, case.Hkv, G, case.D).permute(1, 2, 0, 3)
+    z = torch.einsum("hgnd,hkd->hgnk", q, k) * scale
+    dz = torch.einsum("hgnd,hkd->hgnk", q.abs(), k.abs()) * abs(scale) * (case.D + 8) * U32
+    z = cap * torch.tanh(z / cap)
+    seen = torch.arange(L)[None] <= torch.arange(L - n, L)[:, None]
+    dz = torch.where(seen, dz + z.abs() * 2.0 ** -20, 0.0)
+    z = z.masked_fill(~seen, -math.inf)
+    e = torch.logsumexp(z, -1)
+    p = torch.exp(z - e[..., None])
+    o, absv = (torch.einsum("hgnk,hkd->hgnd", p, x) for x in (v, v.abs()))
+    u = half_step(case.dtype)
+    rel = 2 * dz.amax(-1) + 2.0 ** -20 + (L + 64) * U32
+    tol = (rel[..., None] + u) * absv
+    tol = tol + u * (o.abs() + tol)
+    lse_tol = dz.amax(-1) + 2.0 ** -20 + (L + 64) * U32 + 4 * U32 * e.abs()
+
+    def put(x):
+        return x.permute(2, 0, 1, *range(3, x.dim())).reshape(n, case.Hq, *x.shape[3:])
+    return put(o), put(e), put(tol), put(lse_tol)
+
+
+@pytest.mark.parametrize("new,L", [(1, 700), (3, 90), (90, 400)])
+@pytest.mark.parametrize("cap", [1e3, 1e4, 1e5, 1e6, 1e9, 1e30])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_far_caps(m, new, L, cap, sign):
+    """A cap far beyond the scores leaves them as they are."""
+    case = Batch([new], [L], 8, 2, 128, 16, torch.bfloat16, seed=L)
+    scale = sign * 128 ** -0.5
+    out, lse, code, _ = run_attn(m, case, softcap=cap, scale=scale)
+    assert code == 0
+    o, e, tol, lse_tol = capped_ref(case, scale, cap)
+    within(lse, e, lse_tol, "lse")
+    within(out, o, tol, "out")
+
+
+@pytest.mark.parametrize("new,L", [(1, 700), (90, 400)])
+@pytest.mark.parametrize("cap", [65.0, 300.0, 2000.0])
+def test_scores_around_the_cap(m, new, L, cap):
+    """Scores from far below the cap to past it."""
+    for reach in (0.1, 0.5, 0.6, 3.0):
+        case = Batch([new], [L], 8, 2, 64, 16, torch.bfloat16, seed=L)
+        scale = 64 ** -0.5 * cap * reach / 3  # three standard deviations at reach * cap
+        out, lse, code, _ = run_attn(m, case, softcap=cap, scale=scale)
+        assert code == 0
+        o, e, tol, lse_tol = capped_ref(case, scale, cap)
+        within(lse, e, lse_tol, "lse")
+        within(out, o, tol, "out")
