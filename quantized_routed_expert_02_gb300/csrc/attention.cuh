@@ -157,7 +157,10 @@ struct Items {
     int n, top;
 };
 
-// The run of this CTA from the sequences' costs and items, by one warp.
+// The run of this CTA from the sequences' costs and items, by one warp.  The
+// lengths are read again for the item that is found: should the caller change them
+// under the call (a missing stream order) they need not fit the costs any more, so
+// what is derived from both, here and in join_desc, is bounded by the buffers.
 template <int KT>
 __device__ inline void run_find(const Params &p, int least, int split, const long *scratch, const Items *items,
                                 Run &r) {
@@ -233,7 +236,7 @@ __device__ inline void run_find(const Params &p, int least, int split, const lon
     const long in = r.u - first;
     it.kh = min(int(__fdividef(float(in), float(each))), Hkv - 1);
     while (it.kh * each > in) --it.kh;
-    while ((it.kh + 1) * each <= in) ++it.kh;
+    while (it.kh + 1 < Hkv && (it.kh + 1) * each <= in) ++it.kh;
     r.item_u = first + it.kh * each;
 }
 
@@ -358,7 +361,8 @@ __device__ __forceinline__ float4 ld_l2_v4(const float *p) {
 __device__ __forceinline__ JoinDesc join_desc(const Params &p, const Run &r) {
     const long first = r.item_u + p.extra;
     JoinDesc d;
-    d.parts = int(div_pos(first + r.item.tiles - 1, r.per) - div_pos(first, r.per)) + 1;
+    const long cta = div_pos(first, r.per);
+    d.parts = int(min(div_pos(first + r.item.tiles - 1, r.per), long(gridDim.x) - 1) - cta) + 1;
     d.row0 = r.item.row0;
     d.nt = r.item.nt;
     d.kh = r.item.kh;

@@ -189,9 +189,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // scale, or in any other way (negative and zero scales, caps past kCapNear).
 enum Mode { kScaled, kCapped, kAny };
 
-// kCapped takes the tangent from 1 - 2 / (1 + e^2y) alone: its error is some 2^-22
-// of the cap, up to this cap no more than 2^-16, a few fp32 steps of the scores that
-// the cap lets through.  Caps beyond go to kAny, whose scores are score()'s.
+// kCapped takes the tangent from 1 - 2 / (1 + e^2y) alone: its error is at most
+// 2^-21 of the cap, up to this cap 2^-15, a few fp32 steps of the scores that the cap
+// lets through.  Caps beyond go to kAny, whose scores are score()'s.
 constexpr float kCapNear = 64.f;
 
 template <typename T, int D, int kMode>
