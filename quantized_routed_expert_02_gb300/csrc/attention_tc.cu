@@ -191,7 +191,8 @@ enum Mode { kScaled, kCapped, kAny };
 
 // kCapped takes the tangent from 1 - 2 / (1 + e^2y) alone: its error is at most
 // 2^-21 of the cap, up to this cap 2^-15, a few fp32 steps of the scores that the cap
-// lets through.  Caps beyond go to kAny, whose scores are score()'s.
+// lets through.  Caps beyond go to kAny, whose scores are score()'s (2048 rows over 16384
+// keys: 446 us, by kAny 545).
 constexpr float kCapNear = 64.f;
 
 template <typename T, int D, int kMode>
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     // first pass: the row's maximum (the score grows with sign * q.k, so the maximum
                     // of those gives the maximum of the scores)
                     float v[2][16];
-                    float mt;
+                    float mt, most = 0.f;  // the largest, and the largest magnitude of this thread's keys
                     {
                         float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
                         float u[2][32];
@@ -466,15 +467,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                 m4[(i >> 1) & 3] = kMode == kAny ? max3(m4[(i >> 1) & 3], u[c][i] * sign, u[c][i + 1] * sign)
                                                                  : max3(m4[(i >> 1) & 3], u[c][i], u[c][i + 1]);
                         mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+                        if (kMode == kAny && capped) {
+                            float a4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2)
+                                    a4[(i >> 1) & 3] = max3(a4[(i >> 1) & 3], fabsf(u[c][i]), fabsf(u[c][i + 1]));
+                            most = max3(fmaxf(a4[0], a4[1]), a4[2], a4[3]);
+                        }
                     }
                     tmem_ld16(ts, v[0]);  // for the second pass
                     mt = fmaxf(mt, exchange(mt));
                     // a row of no token holds what was in shared memory, or another sequence's query:
                     // it has no say in the warp's choices below, which show in the live rows' roundings
-                    if (!live) mt = -CUDART_INF_F;
-                    // a capped tile that every row sees whole and whose tangents stay off 1
-                    const bool plain = kMode == kCapped && !edge && !__any_sync(0xffffffffu, mt * p.cap_in > kTanhOne);
-                    if (mt != -CUDART_INF_F) mt = capped ? score<true>(mt * sign, p) : score<false>(mt * sign, p);
+                    if (!live) mt = -CUDART_INF_F, most = 0.f;
+                    // kCapped: a tile that every row sees whole and whose tangents stay off 1; kAny: one
+                    // whose scores all are far below the cap (a hidden score's magnitude is infinite)
+                    const bool plain =
+                        kMode == kCapped ? !edge && !__any_sync(0xffffffffu, mt * p.cap_in > kTanhOne)
+                        : kMode == kAny && capped ? __all_sync(0xffffffffu, most * fabsf(p.cap_y) < kTanhNear)
+                                                  : false;
+                    if (mt != -CUDART_INF_F)
+                        mt = kMode == kCapped ? capped_far(mt, p)
+                             : capped         ? score<true>(mt * sign, p)
+                                              : score<false>(mt * sign, p);
                     if (j == 0) {
                         top = mt;
                     } else if (__any_sync(0xffffffffu, mt - top > kGrowth)) {
@@ -497,25 +514,36 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     // second pass: the weights
                     const float base = top == -CUDART_INF_F ? 0.f : top;
                     unsigned long long s2[2] = {0ull, 0ull};  // pairs of sums
-                    const float scale = capped ? p.cap_in : p.scale_log2;
-                    const float b = capped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
+                    const float scale = kMode == kCapped ? p.cap_in : p.scale_log2;
+                    const float b = kMode == kCapped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
-                    const unsigned long long one2 = pack2(1.f, 1.f);
-                    const unsigned long long hide2 = pack2(1.2e-38f * sign, 1.2e-38f * sign);
+                    const unsigned long long one2 = pack2(1.f, 1.f), near2 = pack2(p.cap_y, p.cap_y);
+                    const unsigned long long hide2 = pack2(1.2e-38f, 1.2e-38f);
                     auto take = [&](auto is_plain, int c, const float (&u)[16]) {
                         constexpr bool kPlain = decltype(is_plain)::value;
                         uint32_t w[8];
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
                             unsigned long long e2[2] = {pack2(u[i], u[i + 1]), pack2(u[i + 2], u[i + 3])};
-                            if (kMode == kAny && capped) {
+                            if (kMode == kAny && kPlain) {  // score()'s polynomial, less the base
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const unsigned long long y = mul2(e2[k], near2), t = mul2(y, y);
+                                    unsigned long long r = fma2(t, pack2(kTanh5, kTanh5), pack2(kTanh4, kTanh4));
+                                    r = fma2(t, r, pack2(kTanh3, kTanh3));
+                                    r = fma2(t, r, pack2(kTanh2, kTanh2));
+                                    r = fma2(t, r, pack2(kTanh1, kTanh1));
+                                    r = fma2(t, r, one2);
+                                    e2[k] = fma2(mul2(e2[k], scale2), r, base2);
+                                }
+                            } else if (kMode == kAny && capped) {
                                 float z[4];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) z[k] = score<true>(u[i + k], p) - base;
                                 e2[0] = pack2(z[0], z[1]);
                                 e2[1] = pack2(z[2], z[3]);
-                            } else if (capped) {
-                                // score() less the base: d = 1 + e^2x, and the four reciprocals from that
+                            } else if (kMode == kCapped) {
+                                // the score less the base: d = 1 + e^2x, and the four reciprocals from that
                                 // of their product (a reciprocal takes twice an exponential's time; d is
                                 // kept below 2^30 for it, where the tangent is 1 in fp32: by the tile's
                                 // maxima where it is plain)
@@ -545,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                 unpack2(e2[k], x, y);
                                 x = exp2_approx(x);
                                 y = exp2_approx(y);
-                                if (kMode == kAny) {  // times 0 an infinity does not give weight 0 by itself
+                                if (kMode == kAny && !kPlain) {  // times 0 an infinity does not give weight 0 by itself
                                     if (u[i + 2 * k] == hidden) x = 0.f;
                                     if (u[i + 2 * k + 1] == hidden) y = 0.f;
                                 }

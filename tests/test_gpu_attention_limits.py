@@ -35,8 +35,9 @@ def test_waits_that_run_out(m, new, lens):
     within(lse, e, lse_tol, "lse")
 
 
-@pytest.mark.parametrize("G,D", [(3, 128), (7, 64), (12, 128)])
-def test_what_ran_before_leaves_no_trace(m, G, D):
+@pytest.mark.parametrize("G,D,cap,sign", [(3, 128, 0.0, 1), (7, 64, 0.0, 1), (12, 128, 0.0, 1), (3, 128, 2.0, 1),
+                                          (7, 128, 500.0, 1), (3, 64, 5.0, -1)])
+def test_what_ran_before_leaves_no_trace(m, G, D, cap, sign):
     """A group that does not fill the tensor cores' 128 rows: the rows left over hold what the call
     before left in shared memory, and the result is the same bit for bit whatever that was."""
     Hkv = 2
@@ -51,8 +52,8 @@ def test_what_ran_before_leaves_no_trace(m, G, D):
         big = e["q"] * size
         torch.cuda.synchronize()
         m.moe_attention_paged(big, e["k"], e["v"], e["table"], e["offs"], e["lens"], 2000, 0.1, out2, ws)
-        m.moe_attention_paged(d["q"], d["k"], d["v"], d["table"], d["offs"], d["lens"], 1200, D ** -0.5, out, ws,
-                              lse=lse)
+        m.moe_attention_paged(d["q"], d["k"], d["v"], d["table"], d["offs"], d["lens"], 1200, sign * D ** -0.5, out,
+                              ws, lse=lse, softcap=cap)
         assert m.moe_read_device_status(ws)[0] == 0
         got.append((out.clone(), lse.clone()))
     for o, s in got[1:]:
