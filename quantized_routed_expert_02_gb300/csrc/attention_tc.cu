@@ -54,6 +54,7 @@ constexpr int kExtra = 2;
 constexpr int kSplit = 5;
 constexpr float kGrowth = 8.f;             // log2 growth of the maximum that forces a rescale
 constexpr float kTanhOne = 30.f;           // 2^-30 from 1 is 1 in fp32
+constexpr float kTanhMinusOne = -64.f;     // 1 + 2^-64 is 1, and the tangent -1
 
 struct TcParams {
     CUtensorMap mq, mk, mv;
@@ -176,6 +177,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The larger and the smaller of two, a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 
@@ -401,7 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         const int tok_h = row / G, head = row % G;
         const bool capped = kMode == kCapped || (kMode == kAny && p.cap_in != 0.f);
         const float sign = kMode == kAny && (capped ? p.cap_in : p.scale_log2) < 0.f ? -1.f : 1.f;
-        const float hidden = -CUDART_INF_F * sign;  // the q.k of a key that a row does not see
+        // The q.k of a key that a row does not see, and the least (by sign) of one that it does: what
+        // is less, an infinity too, has the same capped score, and is not taken for hidden
+        const float hidden = -CUDART_INF_F * sign;
+        const float lowest = kMode == kCapped ? kTanhMinusOne / p.cap_in : -CUDART_MAX_NORMAL_F;
         uint32_t ns = 0, no = 0, nx = 0;  // S tiles and O results taken, exchanges
         bool ok = true;  // after a time-out: no more waits, but every barrier still met
         // a value of the row's other thread, through the space of the results on their way out
@@ -443,8 +459,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                             tmem_ld32(ts + 32 * c, u);
                             wait_ld32(u);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
+                            for (int i = 0; i < 32; ++i) {
+                                if (kMode == kCapped) u[i] = max_nan(u[i], lowest);
+                                if (kMode == kAny && capped && u[i] == hidden) u[i] = lowest * sign;
                                 if (32 * c + i > hi || 32 * c + i <= lo) u[i] = hidden;
+                            }
                             tmem_st32(ts + 32 * c, u);
                         }
                         wait_st();
@@ -479,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     }
                     tmem_ld16(ts, v[0]);  // for the second pass
                     mt = fmaxf(mt, exchange(mt));
+                    if (capped && !edge) mt = fmaxf(mt, lowest);
                     // a row of no token holds what was in shared memory, or another sequence's query:
                     // it has no say in the warp's choices below, which show in the live rows' roundings
                     if (!live) mt = -CUDART_INF_F, most = 0.f;
@@ -518,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     const float b = kMode == kCapped ? p.cap_log2 - base : -base, k2 = -2.f * p.cap_log2;
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
                     const unsigned long long one2 = pack2(1.f, 1.f), near2 = pack2(p.cap_y, p.cap_y);
-                    const unsigned long long hide2 = pack2(1.2e-38f, 1.2e-38f);
+                    const float from = edge ? -CUDART_INF_F : kTanhMinusOne;
+                    const unsigned long long hide2 = pack2(0x1p-100f, 0x1p-100f);
                     auto take = [&](auto is_plain, int c, const float (&u)[16]) {
                         constexpr bool kPlain = decltype(is_plain)::value;
                         uint32_t w[8];
@@ -547,22 +568,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                 // of their product (a reciprocal takes twice an exponential's time; d is
                                 // kept below 2^30 for it, where the tangent is 1 in fp32: by the tile's
                                 // maxima where it is plain)
-                                unsigned long long d2[2];
+                                unsigned long long d2[2], x2[2];
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     float x, y;
                                     unpack2(mul2(e2[k], scale2), x, y);
-                                    if (!kPlain) x = fminf(x, kTanhOne), y = fminf(y, kTanhOne);
+                                    if (!kPlain) {
+                                        x = min_nan(max_nan(x, from), kTanhOne);
+                                        y = min_nan(max_nan(y, from), kTanhOne);
+                                        x2[k] = pack2(x, y);
+                                    }
                                     d2[k] = add2(pack2(exp2_approx(x), exp2_approx(y)), one2);
                                 }
                                 float x, y;
                                 unpack2(mul2(d2[0], d2[1]), x, y);
                                 const float r = rcp_approx(x * y) * k2;
                                 const unsigned long long r2 = mul2(pack2(r, r), pack2(y, x));
-                                // a hidden score (an infinity) is brought back by a product that is
-                                // nothing beside any other score
-                                e2[0] = fma2(r2, d2[1], kPlain ? base2 : fma2(e2[0], hide2, base2));
-                                e2[1] = fma2(r2, d2[0], kPlain ? base2 : fma2(e2[1], hide2, base2));
+                                // a hidden score (an infinity, the only one left) is brought back by a
+                                // product that is nothing beside any other score
+                                e2[0] = fma2(r2, d2[1], kPlain ? base2 : fma2(x2[0], hide2, base2));
+                                e2[1] = fma2(r2, d2[0], kPlain ? base2 : fma2(x2[1], hide2, base2));
                             } else {
                                 e2[0] = fma2(e2[0], scale2, base2);
                                 e2[1] = fma2(e2[1], scale2, base2);
@@ -573,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                 unpack2(e2[k], x, y);
                                 x = exp2_approx(x);
                                 y = exp2_approx(y);
-                                if (kMode == kAny && !kPlain) {  // times 0 an infinity does not give weight 0 by itself
+                                if (kMode == kAny && !kPlain && edge) {  // times 0 an infinity does not give weight 0 by itself
                                     if (u[i + 2 * k] == hidden) x = 0.f;
                                     if (u[i + 2 * k + 1] == hidden) y = 0.f;
                                 }
@@ -730,7 +755,7 @@ cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStrea
         !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
         return cudaErrorInvalidValue;
     const int grid = std::min(num_sms, kMaxGrid);
-    const bool near_cap = a.softcap <= kCapNear;
+    const bool near_cap = a.softcap <= kCapNear && p.cap_in > 1e-30f;  // kCapped: kTanhMinusOne / cap_in is finite
     cudaError_t e;
     if (a.type == MOE_F16)
         e = a.b.D == 64 ? launch<__half, 64>(tp, near_cap, grid, s) : launch<__half, 128>(tp, near_cap, grid, s);

@@ -1,5 +1,5 @@
 """The attention half at the edges of what its entry points promise: waits that run out, contents of
-rows that are nobody's, caps far from the scores."""
+rows that are nobody's, caps far from the scores, products past fp32."""
 import math
 
 import pytest
@@ -60,18 +60,21 @@ def test_what_ran_before_leaves_no_trace(m, G, D, cap, sign):
         assert torch.equal(o, got[0][0]) and torch.equal(s, got[0][1])
 
 
-def capped_ref(case, scale, cap):
+def capped_ref(case, scale, cap, window=0, exact=False):
     """out, lse and their bounds of a batch of one sequence, in fp64.  A score's error: that of its fp32
     products and sum, and 2^-20 of the score itself for the tangent (an exponential and a quotient
     of 2^-22 each, doubled by 1 - 2 / (1 + e^2y) where y is least, or ten roundings of a polynomial).
-    Nothing grows with the cap."""
+    Nothing grows with the cap.  ``exact``: the products are 0 or so far past the cap that the tangent
+    of anything near them is 1."""
     n, L, G = case.new[0], case.lens_list[0], case.Hq // case.Hkv
     k, v = case.cached(0, case.k), case.cached(0, case.v)
     q = case.q[:n].double().view(n, case.Hkv, G, case.D).permute(1, 2, 0, 3)
     z = torch.einsum("hgnd,hkd->hgnk", q, k) * scale
     dz = torch.einsum("hgnd,hkd->hgnk", q.abs(), k.abs()) * abs(scale) * (case.D + 8) * U32
-    z = cap * torch.tanh(z / cap)
+    z, dz = cap * torch.tanh(z / cap), dz * (not exact)
     seen = torch.arange(L)[None] <= torch.arange(L - n, L)[:, None]
+    if window > 0:
+        seen &= torch.arange(L)[None] > torch.arange(L - n, L)[:, None] - window
     dz = torch.where(seen, dz + z.abs() * 2.0 ** -20, 0.0)
     z = z.masked_fill(~seen, -math.inf)
     e = torch.logsumexp(z, -1)
@@ -112,5 +115,23 @@ def test_scores_around_the_cap(m, new, L, cap):
         out, lse, code, _ = run_attn(m, case, softcap=cap, scale=scale)
         assert code == 0
         o, e, tol, lse_tol = capped_ref(case, scale, cap)
+        within(lse, e, lse_tol, "lse")
+        within(out, o, tol, "out")
+
+
+@pytest.mark.parametrize("new,L,window", [(1, 500, 0), (1, 700, 130), (90, 400, 0), (300, 900, 200)])
+@pytest.mark.parametrize("cap,scale", [(30.0, 0.1), (30.0, -0.1), (500.0, 0.1), (5.0, 2.0)])
+@pytest.mark.parametrize("size", [1e19, 1e18])
+def test_products_past_fp32(m, new, L, window, cap, scale, size):
+    """Finite rows whose products leave fp32 (1e38 * 128) or come near its end: the cap brings them back
+    to itself, in tiles that rows see whole and in others; keys of one sign for rows that see no other."""
+    case = Batch([new], [L], 8, 2, 128, 16, torch.bfloat16, seed=L)
+    case.q.fill_(size)
+    for kinds in ((-1.0, 0.0, 1.0), (-1.0,), (1.0,)):
+        for j in range(L):
+            case.k[int(case.table[0, j // 16]), :, j % 16] = size * kinds[j * 7 % 11 % len(kinds)]
+        out, lse, code, _ = run_attn(m, case, softcap=cap, scale=scale, window=window)
+        assert code == 0
+        o, e, tol, lse_tol = capped_ref(case, scale, cap, window, exact=True)
         within(lse, e, lse_tol, "lse")
         within(out, o, tol, "out")
