@@ -378,7 +378,7 @@ MOE_API moe_status moe_add_rmsnorm(const void *x_dev, moe_dtype x_dtype, const f
  *  [0, num_pages), a length outside [0, max_pages * page], offsets that
  *  decrease or leave [0, N]) never leads out of the buffers: the sticky status
  *  records MOE_ERR_CACHE_RANGE (detail: the value), and the rows of that
- *  sequence are not valid output.
+ *  sequence are not valid output (nor rows that two sequences claim).
  *  Limits: 1 <= N <= 2^22, 1 <= B <= 4096, Hkv >= 1, Hq a multiple of Hkv,
  *  Hq <= 256, Hq / Hkv <= 128, num_pages * Hkv and max_pages * page <= 2^30.
  *

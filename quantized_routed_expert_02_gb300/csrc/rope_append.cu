@@ -65,6 +65,16 @@ __device__ __forceinline__ int find_seq_warp(const PagedBatch &p, int row, int l
     return lo;
 }
 
+// Whether every offset is in range and none falls; the whole warp calls it.
+__device__ inline bool offsets_rise(const PagedBatch &p, int lane) {
+    bool ok = true;
+    for (int b = lane; b < p.B; b += 32) {
+        const int lo = p.offs[b], hi = p.offs[b + 1];
+        ok = ok && lo >= 0 && hi >= lo && hi <= p.N;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // The work is a run of steps, 512 / D heads each (what a warp turns at a time),
 // row after row; a warp takes `run` of them, whatever the number of rows.
 // Lane: chunk c = lane % (D / 16) of a head at a time: the channels
@@ -131,9 +141,19 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
         const int turn = (row - row_first) & 31;
         if (turn == 0) {
             const int r = min(row + lane, row_last);
-            const int b = row == row_last ? find_seq_warp(a.b, row, lane) : find_seq(a.b, r);
-            const SeqView sv = seq_view(a.b, b, a.hdr, false);
-            live32 = sv.ok && r >= sv.first && r < sv.first + sv.n;
+            int b = row == row_last ? find_seq_warp(a.b, row, lane) : find_seq(a.b, r);
+            SeqView sv = seq_view(a.b, b, a.hdr, false);
+            auto has_row = [&]() { return sv.ok && r >= sv.first && r < sv.first + sv.n; };
+            live32 = has_row();
+            // A row of no sequence, or one that the search missed over offsets that do not rise: then
+            // every sequence is looked at, so that a bad offset costs no other sequence its rows.
+            if (!__all_sync(0xffffffffu, live32) && !offsets_rise(a.b, lane)) {
+                for (int i = 0; !live32 && i < a.b.B; ++i) {
+                    sv = seq_view(a.b, b = i, a.hdr, false);
+                    live32 = has_row();
+                }
+                __syncwarp();
+            }
             cache32 = -1;
             const int at = sv.len - sv.n + (r - sv.first);  // cache index
             if (live32 && at >= 0) {

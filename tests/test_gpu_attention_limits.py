@@ -1,11 +1,12 @@
 """The attention half at the edges of what its entry points promise: waits that run out, contents of
-rows that are nobody's, caps far from the scores, products past fp32."""
+rows that are nobody's, caps far from the scores, products past fp32, descriptions of the batch
+that are wrong in part."""
 import math
 
 import pytest
 
 from tests.block_cases import U32, Batch, attention_ref, half_step
-from tests.test_gpu_attention_half import run_attn, within
+from tests.test_gpu_attention_half import run_attn, run_rope, within
 from tests.test_gpu_parity import DEV, m  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -135,3 +136,56 @@ def test_products_past_fp32(m, new, L, window, cap, scale, size):
         o, e, tol, lse_tol = capped_ref(case, scale, cap, window, exact=True)
         within(lse, e, lse_tol, "lse")
         within(out, o, tol, "out")
+
+
+def good_rows(case):
+    """(sequence, row) of the new rows of sequences whose offsets and length are in range."""
+    offs, lens = case.offs.tolist(), case.lens.tolist()
+    most = case.table.shape[1] * case.page
+    for b, (lo, hi, L) in enumerate(zip(offs, offs[1:], lens)):
+        if 0 <= lo <= hi <= case.N and 0 <= L <= most:
+            yield from ((b, r) for r in range(lo, hi))
+
+
+def check_rope_in_part(m, case, code):
+    """A batch whose description is wrong in part: recorded, the good sequences' rows right, and no
+    other cache row touched."""
+    r = run_rope(m, case, torch.arange(case.N, dtype=torch.int32)[None], 64)
+    assert m.status_str(r["code"]) == code, r["code"]
+    offs, lens = case.offs.tolist(), case.lens.tolist()
+    kept = torch.ones(case.k.shape[:3], dtype=torch.bool)
+    n = 0
+    for b, row in good_rows(case):
+        within(r["q_out"][row], r["q"][row], r["qe"][row], f"q of row {row}")
+        j = lens[b] - (offs[b + 1] - row)
+        pg = int(case.table[b, j // case.page]) if j >= 0 else -1
+        if not 0 <= pg < case.P:
+            continue
+        at = (pg, slice(None), j % case.page)
+        within(r["k"][at], r["k_ref"][row], r["ke"][row], f"k of row {row}")
+        assert torch.equal(r["v"][at].double(), r["v_ref"][row])
+        kept[at] = False
+        n += 1
+    for new, old in ((r["k"], case.k), (r["v"], case.v)):
+        a, o = new[kept], old[kept]
+        assert torch.equal(a.isnan(), o.isnan()) and torch.equal(a.nan_to_num(), o.nan_to_num())
+    return n
+
+
+@pytest.mark.parametrize("offs", [
+    [0, 100, 3, 5], [0, -1, 3, 6], [4, 2, 4, 6], [1 << 30, 0, 3, 6], [2, 5, 0, 2], [2, 5, 0, 0, 1, 2],
+    [0, 2, -5, 1 << 30, 2, 4, 6], [5, 6, 0, 1, 1, 3, 3, 5], [-(2 ** 31), 2 ** 31 - 1, 0, 6]], ids=str)
+def test_rope_with_offsets_that_do_not_rise(m, offs):
+    """The sequences between good offsets keep their rows, wherever the bad ones stand."""
+    B = len(offs) - 1
+    case = Batch([6] + [0] * (B - 1), [20 + b for b in range(B)], 4, 2, 64, 16, torch.float16)
+    case.offs.copy_(torch.tensor(offs))
+    assert check_rope_in_part(m, case, "MOE_ERR_CACHE_RANGE") > 0
+
+
+def test_rope_with_one_bad_offset_among_many(m):
+    """Rows of many warps, 200 sequences, one offset out of place."""
+    for at, bad in ((0, 500), (1, 1 << 20), (57, -3), (100, 700), (199, 650), (200, 9)):
+        case = Batch([3] * 200, [4 + b % 40 for b in range(200)], 4, 2, 64, 16, torch.float16)
+        case.offs[at] = bad
+        assert check_rope_in_part(m, case, "MOE_ERR_CACHE_RANGE") >= 3 * 100
