@@ -5,7 +5,7 @@ import math
 
 import pytest
 
-from tests.block_cases import U32, Batch, attention_ref, half_step
+from tests.block_cases import U32, Batch, attention_ref, half_step, norm_ref
 from tests.test_gpu_attention_half import run_attn, run_rope, within
 from tests.test_gpu_parity import DEV, m  # noqa: F401
 
@@ -189,3 +189,61 @@ def test_rope_with_one_bad_offset_among_many(m):
         case = Batch([3] * 200, [4 + b % 40 for b in range(200)], 4, 2, 64, 16, torch.float16)
         case.offs[at] = bad
         assert check_rope_in_part(m, case, "MOE_ERR_CACHE_RANGE") >= 3 * 100
+
+
+@pytest.mark.parametrize("what,bad", [("page", -1), ("page", 1 << 30), ("page", -(2 ** 31)), ("length", -1),
+                                      ("length", 49), ("length", 2 ** 31 - 1)])
+def test_rope_writes_nothing_through_a_bad_page_or_length(m, what, bad):
+    case = Batch([2, 3, 4], [20, 33, 40], 4, 2, 64, 16, torch.float16)
+    if what == "page":
+        case.table[1, 2] = bad  # the page of the last of the second sequence's three new tokens
+    else:
+        case.lens[1] = bad
+    assert check_rope_in_part(m, case, "MOE_ERR_CACHE_RANGE") == (8 if what == "page" else 6)
+
+
+@pytest.mark.parametrize("new,lens", [([1, 1, 1], [40, 33, 48]), ([40, 30, 20], [60, 33, 48])])
+def test_a_graph_over_a_table_that_changes(m, new, lens):
+    """Captured once; replayed with other pages and lengths, over which the rows are others."""
+    cases = [Batch(new, [L - d for L in lens], 8, 2, 128, 16, torch.bfloat16, seed=20 + d) for d in (0, 3, 9)]
+    pages, width = max(c.P for c in cases), max(c.table.shape[1] for c in cases)
+    d = cases[0].dev(DEV)
+    k, v = (torch.full((pages, 2, 16, 128), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    table = torch.full((3, width), 1 << 30, dtype=torch.int32, device=DEV)
+    out = torch.empty_like(d["q"])
+    lse = torch.empty(cases[0].N, 8, device=DEV)
+    ws = m.alloc_attention_workspace(8, 2, 128, device=DEV)
+
+    def show(case):
+        k[:case.P].copy_(case.k), v[:case.P].copy_(case.v), d["q"].copy_(case.q), d["lens"].copy_(case.lens)
+        table[:, :case.table.shape[1]].copy_(case.table)
+
+    show(cases[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.moe_attention_paged(d["q"], k, v, table, d["offs"], d["lens"], max(new), 128 ** -0.5, out, ws, lse=lse)
+    for case in cases + cases[:1]:
+        show(case)
+        g.replay()
+        assert m.moe_read_device_status(ws)[0] == 0
+        o, e, tol, lse_tol = attention_ref(case, 128 ** -0.5)
+        within(out, o, tol, "out")
+        within(lse, e, lse_tol, "lse")
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norm_of_a_row_of_zeros(m, eps):
+    """0 / sqrt(eps): zeros, and with eps 0 NaN as the formula has it (the sum stays 0); other rows as ever."""
+    x = torch.zeros(3, 512, device=DEV)
+    x[1] = torch.randn(512, device=DEV)
+    r = torch.zeros(3, 512, device=DEV)
+    s, y = (torch.full((3, 512), 7.0, device=DEV) for _ in range(2))
+    m.moe_add_rmsnorm(x, r, torch.ones(512, device=DEV), eps, sum_out=s, y=y)
+    assert torch.equal(s, x)
+    if eps == 0.0:
+        assert bool(y[::2].isnan().all())
+    else:
+        assert bool((y[::2] == 0).all())
+    want = norm_ref(x[1:2].cpu(), None, torch.ones(512), eps)[1]
+    within(y[1:2], want, want.abs() * (512 / 2 + 8) * U32, "the row between")
