@@ -72,7 +72,8 @@ typedef enum {
     MOE_ERR_INVALID_SHAPE = 1,  /* a dimension is out of range or inconsistent */
     MOE_ERR_NULL = 2,           /* a required pointer is NULL */
     MOE_ERR_MISALIGNED = 3,     /* a pointer breaks the alignment rule */
-    MOE_ERR_WORKSPACE = 4,      /* workspace smaller than moe_workspace_bytes() */
+    MOE_ERR_WORKSPACE = 4,      /* workspace smaller than moe_workspace_bytes(), or (device) one that calls
+                                   of the other half of the block had used */
     MOE_ERR_EXPERT_RANGE = 5,   /* device saw an expert index outside [0,E) */
     MOE_ERR_TIMEOUT = 6,        /* a bounded device-side wait expired */
     MOE_ERR_CUDA = 7,           /* the CUDA runtime reported an error */
@@ -430,7 +431,8 @@ MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
  *  the same tile that do not see it); rows at or past it may hold anything.
  *  One or two launches.  ws_dev: moe_attention_workspace_bytes (0: invalid
  *  shape; never above 48 MiB), a workspace of its own, not one that the FFN
- *  calls use (both keep values behind the header), initialised with
+ *  calls use (both keep values behind the header; where the FFN's would be taken
+ *  for attention's, MOE_ERR_WORKSPACE is recorded), initialised with
  *  moe_workspace_init before its first use and after MOE_ERR_TIMEOUT; one call
  *  at a time may use it.  Results are bitwise repeatable.
  */

@@ -145,8 +145,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     fence_mbar_init();
     pdl_enter();
     if (sp.join_launch && tid == 0) p.desc[blockIdx.x].parts = 0;
+    // Single-token calls of the experts leave tags where the parts are counted: the header says
+    // whether there were any (read beside the search, looked at after it).
+    const bool looks = !sp.join_launch && blockIdx.x == 0 && tid == 0;
+    const unsigned long long tags = looks ? p.hdr->cta_calls : 0ull;
     Run run;
-    if (!run_begin<kTile>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, run)) return;
+    const bool work = run_begin<kTile>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, run);
+    if (tags != 0) record_status(p.hdr, MOE_ERR_WORKSPACE, 0);
+    if (!work) return;
     fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
     __syncthreads();
 

@@ -247,3 +247,24 @@ def test_norm_of_a_row_of_zeros(m, eps):
         assert bool((y[::2] == 0).all())
     want = norm_ref(x[1:2].cpu(), None, torch.ones(512), eps)[1]
     within(y[1:2], want, want.abs() * (512 / 2 + 8) * U32, "the row between")
+
+
+def test_a_workspace_that_the_experts_have_used(m):
+    """The single-token layer's tags lie where the parts of items are counted: recorded, not overlooked;
+    initialised anew the workspace serves."""
+    from quantized_routed_expert_02_gb300 import synth
+    from tests.test_gpu_parity import layer_case, to_dev
+    c = layer_case(synth.SHAPES["tiny"], 0, None)
+    s, d = c["shape"], to_dev(c)
+    ws = m.alloc_attention_workspace(8, 2, 128, device=DEV)
+    assert ws.numel() >= m.moe_workspace_bytes(1, s.H, s.E, s.k, s.I)
+    m.moe_layer(d["x"], d["Wr"], d["bias"], d["gate"], d["up"], d["down"], s.k, s.I, d["idx"], d["w"], d["y"], ws)
+    assert m.moe_read_device_status(ws)[0] == 0
+    case = Batch([1] * 32, [1500] * 32, 8, 2, 128, 16, torch.bfloat16, seed=3)  # parted, joined inside
+    assert m.status_str(run_attn(m, case, ws=ws)[2]) == "MOE_ERR_WORKSPACE"
+    m.moe_workspace_init(ws)
+    out, lse, code, detail = run_attn(m, case, ws=ws)
+    assert code == 0, (m.status_str(code), detail)
+    o, e, tol, lse_tol = attention_ref(case, 128 ** -0.5)
+    within(out, o, tol, "out")
+    within(lse, e, lse_tol, "lse")
