@@ -23,7 +23,10 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _binding  # noqa: E402  (native entry points; needs the library above)
+try:  # native entry points of the attention half; needs the library above
+    from . import _binding  # noqa: E402
+except ImportError as _e:  # not built, or for another Python or PyTorch: the experts' calls work without it
+    _binding, _binding_error = None, _e
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -246,10 +249,22 @@ def moe_ffn_q8k_codes(q, d, sums, idx, w, gate, up, down, E, I, y, ws, stream=No
 
 # moe_add_rmsnorm, moe_rope_append and moe_attention_paged check many tensors against one another;
 # they are native (csrc/binding.cpp), for the calls of single tokens.
-_binding.set_error(MoeError)
-moe_add_rmsnorm = _binding.moe_add_rmsnorm
-moe_rope_append = _binding.moe_rope_append
-moe_attention_paged = _binding.moe_attention_paged
+def _native(name):
+    if _binding is not None:
+        return getattr(_binding, name)
+
+    def missing(*args, **kwargs):
+        raise RuntimeError(f"{name}: the module _binding is missing or was built for another Python or PyTorch "
+                           f"({_binding_error}): build it with `python -m quantized_routed_expert_02_gb300.build`")
+    missing.__name__ = name
+    return missing
+
+
+if _binding is not None:
+    _binding.set_error(MoeError)
+moe_add_rmsnorm = _native("moe_add_rmsnorm")
+moe_rope_append = _native("moe_rope_append")
+moe_attention_paged = _native("moe_attention_paged")
 
 
 def moe_attention_workspace_bytes(Hq, Hkv, D) -> int:
