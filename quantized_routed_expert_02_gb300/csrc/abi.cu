@@ -13,7 +13,7 @@ using namespace moeq4k;
 namespace {
 
 struct DevInfo {
-    bool ready = false;
+    bool ready = false, attention = false;
     int sms = 0;
     int id = 0;
 };
@@ -42,13 +42,25 @@ moe_status moeq4k::device_info(int *sms, int *dev_out) {
         if (init_prefill_tc(dev) != cudaSuccess) return MOE_ERR_CUDA;
         if (init_router_tc() != cudaSuccess) return MOE_ERR_CUDA;
         if (init_decode_stream(dev) != cudaSuccess) return MOE_ERR_CUDA;
-        if (init_attention() != cudaSuccess) return MOE_ERR_CUDA;
         g_dev[dev].sms = n;
         g_dev[dev].id = dev;
         g_dev[dev].ready = true;
     }
     *sms = g_dev[dev].sms;
     if (dev_out) *dev_out = dev;
+    return MOE_OK;
+}
+
+// The same with the attention kernels': they load with their attributes (1.4 ms and
+// 2 MiB of device memory), which calls of the experts need not pay for.
+moe_status moeq4k::attention_info(int *sms) {
+    int dev = 0;
+    MOE_TRY(device_info(sms, &dev));
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_dev[dev].attention) {
+        if (init_attention() != cudaSuccess) return MOE_ERR_CUDA;
+        g_dev[dev].attention = true;
+    }
     return MOE_OK;
 }
 

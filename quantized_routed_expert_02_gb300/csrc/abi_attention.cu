@@ -135,7 +135,7 @@ moe_status moe_attention_paged(const void *q, const void *k_pages, const void *v
     if (ws_bytes < moe_attention_workspace_bytes(Hq, Hkv, D)) return MOE_ERR_WORKSPACE;
     if (stream == MOE_CHECK_ONLY) return MOE_OK;
     int sms = 0;
-    MOE_TRY(device_info(&sms, nullptr));
+    MOE_TRY(attention_info(&sms));
     AttnArgs a = {};
     a.q = q, a.k = k_pages, a.v = v_pages, a.out = out, a.lse = lse, a.b = p;
     a.scale = scale, a.softcap = softcap, a.window = window, a.type = dtype;

@@ -10,6 +10,8 @@ namespace moeq4k {
 // Per-device one-time set-up (kernel attributes, SM count) for the current
 // device; returns the SM count and the device ordinal.
 moe_status device_info(int *sms, int *dev_out);
+// The same for a call of moe_attention_paged, whose kernels are set up by its first.
+moe_status attention_info(int *sms);
 // Shape limits shared by every entry point.
 moe_status validate_shape(int T, int H, int E, int k, int I);
 
