@@ -268,3 +268,15 @@ def test_a_workspace_that_the_experts_have_used(m):
     o, e, tol, lse_tol = attention_ref(case, 128 ** -0.5)
     within(out, o, tol, "out")
     within(lse, e, lse_tol, "lse")
+
+
+@pytest.mark.parametrize("new,lens", [([1, 1], [300, 1]), ([4, 3], [2, 90]), ([70, 150], [40, 900])])
+@pytest.mark.parametrize("window", [(1 << 30) - 1, 1 << 30, 2 ** 31 - 1])
+def test_windows_past_every_length(m, new, lens, window):
+    """The widest windows hide nothing, also from tokens before the cache's start."""
+    case = Batch(new, lens, 8, 2, 128, 16, torch.bfloat16, seed=5)
+    plain = run_attn(m, case)
+    wide = run_attn(m, case, window=window)
+    assert wide[2] == 0
+    used = sum(new)
+    assert torch.equal(wide[0][:used], plain[0][:used]) and torch.equal(wide[1][:used], plain[1][:used])
