@@ -424,7 +424,7 @@ MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
  *  finite, and scale / softcap.
  *  max_new >= 1: the most new tokens of any sequence, as far as the caller
  *  knows; it picks the kernel and may be wrong (only speed depends on it).
- *  Scores, softmax statistics and sums are fp32 (a capped score is within
+ *  Scores (without a cap not past its range), softmax statistics and sums are fp32 (a capped score is within
  *  2^-20 of itself or, with softcap up to 64, 2^-21 of the cap); the weights are rounded to
  *  dtype for their product with V, as the scores' operands are.  The cached
  *  rows below kv_lens must be finite (a non-finite V row reaches the rows of

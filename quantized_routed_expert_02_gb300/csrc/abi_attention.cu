@@ -77,7 +77,7 @@ moe_status moe_add_rmsnorm(const void *x, moe_dtype x_type, const float *residua
     a.x = x, a.residual = residual, a.gamma = gamma, a.sum_out = sum_out, a.y = y;
     a.q = q, a.d = d, a.sums = sums, a.eps = eps, a.T = T, a.H = H;
     a.x_type = x_type, a.y_type = y_type;
-    return cuda_status(launch_add_rmsnorm(a, sms, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_add_rmsnorm(a, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_rope_append(const void *qkv, const int32_t *pos, const double *inv_freq,

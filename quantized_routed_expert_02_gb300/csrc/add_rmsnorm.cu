@@ -177,8 +177,7 @@ cudaError_t launch_x(const AddNormArgs &a, cudaStream_t s) {
 
 }  // namespace arn
 
-cudaError_t launch_add_rmsnorm(const AddNormArgs &a, int num_sms, cudaStream_t s) {
-    (void)num_sms;
+cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t s) {
     switch (a.x_type) {
         case MOE_F16: return arn::launch_x<__half>(a, s);
         case MOE_BF16: return arn::launch_x<__nv_bfloat16>(a, s);

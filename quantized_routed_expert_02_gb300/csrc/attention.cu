@@ -15,9 +15,11 @@
 // Measured (32/4 heads of 128, bf16): 64 sequences of 4000 tokens 89 us
 // = 5.9 TB/s, eight of 20000 with 16/16 heads 207 us = 6.3 TB/s; a bare loop of the
 // same copies over 268 MB reaches 6.3 to 6.6 TB/s whatever its box.  Short
-// batches pay about 7 us from the launch to the first keys (offsets, the search for the
-// run, page table, keys: four dependent reads) and, with many parts, 4 us for
-// the joining launch: one token over 131071 52 us, over 2000 9.1, over 93 5.9 us.
+// batches pay for the chain from the launch to the first keys (offsets, the search for the
+// run, page table, keys: four dependent reads; of one token over 93, 6.0 us, nearly all, of a
+// ragged batch some 7 us) and, with many parts, 4 us for the joining launch: one
+// token over 131071 53 us, over 2000 9.1.  A cap's polynomial costs batches that the
+// bytes do not fill 1.5 us (48 tokens over 1500 30.1 -> 31.8) and the others nothing.
 #include <algorithm>
 
 #include <cuda.h>
@@ -280,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 l[h] = l[h] * cor[h] + ((s[0][2 * h] + s[0][2 * h + 1]) +
                                               (s[1][2 * h] + s[1][2 * h + 1]));
             }
-            // the weights rounded to the 16-bit type for the product; the sum l keeps them whole
+            // the weights rounded to the 16-bit type for the product: its two operands have one type, and
+            // the values beside them were rounded to it by the same half step; the sum l keeps them whole
             pa[0] = Pair<T>::make(s[0][0], s[0][1]);
             pa[1] = Pair<T>::make(s[0][2], s[0][3]);
             pa[2] = Pair<T>::make(s[1][0], s[1][1]);

@@ -10,9 +10,9 @@
 // run is a few segments, each a range of key tiles of one item.  An item
 // inside one run is finished there; one that crosses a cut leaves a partial
 // result (unnormalised sums, running maximum and sum) per segment.  These are
-// joined in a fixed order, by the CTA that arrives last (few rows) or by a second
-// launch over the whole GPU (many rows), so that the order of every sum depends
-// on the shapes alone and results repeat bit for bit.
+// joined in a fixed order, by the CTA that arrives last (few rows in few parts) or by
+// a second launch over the whole GPU (many parts, many rows), so that the order of
+// every sum depends on the shapes alone and results repeat bit for bit.
 #pragma once
 
 #include <math_constants.h>

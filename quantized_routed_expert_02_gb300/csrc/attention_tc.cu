@@ -19,7 +19,7 @@
 // its 32 KB tile from there once per half, next to the copies' writes) and the tensor
 // pipe: a chunk of 2048 rows over 16384 keys, 32/4 heads of 128, takes 337 us
 // = 1.53 PFLOP/s.  With a cap the exponentials and reciprocals, 10 cycles a
-// warp for 32 scores, and their arithmetic do: 446 us.  Short ranges pay for
+// warp for 32 scores, and their arithmetic do: 448 us.  Short ranges pay for
 // their segments' ends (the last softmax, the result, the first softmax: 3 tiles'
 // time): a prompt of 4096, 117 us = 1.18 PFLOP/s.  One thread per row
 // (four warps a half) was slower by the latency of its chain: the capped chunk 613
@@ -205,7 +205,7 @@ enum Mode { kScaled, kCapped, kAny };
 // kCapped takes the tangent from 1 - 2 / (1 + e^2y) alone: its error is at most
 // 2^-21 of the cap, up to this cap 2^-15, a few fp32 steps of the scores that the cap
 // lets through.  Caps beyond go to kAny, whose scores are score()'s (2048 rows over 16384
-// keys: 446 us, by kAny 545).
+// keys: 448 us, by kAny 550; 939 before scores far below the cap left out the exponential).
 constexpr float kCapNear = 64.f;
 
 template <typename T, int D, int kMode>
@@ -603,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                     if (u[i + 2 * k + 1] == hidden) y = 0.f;
                                 }
                                 s2[k] = add2(s2[k], pack2(x, y));
-                                // rounded for the product; the sum keeps the weight whole
+                                // rounded for the product, whose operands have one type (V's values were
+                                // rounded to it by the same half step); the sum keeps the weight whole
                                 w[i / 2 + k] = Pair<T>::make(x, y);
                             }
                         }

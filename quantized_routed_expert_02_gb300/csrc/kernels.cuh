@@ -136,7 +136,7 @@ struct AddNormArgs {
     int T, H;
     moe_dtype x_type, y_type;
 };
-cudaError_t launch_add_rmsnorm(const AddNormArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_add_rmsnorm(const AddNormArgs &a, cudaStream_t s);
 
 // A paged K/V cache and the batch of sequences that a call works on.
 struct PagedBatch {
