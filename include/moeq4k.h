@@ -72,8 +72,8 @@ typedef enum {
     MOE_ERR_INVALID_SHAPE = 1,  /* a dimension is out of range or inconsistent */
     MOE_ERR_NULL = 2,           /* a required pointer is NULL */
     MOE_ERR_MISALIGNED = 3,     /* a pointer breaks the alignment rule */
-    MOE_ERR_WORKSPACE = 4,      /* workspace smaller than moe_workspace_bytes(), or (device) one that calls
-                                   of the other half of the block had used */
+    MOE_ERR_WORKSPACE = 4,      /* workspace smaller than moe_workspace_bytes(); on the device: one that
+                                   calls of the other half of the block have used */
     MOE_ERR_EXPERT_RANGE = 5,   /* device saw an expert index outside [0,E) */
     MOE_ERR_TIMEOUT = 6,        /* a bounded device-side wait expired */
     MOE_ERR_CUDA = 7,           /* the CUDA runtime reported an error */
@@ -424,9 +424,10 @@ MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
  *  finite, and scale / softcap.
  *  max_new >= 1: the most new tokens of any sequence, as far as the caller
  *  knows; it picks the kernel and may be wrong (only speed depends on it).
- *  Scores (without a cap not past its range), softmax statistics and sums are fp32 (a capped score is within
- *  2^-20 of itself or, with softcap up to 64, 2^-21 of the cap); the weights are rounded to
- *  dtype for their product with V, as the scores' operands are.  The cached
+ *  Scores, softmax statistics and sums are fp32; without a cap q . k has to stay
+ *  in its range, with one a score is within 2^-20 of itself or (softcap up to 64)
+ *  2^-21 of the cap.  The weights are rounded to dtype for their product with
+ *  V, as the scores' operands are.  The cached
  *  rows below kv_lens must be finite (a non-finite V row reaches the rows of
  *  the same tile that do not see it); rows at or past it may hold anything.
  *  One or two launches.  ws_dev: moe_attention_workspace_bytes (0: invalid
