@@ -342,8 +342,9 @@ MOE_API moe_status moe_layer_noalloc(const float *x_dev, const float *Wr_dev, co
  * The attention half of a decoder block: residual addition with RMSNorm,
  * rotary positions with the append to a paged cache, and attention over that
  * cache.  The projections between them are the caller's.  With
- * MOE_CHECK_ONLY in place of a stream the three calls check their arguments and
- * enqueue nothing (MOE_OK: a call with a stream would be enqueued).
+ * MOE_CHECK_ONLY in place of a stream these calls (and those on the cache in 8
+ * bits, below) check their arguments and enqueue nothing (MOE_OK: a call with a
+ * stream would be enqueued).
  *
  * moe_add_rmsnorm, per row of H values:
  *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * gamma
@@ -444,6 +445,81 @@ MOE_API moe_status moe_attention_paged(const void *q_dev, const void *k_pages_de
                        int max_new, int max_pages, int num_pages, int page, int Hq, int Hkv, int D,
                        moe_dtype dtype, float scale, float softcap, int window, void *out_dev,
                        float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
+/*
+ * The cache in 8 bits: k_codes_dev, v_codes_dev int8 [num_pages, Hkv, page, D]
+ * and k_scales_dev, v_scales_dev fp32 [num_pages, Hkv, page]: a cached token's
+ * head is scale * code.  A quarter of a 32-bit cache's bytes, half of a 16-bit one's.
+ *
+ * moe_rope_append_q8: moe_rope_append with keys and values (after norm and
+ * rotation, in fp32) quantised as they are written, one head of one token a
+ * block, by the steps of moe_quantize_q8k: amax = max |v|, d = amax / 127, codes
+ * v * (127 / amax) rounded to the nearest integer, halves to even.  A head whose
+ * amax is 0 or too small for 127 / amax in fp32 (below 2^-121) is stored as
+ * zeros; one that holds an infinity or a NaN gets that as its scale and codes 0.
+ * Queries as there.  Arguments, limits and errors as moe_rope_append; the scales
+ * are 16-byte aligned.  One launch.
+ */
+MOE_API moe_status moe_rope_append_q8(const void *qkv_dev, const int32_t *pos_dev,
+                       const double *inv_freq_dev, const int32_t *axis_dev, int axes, int rot_dim,
+                       int interleaved, const float *q_norm_w_dev, const float *k_norm_w_dev,
+                       float norm_eps, void *q_out_dev, int8_t *k_codes_dev, int8_t *v_codes_dev,
+                       float *k_scales_dev, float *v_scales_dev, const int32_t *page_table_dev,
+                       const int32_t *q_offs_dev, const int32_t *kv_lens_dev, int N, int B,
+                       int max_pages, int num_pages, int page, int Hq, int Hkv, int D,
+                       moe_dtype dtype, void *ws_dev, size_t ws_bytes, void *stream);
+
+/*
+ * moe_attention_cache: moe_attention_paged over either cache and with more masks.
+ *  Codes: with k_scales_dev and v_scales_dev (both or neither) k_pages_dev and
+ *  v_pages_dev are the int8 codes above; dtype is that of q and out.  The codes are
+ *  exact in dtype: q . code and its scale are taken in fp32 (q . code has to stay in
+ *  its range, with a cap too), and a weight times its value's scale is rounded to
+ *  dtype once.  Scales below kv_lens are finite and not negative.
+ *  Sinks: with window > 0 a row at cache index t sees the keys j <= t with
+ *  j > t - window or j < sinks (sinks >= 0; without a window they change nothing).
+ *  Table entries of pages between the two that no new token sees are not read.
+ *  Tree: with tree_dev int32 [N, tree_words] (1 <= tree_words <= 32; NULL: the new
+ *  tokens of a sequence are a chain, tree_words 0) the new tokens of a sequence are
+ *  the nodes of a tree, and bit i % 32 of word i / 32 of a row says that the row
+ *  sees the sequence's new token i (itself where its own bit is set; parents may
+ *  come in any order, bits at or past n are ignored, new tokens at or past
+ *  32 tree_words are seen by none).  All rows see the sequence's older tokens, but
+ *  for the window, which counts from the node's place in the text: a row with m of its
+ *  bits 0 .. n-1 set is at t = kv_lens[b] - n + max(m, 1) - 1 and of the older tokens
+ *  sees those above; the tree's bits are not subject to the window.
+ *  The workspace, max_new, the cap and everything else as moe_attention_paged, whose
+ *  results it gives bit for bit where none of the three is used.
+ */
+MOE_API moe_status moe_attention_cache(const void *q_dev, const void *k_pages_dev,
+                       const void *v_pages_dev, const float *k_scales_dev, const float *v_scales_dev,
+                       const int32_t *page_table_dev, const int32_t *q_offs_dev,
+                       const int32_t *kv_lens_dev, const int32_t *tree_dev, int tree_words, int N, int B,
+                       int max_new, int max_pages, int num_pages, int page, int Hq, int Hkv, int D,
+                       moe_dtype dtype, float scale, float softcap, int window, int sinks, void *out_dev,
+                       float *lse_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
+/*
+ * moe_cache_keep: of each sequence's n new tokens the kept_dev[b] that were
+ * accepted move to the front, so that they follow the older ones as a chain:
+ * cache row kv_lens[b] - n + keep_dev[b][d] -> kv_lens[b] - n + d, for d <
+ * kept[b], keys, values and (or NULL, both) scales.  keep_dev int32 [B, max_keep],
+ * rising strictly in each sequence and below n (a path of a tree whose parents
+ * come before their children); kept_dev int32 [B], from 0 (nothing moves) to
+ * max_keep.  k_pages_dev, v_pages_dev of elem_bytes 2 (no scales) or 1 (with
+ * scales) an element.  q_offs_dev and kv_lens_dev are those of the call that cached
+ * the tokens; the caller's next kv_lens is kv_lens[b] - n + kept[b].  The rows from
+ * there on hold anything.  A sequence with entries out of range (the
+ * lengths and offsets, a page, keep or kept) stays as it was, and the status
+ * records MOE_ERR_CACHE_RANGE.  Sequences share no pages that are written.
+ *  Limits: 1 <= max_keep <= 2^20; B, pages and heads as above.  ws_dev: at least 256
+ *  bytes, initialised (status word only).  One launch.
+ */
+MOE_API moe_status moe_cache_keep(void *k_pages_dev, void *v_pages_dev, float *k_scales_dev,
+                       float *v_scales_dev, const int32_t *page_table_dev, const int32_t *q_offs_dev,
+                       const int32_t *kv_lens_dev, const int32_t *keep_dev, const int32_t *kept_dev, int B,
+                       int max_keep, int max_pages, int num_pages, int page, int Hkv, int D, int elem_bytes,
+                       void *ws_dev, size_t ws_bytes, void *stream);
 
 /*
  * Test hooks for the bounded device-side waits (not for production use).

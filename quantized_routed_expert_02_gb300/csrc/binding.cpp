@@ -259,20 +259,66 @@ struct Cache : Place {
     at::ScalarType type;
     moe_dtype dtype;
 
-    Cache(PyObject *kp, PyObject *vp, PyObject *table_, PyObject *offs_, PyObject *lens_)
-        : Place(tensor(kp, "k_pages")) {
-        const at::Tensor &kt = tensor(kp, "k_pages"), &tt = tensor(table_, "page_table");
-        const at::IntArrayRef c = sizes(kt, 4, "k_pages"), t = sizes(tt, 2, "page_table");
-        pages = extent(c[0], "k_pages"), Hkv = extent(c[1], "k_pages");
-        page = extent(c[2], "k_pages"), D = extent(c[3], "k_pages");
+    float *ks = nullptr, *vs = nullptr;  // of 8-bit codes
+
+    // `ksp`, `vsp`: the scales of a cache of 8-bit codes (both), or null or None; then `rows` gives the type
+    // of what else a call takes.
+    Cache(PyObject *kp, PyObject *vp, PyObject *table_, PyObject *offs_, PyObject *lens_, PyObject *ksp = nullptr,
+          PyObject *vsp = nullptr, const at::Tensor *rows = nullptr, const char *rows_name = "",
+          const char *k_name = "k_pages", const char *v_name = "v_pages")
+        : Place(tensor(kp, k_name)) {
+        const at::Tensor &kt = tensor(kp, k_name), &tt = tensor(table_, "page_table");
+        const at::IntArrayRef c = sizes(kt, 4, k_name), t = sizes(tt, 2, "page_table");
+        pages = extent(c[0], k_name), Hkv = extent(c[1], k_name);
+        page = extent(c[2], k_name), D = extent(c[3], k_name);
         B = extent(t[0], "page_table"), max_pages = extent(t[1], "page_table");
-        type = kt.scalar_type();
-        dtype = dtype_of(kt, "k_pages");
-        k = pointer(kt, c, type, "k_pages");
-        v = pointer(vp, c, type, "v_pages");
+        const bool codes = (ksp != nullptr && ksp != Py_None) || (vsp != nullptr && vsp != Py_None);
+        if (codes) {
+            k = pointer(kt, c, at::kChar, k_name);
+            v = pointer(vp, c, at::kChar, v_name);
+            ks = pointer<float>(ksp, c.slice(0, 3), at::kFloat, "k_scales");
+            vs = pointer<float>(vsp, c.slice(0, 3), at::kFloat, "v_scales");
+        }
+        const at::Tensor &typed = codes && rows != nullptr ? *rows : kt;
+        type = typed.scalar_type();
+        if (!codes || rows != nullptr) dtype = dtype_of(typed, codes ? rows_name : k_name);
+        if (!codes) {
+            k = pointer(kt, c, type, k_name);
+            v = pointer(vp, c, type, v_name);
+        }
         table = pointer<int32_t>(tt, t, at::kInt, "page_table");
         offs = pointer<int32_t>(offs_, {B + 1}, at::kInt, "q_offs");
         lens = pointer<int32_t>(lens_, {B}, at::kInt, "kv_lens");
+    }
+};
+
+// moe_rope_append's tensors but the cache's, in the order of its arguments.
+struct Rope {
+    const void *qkv;
+    const int32_t *pos, *axis;
+    const double *freq;
+    const float *qw, *kw;
+    void *q_out;
+    int N, Hq, axes, half, turned;
+    float eps;
+
+    Rope(const Cache &c, PyObject *qkv_, PyObject *pos_, PyObject *freq_, PyObject *q_out_, PyObject *axis_,
+         PyObject *qw_, PyObject *kw_, PyObject *eps_, PyObject *interleaved) {
+        const at::Tensor &out = tensor(q_out_, "q_out"), &p = tensor(pos_, "pos"), &f = tensor(freq_, "inv_freq");
+        const at::IntArrayRef o = sizes(out, 3, "q_out");
+        N = extent(o[0], "q_out"), Hq = extent(o[1], "q_out");
+        axes = extent(sizes(p, 2, "pos")[0], "pos");
+        half = extent(sizes(f, 1, "inv_freq")[0], "inv_freq");
+        qkv = c.pointer(qkv_, {N, int64_t(Hq + 2 * int64_t(c.Hkv)) * c.D}, c.type, "qkv");
+        pos = c.pointer<int32_t>(p, {axes, N}, at::kInt, "pos");
+        freq = c.pointer<double>(f, {half}, at::kDouble, "inv_freq");
+        axis = c.optional<int32_t>(axis_, {half}, at::kInt, "axis");
+        qw = c.optional<float>(qw_, {c.D}, at::kFloat, "q_norm_w");
+        kw = c.optional<float>(kw_, {c.D}, at::kFloat, "k_norm_w");
+        eps = eps_ == Py_None ? 1e-6f : as_float(eps_);
+        turned = interleaved == Py_None ? 0 : PyObject_IsTrue(interleaved);
+        if (turned < 0) throw Raised();
+        q_out = c.pointer(out, {N, Hq, c.D}, c.type, "q_out");
     }
 };
 
@@ -283,27 +329,33 @@ PyObject *rope_append(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
                                             "k_norm_w", "eps",   "interleaved", "stream"};
         const Args<16> a("moe_rope_append", names, 10, args, n, kwnames);
         const Cache c(a[4], a[5], a[6], a[7], a[8]);
-        const at::Tensor &out = tensor(a[3], "q_out"), &pos = tensor(a[1], "pos"), &freq = tensor(a[2], "inv_freq");
-        const at::IntArrayRef o = sizes(out, 3, "q_out");
-        const int N = extent(o[0], "q_out"), Hq = extent(o[1], "q_out");
-        const int axes = extent(sizes(pos, 2, "pos")[0], "pos");
-        const int half = extent(sizes(freq, 1, "inv_freq")[0], "inv_freq");
-        const void *qkv = c.pointer(a[0], {N, int64_t(Hq + 2 * int64_t(c.Hkv)) * c.D}, c.type, "qkv");
-        const int32_t *at_pos = c.pointer<int32_t>(pos, {axes, N}, at::kInt, "pos");
-        const double *f = c.pointer<double>(freq, {half}, at::kDouble, "inv_freq");
-        const int32_t *axis = c.optional<int32_t>(a[10], {half}, at::kInt, "axis");
-        const float *qw = c.optional<float>(a[11], {c.D}, at::kFloat, "q_norm_w");
-        const float *kw = c.optional<float>(a[12], {c.D}, at::kFloat, "k_norm_w");
-        const float eps = a[13] == Py_None ? 1e-6f : as_float(a[13]);
-        const int turned = a[14] == Py_None ? 0 : PyObject_IsTrue(a[14]);
-        if (turned < 0) throw Raised();
-        void *q_out = c.pointer(out, {N, Hq, c.D}, c.type, "q_out");
+        const Rope r(c, a[0], a[1], a[2], a[3], a[10], a[11], a[12], a[13], a[14]);
         const at::Tensor &ws = tensor(a[9], "ws");
         void *w = c.workspace(ws), *s = as_stream(a[15], c);
         run("moe_rope_append", c, [&] {
-            return moe_rope_append(qkv, at_pos, f, axis, axes, 2 * half, turned, qw, kw, eps, q_out, c.k, c.v,
-                                   c.table, c.offs, c.lens, N, c.B, c.max_pages, c.pages, c.page, Hq, c.Hkv, c.D,
-                                   c.dtype, w, ws.nbytes(), s);
+            return moe_rope_append(r.qkv, r.pos, r.freq, r.axis, r.axes, 2 * r.half, r.turned, r.qw, r.kw, r.eps,
+                                   r.q_out, c.k, c.v, c.table, c.offs, c.lens, r.N, c.B, c.max_pages, c.pages,
+                                   c.page, r.Hq, c.Hkv, c.D, c.dtype, w, ws.nbytes(), s);
+        });
+    });
+}
+
+PyObject *rope_append_q8(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwnames) {
+    return entry([&] {
+        static const char *const names[] = {"qkv",      "pos",        "inv_freq", "q_out",   "k_codes", "v_codes",
+                                            "k_scales", "v_scales",   "page_table", "q_offs", "kv_lens", "ws",
+                                            "axis",     "q_norm_w",   "k_norm_w", "eps",     "interleaved", "stream"};
+        const Args<18> a("moe_rope_append_q8", names, 12, args, n, kwnames);
+        for (int i = 6; i < 8; ++i) tensor(a[i], names[i]);
+        const Cache c(a[4], a[5], a[8], a[9], a[10], a[6], a[7], &tensor(a[0], "qkv"), "qkv", "k_codes", "v_codes");
+        const Rope r(c, a[0], a[1], a[2], a[3], a[12], a[13], a[14], a[15], a[16]);
+        const at::Tensor &ws = tensor(a[11], "ws");
+        void *w = c.workspace(ws), *s = as_stream(a[17], c);
+        run("moe_rope_append_q8", c, [&] {
+            return moe_rope_append_q8(r.qkv, r.pos, r.freq, r.axis, r.axes, 2 * r.half, r.turned, r.qw, r.kw, r.eps,
+                                      r.q_out, static_cast<int8_t *>(c.k), static_cast<int8_t *>(c.v), c.ks, c.vs,
+                                      c.table, c.offs, c.lens, r.N, c.B, c.max_pages, c.pages, c.page, r.Hq, c.Hkv,
+                                      c.D, c.dtype, w, ws.nbytes(), s);
         });
     });
 }
@@ -332,6 +384,60 @@ PyObject *attention_paged(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
     });
 }
 
+PyObject *attention_cache(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwnames) {
+    return entry([&] {
+        static const char *const names[] = {"q",   "k_pages", "v_pages",  "page_table", "q_offs", "kv_lens",
+                                            "max_new", "scale", "out",    "ws",         "k_scales", "v_scales",
+                                            "tree", "sinks",  "lse",      "window",     "softcap", "stream"};
+        const Args<18> a("moe_attention_cache", names, 10, args, n, kwnames);
+        const at::Tensor &qt = tensor(a[0], "q");
+        const Cache c(a[1], a[2], a[3], a[4], a[5], a[10], a[11], &qt, "q");
+        const at::IntArrayRef r = sizes(qt, 3, "q");
+        const int N = extent(r[0], "q"), Hq = extent(r[1], "q");
+        const void *q = c.pointer(qt, {N, Hq, c.D}, c.type, "q");
+        const int most = as_int(a[6]), window = a[15] == Py_None ? 0 : as_int(a[15]);
+        const int sinks = a[13] == Py_None ? 0 : as_int(a[13]);
+        const float scale = as_float(a[7]), softcap = a[16] == Py_None ? 0.f : as_float(a[16]);
+        void *out = c.pointer(a[8], {N, Hq, c.D}, c.type, "out");
+        float *lse = c.optional<float>(a[14], {N, Hq}, at::kFloat, "lse");
+        const int32_t *tree = nullptr;
+        int words = 0;
+        if (a[12] != Py_None) {
+            const at::Tensor &t = tensor(a[12], "tree");
+            words = extent(sizes(t, 2, "tree")[1], "tree");
+            tree = c.pointer<int32_t>(t, {N, words}, at::kInt, "tree");
+            if (words < 1) refuse(PyExc_ValueError, "tree: no words");
+        }
+        const at::Tensor &ws = tensor(a[9], "ws");
+        void *w = c.workspace(ws), *s = as_stream(a[17], c);
+        run("moe_attention_cache", c, [&] {
+            return moe_attention_cache(q, c.k, c.v, c.ks, c.vs, c.table, c.offs, c.lens, tree, words, N, c.B, most,
+                                       c.max_pages, c.pages, c.page, Hq, c.Hkv, c.D, c.dtype, scale, softcap, window,
+                                       sinks, out, lse, w, ws.nbytes(), s);
+        });
+    });
+}
+
+PyObject *cache_keep(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kwnames) {
+    return entry([&] {
+        static const char *const names[] = {"k_pages", "v_pages", "page_table", "q_offs", "kv_lens", "keep",
+                                            "kept", "ws", "k_scales", "v_scales", "stream"};
+        const Args<11> a("moe_cache_keep", names, 8, args, n, kwnames);
+        const Cache c(a[0], a[1], a[2], a[3], a[4], a[8], a[9]);
+        if (c.ks == nullptr && c.dtype == MOE_F32) refuse(PyExc_TypeError, "k_pages: torch.float32, not a cache's type");
+        const at::Tensor &kt = tensor(a[5], "keep");
+        const int most = extent(sizes(kt, 2, "keep")[1], "keep");
+        const int32_t *keep = c.pointer<int32_t>(kt, {c.B, most}, at::kInt, "keep");
+        const int32_t *kept = c.pointer<int32_t>(a[6], {c.B}, at::kInt, "kept");
+        const at::Tensor &ws = tensor(a[7], "ws");
+        void *w = c.workspace(ws), *s = as_stream(a[10], c);
+        run("moe_cache_keep", c, [&] {
+            return moe_cache_keep(c.k, c.v, c.ks, c.vs, c.table, c.offs, c.lens, keep, kept, c.B, most, c.max_pages,
+                                  c.pages, c.page, c.Hkv, c.D, c.ks != nullptr ? 1 : 2, w, ws.nbytes(), s);
+        });
+    });
+}
+
 PyObject *set_error(PyObject *, PyObject *type) {
     Py_XSETREF(moe_error, Py_NewRef(type));
     Py_RETURN_NONE;
@@ -356,6 +462,24 @@ PyMethodDef methods[] = {
      "                    lse=None, window=0, softcap=0.0, stream=None)\n--\n\n"
      "Attention of the new rows ``q`` [N, Hq, D] over each sequence's cached tokens -> ``out``\n"
      "[N, Hq, D], ``lse`` [N, Hq] (optional).  ``max_new``: the most new tokens of a sequence."},
+    {"moe_rope_append_q8", FAST(rope_append_q8),
+     "moe_rope_append_q8(qkv, pos, inv_freq, q_out, k_codes, v_codes, k_scales, v_scales, page_table, q_offs,\n"
+     "                   kv_lens, ws, axis=None, q_norm_w=None, k_norm_w=None, eps=1e-6, interleaved=False,\n"
+     "                   stream=None)\n--\n\n"
+     "moe_rope_append into a cache of 8-bit codes: ``k_codes``, ``v_codes`` int8 [pages, Hkv, page, D],\n"
+     "``k_scales``, ``v_scales`` fp32 [pages, Hkv, page], one scale per token and head."},
+    {"moe_attention_cache", FAST(attention_cache),
+     "moe_attention_cache(q, k_pages, v_pages, page_table, q_offs, kv_lens, max_new, scale, out, ws,\n"
+     "                    k_scales=None, v_scales=None, tree=None, sinks=0, lse=None, window=0, softcap=0.0,\n"
+     "                    stream=None)\n--\n\n"
+     "moe_attention_paged over either cache (8-bit codes with ``k_scales``, ``v_scales``), of a tree of\n"
+     "drafted tokens (``tree`` int32 [N, words]: bit i of a row's words: it sees its sequence's new token i),\n"
+     "and with ``sinks`` first tokens that stay visible beside a window."},
+    {"moe_cache_keep", FAST(cache_keep),
+     "moe_cache_keep(k_pages, v_pages, page_table, q_offs, kv_lens, keep, kept, ws, k_scales=None,\n"
+     "               v_scales=None, stream=None)\n--\n\n"
+     "The accepted ones of each sequence's new tokens (``keep`` int32 [B, max_keep], rising; ``kept``\n"
+     "int32 [B] of them) move to the front of the new ones' places in the cache."},
     {"set_error", set_error, METH_O, "The exception type of refused calls."},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -154,6 +154,7 @@ struct RopeArgs {
     const float *qw, *kw;     // [D] or null
     void *q_out;              // [N, Hq, D]
     void *k, *v;              // pages
+    float *ks, *vs;           // scales [num_pages, Hkv, page]: k and v are 8-bit codes; or null
     PagedBatch b;
     int axes, rot;
     float eps;
@@ -166,11 +167,15 @@ cudaError_t launch_rope_append(const RopeArgs &a, int num_sms, cudaStream_t s);
 struct AttnArgs {
     const void *q;            // [N, Hq, D]
     const void *k, *v;        // pages
+    const float *ks, *vs;     // scales [num_pages, Hkv, page]: k and v are 8-bit codes; or null
     void *out;                // [N, Hq, D]
     float *lse;               // [N, Hq] or null
     PagedBatch b;
     float scale, softcap;     // softcap 0: none
     int window;               // 0: none
+    int sinks;                // first tokens that a window leaves visible
+    const uint32_t *tree;     // [N, words] or null: the new tokens are a chain
+    int words;
     moe_dtype type;
     WsHeader *hdr;
     uint8_t *scratch;         // counters, then partial results (attention_part_bytes)
@@ -190,5 +195,17 @@ bool encode_rows_map(CUtensorMap *map, const void *base, const PagedBatch &b, mo
 size_t attention_part_bytes(int D);
 cudaError_t init_attention();
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s);
+cudaError_t launch_attention_cache(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s);
+
+struct KeepArgs {
+    void *k, *v;
+    float *ks, *vs;           // or null
+    const int32_t *keep;      // [B, most]
+    const int32_t *kept;      // [B]
+    PagedBatch b;
+    int most, elem;           // bytes of an element
+    WsHeader *hdr;
+};
+cudaError_t launch_cache_keep(const KeepArgs &a, cudaStream_t s);
 
 }  // namespace moeq4k

@@ -1,5 +1,5 @@
 // Per-head RMSNorm, rotary positions and the append to a paged cache
-// (moe_rope_append).  Pair (a, b) of channel j turns by the angle
+// (moe_rope_append, and in 8-bit codes moe_rope_append_q8).  Pair (a, b) of channel j turns by the angle
 // pos[axis[j]] * inv_freq[j]:  (a cos - b sin, b cos + a sin).
 //
 // The angle is kept in turns as a 64-bit binary fraction: F_j = inv_freq_j /
@@ -18,6 +18,7 @@
 // the sines (fewer operations, more registers) took 33.4 us, a ring of bulk
 // copies and more warps with fewer chunks in flight no less than this.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -75,6 +76,39 @@ __device__ inline bool offsets_rise(const PagedBatch &p, int lane) {
     return __all_sync(0xffffffffu, ok);
 }
 
+__device__ __forceinline__ float max_abs_nan(float a, float b) {  // a NaN if either is one
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
+}
+
+// 8-bit codes of a head whose values `per` lanes hold, 16 each (in v two at a time), and its
+// scale: the steps of moe_quantize_q8k with the head for its block.  The scale of a head
+// that holds an infinity or a NaN is that, of one too small for 127 / amax in fp32 it is 0;
+// the codes of both are 0.  The whole warp calls it.
+__device__ __forceinline__ void quantise(const unsigned long long (&v)[8], int per, float &d, uint2 &w0, uint2 &w1) {
+    float x[16], most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        unpack2(v[i], x[2 * i], x[2 * i + 1]);
+        most = max_abs_nan(max_abs_nan(most, x[2 * i]), x[2 * i + 1]);
+    }
+    for (int o = per >> 1; o > 0; o >>= 1) most = max_abs_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float f = __fdiv_rn(127.f, most);
+    const bool some = f <= 3.402823466e38f;  // neither an infinity (of a zero, too) nor a NaN
+    d = some ? __fdiv_rn(most, 127.f) : most != most ? most : 0.f;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // an infinity times 0 is a NaN and converts to 0
+            w[i] |= (uint32_t(__float2int_rn(__fmul_rn(x[4 * i + j], some ? f : 0.f))) & 255u) << (8 * j);
+    }
+    w0 = make_uint2(w[0], w[1]);
+    w1 = make_uint2(w[2], w[3]);
+}
+
 // The work is a run of steps, 512 / D heads each (what a warp turns at a time),
 // row after row; a warp takes `run` of them, whatever the number of rows.
 // Lane: chunk c = lane % (D / 16) of a head at a time: the channels
@@ -82,7 +116,7 @@ __device__ inline bool offsets_rise(const PagedBatch &p, int lane) {
 // kBatch of them are loaded ahead, over the ends of rows too, each slot again
 // as soon as it is used; the places in the cache of a warp's next 32 rows are looked
 // up together, a row per lane, so that no row waits for the chain of table loads.
-template <typename T, bool kInterleaved>
+template <typename T, bool kInterleaved, bool kCodes>
 __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const RopeArgs a, int run) {
     __shared__ __align__(16) float co_sh[kWarps][kMaxPairs], si_sh[kWarps][kMaxPairs];
     pdl_enter();
@@ -167,8 +201,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
         const int nrow = min(row + 1, row_last);
         int nh0, nh1;  // the next row's
         heads_of(row + 1, nh0, nh1);
+        using C = std::conditional_t<kCodes, int8_t, T>;
         T *q_row = static_cast<T *>(a.q_out) + size_t(row) * Hq * D;
-        T *k_row = static_cast<T *>(a.k) + max(cache, 0l) * D, *v_row = static_cast<T *>(a.v) + max(cache, 0l) * D;
+        C *k_row = static_cast<C *>(a.k) + max(cache, 0l) * D, *v_row = static_cast<C *>(a.v) + max(cache, 0l) * D;
         __syncwarp();  // the row before has read its sines
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -247,9 +282,24 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) rope_append_kernel(const R
                     }
                 }
                 // heads are D apart in the queries, a page's rows apart in the cache
-                T *dst = query ? q_row + head * D : value ? v_row + (head - Hq - Hkv) * (a.b.page * D)
-                                                          : k_row + (head - Hq) * (a.b.page * D);
-                if (mine && live && (query || cache >= 0)) {
+                C *cached = value ? v_row + (head - Hq - Hkv) * (a.b.page * D) : k_row + (head - Hq) * (a.b.page * D);
+                if constexpr (kCodes) {
+                    // the whole warp, where any of its lanes has a key or a value
+                    if (h + k * step + step > Hq) {
+                        float d;
+                        uint2 w0, w1;
+                        quantise(v, per, d, w0, w1);
+                        if (mine && live && cache >= 0 && !query) {
+                            *reinterpret_cast<uint2 *>(cached + c0) = w0;
+                            *reinterpret_cast<uint2 *>(cached + c1) = w1;
+                            if (c == 0)
+                                (value ? a.vs : a.ks)[cache + (head - Hq - (value ? Hkv : 0)) * a.b.page] = d;
+                        }
+                        __syncwarp();
+                    }
+                }
+                T *dst = query || kCodes ? q_row + head * D : reinterpret_cast<T *>(cached);
+                if (mine && live && (query || (!kCodes && cache >= 0))) {
                     uint32_t o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -277,8 +327,13 @@ cudaError_t launch_rope_append(const RopeArgs &a, int num_sms, cudaStream_t s) {
     const int used = (total + run - 1) / run;
     const dim3 grid((used + kWarps - 1) / kWarps), block(kWarps * 32);
     auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, size_t(0), s, a, run); };
-    if (a.type == MOE_F16) return a.interleaved ? go(rope_append_kernel<__half, true>) : go(rope_append_kernel<__half, false>);
-    return a.interleaved ? go(rope_append_kernel<__nv_bfloat16, true>) : go(rope_append_kernel<__nv_bfloat16, false>);
+    auto of = [&](auto type, auto codes) {
+        using T = decltype(type);
+        constexpr bool kCodes = decltype(codes)::value;
+        return a.interleaved ? go(rope_append_kernel<T, true, kCodes>) : go(rope_append_kernel<T, false, kCodes>);
+    };
+    auto with = [&](auto codes) { return a.type == MOE_F16 ? of(__half(), codes) : of(__nv_bfloat16(), codes); };
+    return a.ks != nullptr ? with(std::true_type()) : with(std::false_type());
 }
 
 }  // namespace moeq4k

@@ -62,6 +62,11 @@ _SIGS = {
     "moe_attention_workspace_bytes": ([_I, _I, _I], _S),
     "moe_attention_paged": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                              ctypes.c_float, ctypes.c_float, _I, _P, _P, _P, _S, _P], ctypes.c_int),
+    "moe_rope_append_q8": ([_P] * 4 + [_I] * 3 + [_P, _P, ctypes.c_float] + [_P] * 8 + [_I] * 9 + [_P, _S, _P],
+                           ctypes.c_int),
+    "moe_attention_cache": ([_P] * 9 + [_I] * 11 + [ctypes.c_float, ctypes.c_float, _I, _I, _P, _P, _P, _S, _P],
+                            ctypes.c_int),
+    "moe_cache_keep": ([_P] * 9 + [_I] * 8 + [_P, _S, _P], ctypes.c_int),
     "moe_read_device_status": ([_P, _P, ctypes.POINTER(ctypes.c_int32)], ctypes.c_int),
     "moe_layer_noalloc": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P],
                           ctypes.c_int),
@@ -247,7 +252,7 @@ def moe_ffn_q8k_codes(q, d, sums, idx, w, gate, up, down, E, I, y, ws, stream=No
                                   ws.numel(), _stream(stream)), "moe_ffn_q8k_codes")
 
 
-# moe_add_rmsnorm, moe_rope_append and moe_attention_paged check many tensors against one another;
+# moe_add_rmsnorm and the calls on the paged cache check many tensors against one another;
 # they are native (csrc/binding.cpp), for the calls of single tokens.
 def _native(name):
     if _binding is not None:
@@ -265,6 +270,9 @@ if _binding is not None:
 moe_add_rmsnorm = _native("moe_add_rmsnorm")
 moe_rope_append = _native("moe_rope_append")
 moe_attention_paged = _native("moe_attention_paged")
+moe_rope_append_q8 = _native("moe_rope_append_q8")
+moe_attention_cache = _native("moe_attention_cache")
+moe_cache_keep = _native("moe_cache_keep")
 
 
 def moe_attention_workspace_bytes(Hq, Hkv, D) -> int:
