@@ -21,6 +21,7 @@
 // token over 131071 53 us, over 2000 9.1.  A cap's polynomial costs batches that the
 // bytes do not fill 1.5 us (48 tokens over 1500 30.1 -> 31.8) and the others nothing.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -116,7 +117,7 @@ __device__ __forceinline__ void store_row(const Params &p, size_t row, int lane,
     __syncwarp();
 }
 
-template <typename T, int D, bool kCap>
+template <typename T, int D, bool kCap, bool kMasks>
 __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __grid_constant__ StreamParams sp) {
     constexpr int kHalves = D / 64;                      // boxes of a row
     constexpr int kBox = kPiece * 128;                   // bytes of a box
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     const bool looks = !sp.join_launch && blockIdx.x == 0 && tid == 0;
     const unsigned long long tags = looks ? p.hdr->cta_calls : 0ull;
     Run run;
-    const bool work = run_begin<kTile>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, run);
+    const bool work = run_begin<kTile, kMasks>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, run);
     if (tags != 0) record_status(p.hdr, MOE_ERR_WORKSPACE, 0);
     if (!work) return;
     fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
@@ -163,22 +164,27 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         int s0, s1;
         if (!run_segment(p, run, s0, s1)) break;
         const Item it = run.item;
-        const int key_first = (it.t0 + s0) * kTile + warp * kPiece;  // this warp's first piece
-        const int last = it.pos0 + it.nt - 1;                       // the last key any row sees
-        int n = s1 - s0;  // pieces of this warp that hold such keys
-        n = max(0, min(n, last >= key_first ? (last - key_first) / kTile + 1 : 0));
+        auto key_of = [&](int i) { return tile_key<kTile, kMasks>(it, s0 + i) + warp * kPiece; };  // this warp's pieces
+        const int last = last_key<kMasks>(p, it);
+        int n = s1 - s0;  // pieces of this warp that hold keys that a row sees
+        if (kMasks) {
+            if (key_of(n - 1) > last) --n;
+        } else {
+            n = max(0, min(n, last >= key_of(0) ? (last - key_of(0)) / kTile + 1 : 0));
+        }
         // the pages of 32 pieces at a time, and of the 32 after them
         auto page_at = [&](int i) {
             if (i >= n) return 0;
             // past the tensor, read as zeros: a piece before every row's window (its page may be
             // gone already) and a bad page
-            const int key = key_first + i * kTile;
-            const int pg = key + kPiece <= it.seen ? -1 : page_of(p.b, it.b, key, p.hdr);
+            const int key = key_of(i);
+            const int pg = key + kPiece <= it.seen && (!kMasks || key >= p.sinks) ? -1 : page_of(p.b, it.b, key, p.hdr);
             return pg < 0 ? p.b.num_pages : pg;
         };
         int pages = page_at(lane), pages_next = n > 32 ? page_at(32 + lane) : 0;
         // this thread's rows: gid, gid + 8 of each 16; their position, -1 for rows past the tile
         int pos[2];
+        Sight sight[2];
         uint32_t qa[D / 16][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -186,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
             const int tok = r / G;
             const bool live = tok < it.nt;
             pos[h] = live ? it.pos0 + tok : -1;
+            if (kMasks) sight[h] = row_sight(p, run.seq, live, it.row0 + tok, it.qt * p.tt + tok);
             const T *row = static_cast<const T *>(p.q) +
                            (size_t(it.row0 + (live ? tok : 0)) * p.b.Hq + it.kh * G + r % G) * D;
 #pragma unroll
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 const uint32_t st = issued % kStages;
                 uint8_t *dst = ring + st * kStage;
                 uint64_t *bar = &full[warp][st];
-                const int row = (key_first + sent * kTile) & (p.b.page - 1);
+                const int row = key_of(sent) & (p.b.page - 1);
                 mbar_arrive_expect_tx(bar, kStage);
 #pragma unroll
                 for (int c = 0; c < kHalves; ++c) tma_box(dst + c * kBox, &sp.mk, c * 64, row, z, bar);
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 ok = false;
                 break;
             }
-            const int key0 = key_first + i * kTile;
+            const int key0 = key_of(i);
             const uint32_t kb = smem_addr(ring + st * kStage), vb = kb + kHalves * kBox;
             float s[2][4];
 #pragma unroll
@@ -250,14 +257,25 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                 mma16816<T>(s[0], qa[k], b[0], b[1]);
                 mma16816<T>(s[1], qa[k], b[2], b[3]);
             }
-            const bool edge = key0 + kPiece - 1 > it.pos0 || (p.window > 0 && key0 <= last - p.window);
+            // keys that some row does not see
+            const int all = kMasks && p.tree != nullptr ? run.seq.len - run.seq.n - 1 : it.pos0;
+            const bool edge = key0 + kPiece - 1 > all || (p.window > 0 && key0 <= last - p.window &&
+                                                         (!kMasks || key0 + kPiece > p.sinks));
+            uint32_t sees[2] = {0u, 0u};
+            if (kMasks && edge) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) sees[h] = sight32(p, run.seq, sight[h], key0) >> (2 * tig);
+                __syncwarp();
+            }
             uint32_t pa[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     s[j][c] = score<kCap>(s[j][c], p);
-                    if (edge) {
+                    if (kMasks && edge) {
+                        if ((sees[c >> 1] >> (8 * j + (c & 1)) & 1u) == 0u) s[j][c] = -CUDART_INF_F;
+                    } else if (edge) {
                         const int key = key0 + 8 * j + 2 * tig + (c & 1), at = pos[c >> 1];
                         if (key > at || (p.window > 0 && at - key >= p.window))
                             s[j][c] = -CUDART_INF_F;
@@ -406,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
                                         reinterpret_cast<float *>(smem), &sm_m[0][0], &sm_l[0][0]);
             }
         }
-        run_next<kTile>(p, run);
+        run_next<kTile, kMasks>(p, run);
         if (run.u < run.end) {
             fence_proxy_async_smem();  // the sums in the rings (generic) before the next copies
             __syncthreads();
@@ -434,10 +452,15 @@ cudaError_t each_stream(F f) {
     cudaError_t e = cudaSuccess;
     auto of = [&](auto type) {
         using T = decltype(type);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, false>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, true>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, false>);
-        if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, true>);
+        auto with = [&](auto masks) {
+            constexpr bool kMasks = decltype(masks)::value;
+            if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, false, kMasks>);
+            if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, true, kMasks>);
+            if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, false, kMasks>);
+            if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, true, kMasks>);
+        };
+        with(std::false_type());
+        with(std::true_type());
     };
     of(__half());
     of(__nv_bfloat16());
@@ -445,11 +468,15 @@ cudaError_t each_stream(F f) {
 }
 
 template <typename T, int D>
-cudaError_t launch_stream(const StreamParams &sp, int grid, cudaStream_t s) {
+cudaError_t launch_stream(const StreamParams &sp, bool masks, int grid, cudaStream_t s) {
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(kStreamSmem), s, sp);
     };
-    return sp.p.cap_in != 0.f ? go(attention_stream_kernel<T, D, true>) : go(attention_stream_kernel<T, D, false>);
+    if (masks)
+        return sp.p.cap_in != 0.f ? go(attention_stream_kernel<T, D, true, true>)
+                                  : go(attention_stream_kernel<T, D, false, true>);
+    return sp.p.cap_in != 0.f ? go(attention_stream_kernel<T, D, true, false>)
+                              : go(attention_stream_kernel<T, D, false, false>);
 }
 
 Params make_params(const AttnArgs &a) {
@@ -464,6 +491,11 @@ Params make_params(const AttnArgs &a) {
     p.cap_y = a.softcap > 0.f ? a.scale / a.softcap : 0.f;
     p.cap_log2 = a.softcap * kLog2e;
     p.window = a.window;
+    p.sinks = a.sinks;
+    p.tree = a.tree;
+    p.words = a.words;
+    p.ks = a.ks;
+    p.vs = a.vs;
     p.hdr = a.hdr;
     p.count = reinterpret_cast<unsigned *>(a.scratch);
     p.desc = reinterpret_cast<JoinDesc *>(a.scratch + kCountBytes);
@@ -495,19 +527,22 @@ cudaError_t init_attention() {
     const cudaError_t e = each_stream([](auto kernel) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
     });
-    return e != cudaSuccess ? e : init_tc();
+    if (e != cudaSuccess) return e;
+    const cudaError_t t = init_tc();
+    return t != cudaSuccess ? t : init_tc_masks();
 }
 
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s) {
     using namespace attn;
     const int G = a.b.Hq / a.b.Hkv;
     const Params base = make_params(a);
+    const bool masks = a.tree != nullptr || a.sinks > 0;
     // More than 16 rows are faster on the tensor cores' own tile, although most of its rows are
     // padding (32 rows over 6000 keys of 32 sequences 75 us, with a second instruction tile here
     // 84; 32 over 900 of one 11.8 and 18.3; 24 over 2000 of eight 18.8 and 24.8); up to 16 this
     // kernel is (16 rows over 2000 keys of eight 16.7 and 18.7; 8 over 12000 and less of 48
     // 57.5 and 58.3; 8 over 93 of one 5.5 and 9.7).
-    if (long(max_new) * G > kMaxRows) return launch_tc(a, base, num_sms, s);
+    if (long(max_new) * G > kMaxRows) return (masks ? launch_tc_masks : launch_tc)(a, base, num_sms, s);
     StreamParams sp = {};
     sp.p = base;
     sp.p.tt = kMaxRows / G;
@@ -527,10 +562,10 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     sp.join_launch = std::min(grid / items, tiles / kLeast) + 1 > kJoinInside;
     cudaError_t e;
     if (a.type == MOE_F16)
-        e = a.b.D == 64 ? launch_stream<__half, 64>(sp, grid, s) : launch_stream<__half, 128>(sp, grid, s);
+        e = a.b.D == 64 ? launch_stream<__half, 64>(sp, masks, grid, s) : launch_stream<__half, 128>(sp, masks, grid, s);
     else
-        e = a.b.D == 64 ? launch_stream<__nv_bfloat16, 64>(sp, grid, s)
-                        : launch_stream<__nv_bfloat16, 128>(sp, grid, s);
+        e = a.b.D == 64 ? launch_stream<__nv_bfloat16, 64>(sp, masks, grid, s)
+                        : launch_stream<__nv_bfloat16, 128>(sp, masks, grid, s);
     if (e != cudaSuccess || !sp.join_launch) return e;
     return launch_join(sp.p, a.type, grid, kPartRows, kPartRows, sp.p.tt, s);
 }

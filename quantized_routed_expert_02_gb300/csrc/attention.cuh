@@ -49,6 +49,10 @@ struct Params {
     float cap_y;        // scale / cap
     float cap_log2;     // softcap * log2(e)
     int window;
+    int sinks;            // first tokens that the window leaves visible (0: no window)
+    const uint32_t *tree; // [N, words] or null
+    int words;
+    const float *ks, *vs; // the scales of 8-bit codes
     int tt;             // tokens of a query tile
     unsigned tt_magic;  // ceil(2^32 / tt), tt > 1: n / tt as a high product (n < 2^23)
     int extra;          // fixed cost of an item, in key tiles
@@ -111,25 +115,43 @@ struct Item {
     int nt;      // tokens in it
     int pos0;    // cache index of the first
     int len;     // cached tokens
-    int seen;    // first key that a row sees
-    int t0;      // first key tile
+    int seen;    // first key that a row sees, but the sinks
+    int t0;      // its key tile
+    int ts;      // tiles of sinks ahead of it (kMasks)
     int tiles;   // key tiles, at least 1 (a tile whose rows see nothing has one, all masked)
 };
+
+// The first key of an item's i-th tile: the sinks' tiles, then those from t0 on.
+template <int KT, bool kMasks>
+__device__ __forceinline__ int tile_key(const Item &it, int i) {
+    return (kMasks && i < it.ts ? i : it.t0 - (kMasks ? it.ts : 0) + i) * KT;
+}
+// The last key that any row of the item sees.
+template <bool kMasks>
+__device__ __forceinline__ int last_key(const Params &p, const Item &it) {
+    return kMasks && p.tree != nullptr ? it.len - 1 : it.pos0 + it.nt - 1;
+}
 
 // Query tiles of a sequence with n new rows.
 __device__ __forceinline__ int query_tiles(const Params &p, int n) {
     return p.tt == 1 ? n : int(__umulhi(unsigned(n + p.tt - 1), p.tt_magic));
 }
 
-template <int KT>
-__device__ __forceinline__ void item_tiles(int window, int tt, const SeqView &s, int qt, int &nt,
-                                           int &pos0, int &seen, int &t0, int &tiles) {
-    nt = min(tt, s.n - qt * tt);
-    pos0 = s.len - s.n + qt * tt;
-    const int last = pos0 + nt - 1;
-    seen = window > 0 && pos0 >= window ? pos0 - window + 1 : 0;
+template <int KT, bool kMasks>
+__device__ __forceinline__ void item_tiles(const Params &p, const SeqView &s, int qt, int &nt, int &pos0, int &seen,
+                                           int &t0, int &ts, int &tiles) {
+    nt = min(p.tt, s.n - qt * p.tt);
+    pos0 = s.len - s.n + qt * p.tt;
+    int last = pos0 + nt - 1, from = pos0;  // the window of the first token begins first
+    if (kMasks && p.tree != nullptr) {
+        // the nodes of a tree stand at the older tokens' end or beyond, and may see any of one another
+        from = s.len - s.n;
+        last = s.len - 1;
+    }
+    seen = p.window > 0 && from >= p.window ? from - p.window + 1 : 0;
     t0 = seen / KT;
-    tiles = last >= seen ? last / KT + 1 - t0 : 1;
+    ts = kMasks ? min(t0, p.sinks / KT + (p.sinks % KT != 0)) : 0;
+    tiles = last >= seen ? last / KT + 1 - t0 + ts : 1;
 }
 
 // The CTA's run: positions [u, end) of the whole work; u is inside `item`,
@@ -144,10 +166,10 @@ struct Run {
 
 // The work of a sequence: its query tiles' key tiles and fixed costs, of one
 // key/value head.
-template <int KT>
+template <int KT, bool kMasks>
 __device__ __forceinline__ long tile_cost(const Params &p, const SeqView &s, int qt) {
-    int nt, pos0, seen, t0, tiles;
-    item_tiles<KT>(p.window, p.tt, s, qt, nt, pos0, seen, t0, tiles);
+    int nt, pos0, seen, t0, ts, tiles;
+    item_tiles<KT, kMasks>(p, s, qt, nt, pos0, seen, t0, ts, tiles);
     return tiles + p.extra;
 }
 
@@ -166,7 +188,7 @@ struct Items {
 // lengths are read again for the item that is found: should the caller change them
 // under the call (a missing stream order) they need not fit the costs any more, so
 // what is derived from both, here and in join_desc, is bounded by the buffers.
-template <int KT>
+template <int KT, bool kMasks>
 __device__ inline void run_find(const Params &p, int least, int split, const long *scratch, const Items *items,
                                 Run &r) {
     const int lane = threadIdx.x & 31, B = p.b.B, Hkv = p.b.Hkv;
@@ -229,13 +251,13 @@ __device__ inline void run_find(const Params &p, int least, int split, const lon
     r.seq = seq_view(p.b, it.b, p.hdr, false);
     const int nq = query_tiles(p, r.seq.n);
     if (nq > 1)
-        locate(nq, at, [&](int qt) { return (r.pad != 0 ? long(r.pad) : tile_cost<KT>(p, r.seq, qt)) * Hkv; }, it.qt,
+        locate(nq, at, [&](int qt) { return (r.pad != 0 ? long(r.pad) : tile_cost<KT, kMasks>(p, r.seq, qt)) * Hkv; }, it.qt,
                first);
     else
         first = at;
     it.len = r.seq.len;
     it.row0 = r.seq.first + it.qt * p.tt;
-    item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.seen, it.t0, it.tiles);
+    item_tiles<KT, kMasks>(p, r.seq, it.qt, it.nt, it.pos0, it.seen, it.t0, it.ts, it.tiles);
     const long each = r.pad != 0 ? r.pad : it.tiles + p.extra;
     // the head, of few: a quotient in fp32, put right
     const long in = r.u - first;
@@ -251,7 +273,7 @@ __device__ inline void run_find(const Params &p, int least, int split, const lon
 // than an even share and `split`, the time (in key tiles) of leaving parts and
 // joining them.  False: nothing to do.  A thread per sequence where its tiles are
 // few (decode), a warp where they are many, then one warp sums and searches.
-template <int KT>
+template <int KT, bool kMasks>
 __device__ inline bool run_begin(const Params &p, int least, int split, long *scratch, Run *out, Run &run) {
     constexpr int kFew = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -266,7 +288,7 @@ __device__ inline bool run_begin(const Params &p, int least, int split, long *sc
             nq = query_tiles(p, s.n);
             if (nq <= kFew) {
                 for (int qt = 0; qt < nq; ++qt) {
-                    const long c = tile_cost<KT>(p, s, qt);
+                    const long c = tile_cost<KT, kMasks>(p, s, qt);
                     total += c;
                     top = max(top, c);
                 }
@@ -281,7 +303,7 @@ __device__ inline bool run_begin(const Params &p, int least, int split, long *sc
             total = 0;
             unsigned most = 0;
             for (int qt = lane; qt < nqs; qt += 32) {
-                const long c = tile_cost<KT>(p, s, qt);
+                const long c = tile_cost<KT, kMasks>(p, s, qt);
                 total += c;
                 most = max(most, unsigned(c));
             }
@@ -302,7 +324,7 @@ __device__ inline bool run_begin(const Params &p, int least, int split, long *sc
         // single lanes have just worked, here and in the kernels.
         __syncwarp();
         Run r;
-        run_find<KT>(p, least, split, scratch, items, r);
+        run_find<KT, kMasks>(p, least, split, scratch, items, r);
         if (lane == 0) *out = r;
     }
     __syncthreads();
@@ -320,7 +342,7 @@ __device__ __forceinline__ bool run_segment(const Params &p, const Run &r, int &
 }
 
 // On to the item after r.item, if the run reaches it.
-template <int KT>
+template <int KT, bool kMasks>
 __device__ inline void run_next(const Params &p, Run &r) {
     Item &it = r.item;
     r.u = r.item_u = r.item_u + (r.pad != 0 ? r.pad : p.extra + it.tiles);
@@ -334,7 +356,56 @@ __device__ inline void run_next(const Params &p, Run &r) {
     }
     it.len = r.seq.len;
     it.row0 = r.seq.first + it.qt * p.tt;
-    item_tiles<KT>(p.window, p.tt, r.seq, it.qt, it.nt, it.pos0, it.seen, it.t0, it.tiles);
+    item_tiles<KT, kMasks>(p, r.seq, it.qt, it.nt, it.pos0, it.seen, it.t0, it.ts, it.tiles);
+}
+
+// What a row sees (kMasks): the keys below `ctx` that are at `lo` or beyond or among the
+// sinks, and of a tree's new tokens (from key `base` on, `nbits` of them) those of its bits.
+struct Sight {
+    int ctx, lo;
+    const uint32_t *bits;
+};
+// Of row `row` of the batch, which is token `tok` of its sequence's n new ones; dead rows see nothing.
+__device__ inline Sight row_sight(const Params &p, const SeqView &s, bool live, int row, int tok) {
+    Sight v;
+    const int base = s.len - s.n;
+    int at = base + tok;
+    v.bits = nullptr;
+    if (!live || at < 0) {
+        v.ctx = v.lo = 0;
+        return v;
+    }
+    v.ctx = at + 1;
+    if (p.tree != nullptr) {
+        v.bits = p.tree + size_t(row) * p.words;
+        v.ctx = base;
+        if (p.window > 0) {  // the window counts from the node's place: behind its ancestors
+            int m = 0, left = s.n;
+            for (int i = 0; i < p.words && left > 0; ++i, left -= 32)
+                m += __popc(v.bits[i] & (left < 32 ? (1u << left) - 1 : 0xffffffffu));
+            at = base + max(m, 1) - 1;
+        }
+    }
+    v.lo = p.window > 0 ? max(0, at - p.window + 1) : 0;
+    return v;
+}
+// Bits 0 .. x - 1.
+__device__ __forceinline__ uint32_t bits_below(int x) {
+    return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1;
+}
+// The row's sight of the 32 keys from key0 on.
+__device__ __forceinline__ uint32_t sight32(const Params &p, const SeqView &s, const Sight &v, int key0) {
+    uint32_t m = bits_below(v.ctx - key0);
+    if (p.window > 0) m &= ~bits_below(v.lo - key0) | bits_below(p.sinks - key0);
+    if (v.bits != nullptr) {
+        const int o = key0 - (s.len - s.n), n = min(s.n, 32 * p.words);  // the keys are new tokens o ..
+        if (o > -32 && o < n) {
+            const int w = o >> 5;
+            const uint32_t a = w >= 0 ? v.bits[w] : 0u, b = w + 1 < p.words ? v.bits[w + 1] : 0u;
+            m |= __funnelshift_r(a, b, o & 31) & bits_below(n - o);
+        }
+    }
+    return m;
 }
 
 // A partial result: `rows` (a multiple of 32) rows of D sums, then their maxima,
@@ -497,10 +568,12 @@ __device__ inline void join_rows(const Params &p, const JoinDesc &d, int first_c
 // The second launch: joins the items that start in each CTA's run.
 cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int half, int tth, cudaStream_t s);
 
-// The tensor-core kernel (many rows per key/value head).
+// The tensor-core kernel (many rows per key/value head), and its form with masks (kMasks).
 size_t tc_part_bytes(int D);
 cudaError_t init_tc();
 cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s);
+cudaError_t init_tc_masks();
+cudaError_t launch_tc_masks(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace moeq4k

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(32 * kPlainWarps) attention_plain_kernel(const
 
 cudaError_t launch_attention_cache(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s) {
     using namespace attn;
-    if (a.ks == nullptr && a.tree == nullptr && (a.window == 0 || a.sinks == 0))
+    if (a.ks == nullptr)
         return launch_attention(a, max_new, num_sms, s);
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(a.b.N, a.b.Hq), dim3(32 * kPlainWarps), size_t(0), s, a);
