@@ -25,64 +25,19 @@
 
 #include <cuda.h>
 
-#include "attention.cuh"
+#include "attention_stream.cuh"
 
 namespace moeq4k {
 namespace attn {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kPiece = 16;                // keys of a piece
 constexpr int kTile = kWarps * kPiece;    // keys of a tile: a piece for every warp
-constexpr int kRing = 24 * 1024;          // bytes of a warp's ring: two CTAs' fill an SM
-constexpr int kMaxRows = 16;              // of the instruction
-// The least work of a CTA, in key tiles (1, 3, 5, 8: one token over 2000 9.1, 11.1, 12.7,
-// 15.2 us), and an item's fixed cost (2, 3, 4: 48 tokens over 1500 34.0, 33.1, 34.1 us).
-constexpr int kLeast = 1;
-constexpr int kExtra = 3;
-// What parting items costs, in key tiles: of one sequence, 300 tokens take 8.2 us whole
-// and 8.9 in parts, 400 9.6 and 8.8; of 64 sequences, 300 10.0 and 14.9, 1000 27 and 31.
-constexpr int kSplit = 9;
-constexpr int kPartRows = 32;             // rows of a partial result (a multiple of 32)
 
 struct StreamParams {
     CUtensorMap mk, mv;
     Params p;
     bool join_launch;  // split items are joined by a second launch
 };
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t a) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(a)
-                 : "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1);
-template <>
-__device__ __forceinline__ void mma16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                                 uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4],
-                                                        uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 // Box of 64 channels x 16 cache rows of page-head z; out-of-range z reads as zeros.
 __device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int ch, int row, int z,
@@ -94,29 +49,6 @@ __device__ __forceinline__ void tma_box(void *dst, const CUtensorMap *map, int c
         : "memory");
 }
 
-__device__ __forceinline__ void put_vec(float *p, const float (&v)[4]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void put_vec(float *p, const float (&v)[2]) {
-    *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
-}
-// A finished row: sums v (this lane's kPer channels) over the weights' sum; a
-// row that saw nothing is 0, its logarithm -inf.
-template <typename T, int kPer>
-__device__ __forceinline__ void store_row(const Params &p, size_t row, int lane, float top, float sum,
-                                          const float (&v)[kPer]) {
-    const float inv = over_sum(sum);
-    uint32_t w[kPer / 2];
-#pragma unroll
-    for (int c = 0; c < kPer / 2; ++c) w[c] = Pair<T>::make(v[2 * c] * inv, v[2 * c + 1] * inv);
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + (row * 32 + lane) * kPer);
-    if (kPer == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[kPer / 2 - 1]);
-    else dst[0] = w[0];
-    if (p.lse != nullptr && lane == 0)
-        p.lse[row] = log_sum(top, sum);
-    __syncwarp();
-}
-
 template <typename T, int D, bool kCap, bool kMasks>
 __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __grid_constant__ StreamParams sp) {
     constexpr int kHalves = D / 64;                      // boxes of a row
@@ -124,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
     constexpr int kStage = 2 * kHalves * kBox;           // K and V of a piece
     constexpr int kStages = kRing / kStage;
     constexpr int kRows = kMaxRows;
-    constexpr int kOS = D + 8;                           // floats of a row of the warps' meeting buffer
+    constexpr int kOS = row_floats(D);
     static_assert(kRows * kOS * 4 <= kRing, "a warp's sums fit its ring");
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[kWarps][kStages];
@@ -373,57 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_stream_kernel(const __g
         __syncthreads();
         __syncwarp();
         if (failed != 0) return;
-        const bool whole = s0 == 0 && s1 == it.tiles;
-        const int rows = it.nt * G;
-        constexpr int kPer = D / 32;  // channels a lane joins
-        float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(kPartRows, D);
-        for (int r = warp; r < rows; r += kWarps) {
-            float top = sm_m[0][r];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm_m[w][r]);
-            const float base = top == -CUDART_INF_F ? 0.f : top;
-            float sum = 0.f, v[kPer];
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) v[c] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2_approx(sm_m[w][r] - base);
-                sum = fmaf(sm_l[w][r], f, sum);
-                const float *src = reinterpret_cast<const float *>(smem + w * kRing) + r * kOS + lane * kPer;
-#pragma unroll
-                for (int c = 0; c < kPer; ++c) v[c] = fmaf(src[c], f, v[c]);
-            }
-            if (whole) {
-                store_row<T, kPer>(p, size_t(it.row0 + r / G) * p.b.Hq + it.kh * G + r % G, lane, top, sum, v);
-            } else {
-                put_vec(mine + part_at(r, lane * kPer, D), v);
-                if (lane == 0) {
-                    mine[kPartRows * D + r] = top;
-                    mine[kPartRows * (D + 1) + r] = sum;
-                }
-                __syncwarp();
-            }
-        }
-        if (sp.join_launch) {
-            if (tid == 0 && s0 == 0 && !whole) p.desc[blockIdx.x] = join_desc(p, run);
-        } else if (!whole) {
-            // the CTA that arrives last joins the parts (all are stored and seen then)
-            const int first_cta = int(div_pos(run.item_u + p.extra, run.per));
-            const JoinDesc d = join_desc(p, run);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                joins = atomicAdd(p.count + first_cta, 1u) + 1 == unsigned(d.parts);
-                if (joins) p.count[first_cta] = 0u;  // for the next call
-            }
-            __syncthreads();
-            __syncwarp();
-            if (joins) {
-                __threadfence();
-                join_rows<T, D, kWarps>(p, d, first_cta, kPartRows, kPartRows, p.tt, 0, 1,
-                                        reinterpret_cast<float *>(smem), &sm_m[0][0], &sm_l[0][0]);
-            }
-        }
+        segment_result<T, D>(p, run, s0, s1, smem, sm_m, sm_l, sp.join_launch, joins);
         run_next<kTile, kMasks>(p, run);
         if (run.u < run.end) {
             fence_proxy_async_smem();  // the sums in the rings (generic) before the next copies
@@ -529,7 +411,9 @@ cudaError_t init_attention() {
     });
     if (e != cudaSuccess) return e;
     const cudaError_t t = init_tc();
-    return t != cudaSuccess ? t : init_tc_masks();
+    if (t != cudaSuccess) return t;
+    const cudaError_t m = init_tc_masks();
+    return m != cudaSuccess ? m : init_stream_codes();
 }
 
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s) {
@@ -551,15 +435,7 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     if (!encode_pages_map(&sp.mk, a.k, a.b, a.type, kPiece) || !encode_pages_map(&sp.mv, a.v, a.b, a.type, kPiece))
         return cudaErrorInvalidValue;
     const int grid = std::min(2 * num_sms, kMaxCtas);
-    // Few items over many CTAs make many parts of each.  Up to kJoinInside of them the last
-    // CTA joins them on its way out (one token over 93: 9.6 us with the launch, 5.9 without);
-    // more take it longer than a second launch that spreads them over the GPU (one token
-    // over 600, 10 parts and more: 8.8 us with the launch, 9.4 without; over 131071, 76
-    // parts: 52 and 56).
-    constexpr long kJoinInside = 10;
-    const long items = long(a.b.B) * a.b.Hkv;
-    const long tiles = (long(a.b.max_pages) * a.b.page + kTile - 1) / kTile + kExtra;  // of an item, at most
-    sp.join_launch = std::min(grid / items, tiles / kLeast) + 1 > kJoinInside;
+    sp.join_launch = joins_by_launch(a.b, grid, kTile);
     cudaError_t e;
     if (a.type == MOE_F16)
         e = a.b.D == 64 ? launch_stream<__half, 64>(sp, masks, grid, s) : launch_stream<__half, 128>(sp, masks, grid, s);

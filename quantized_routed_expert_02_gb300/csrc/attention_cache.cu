@@ -1,7 +1,7 @@
 // Attention over a cache of 16-bit values or of 8-bit codes, with sinks and trees
 // (moe_attention_cache), in its plainest form: a CTA per row and query head, a warp
 // per key, the softmax's running maximum and sum in fp32.
-#include "attention.cuh"
+#include "attention_stream.cuh"
 
 namespace moeq4k {
 namespace attn {
@@ -93,6 +93,7 @@ cudaError_t launch_attention_cache(const AttnArgs &a, int max_new, int num_sms, 
     using namespace attn;
     if (a.ks == nullptr)
         return launch_attention(a, max_new, num_sms, s);
+    if (long(max_new) * (a.b.Hq / a.b.Hkv) <= kMaxRows) return launch_stream_codes(a, make_params(a), num_sms, s);
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(a.b.N, a.b.Hq), dim3(32 * kPlainWarps), size_t(0), s, a);
     };
