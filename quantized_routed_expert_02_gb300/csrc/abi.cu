@@ -13,7 +13,7 @@ using namespace moeq4k;
 namespace {
 
 struct DevInfo {
-    bool ready = false, attention = false;
+    bool ready = false, attention[3] = {};
     int sms = 0;
     int id = 0;
 };
@@ -53,13 +53,13 @@ moe_status moeq4k::device_info(int *sms, int *dev_out) {
 
 // The same with the attention kernels': they load with their attributes (1.4 ms and
 // 2 MiB of device memory), which calls of the experts need not pay for.
-moe_status moeq4k::attention_info(int *sms) {
+moe_status moeq4k::attention_info(int *sms, int form) {
     int dev = 0;
     MOE_TRY(device_info(sms, &dev));
     std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_dev[dev].attention) {
-        if (init_attention() != cudaSuccess) return MOE_ERR_CUDA;
-        g_dev[dev].attention = true;
+    if (!g_dev[dev].attention[form]) {
+        if (init_attention(form) != cudaSuccess) return MOE_ERR_CUDA;
+        g_dev[dev].attention[form] = true;
     }
     return MOE_OK;
 }

@@ -72,9 +72,8 @@ moe_status rope_append(RopeArgs &a, void *ws, size_t ws_bytes, void *stream) {
     return cuda_status(launch_rope_append(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
-// What both attention calls check, and the launch of one of them.
-moe_status attention(AttnArgs &a, int max_new, void *ws, size_t ws_bytes, void *stream,
-                     cudaError_t (*launch)(const AttnArgs &, int, int, cudaStream_t)) {
+// What both attention calls check, and their launch.
+moe_status attention(AttnArgs &a, int max_new, void *ws, size_t ws_bytes, void *stream) {
     MOE_TRY(check_batch(a.b, a.type));
     if (max_new < 1 || a.window < 0 || !finite_f(a.scale) || !(a.softcap >= 0.f) || !finite_f(a.softcap))
         return MOE_ERR_INVALID_SHAPE;
@@ -86,12 +85,12 @@ moe_status attention(AttnArgs &a, int max_new, void *ws, size_t ws_bytes, void *
     if (ws_bytes < moe_attention_workspace_bytes(a.b.Hq, a.b.Hkv, a.b.D)) return MOE_ERR_WORKSPACE;
     if (stream == MOE_CHECK_ONLY) return MOE_OK;
     int sms = 0;
-    MOE_TRY(attention_info(&sms));
+    MOE_TRY(attention_info(&sms, attention_form(a)));
     a.hdr = static_cast<WsHeader *>(ws);
     a.scratch = static_cast<uint8_t *>(ws) + sizeof(WsHeader);
     a.wait_ns = device_wait_ns();
     a.withhold = device_withhold();
-    return cuda_status(launch(a, max_new, sms, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_attention(a, max_new, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -175,7 +174,7 @@ moe_status moe_attention_paged(const void *q, const void *k_pages, const void *v
     a.q = q, a.k = k_pages, a.v = v_pages, a.out = out, a.lse = lse;
     a.b = {page_table, q_offs, kv_lens, N, B, max_pages, num_pages, page, Hq, Hkv, D};
     a.scale = scale, a.softcap = softcap, a.window = window, a.type = dtype;
-    return attention(a, max_new, ws, ws_bytes, stream, launch_attention);
+    return attention(a, max_new, ws, ws_bytes, stream);
 }
 
 moe_status moe_attention_cache(const void *q, const void *k_pages, const void *v_pages,
@@ -198,7 +197,7 @@ moe_status moe_attention_cache(const void *q, const void *k_pages, const void *v
     a.scale = scale, a.softcap = softcap, a.window = window, a.type = dtype;
     a.sinks = window > 0 ? sinks : 0;
     a.tree = reinterpret_cast<const uint32_t *>(tree), a.words = tree_words;
-    return attention(a, max_new, ws, ws_bytes, stream, launch_attention_cache);
+    return attention(a, max_new, ws, ws_bytes, stream);
 }
 
 moe_status moe_cache_keep(void *k_pages, void *v_pages, float *k_scales, float *v_scales,

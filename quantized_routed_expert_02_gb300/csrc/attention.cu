@@ -328,21 +328,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) attention_join_kernel(cons
 
 constexpr int kStreamSmem = kWarps * kRing;
 
-// f on every form of the kernel, until one fails.
-template <typename F>
-cudaError_t each_stream(F f) {
+template <bool kMasks>
+cudaError_t init_stream() {
     cudaError_t e = cudaSuccess;
+    auto set = [&](auto kernel) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
+    };
     auto of = [&](auto type) {
         using T = decltype(type);
-        auto with = [&](auto masks) {
-            constexpr bool kMasks = decltype(masks)::value;
-            if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, false, kMasks>);
-            if (e == cudaSuccess) e = f(attention_stream_kernel<T, 64, true, kMasks>);
-            if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, false, kMasks>);
-            if (e == cudaSuccess) e = f(attention_stream_kernel<T, 128, true, kMasks>);
-        };
-        with(std::false_type());
-        with(std::true_type());
+        set(attention_stream_kernel<T, 64, false, kMasks>);
+        set(attention_stream_kernel<T, 64, true, kMasks>);
+        set(attention_stream_kernel<T, 128, false, kMasks>);
+        set(attention_stream_kernel<T, 128, true, kMasks>);
     };
     of(__half());
     of(__nv_bfloat16());
@@ -404,29 +402,28 @@ size_t attention_part_bytes(int D) {
            std::max(size_t(2) * kMaxCtas * part_floats(kPartRows, D) * sizeof(float), tc_part_bytes(D));
 }
 
-cudaError_t init_attention() {
+int attention_form(const AttnArgs &a) { return a.ks != nullptr ? 2 : a.tree != nullptr || a.sinks > 0 ? 1 : 0; }
+
+cudaError_t init_attention(int form) {
     using namespace attn;
-    const cudaError_t e = each_stream([](auto kernel) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamSmem);
-    });
+    const cudaError_t e = form == 0 ? init_stream<false>() : form == 1 ? init_stream<true>() : init_stream_codes();
     if (e != cudaSuccess) return e;
-    const cudaError_t t = init_tc();
-    if (t != cudaSuccess) return t;
-    const cudaError_t m = init_tc_masks();
-    return m != cudaSuccess ? m : init_stream_codes();
+    return form == 0 ? init_tc() : form == 1 ? init_tc_masks() : init_tc_codes();
 }
 
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s) {
     using namespace attn;
     const int G = a.b.Hq / a.b.Hkv;
     const Params base = make_params(a);
-    const bool masks = a.tree != nullptr || a.sinks > 0;
+    const int form = attention_form(a);
     // More than 16 rows are faster on the tensor cores' own tile, although most of its rows are
     // padding (32 rows over 6000 keys of 32 sequences 75 us, with a second instruction tile here
     // 84; 32 over 900 of one 11.8 and 18.3; 24 over 2000 of eight 18.8 and 24.8); up to 16 this
     // kernel is (16 rows over 2000 keys of eight 16.7 and 18.7; 8 over 12000 and less of 48
     // 57.5 and 58.3; 8 over 93 of one 5.5 and 9.7).
-    if (long(max_new) * G > kMaxRows) return (masks ? launch_tc_masks : launch_tc)(a, base, num_sms, s);
+    if (long(max_new) * G > kMaxRows)
+        return (form == 0 ? launch_tc : form == 1 ? launch_tc_masks : launch_tc_codes)(a, base, num_sms, s);
+    if (form == 2) return launch_stream_codes(a, base, num_sms, s);
     StreamParams sp = {};
     sp.p = base;
     sp.p.tt = kMaxRows / G;
@@ -438,10 +435,10 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     sp.join_launch = joins_by_launch(a.b, grid, kTile);
     cudaError_t e;
     if (a.type == MOE_F16)
-        e = a.b.D == 64 ? launch_stream<__half, 64>(sp, masks, grid, s) : launch_stream<__half, 128>(sp, masks, grid, s);
+        e = a.b.D == 64 ? launch_stream<__half, 64>(sp, form == 1, grid, s) : launch_stream<__half, 128>(sp, form == 1, grid, s);
     else
-        e = a.b.D == 64 ? launch_stream<__nv_bfloat16, 64>(sp, masks, grid, s)
-                        : launch_stream<__nv_bfloat16, 128>(sp, masks, grid, s);
+        e = a.b.D == 64 ? launch_stream<__nv_bfloat16, 64>(sp, form == 1, grid, s)
+                        : launch_stream<__nv_bfloat16, 128>(sp, form == 1, grid, s);
     if (e != cudaSuccess || !sp.join_launch) return e;
     return launch_join(sp.p, a.type, grid, kPartRows, kPartRows, sp.p.tt, s);
 }

@@ -568,12 +568,15 @@ __device__ inline void join_rows(const Params &p, const JoinDesc &d, int first_c
 // The second launch: joins the items that start in each CTA's run.
 cudaError_t launch_join(const Params &p, moe_dtype type, int grid, int rows, int half, int tth, cudaStream_t s);
 
-// The tensor-core kernel (many rows per key/value head), and its form with masks (kMasks).
+// The tensor-core kernel (many rows per key/value head), its form with masks (kMasks) and
+// the one over codes (with masks).
 size_t tc_part_bytes(int D);
 cudaError_t init_tc();
 cudaError_t launch_tc(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s);
 cudaError_t init_tc_masks();
 cudaError_t launch_tc_masks(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s);
+cudaError_t init_tc_codes();
+cudaError_t launch_tc_codes(const AttnArgs &a, const Params &p, int num_sms, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace moeq4k

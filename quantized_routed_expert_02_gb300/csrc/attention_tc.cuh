@@ -32,6 +32,7 @@
 #include <cuda.h>
 
 #include "attention.cuh"
+#include "codes.cuh"
 #include "f32x2.cuh"
 #include "tcgen05.cuh"
 
@@ -45,6 +46,9 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kCopyWarps = 2;               // K tiles, V tiles
 constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kCopyWarps);
+// Over 8-bit codes: one warp idle, so that four more make a warpgroup of their own.
+constexpr int kConvertWarp = kCopyWarp + kCopyWarps + 1, kConvertWarps = 4;
+constexpr int kCodesThreads = 32 * (kConvertWarp + kConvertWarps);
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 // The least work of a CTA, and an item's fixed cost, in key tiles (a cost of 1, 2, 3:
 // a prompt of 4096 139, 117, 118 us, four of 1024 64, 52.5, 55 us).
@@ -58,6 +62,11 @@ constexpr float kGrowth = 8.f;             // log2 growth of the maximum that fo
 constexpr float kTanhOne = 30.f;           // 2^-30 from 1 is 1 in fp32
 constexpr float kTanhMinusOne = -64.f;     // 1 + 2^-64 is 1, and the tangent -1
 
+// What a kernel is built for: chains in a window (moe_attention_paged), trees and sinks, or
+// both over 8-bit codes.
+enum Form { kPaged, kMasked, kCodes };
+constexpr int form_threads(int form) { return form == kCodes ? kCodesThreads : kThreads; }
+
 struct TcParams {
     CUtensorMap mq, mk, mv;
     Params p;          // p.tt: tokens of an item (both halves)
@@ -66,14 +75,20 @@ struct TcParams {
     uint32_t idesc_qk, idesc_pv;
 };
 
-template <int D>
+template <int D, int kForm>
 struct Cfg {
     static constexpr int kCh = D / 64;                 // 64-channel slabs of a row
     static constexpr int kSlab = 128 * 128;            // bytes of a 128-row slab
     static constexpr int kTileB = kCh * kSlab;         // a tile of K, of V, or of a half's Q
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStages = D == 128 ? 4 : kForm == kCodes ? 6 : 8;
+    // Where a tile's codes land: in its own second slab, whose every row they are spread from in
+    // place, or behind it, where there is only one.
+    static constexpr int kCodesAt = D == 128 ? kSlab : kTileB;
+    static constexpr int kStageB = kTileB + (kForm == kCodes && D == 64 ? kKeys * D : 0);
     static constexpr int kStageOut = 32 * 64;          // a softmax warp's 32 rows x 32 channels on their way out
-    static constexpr int kSmem = kStages * kTileB + 2 * kTileB + kSoftmaxWarps * kStageOut;
+    static constexpr int kOutAt = kStages * kStageB + 2 * kTileB;
+    static constexpr int kScalesAt = kOutAt + kSoftmaxWarps * kStageOut;  // of a V stage's tile: K's and V's
+    static constexpr int kSmem = kScalesAt + (kForm == kCodes ? kStages / 2 * 2 * kKeys * 4 : 0);
 };
 
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
@@ -200,6 +215,91 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
+// Four values times four scales (16-byte aligned).
+__device__ __forceinline__ void scaled(const float *v, const float *scales, float *r) {
+    const float4 f = *reinterpret_cast<const float4 *>(scales);
+    unpack2(mul2(pack2(v[0], v[1]), pack2(f.x, f.y)), r[0], r[1]);
+    unpack2(mul2(pack2(v[2], v[3]), pack2(f.z, f.w)), r[2], r[3]);
+}
+
+// The converting warps of the form over codes: every tile of the ring, once its codes have
+// landed, is spread to the 16-bit tile that the products read (8-row groups of 1024 bytes,
+// 128 a row, swizzled), and the scales of its keys go beside the V tiles.  A thread has 16
+// codes of a row at a time: the two chunks that they become are stored in an order that
+// keeps the eight lanes of a row on different banks.
+template <typename T, int D>
+__device__ __forceinline__ void convert_tiles(const Params &p, Run run, int box_rows, uint8_t *smem, float *scales,
+                                              uint64_t *full, uint64_t *conv) {
+    using C = Cfg<D, kCodes>;
+    constexpr int kLanes = D / 16, kRowsAtOnce = 32 / kLanes, kSteps = 32 / kRowsAtOnce;  // of a row; of a warp
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp, key_in = 32 * warp + lane;
+    const int c = lane % kLanes, slab = c >> 2, odd = (c ^ (c >> 2)) & 1;
+    uint32_t g = 0;
+    bool ok = true;
+    while (ok && run.u < run.end) {
+        int s0, s1;
+        if (!run_segment(p, run, s0, s1)) break;
+        const Item it = run.item;
+        const int n = s1 - s0;
+        // where this thread's key of tile j has its scales, or -1: past the end, between the sinks and
+        // every row's window (its page may be gone already) or a bad page
+        auto place = [&](int j) {
+            const int key = tile_key<kKeys, true>(it, s0 + j) + key_in, box = key & ~(box_rows - 1);
+            if (j >= n || key >= it.len || (box + box_rows <= it.seen && box >= p.sinks)) return -1l;
+            const int pg = page_of(p.b, it.b, key, p.hdr);
+            return pg < 0 ? -1l : (long(pg) * p.b.Hkv + it.kh) * p.b.page + key % p.b.page;
+        };
+        long at = place(0), next = place(1);
+        float k_scale = at < 0 ? 1.f : p.ks[at], v_scale = at < 0 ? 0.f : p.vs[at];
+        for (int j = 0; ok && j < n; ++j) {
+            for (int kv = 0; kv < 2; ++kv, ++g) {
+                const uint32_t st = g % C::kStages;
+                if (!(ok = warp_wait(&full[st], (g / C::kStages) & 1u, p, 67))) break;
+                uint8_t *tile = smem + st * C::kStageB;
+                if (kv == 1) {
+                    // above 0: a key's hidden score is an infinity, which a scale of 0 would make a NaN (the
+                    // codes of a scale of 0 are 0 themselves)
+                    float *to = scales + (st >> 1) * (2 * kKeys) + key_in;
+                    to[0] = k_scale <= 1.17549435e-38f ? 1.17549435e-38f : k_scale;
+                    to[kKeys] = v_scale;
+                    at = next;
+                    k_scale = at < 0 ? 1.f : p.ks[at];
+                    v_scale = at < 0 ? 0.f : p.vs[at];
+                    next = place(j + 2);
+                }
+#pragma unroll
+                for (int i0 = 0; i0 < kSteps; i0 += 4) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 32 * warp + (i0 + i) * kRowsAtOnce + lane / kLanes;
+                        x[i] = *reinterpret_cast<const uint4 *>(tile + C::kCodesAt + r * D + 16 * c);
+                    }
+                    __syncwarp();  // D = 128: what is stored lies over these rows' codes
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 32 * warp + (i0 + i) * kRowsAtOnce + lane / kLanes;
+                        const CodePair<T> a(x[i].x), b(x[i].y), d(x[i].z), e(x[i].w);
+                        const uint4 lo = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(),
+                                                    b.template take<0, 1>(), b.template take<2, 3>());
+                        const uint4 hi = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(),
+                                                    e.template take<0, 1>(), e.template take<2, 3>());
+                        uint8_t *row = tile + slab * C::kSlab + r * 128;
+                        const int first = 2 * (c & 3) + odd;
+                        *reinterpret_cast<uint4 *>(row + ((first ^ (r & 7)) << 4)) = odd != 0 ? hi : lo;
+                        *reinterpret_cast<uint4 *>(row + ((first ^ 1 ^ (r & 7)) << 4)) = odd != 0 ? lo : hi;
+                    }
+                }
+                fence_proxy_async_smem();  // these stores before the products' reads of them
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&conv[st]);
+                __syncwarp();
+            }
+        }
+        run_next<kKeys, true>(p, run);
+    }
+}
+
 // How a score follows from q.k: by a positive scale, capped after a positive
 // scale, or in any other way (negative and zero scales, caps past kCapNear).
 enum Mode { kScaled, kCapped, kAny };
@@ -210,28 +310,28 @@ enum Mode { kScaled, kCapped, kAny };
 // keys: 448 us, by kAny 550; 939 before scores far below the cap left out the exponential).
 constexpr float kCapNear = 64.f;
 
-// What a kernel is built for: chains in a window (moe_attention_paged), or trees and sinks.
-enum Form { kPaged, kMasked };
-
 template <typename T, int D, int kMode, int kForm>
-__global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_constant__ TcParams tp) {
-    using C = Cfg<D>;
-    constexpr bool kMasks = kForm != kPaged;
+__global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(const __grid_constant__ TcParams tp) {
+    using C = Cfg<D, kForm>;
+    constexpr bool kMasks = kForm != kPaged, kQ8 = kForm == kCodes, kRef = kQ8 && ScaleRef<T>::kUsed;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2][2],
-        o_full[2], drain;
+        o_full[2], drain, conv[kQ8 ? C::kStages : 1];
     __shared__ uint32_t tmem_base;
     __shared__ Run run_sh;
     const Params &p = tp.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = p.b.Hq / p.b.Hkv;
-    uint8_t *q_smem = smem + C::kStages * C::kTileB;
+    uint8_t *q_smem = smem + C::kStages * C::kStageB;
+    float *scales = reinterpret_cast<float *>(smem + C::kScalesAt);  // [V stage][K's, V's][kKeys]
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
         for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 8 + withheld(p)), mbar_init(&p_ready[h][1], 8), mbar_init(&o_full[h], 1);
         mbar_init(&drain, 1);
+        if (kQ8)
+            for (int i = 0; i < C::kStages; ++i) mbar_init(&conv[i], kConvertWarps);
         prefetch_map(&tp.mq);
         prefetch_map(&tp.mk);
         prefetch_map(&tp.mv);
@@ -254,7 +354,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
     fence_proxy_async_smem();  // the sequences' costs (generic) before the copies into the ring
     __syncthreads();
 
-    if (warp >= kCopyWarp) {
+    // The registers of the launch, 80 a thread, by what the warpgroups need: 4 x 96 + 40 + 56 = 6 x 80.
+    if (kQ8) {
+        if (warp < kSoftmaxWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
+        else if (warp < kConvertWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    }
+
+    if (kQ8 && warp >= kConvertWarp) {
+        convert_tiles<T, D>(p, run, tp.box_rows, smem, scales, full, conv);
+    } else if (warp >= kCopyWarp && warp < kCopyWarp + kCopyWarps) {
         // ---- Q of each segment and its K tiles, or its V tiles
         const int me = warp - kCopyWarp;
         const int nbox = kKeys / tp.box_rows;  // boxes of a tile, one lane each
@@ -300,10 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     if (g >= uint32_t(C::kStages) &&
                         !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 51 + kv)))
                         break;
-                    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * C::kCh * tp.box_rows * 128);
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full[st], boxes * (kQ8 ? D : C::kCh * 128) * tp.box_rows);
                     __syncwarp();
-                    if (mine) {
-                        const uint32_t dst = smem_addr(smem) + st * C::kTileB + lane * tp.box_rows * 128;
+                    if (mine && kQ8) {
+                        tma_box3(smem_addr(smem) + st * C::kStageB + C::kCodesAt + lane * tp.box_rows * D,
+                                 kv == 0 ? &tp.mk : &tp.mv, 0, row, z, &full[st]);
+                    } else if (mine) {
+                        const uint32_t dst = smem_addr(smem) + st * C::kStageB + lane * tp.box_rows * 128;
 #pragma unroll
                         for (int c = 0; c < C::kCh; ++c)
                             tma_box3(dst + c * C::kSlab, kv == 0 ? &tp.mk : &tp.mv, c * 64, row, z, &full[st]);
@@ -326,20 +439,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         uint32_t g = 0, seg = 0, np[2] = {0, 0};  // ring tiles, segments, P tiles of each half
         const uint32_t ring = smem_addr(smem), qs = smem_addr(q_smem);
         bool ok = true;
+        uint64_t *tiles = kQ8 ? conv : full;  // a tile of the ring is there
         auto qk = [&](int h, uint32_t st) {
             if (leader) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     tc::mma_f16(tmem + 128u * h,
                                 tc::smem_desc_sw128(qs + h * C::kTileB + (k / 4) * C::kSlab) + uint64_t(2 * (k % 4)),
-                                tc::smem_desc_sw128(ring + st * C::kTileB + (k / 4) * C::kSlab) + uint64_t(2 * (k % 4)),
+                                tc::smem_desc_sw128(ring + st * C::kStageB + (k / 4) * C::kSlab) + uint64_t(2 * (k % 4)),
                                 tp.idesc_qk, k > 0);
                 tc::commit_arrive(&s_full[h]);
             }
         };
         auto pv = [&](int h, uint32_t st, int chunk, bool acc) {  // 32 keys
             if (leader) {
-                const uint64_t dv = desc_mn_sw128(ring + st * C::kTileB, C::kSlab);
+                const uint64_t dv = desc_mn_sw128(ring + st * C::kStageB, C::kSlab);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
                     mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 32u * chunk + 8u * k,
@@ -353,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
             const int n = s1 - s0, halves = it.nt > tp.tth ? 2 : 1;
             uint32_t ks = g % C::kStages;
             if (!(ok = warp_wait(&q_full, seg & 1u, p, 55)) ||
-                !(ok = warp_wait(&full[ks], (g / C::kStages) & 1u, p, 56)))
+                !(ok = warp_wait(&tiles[ks], (g / C::kStages) & 1u, p, 56)))
                 break;
             tc::fence_after_sync();
             for (int h = 0; h < halves; ++h) qk(h, ks);
@@ -363,16 +477,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
             }
             for (int j = 0; ok && j < n; ++j) {
                 const uint32_t vs = (g + 2 * j + 1) % C::kStages, vph = ((g + 2 * j + 1) / C::kStages) & 1u;
-                if (!(ok = warp_wait(&full[vs], vph, p, 57))) break;
+                if (!(ok = warp_wait(&tiles[vs], vph, p, 57))) break;
                 const int key0 = tile_key<kKeys, kMasks>(it, s0 + j);
-                if (key0 + kKeys > it.len) {
+                if (!kQ8 && key0 + kKeys > it.len) {  // (any code is finite)
                     // rows at or past the sequence's end hold anything (or an earlier tile's
                     // values): their weights are 0, and so must they be
                     const int first = max(0, it.len - key0);
                     for (int i = first * 8 + lane; i < kKeys * 8; i += 32)
 #pragma unroll
                         for (int c = 0; c < C::kCh; ++c)
-                            *reinterpret_cast<uint4 *>(smem + vs * C::kTileB + c * C::kSlab + i * 16) =
+                            *reinterpret_cast<uint4 *>(smem + vs * C::kStageB + c * C::kSlab + i * 16) =
                                 make_uint4(0, 0, 0, 0);
                     __syncwarp();
                     fence_proxy_async_smem();
@@ -380,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 }
                 if (j + 1 < n) {
                     ks = (g + 2 * j + 2) % C::kStages;
-                    if (!(ok = warp_wait(&full[ks], ((g + 2 * j + 2) / C::kStages) & 1u, p, 58))) break;
+                    if (!(ok = warp_wait(&tiles[ks], ((g + 2 * j + 2) / C::kStages) & 1u, p, 58))) break;
                 }
                 for (int h = 0; ok && h < halves; ++h) {
                     if (!(ok = warp_wait(&p_ready[h][0], np[h] & 1u, p, 59))) break;
@@ -411,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         if (leader) tc::commit_arrive(&drain);
         __syncwarp();
         warp_wait(&drain, 0, p, 60, kDrainNs);
-    } else {
+    } else if (warp < kSoftmaxWarps) {
         // ---- softmax: half h, rows 32 q4 + lane, keys 64 ch .. of each tile (and of the
         // result the channels D/2 ch ..)
         const int q4 = warp & 3, h = (warp >> 2) & 1, ch = warp >> 3, row = 32 * q4 + lane;
@@ -425,9 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
         const float hidden = -CUDART_INF_F * sign;
         const float lowest = kMode == kCapped ? kTanhMinusOne / p.cap_in : -CUDART_MAX_NORMAL_F;
         uint32_t ns = 0, no = 0, nx = 0;  // S tiles and O results taken, exchanges
+        uint32_t gt = 0;                  // tiles of all segments (kQ8)
         bool ok = true;  // after a time-out: no more waits, but every barrier still met
         // a value of the row's other thread, through the space of the results on their way out
-        uint8_t *stage = smem + (C::kStages + 2) * C::kTileB + warp * C::kStageOut;
+        uint8_t *stage = smem + C::kOutAt + warp * C::kStageOut;
         float *mine_x = reinterpret_cast<float *>(stage) + lane;  // in turns at 0 and 32
         const float *other_x = reinterpret_cast<float *>(stage + ((warp ^ 8) - warp) * C::kStageOut) + lane;
         auto meet = [&]() { named_bar_sync(1 + (warp & 7), 64); };
@@ -455,9 +570,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 const bool tree = kMasks && p.tree != nullptr;
                 const int all = tree ? run.seq.len - run.seq.n - 1 : first, late = tree ? it.len - 1 : first + nth - 1;
                 float top = -CUDART_INF_F, sum = 0.f;  // reference maximum (log2), sum of weights
+                uint32_t ref = kRefLeast;              // of the values' scales
                 for (int j = 0; j < s1 - s0; ++j) {
                     ok = ok && warp_wait(&s_full[h], ns & 1u, p, 61 + h);
                     ++ns;
+                    // S is there, so the tiles before this one's V are spread: of the barrier of its stage only
+                    // that phase is to come
+                    const uint32_t vg = 2 * (gt + j) + 1, vst = vg % C::kStages;
+                    if (kQ8) ok = ok && warp_wait(&conv[vst], (vg / C::kStages) & 1u, p, 65 + h);
+                    const float *ks = scales + (vst >> 1) * (2 * kKeys) + 64 * ch, *vs = ks + kKeys;
                     tc::fence_after_sync();
                     const int key0 = tile_key<kKeys, kMasks>(it, s0 + j);
                     const bool edge = key0 + kKeys - 1 > all ||
@@ -479,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                             wait_ld32(u);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                if (kMode == kCapped) u[i] = max_nan(u[i], lowest);
-                                if (kMode == kAny && capped && u[i] == hidden) u[i] = lowest * sign;
+                                if (kMode == kCapped && !kQ8) u[i] = max_nan(u[i], lowest);
+                                if (kMode == kAny && !kQ8 && capped && u[i] == hidden) u[i] = lowest * sign;
                                 if (kMasks ? (sees >> i & 1u) == 0u : 32 * c + i > hi || 32 * c + i <= lo) u[i] = hidden;
                             }
                             tmem_st32(ts + 32 * c, u);
@@ -493,27 +614,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     float mt, most = 0.f;  // the largest, and the largest magnitude of this thread's keys
                     {
                         float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                        float u[2][32];
-                        tmem_ld32(ts, u[0]);
-                        tmem_ld32(ts + 32, u[1]);
-                        wait_ld32(u[0]);
-                        wait_ld32(u[1]);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                        float a4[4] = {0.f, 0.f, 0.f, 0.f};
+                        auto larger = [&](const float (&u)[32]) {
 #pragma unroll
                             for (int i = 0; i < 32; i += 2)
-                                m4[(i >> 1) & 3] = kMode == kAny ? max3(m4[(i >> 1) & 3], u[c][i] * sign, u[c][i + 1] * sign)
-                                                                 : max3(m4[(i >> 1) & 3], u[c][i], u[c][i + 1]);
-                        mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
-                        if (kMode == kAny && capped) {
-                            float a4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
+                                m4[(i >> 1) & 3] = kMode == kAny ? max3(m4[(i >> 1) & 3], u[i] * sign, u[i + 1] * sign)
+                                                                 : max3(m4[(i >> 1) & 3], u[i], u[i + 1]);
+                            if (kMode == kAny && capped)
 #pragma unroll
                                 for (int i = 0; i < 32; i += 2)
-                                    a4[(i >> 1) & 3] = max3(a4[(i >> 1) & 3], fabsf(u[c][i]), fabsf(u[c][i + 1]));
-                            most = max3(fmaxf(a4[0], a4[1]), a4[2], a4[3]);
+                                    a4[(i >> 1) & 3] = max3(a4[(i >> 1) & 3], fabsf(u[i]), fabsf(u[i + 1]));
+                        };
+                        if (kQ8) {  // (both at once leave no registers for the scales)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                float u[32];
+                                tmem_ld32(ts + 32 * c, u);
+                                wait_ld32(u);
+#pragma unroll
+                                for (int i = 0; i < 32; i += 4) scaled(u + i, ks + 32 * c + i, u + i);
+                                larger(u);
+                            }
+                        } else {
+                            float u[2][32];
+                            tmem_ld32(ts, u[0]);
+                            tmem_ld32(ts + 32, u[1]);
+                            wait_ld32(u[0]);
+                            wait_ld32(u[1]);
+                            larger(u[0]);
+                            larger(u[1]);
                         }
+                        mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+                        if (kMode == kAny && capped) most = max3(fmaxf(a4[0], a4[1]), a4[2], a4[3]);
                     }
                     tmem_ld16(ts, v[0]);  // for the second pass
                     mt = fmaxf(mt, exchange(mt));
@@ -531,14 +663,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                         mt = kMode == kCapped ? capped_far(mt, p)
                              : capped         ? score<true>(mt * sign, p)
                                               : score<false>(mt * sign, p);
+                    uint32_t ref_up = ref;  // with this tile's scales
+                    if (kRef) {
+                        const float4 x = *reinterpret_cast<const float4 *>(vs - 64 * ch + 4 * lane);
+                        ref_up = max(ref, ref_bits(__reduce_max_sync(0xffffffffu,
+                                                                     max(max(__float_as_uint(x.x), __float_as_uint(x.y)),
+                                                                         max(__float_as_uint(x.z), __float_as_uint(x.w))))));
+                    }
                     if (j == 0) {
                         top = mt;
-                    } else if (__any_sync(0xffffffffu, mt - top > kGrowth)) {
+                        ref = ref_up;
+                    } else if (__any_sync(0xffffffffu, mt - top > kGrowth) || ref_up != ref) {
                         // this half's P V of the tile before is complete: its S came after it
                         const float up = fmaxf(top, mt);
-                        const float f = exp2_approx(top - (up == -CUDART_INF_F ? 0.f : up));
+                        float f = exp2_approx(top - (up == -CUDART_INF_F ? 0.f : up));
                         sum *= f;
                         top = up;
+                        if (kRef) {
+                            f *= __uint_as_float(ref) * over_ref(ref_up);
+                            ref = ref_up;
+                        }
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[16];
@@ -558,12 +702,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
                     const unsigned long long one2 = pack2(1.f, 1.f), near2 = pack2(p.cap_y, p.cap_y);
                     const float from = edge ? -CUDART_INF_F : kTanhMinusOne;
+                    const float per_ref = kRef ? over_ref(ref) : 1.f;
                     const unsigned long long hide2 = pack2(0x1p-100f, 0x1p-100f);
-                    auto take = [&](auto is_plain, int c, const float (&u)[16]) {
+                    auto take = [&](auto is_plain, int c, const float (&raw)[16]) {
                         constexpr bool kPlain = decltype(is_plain)::value;
                         uint32_t w[8];
+                        float u[16];
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
+                            if (kQ8) {
+                                scaled(raw + i, ks + 16 * c + i, u + i);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) u[i + k] = raw[i + k];
+                            }
                             unsigned long long e2[2] = {pack2(u[i], u[i + 1]), pack2(u[i + 2], u[i + 3])};
                             if (kMode == kAny && kPlain) {  // score()'s polynomial, less the base
 #pragma unroll
@@ -611,6 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                 e2[0] = fma2(e2[0], scale2, base2);
                                 e2[1] = fma2(e2[1], scale2, base2);
                             }
+                            // codes: the values' scales join the weights
+                            float4 vsc = make_float4(1.f, 1.f, 1.f, 1.f);
+                            if (kQ8) vsc = *reinterpret_cast<const float4 *>(vs + 16 * c + i);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 float x, y;
@@ -624,6 +779,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                 s2[k] = add2(s2[k], pack2(x, y));
                                 // rounded for the product, whose operands have one type (V's values were
                                 // rounded to it by the same half step); the sum keeps the weight whole
+                                if (kQ8) {
+                                    unsigned long long v2 = k == 0 ? pack2(vsc.x, vsc.y) : pack2(vsc.z, vsc.w);
+                                    if (kRef) v2 = mul2(v2, pack2(per_ref, per_ref));
+                                    unpack2(mul2(pack2(x, y), v2), x, y);
+                                }
                                 w[i / 2 + k] = Pair<T>::make(x, y);
                             }
                         }
@@ -668,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 const int out_row = live ? (it.row0 + h * tp.tth + tok_h) * p.b.Hq + it.kh * G + head : -1;
                 float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(2 * kHalf, D);
                 const int prow = h * kHalf + row;
-                const float inv = over_sum(sum);
+                const float unit = kRef ? __uint_as_float(ref) : 1.f, inv = over_sum(sum) * unit;
 #pragma unroll 1
                 for (int c = 0; ok && c < D / 64; ++c) {
                     const int ch0 = D / 2 * ch + 32 * c;  // first of 32 channels
@@ -695,6 +855,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                                 *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + size_t(dst) * D + ch0 + 8 * k) = w;
                         }
                     } else if (live) {
+                        if (kRef)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= unit;
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             tc::st_global_v8(mine + part_at(prow, ch0 + i, D),
@@ -714,6 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
                 __syncwarp();
                 tc::fence_before_sync();
             }
+            gt += s1 - s0;
             run_next<kKeys, kMasks>(p, run);
         }
     }
@@ -726,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tc_kernel(const __grid_
 template <int kForm, typename T, int D>
 cudaError_t launch(const TcParams &tp, bool near_cap, int grid, cudaStream_t s) {
     auto go = [&](auto kernel) {
-        return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(Cfg<D>::kSmem), s, tp);
+        return launch_pdl(kernel, dim3(grid), dim3(form_threads(kForm)), size_t(Cfg<D, kForm>::kSmem), s, tp);
     };
     if (tp.p.cap_in > 0.f && near_cap) return go(attention_tc_kernel<T, D, kCapped, kForm>);
     if (tp.p.cap_in == 0.f && tp.p.scale_log2 > 0.f) return go(attention_tc_kernel<T, D, kScaled, kForm>);
@@ -736,7 +900,7 @@ cudaError_t launch(const TcParams &tp, bool near_cap, int grid, cudaStream_t s) 
 template <int kForm, typename T, int D>
 cudaError_t init() {
     auto set = [](auto kernel) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, kForm>::kSmem);
     };
     cudaError_t e = set(attention_tc_kernel<T, D, kScaled, kForm>);
     if (e == cudaSuccess) e = set(attention_tc_kernel<T, D, kAny, kForm>);
@@ -767,9 +931,11 @@ cudaError_t launch_form(const AttnArgs &a, const Params &p, int num_sms, cudaStr
     const uint32_t fmt = a.type == MOE_BF16 ? (1u << 7) | (1u << 10) : 0u;  // A and B bf16
     tp.idesc_qk = tc::idesc_f16_f32(kHalf, kKeys) | fmt;
     tp.idesc_pv = tc::idesc_f16_f32(kHalf, a.b.D) | fmt | (1u << 16);       // B: N contiguous
-    if (!encode_pages_map(&tp.mk, a.k, a.b, a.type, tp.box_rows) ||
-        !encode_pages_map(&tp.mv, a.v, a.b, a.type, tp.box_rows) ||
-        !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
+    auto pages = [&](CUtensorMap *map, const void *base) {
+        return kForm == kCodes ? encode_codes_map(map, base, a.b, tp.box_rows, true)
+                               : encode_pages_map(map, base, a.b, a.type, tp.box_rows);
+    };
+    if (!pages(&tp.mk, a.k) || !pages(&tp.mv, a.v) || !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
         return cudaErrorInvalidValue;
     const int grid = std::min(num_sms, kMaxGrid);
     const bool near_cap = a.softcap <= kCapNear && p.cap_in > 1e-30f;  // kCapped: kTanhMinusOne / cap_in is finite

@@ -10,8 +10,8 @@ namespace moeq4k {
 // Per-device one-time set-up (kernel attributes, SM count) for the current
 // device; returns the SM count and the device ordinal.
 moe_status device_info(int *sms, int *dev_out);
-// The same for a call of moe_attention_paged, whose kernels are set up by its first.
-moe_status attention_info(int *sms);
+// The same for an attention call, whose form's kernels are set up by its first.
+moe_status attention_info(int *sms, int form);
 // Shape limits shared by every entry point.
 moe_status validate_shape(int T, int H, int E, int k, int I);
 
@@ -197,9 +197,11 @@ bool encode_rows_map(CUtensorMap *map, const void *base, const PagedBatch &b, mo
                      int tokens);
 // Counters and scratch for partial results of split key ranges.
 size_t attention_part_bytes(int D);
-cudaError_t init_attention();
+// The kernels come in three forms, each set up by its first call: chains in a window (0),
+// trees and sinks (1), 8-bit codes (2).
+int attention_form(const AttnArgs &a);
+cudaError_t init_attention(int form);
 cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s);
-cudaError_t launch_attention_cache(const AttnArgs &a, int max_new, int num_sms, cudaStream_t s);
 
 struct KeepArgs {
     void *k, *v;
