@@ -46,8 +46,10 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kCopyWarps = 2;               // K tiles, V tiles
 constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kCopyWarps);
-// Over 8-bit codes: one warp idle, so that four more make a warpgroup of their own.
-constexpr int kConvertWarp = kCopyWarp + kCopyWarps + 1, kConvertWarps = 4;
+// Over 8-bit codes: a copying warp for the queries and, in a warpgroup of their own, four that
+// copy the keys' and values' codes and spread them.
+constexpr int kConvertWarp = kSoftmaxWarps + 4, kConvertWarps = 4;
+constexpr int kConvertRows = kKeys / kConvertWarps;  // of a tile, each warp's
 constexpr int kCodesThreads = 32 * (kConvertWarp + kConvertWarps);
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 // The least work of a CTA, and an item's fixed cost, in key tiles (a cost of 1, 2, 3:
@@ -69,6 +71,7 @@ constexpr int form_threads(int form) { return form == kCodes ? kCodesThreads : k
 
 struct TcParams {
     CUtensorMap mq, mk, mv;
+    CUtensorMap mks, mvs;  // the scales of codes
     Params p;          // p.tt: tokens of an item (both halves)
     int tth;           // tokens of a half
     int box_rows;      // rows of a K/V box
@@ -80,15 +83,23 @@ struct Cfg {
     static constexpr int kCh = D / 64;                 // 64-channel slabs of a row
     static constexpr int kSlab = 128 * 128;            // bytes of a 128-row slab
     static constexpr int kTileB = kCh * kSlab;         // a tile of K, of V, or of a half's Q
-    static constexpr int kStages = D == 128 ? 4 : kForm == kCodes ? 6 : 8;
-    // Where a tile's codes land: in its own second slab, whose every row they are spread from in
-    // place, or behind it, where there is only one.
-    static constexpr int kCodesAt = D == 128 ? kSlab : kTileB;
-    static constexpr int kStageB = kTileB + (kForm == kCodes && D == 64 ? kKeys * D : 0);
-    static constexpr int kStageOut = 32 * 64;          // a softmax warp's 32 rows x 32 channels on their way out
-    static constexpr int kOutAt = kStages * kStageB + 2 * kTileB;
-    static constexpr int kScalesAt = kOutAt + kSoftmaxWarps * kStageOut;  // of a V stage's tile: K's and V's
-    static constexpr int kSmem = kScalesAt + (kForm == kCodes ? kStages / 2 * 2 * kKeys * 4 : 0);
+    static constexpr bool kQ8 = kForm == kCodes;
+    static constexpr int kStages = kQ8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+    static constexpr int kQAt = kStages * kTileB;
+    // Results on their way out, 32 rows x 32 channels of each softmax warp (over codes, whose form has
+    // no room for them, only what two warps exchange).
+    static constexpr int kStageOut = kQ8 ? 256 : 32 * 64;
+    static constexpr int kOutAt = kQAt + 2 * kTileB;
+    // Codes: each converting warp's ring of its rows' codes and their scales, and the scales as the
+    // softmax reads them, K's and V's of a tile.  A slot of those is written again when the tiles
+    // kStages before are used up, which for the keys' (the first) is kScaleTiles tiles before.
+    static constexpr int kRing = kStages;
+    static constexpr int kPiece = kConvertRows * D;
+    static constexpr int kCodesAt = kOutAt + kSoftmaxWarps * kStageOut;
+    static constexpr int kCodeScalesAt = kCodesAt + (kQ8 ? kConvertWarps * kRing * kPiece : 0);
+    static constexpr int kScalesAt = kCodeScalesAt + (kQ8 ? kConvertWarps * kRing * 256 : 0);
+    static constexpr int kScaleTiles = D == 128 ? 2 : 4;
+    static constexpr int kSmem = kScalesAt + (kQ8 ? kScaleTiles * 2 * kKeys * 4 : 0);
 };
 
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
@@ -97,6 +108,14 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, i
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
         "{%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_box2(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
 }
 
@@ -222,82 +241,130 @@ __device__ __forceinline__ void scaled(const float *v, const float *scales, floa
     unpack2(mul2(pack2(v[2], v[3]), pack2(f.z, f.w)), r[2], r[3]);
 }
 
-// The converting warps of the form over codes: every tile of the ring, once its codes have
-// landed, is spread to the 16-bit tile that the products read (8-row groups of 1024 bytes,
-// 128 a row, swizzled), and the scales of its keys go beside the V tiles.  A thread has 16
-// codes of a row at a time: the two chunks that they become are stored in an order that
-// keeps the eight lanes of a row on different banks.
-template <typename T, int D>
-__device__ __forceinline__ void convert_tiles(const Params &p, Run run, int box_rows, uint8_t *smem, float *scales,
-                                              uint64_t *full, uint64_t *conv) {
+// The CTA's run in registers, or in shared memory as each warp's own.
+template <bool kShared>
+__device__ __forceinline__ Run &run_place(Run &found, Run &mine) {
+    if (!kShared) return found;
+    if ((threadIdx.x & 31) == 0) mine = found;
+    __syncwarp();
+    return mine;
+}
+
+// A converting warp of the form over codes.  It copies its 32 rows of every K and V tile (and
+// their scales) into a ring of its own, a few tiles ahead, spreads them to the 16-bit tile that
+// the products read (8-row groups of 1024 bytes, 128 a row, swizzled) once that place is
+// free, and puts the scales where the softmax reads them.  So the copies wait for nobody
+// but their warp: with codes copied to the products' own places and spread there, a tile's
+// copy began with its place's release, and the chunk of 2048 over 16384 took 821 us.
+// A thread has 16 codes of a row at a time: the two chunks that they become are stored in
+// an order that keeps the eight lanes of a row on different banks.
+template <typename T, int D, typename F>
+__device__ __forceinline__ void convert_tiles(const TcParams &tp, const Run &run, F next, uint8_t *smem,
+                                              uint64_t *landed, uint64_t *empty, uint64_t *conv) {
     using C = Cfg<D, kCodes>;
     constexpr int kLanes = D / 16, kRowsAtOnce = 32 / kLanes, kSteps = 32 / kRowsAtOnce;  // of a row; of a warp
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp, key_in = 32 * warp + lane;
-    const int c = lane % kLanes, slab = c >> 2, odd = (c ^ (c >> 2)) & 1;
-    uint32_t g = 0;
+    const Params &p = tp.p;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
+    const int c = lane % kLanes, odd = (c ^ (c >> 2)) & 1, row0 = kConvertRows * warp;
+    const int nb = kConvertRows / tp.box_rows;  // boxes of the rows: 1, or 2 where pages have 16
+    uint8_t *codes = smem + C::kCodesAt + warp * C::kRing * C::kPiece;
+    uint8_t *code_scales = smem + C::kCodeScalesAt + warp * C::kRing * 256;
+    landed += warp * C::kRing;
+    uint32_t g = 0, issued = 0;  // tiles (K, V, K, ..) spread and copied, over all segments
     bool ok = true;
     while (ok && run.u < run.end) {
         int s0, s1;
         if (!run_segment(p, run, s0, s1)) break;
-        const Item it = run.item;
+        const Item &it = run.item;
         const int n = s1 - s0;
-        // where this thread's key of tile j has its scales, or -1: past the end, between the sinks and
-        // every row's window (its page may be gone already) or a bad page
-        auto place = [&](int j) {
-            const int key = tile_key<kKeys, true>(it, s0 + j) + key_in, box = key & ~(box_rows - 1);
-            if (j >= n || key >= it.len || (box + box_rows <= it.seen && box >= p.sinks)) return -1l;
-            const int pg = page_of(p.b, it.b, key, p.hdr);
-            return pg < 0 ? -1l : (long(pg) * p.b.Hkv + it.kh) * p.b.page + key % p.b.page;
+        const uint32_t end = g + 2 * n, first = g;
+        // the pages of 32 boxes at a time, nb of a tile, and of the 32 after them
+        auto page_at = [&](int i) {
+            const int j = nb == 2 ? i >> 1 : i;
+            if (j >= n) return 0;
+            // past the tensor, read as zeros: a box past the end, one between the sinks and every row's
+            // window (its page may be gone already) and a bad page
+            const int key = tile_key<kKeys, true>(it, s0 + j) + row0 + (nb == 2 ? (i & 1) * tp.box_rows : 0);
+            const int pg = key >= it.len || (key + tp.box_rows <= it.seen && key >= p.sinks)
+                               ? -1
+                               : page_of(p.b, it.b, key, p.hdr);
+            return pg < 0 ? p.b.num_pages : pg;
         };
-        long at = place(0), next = place(1);
-        float k_scale = at < 0 ? 1.f : p.ks[at], v_scale = at < 0 ? 0.f : p.vs[at];
-        for (int j = 0; ok && j < n; ++j) {
-            for (int kv = 0; kv < 2; ++kv, ++g) {
-                const uint32_t st = g % C::kStages;
-                if (!(ok = warp_wait(&full[st], (g / C::kStages) & 1u, p, 67))) break;
-                uint8_t *tile = smem + st * C::kStageB;
-                if (kv == 1) {
-                    // above 0: a key's hidden score is an infinity, which a scale of 0 would make a NaN (the
-                    // codes of a scale of 0 are 0 themselves)
-                    float *to = scales + (st >> 1) * (2 * kKeys) + key_in;
-                    to[0] = k_scale <= 1.17549435e-38f ? 1.17549435e-38f : k_scale;
-                    to[kKeys] = v_scale;
-                    at = next;
-                    k_scale = at < 0 ? 1.f : p.ks[at];
-                    v_scale = at < 0 ? 0.f : p.vs[at];
-                    next = place(j + 2);
-                }
-#pragma unroll
-                for (int i0 = 0; i0 < kSteps; i0 += 4) {
-                    uint4 x[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 32 * warp + (i0 + i) * kRowsAtOnce + lane / kLanes;
-                        x[i] = *reinterpret_cast<const uint4 *>(tile + C::kCodesAt + r * D + 16 * c);
-                    }
-                    __syncwarp();  // D = 128: what is stored lies over these rows' codes
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 32 * warp + (i0 + i) * kRowsAtOnce + lane / kLanes;
-                        const CodePair<T> a(x[i].x), b(x[i].y), d(x[i].z), e(x[i].w);
-                        const uint4 lo = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(),
-                                                    b.template take<0, 1>(), b.template take<2, 3>());
-                        const uint4 hi = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(),
-                                                    e.template take<0, 1>(), e.template take<2, 3>());
-                        uint8_t *row = tile + slab * C::kSlab + r * 128;
-                        const int first = 2 * (c & 3) + odd;
-                        *reinterpret_cast<uint4 *>(row + ((first ^ (r & 7)) << 4)) = odd != 0 ? hi : lo;
-                        *reinterpret_cast<uint4 *>(row + ((first ^ 1 ^ (r & 7)) << 4)) = odd != 0 ? lo : hi;
-                    }
-                }
-                fence_proxy_async_smem();  // these stores before the products' reads of them
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&conv[st]);
+        int pages = page_at(lane), pages_next = n * nb > 32 ? page_at(32 + lane) : 0;
+        auto issue = [&]() {
+            const int j = int(issued - first) >> 1, kv = int(issued - first) & 1;
+            if (kv == 0 && j > 0 && ((j * nb) & 31) == 0) {
+                pages = pages_next;
+                pages_next = page_at(j * nb + 32 + lane);
                 __syncwarp();
             }
+            const int box = lane >> 1;  // lanes 0 .. 2 nb - 1: a box's codes, its scales
+            const int z = __shfl_sync(0xffffffffu, pages, (j * nb + box) & 31) * p.b.Hkv + it.kh;
+            const uint32_t slot = issued % C::kRing;
+            uint64_t *bar = &landed[slot];
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::kPiece + kConvertRows * 4);
+            __syncwarp();
+            if (box < nb) {
+                const int row = (tile_key<kKeys, true>(it, s0 + j) + row0 + box * tp.box_rows) & (p.b.page - 1);
+                if ((lane & 1) == 0)
+                    tma_box3(smem_addr(codes + slot * C::kPiece + box * tp.box_rows * D), kv == 0 ? &tp.mk : &tp.mv, 0,
+                             row, z, bar);
+                else
+                    tma_box2(smem_addr(code_scales + slot * 256 + box * 128), kv == 0 ? &tp.mks : &tp.mvs, row, z, bar);
+            }
+            __syncwarp();
+            ++issued;
+        };
+        for (int i = 0; i < C::kRing && issued < end; ++i) issue();
+        for (; ok && g < end; ++g) {
+            const uint32_t slot = g % C::kRing, st = g % C::kStages;
+            if (!(ok = warp_wait(&landed[slot], (g / C::kRing) & 1u, p, 67))) break;
+            if (g >= uint32_t(C::kStages) && !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 68))) break;
+            const uint8_t *from = codes + slot * C::kPiece;
+            uint8_t *tile = smem + st * C::kTileB;
+#pragma unroll
+            for (int i0 = 0; i0 < kSteps; i0 += 4) {
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = *reinterpret_cast<const uint4 *>(from + ((i0 + i) * 32 + lane) * 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = row0 + (i0 + i) * kRowsAtOnce + lane / kLanes;
+                    const CodePair<T> a(x[i].x), b(x[i].y), d(x[i].z), e(x[i].w);
+                    const uint4 lo = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(),
+                                                b.template take<0, 1>(), b.template take<2, 3>());
+                    const uint4 hi = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(),
+                                                e.template take<0, 1>(), e.template take<2, 3>());
+                    uint8_t *row = tile + (c >> 2) * C::kSlab + r * 128;
+                    const int at = 2 * (c & 3) + odd;
+                    *reinterpret_cast<uint4 *>(row + ((at ^ (r & 7)) << 4)) = odd != 0 ? hi : lo;
+                    *reinterpret_cast<uint4 *>(row + ((at ^ 1 ^ (r & 7)) << 4)) = odd != 0 ? lo : hi;
+                }
+            }
+            {
+                // past the sequence's end the scales may be anything.  A key's is above 0: a hidden score is an
+                // infinity, which 0 would make a NaN (the codes of a scale of 0 are 0 themselves).
+                const int j = int(g - first) >> 1, kv = int(g - first) & 1;
+                const bool past = tile_key<kKeys, true>(it, s0 + j) + row0 + lane >= it.len;
+                const int gap = nb == 2 ? (lane >> 4) * 16 : 0;
+                float f = reinterpret_cast<const float *>(code_scales + slot * 256)[lane + gap];
+                if (kv == 0) f = past ? 1.f : f <= 1.17549435e-38f ? 1.17549435e-38f : f;
+                else f = past ? 0.f : f;
+                reinterpret_cast<float *>(smem + C::kScalesAt)[((g >> 1) % C::kScaleTiles) * (2 * kKeys) + kv * kKeys +
+                                                               row0 + lane] = f;
+            }
+            // these stores before the products' reads of them, the reads before the copy into their place
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&conv[st]);
+            __syncwarp();
+            if (issued < end) issue();
         }
-        run_next<kKeys, true>(p, run);
+        next();
     }
+    for (uint32_t i = g; i < issued; ++i)  // copies in flight after a time-out land before the CTA exits
+        warp_wait(&landed[i % C::kRing], (i / C::kRing) & 1u, p, 53, kDrainNs);
 }
 
 // How a score follows from q.k: by a positive scale, capped after a positive
@@ -316,35 +383,48 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     constexpr bool kMasks = kForm != kPaged, kQ8 = kForm == kCodes, kRef = kQ8 && ScaleRef<T>::kUsed;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2][2],
-        o_full[2], drain, conv[kQ8 ? C::kStages : 1];
+        o_full[2], drain, conv[kQ8 ? C::kStages : 1], landed[kQ8 ? kConvertWarps * C::kRing : 1];
     __shared__ uint32_t tmem_base;
     __shared__ Run run_sh;
+    __shared__ Run run_of[kQ8 ? kCodesThreads / 32 : 1];  // each warp's own, where registers are few
     const Params &p = tp.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = p.b.Hq / p.b.Hkv;
-    uint8_t *q_smem = smem + C::kStages * C::kStageB;
-    float *scales = reinterpret_cast<float *>(smem + C::kScalesAt);  // [V stage][K's, V's][kKeys]
+    uint8_t *q_smem = smem + C::kQAt;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
         for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 8 + withheld(p)), mbar_init(&p_ready[h][1], 8), mbar_init(&o_full[h], 1);
         mbar_init(&drain, 1);
-        if (kQ8)
+        if (kQ8) {
             for (int i = 0; i < C::kStages; ++i) mbar_init(&conv[i], kConvertWarps);
+            for (int i = 0; i < kConvertWarps * C::kRing; ++i) mbar_init(&landed[i], 1);
+        }
         prefetch_map(&tp.mq);
         prefetch_map(&tp.mk);
         prefetch_map(&tp.mv);
+        if (kQ8) prefetch_map(&tp.mks), prefetch_map(&tp.mvs);
     }
     __syncwarp();
     fence_mbar_init();
     pdl_enter();
     if (tid == kCopyWarp * 32) p.desc[blockIdx.x].parts = 0;
     __syncwarp();
-    Run run;
+    Run found;
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, 512);  // beside the search
     tc::fence_before_sync();
-    const bool work = run_begin<kKeys, kMasks>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, run);
+    const bool work = run_begin<kKeys, kMasks>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, found);
+    Run &run = run_place<kQ8>(found, run_of[kQ8 ? warp : 0]);
+    auto next = [&]() {
+        if (kQ8) {
+            __syncwarp();
+            if (lane == 0) run_next<kKeys, kMasks>(p, run);
+            __syncwarp();
+        } else {
+            run_next<kKeys, kMasks>(p, run);
+        }
+    };
     tc::fence_after_sync();
     const uint32_t tmem = tmem_base;
     if (!work) {
@@ -354,16 +434,9 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     fence_proxy_async_smem();  // the sequences' costs (generic) before the copies into the ring
     __syncthreads();
 
-    // The registers of the launch, 80 a thread, by what the warpgroups need: 4 x 96 + 40 + 56 = 6 x 80.
-    if (kQ8) {
-        if (warp < kSoftmaxWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
-        else if (warp < kConvertWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    }
-
     if (kQ8 && warp >= kConvertWarp) {
-        convert_tiles<T, D>(p, run, tp.box_rows, smem, scales, full, conv);
-    } else if (warp >= kCopyWarp && warp < kCopyWarp + kCopyWarps) {
+        convert_tiles<T, D>(tp, run, next, smem, landed, empty, conv);
+    } else if (warp >= kCopyWarp && warp < kCopyWarp + (kQ8 ? 1 : kCopyWarps)) {
         // ---- Q of each segment and its K tiles, or its V tiles
         const int me = warp - kCopyWarp;
         const int nbox = kKeys / tp.box_rows;  // boxes of a tile, one lane each
@@ -372,7 +445,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         while (ok && run.u < run.end) {
             int s0, s1;
             if (!run_segment(p, run, s0, s1)) break;
-            const Item it = run.item;
+            const std::conditional_t<kQ8, const Item &, const Item> it = run.item;
             const int halves = it.nt > tp.tth ? 2 : 1;
             if (me == 0 && seg > 0 && !(ok = warp_wait(&q_empty, (seg - 1) & 1u, p, 50))) break;
             if (me == 0 && lane == 0) {
@@ -385,6 +458,10 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
             ++seg;
             if (me == 0 && lane == 0 && s0 == 0 && s1 < it.tiles) p.desc[blockIdx.x] = join_desc(p, run);
             __syncwarp();
+            if (kQ8) {
+                next();
+                continue;
+            }
             auto page_z = [&](int j) {  // page-head of this lane's box of tile j
                 const int key = tile_key<kKeys, kMasks>(it, s0 + j) + lane * tp.box_rows;
                 if (j >= s1 - s0 || lane >= nbox || key >= it.len) return 0;
@@ -409,14 +486,10 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     if (g >= uint32_t(C::kStages) &&
                         !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 51 + kv)))
                         break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&full[st], boxes * (kQ8 ? D : C::kCh * 128) * tp.box_rows);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * C::kCh * tp.box_rows * 128);
                     __syncwarp();
-                    if (mine && kQ8) {
-                        tma_box3(smem_addr(smem) + st * C::kStageB + C::kCodesAt + lane * tp.box_rows * D,
-                                 kv == 0 ? &tp.mk : &tp.mv, 0, row, z, &full[st]);
-                    } else if (mine) {
-                        const uint32_t dst = smem_addr(smem) + st * C::kStageB + lane * tp.box_rows * 128;
+                    if (mine) {
+                        const uint32_t dst = smem_addr(smem) + st * C::kTileB + lane * tp.box_rows * 128;
 #pragma unroll
                         for (int c = 0; c < C::kCh; ++c)
                             tma_box3(dst + c * C::kSlab, kv == 0 ? &tp.mk : &tp.mv, c * 64, row, z, &full[st]);
@@ -424,7 +497,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     __syncwarp();
                 }
             }
-            run_next<kKeys, kMasks>(p, run);
+            next();
         }
         // this warp's last copies land before the CTA exits, whoever else gave up on what: the MMA
         // warp may have left by a time-out of its own and not waited for them
@@ -446,14 +519,14 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                 for (int k = 0; k < D / 16; ++k)
                     tc::mma_f16(tmem + 128u * h,
                                 tc::smem_desc_sw128(qs + h * C::kTileB + (k / 4) * C::kSlab) + uint64_t(2 * (k % 4)),
-                                tc::smem_desc_sw128(ring + st * C::kStageB + (k / 4) * C::kSlab) + uint64_t(2 * (k % 4)),
+                                tc::smem_desc_sw128(ring + st * C::kTileB + (k / 4) * C::kSlab) + uint64_t(2 * (k % 4)),
                                 tp.idesc_qk, k > 0);
                 tc::commit_arrive(&s_full[h]);
             }
         };
         auto pv = [&](int h, uint32_t st, int chunk, bool acc) {  // 32 keys
             if (leader) {
-                const uint64_t dv = desc_mn_sw128(ring + st * C::kStageB, C::kSlab);
+                const uint64_t dv = desc_mn_sw128(ring + st * C::kTileB, C::kSlab);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)  // 16 keys: 8 columns of P, 2048 bytes of V
                     mma_ts(tmem + 256u + 128u * h, tmem + 128u * h + 32u * chunk + 8u * k,
@@ -463,7 +536,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         while (ok && run.u < run.end) {
             int s0, s1;
             if (!run_segment(p, run, s0, s1)) break;
-            const Item it = run.item;
+            const std::conditional_t<kQ8, const Item &, const Item> it = run.item;
             const int n = s1 - s0, halves = it.nt > tp.tth ? 2 : 1;
             uint32_t ks = g % C::kStages;
             if (!(ok = warp_wait(&q_full, seg & 1u, p, 55)) ||
@@ -486,7 +559,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     for (int i = first * 8 + lane; i < kKeys * 8; i += 32)
 #pragma unroll
                         for (int c = 0; c < C::kCh; ++c)
-                            *reinterpret_cast<uint4 *>(smem + vs * C::kStageB + c * C::kSlab + i * 16) =
+                            *reinterpret_cast<uint4 *>(smem + vs * C::kTileB + c * C::kSlab + i * 16) =
                                 make_uint4(0, 0, 0, 0);
                     __syncwarp();
                     fence_proxy_async_smem();
@@ -519,7 +592,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
             }
             g += 2 * n;
             ++seg;
-            run_next<kKeys, kMasks>(p, run);
+            next();
         }
         // every MMA complete before the tensor memory is released
         if (leader) tc::commit_arrive(&drain);
@@ -555,7 +628,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         while (run.u < run.end) {
             int s0, s1;
             if (!run_segment(p, run, s0, s1)) break;
-            const Item it = run.item;
+            const std::conditional_t<kQ8, const Item &, const Item> it = run.item;
             const int nth = min(tp.tth, it.nt - h * tp.tth);  // this half's tokens
             if (nth > 0) {
                 const int first = it.pos0 + h * tp.tth;  // position of the half's first token
@@ -578,7 +651,9 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     // that phase is to come
                     const uint32_t vg = 2 * (gt + j) + 1, vst = vg % C::kStages;
                     if (kQ8) ok = ok && warp_wait(&conv[vst], (vg / C::kStages) & 1u, p, 65 + h);
-                    const float *ks = scales + (vst >> 1) * (2 * kKeys) + 64 * ch, *vs = ks + kKeys;
+                    const float *ks = reinterpret_cast<const float *>(smem + C::kScalesAt) +
+                                      ((gt + j) % C::kScaleTiles) * (2 * kKeys) + 64 * ch;
+                    const float *vs = ks + kKeys;
                     tc::fence_after_sync();
                     const int key0 = tile_key<kKeys, kMasks>(it, s0 + j);
                     const bool edge = key0 + kKeys - 1 > all ||
@@ -835,7 +910,17 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     float o[32];
                     tmem_ld32(to + 32 * c, o);
                     wait_ld32(o);
-                    if (whole) {
+                    if (whole && kQ8) {
+                        if (live) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + size_t(out_row) * D + ch0);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float *x = &o[8 * k];
+                                dst[k] = make_uint4(Pair<T>::make(x[0] * inv, x[1] * inv), Pair<T>::make(x[2] * inv, x[3] * inv),
+                                                    Pair<T>::make(x[4] * inv, x[5] * inv), Pair<T>::make(x[6] * inv, x[7] * inv));
+                            }
+                        }
+                    } else if (whole) {
                         // through shared memory: a row per lane in (16-byte chunks, swizzled),
                         // 64-byte runs of eight rows at a time out
 #pragma unroll
@@ -878,7 +963,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                 tc::fence_before_sync();
             }
             gt += s1 - s0;
-            run_next<kKeys, kMasks>(p, run);
+            next();
         }
     }
     tc::fence_before_sync();
@@ -927,7 +1012,7 @@ cudaError_t launch_form(const AttnArgs &a, const Params &p, int num_sms, cudaStr
     tp.p.tt = 2 * tp.tth;
     tp.p.tt_magic = 0xffffffffu / unsigned(tp.p.tt) + 1;
     tp.p.extra = kExtra;
-    tp.box_rows = std::min(a.b.page, kKeys);
+    tp.box_rows = std::min(a.b.page, kForm == kCodes ? kConvertRows : kKeys);
     const uint32_t fmt = a.type == MOE_BF16 ? (1u << 7) | (1u << 10) : 0u;  // A and B bf16
     tp.idesc_qk = tc::idesc_f16_f32(kHalf, kKeys) | fmt;
     tp.idesc_pv = tc::idesc_f16_f32(kHalf, a.b.D) | fmt | (1u << 16);       // B: N contiguous
@@ -936,6 +1021,9 @@ cudaError_t launch_form(const AttnArgs &a, const Params &p, int num_sms, cudaStr
                                : encode_pages_map(map, base, a.b, a.type, tp.box_rows);
     };
     if (!pages(&tp.mk, a.k) || !pages(&tp.mv, a.v) || !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
+        return cudaErrorInvalidValue;
+    if (kForm == kCodes && (!encode_scales_map(&tp.mks, a.ks, a.b, tp.box_rows) ||
+                            !encode_scales_map(&tp.mvs, a.vs, a.b, tp.box_rows)))
         return cudaErrorInvalidValue;
     const int grid = std::min(num_sms, kMaxGrid);
     const bool near_cap = a.softcap <= kCapNear && p.cap_in > 1e-30f;  // kCapped: kTanhMinusOne / cap_in is finite
