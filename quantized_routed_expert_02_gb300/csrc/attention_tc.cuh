@@ -46,10 +46,10 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kCopyWarps = 2;               // K tiles, V tiles
 constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kCopyWarps);
-// Over 8-bit codes: a copying warp for the queries and, in a warpgroup of their own, four that
-// copy the keys' and values' codes and spread them.
-constexpr int kConvertWarp = kSoftmaxWarps + 4, kConvertWarps = 4;
-constexpr int kConvertRows = kKeys / kConvertWarps;  // of a tile, each warp's
+// Over 8-bit codes: a copying warp for the queries, and six that copy the keys' and values' codes
+// and spread them, a piece of a tile each in turn.
+constexpr int kConvertWarp = kCopyWarp + 1, kConvertWarps = 6;
+constexpr int kPieceRows = 32;
 constexpr int kCodesThreads = 32 * (kConvertWarp + kConvertWarps);
 constexpr int kMaxGrid = kMaxCtas / 2;     // one CTA per SM
 // The least work of a CTA, and an item's fixed cost, in key tiles (a cost of 1, 2, 3:
@@ -90,16 +90,18 @@ struct Cfg {
     // no room for them, only what two warps exchange).
     static constexpr int kStageOut = kQ8 ? 256 : 32 * 64;
     static constexpr int kOutAt = kQAt + 2 * kTileB;
-    // Codes: each converting warp's ring of its rows' codes and their scales, and the scales as the
-    // softmax reads them, K's and V's of a tile.  A slot of those is written again when the tiles
-    // kStages before are used up, which for the keys' (the first) is kScaleTiles tiles before.
-    static constexpr int kRing = kStages;
-    static constexpr int kPiece = kConvertRows * D;
+    // Codes: each converting warp's ring of pieces and their scales, and the scales as the softmax reads
+    // them, K's and V's of a tile.  Those are written when the tile kStages before has been used: for
+    // the keys' then the softmax is done with the tile kScaleTiles before.
+    static constexpr int kRing = 2;
+    static constexpr int kPiece = kPieceRows * D;
     static constexpr int kCodesAt = kOutAt + kSoftmaxWarps * kStageOut;
     static constexpr int kCodeScalesAt = kCodesAt + (kQ8 ? kConvertWarps * kRing * kPiece : 0);
     static constexpr int kScalesAt = kCodeScalesAt + (kQ8 ? kConvertWarps * kRing * 256 : 0);
     static constexpr int kScaleTiles = D == 128 ? 2 : 4;
     static constexpr int kSmem = kScalesAt + (kQ8 ? kScaleTiles * 2 * kKeys * 4 : 0);
+    // A converting warp waits for each release of the stages that it uses, in turn.
+    static_assert(!kQ8 || kStages * (kKeys / kPieceRows) % kConvertWarps == 0, "the warps' pieces repeat with the ring");
 };
 
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
@@ -250,121 +252,130 @@ __device__ __forceinline__ Run &run_place(Run &found, Run &mine) {
     return mine;
 }
 
-// A converting warp of the form over codes.  It copies its 32 rows of every K and V tile (and
-// their scales) into a ring of its own, a few tiles ahead, spreads them to the 16-bit tile that
-// the products read (8-row groups of 1024 bytes, 128 a row, swizzled) once that place is
-// free, and puts the scales where the softmax reads them.  So the copies wait for nobody
-// but their warp: with codes copied to the products' own places and spread there, a tile's
-// copy began with its place's release, and the chunk of 2048 over 16384 took 821 us.
-// A thread has 16 codes of a row at a time: the two chunks that they become are stored in
-// an order that keeps the eight lanes of a row on different banks.
+// A converting warp of the form over codes.  The pieces of the tiles (K, V, K, ..), 32 rows each,
+// go round the warps.  A warp copies its pieces (and their scales) ahead into a ring of its
+// own, spreads them to the 16-bit tile that the products read (8-row groups of 1024
+// bytes, 128 a row, swizzled) once that place is free, and puts the scales where the
+// softmax reads them (K's times `k_unit`).  A thread has 16 codes of a row at a time: the
+// two chunks that they become are stored in an order that keeps the eight lanes of a row
+// on different banks.
 template <typename T, int D, typename F>
-__device__ __forceinline__ void convert_tiles(const TcParams &tp, const Run &run, F next, uint8_t *smem,
+__device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, const Run &run, F next, uint8_t *smem,
                                               uint64_t *landed, uint64_t *empty, uint64_t *conv) {
     using C = Cfg<D, kCodes>;
-    constexpr int kLanes = D / 16, kRowsAtOnce = 32 / kLanes, kSteps = 32 / kRowsAtOnce;  // of a row; of a warp
+    constexpr int kLanes = D / 16, kRowsAtOnce = 32 / kLanes, kSteps = kPieceRows / kRowsAtOnce;  // of a row; of a piece
+    constexpr int kTilePieces = kKeys / kPieceRows;
     const Params &p = tp.p;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
-    const int c = lane % kLanes, odd = (c ^ (c >> 2)) & 1, row0 = kConvertRows * warp;
-    const int nb = kConvertRows / tp.box_rows;  // boxes of the rows: 1, or 2 where pages have 16
+    const int c = lane % kLanes, odd = (c ^ (c >> 2)) & 1;
+    const int nb = kPieceRows / tp.box_rows, gap = nb == 2 ? (lane >> 4) * 16 : 0;  // boxes of a piece: 2 where pages have 16 rows
     uint8_t *codes = smem + C::kCodesAt + warp * C::kRing * C::kPiece;
     uint8_t *code_scales = smem + C::kCodeScalesAt + warp * C::kRing * 256;
     landed += warp * C::kRing;
-    uint32_t g = 0, issued = 0;  // tiles (K, V, K, ..) spread and copied, over all segments
+    uint32_t g0 = 0;               // tiles of the segments before
+    uint32_t taken = 0, sent = 0;  // pieces of this warp, over all segments
     bool ok = true;
     while (ok && run.u < run.end) {
         int s0, s1;
         if (!run_segment(p, run, s0, s1)) break;
         const Item &it = run.item;
         const int n = s1 - s0;
-        const uint32_t end = g + 2 * n, first = g;
-        // the pages of 32 boxes at a time, nb of a tile, and of the 32 after them
+        // the segment's pieces first, first + kConvertWarps, ..: tile i / kTilePieces (K and V in turn)
+        const int first = int((warp + kConvertWarps - (g0 * kTilePieces) % kConvertWarps) % kConvertWarps);
+        const int all = 2 * n * kTilePieces, mine = first < all ? (all - 1 - first) / kConvertWarps + 1 : 0;
+        auto key_of = [&](int i) {  // of this warp's i-th piece
+            const int at = first + i * kConvertWarps;
+            return tile_key<kKeys, true>(it, s0 + at / (2 * kTilePieces)) + at % kTilePieces * kPieceRows;
+        };
+        // the pages of 32 boxes at a time, and of the 32 after them
         auto page_at = [&](int i) {
-            const int j = nb == 2 ? i >> 1 : i;
-            if (j >= n) return 0;
+            const int piece = nb == 2 ? i >> 1 : i;
+            if (piece >= mine) return 0;
             // past the tensor, read as zeros: a box past the end, one between the sinks and every row's
             // window (its page may be gone already) and a bad page
-            const int key = tile_key<kKeys, true>(it, s0 + j) + row0 + (nb == 2 ? (i & 1) * tp.box_rows : 0);
+            const int key = key_of(piece) + (nb == 2 ? (i & 1) * tp.box_rows : 0);
             const int pg = key >= it.len || (key + tp.box_rows <= it.seen && key >= p.sinks)
                                ? -1
                                : page_of(p.b, it.b, key, p.hdr);
             return pg < 0 ? p.b.num_pages : pg;
         };
-        int pages = page_at(lane), pages_next = n * nb > 32 ? page_at(32 + lane) : 0;
+        int pages = page_at(lane), pages_next = mine * nb > 32 ? page_at(32 + lane) : 0;
+        int i_sent = 0;
         auto issue = [&]() {
-            const int j = int(issued - first) >> 1, kv = int(issued - first) & 1;
-            if (kv == 0 && j > 0 && ((j * nb) & 31) == 0) {
+            if (i_sent > 0 && ((i_sent * nb) & 31) == 0) {
                 pages = pages_next;
-                pages_next = page_at(j * nb + 32 + lane);
+                pages_next = page_at(i_sent * nb + 32 + lane);
                 __syncwarp();
             }
             const int box = lane >> 1;  // lanes 0 .. 2 nb - 1: a box's codes, its scales
-            const int z = __shfl_sync(0xffffffffu, pages, (j * nb + box) & 31) * p.b.Hkv + it.kh;
-            const uint32_t slot = issued % C::kRing;
+            const int z = __shfl_sync(0xffffffffu, pages, (i_sent * nb + box) & 31) * p.b.Hkv + it.kh;
+            const bool value = ((first + i_sent * kConvertWarps) / kTilePieces & 1) != 0;
+            const uint32_t slot = sent % C::kRing;
             uint64_t *bar = &landed[slot];
-            if (lane == 0) mbar_arrive_expect_tx(bar, C::kPiece + kConvertRows * 4);
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::kPiece + kPieceRows * 4);
             __syncwarp();
             if (box < nb) {
-                const int row = (tile_key<kKeys, true>(it, s0 + j) + row0 + box * tp.box_rows) & (p.b.page - 1);
+                const int row = (key_of(i_sent) + box * tp.box_rows) & (p.b.page - 1);
                 if ((lane & 1) == 0)
-                    tma_box3(smem_addr(codes + slot * C::kPiece + box * tp.box_rows * D), kv == 0 ? &tp.mk : &tp.mv, 0,
+                    tma_box3(smem_addr(codes + slot * C::kPiece + box * tp.box_rows * D), value ? &tp.mv : &tp.mk, 0,
                              row, z, bar);
                 else
-                    tma_box2(smem_addr(code_scales + slot * 256 + box * 128), kv == 0 ? &tp.mks : &tp.mvs, row, z, bar);
+                    tma_box2(smem_addr(code_scales + slot * 256 + box * 128), value ? &tp.mvs : &tp.mks, row, z, bar);
             }
             __syncwarp();
-            ++issued;
+            ++i_sent;
+            ++sent;
         };
-        for (int i = 0; i < C::kRing && issued < end; ++i) issue();
-        for (; ok && g < end; ++g) {
-            const uint32_t slot = g % C::kRing, st = g % C::kStages;
-            if (!(ok = warp_wait(&landed[slot], (g / C::kRing) & 1u, p, 67))) break;
+        for (int i = 0; i < C::kRing && i < mine; ++i) issue();
+        for (int i = 0; i < mine; ++i) {
+            const int at = first + i * kConvertWarps, quarter = at % kTilePieces;
+            const uint32_t g = g0 + uint32_t(at / kTilePieces), st = g % C::kStages, slot = taken % C::kRing;
+            if (!(ok = warp_wait(&landed[slot], (taken / C::kRing) & 1u, p, 67))) break;
+            ++taken;
             if (g >= uint32_t(C::kStages) && !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 68))) break;
             const uint8_t *from = codes + slot * C::kPiece;
-            uint8_t *tile = smem + st * C::kTileB;
+            uint8_t *tile = smem + st * C::kTileB + quarter * kPieceRows * 128;
+            const float f = reinterpret_cast<const float *>(code_scales + slot * 256)[lane + gap];
 #pragma unroll
-            for (int i0 = 0; i0 < kSteps; i0 += 4) {
+            for (int k0 = 0; k0 < kSteps; k0 += 4) {
                 uint4 x[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = *reinterpret_cast<const uint4 *>(from + ((i0 + i) * 32 + lane) * 16);
+                for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const uint4 *>(from + ((k0 + k) * 32 + lane) * 16);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = row0 + (i0 + i) * kRowsAtOnce + lane / kLanes;
-                    const CodePair<T> a(x[i].x), b(x[i].y), d(x[i].z), e(x[i].w);
+                for (int k = 0; k < 4; ++k) {
+                    const int r = (k0 + k) * kRowsAtOnce + lane / kLanes;
+                    const CodePair<T> a(x[k].x), b(x[k].y), d(x[k].z), e(x[k].w);
                     const uint4 lo = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(),
                                                 b.template take<0, 1>(), b.template take<2, 3>());
                     const uint4 hi = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(),
                                                 e.template take<0, 1>(), e.template take<2, 3>());
                     uint8_t *row = tile + (c >> 2) * C::kSlab + r * 128;
-                    const int at = 2 * (c & 3) + odd;
-                    *reinterpret_cast<uint4 *>(row + ((at ^ (r & 7)) << 4)) = odd != 0 ? hi : lo;
-                    *reinterpret_cast<uint4 *>(row + ((at ^ 1 ^ (r & 7)) << 4)) = odd != 0 ? lo : hi;
+                    const int chunk = 2 * (c & 3) + odd;
+                    *reinterpret_cast<uint4 *>(row + ((chunk ^ (r & 7)) << 4)) = odd != 0 ? hi : lo;
+                    *reinterpret_cast<uint4 *>(row + ((chunk ^ 1 ^ (r & 7)) << 4)) = odd != 0 ? lo : hi;
                 }
             }
-            {
-                // past the sequence's end the scales may be anything.  A key's is above 0: a hidden score is an
-                // infinity, which 0 would make a NaN (the codes of a scale of 0 are 0 themselves).
-                const int j = int(g - first) >> 1, kv = int(g - first) & 1;
-                const bool past = tile_key<kKeys, true>(it, s0 + j) + row0 + lane >= it.len;
-                const int gap = nb == 2 ? (lane >> 4) * 16 : 0;
-                float f = reinterpret_cast<const float *>(code_scales + slot * 256)[lane + gap];
-                if (kv == 0) f = past ? 1.f : f <= 1.17549435e-38f ? 1.17549435e-38f : f;
-                else f = past ? 0.f : f;
-                reinterpret_cast<float *>(smem + C::kScalesAt)[((g >> 1) % C::kScaleTiles) * (2 * kKeys) + kv * kKeys +
-                                                               row0 + lane] = f;
-            }
+            // past the sequence's end the scales may be anything.  A key's is above 0: a hidden score is an
+            // infinity, which 0 would make a NaN (the codes of a scale of 0 are 0 themselves).
+            const bool past = key_of(i) + lane >= it.len, value = (at / kTilePieces & 1) != 0;
+            const float kf = f * k_unit;
+            reinterpret_cast<float *>(smem + C::kScalesAt)[((g >> 1) % C::kScaleTiles) * (2 * kKeys) +
+                                                           (value ? kKeys : 0) + quarter * kPieceRows + lane] =
+                value  ? (past ? 0.f : f)
+                : past ? 1.f
+                       : (kf <= 1.17549435e-38f ? 1.17549435e-38f : kf);
             // these stores before the products' reads of them, the reads before the copy into their place
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&conv[st]);
             __syncwarp();
-            if (issued < end) issue();
+            if (i_sent < mine) issue();
         }
+        g0 += 2 * n;
         next();
     }
-    for (uint32_t i = g; i < issued; ++i)  // copies in flight after a time-out land before the CTA exits
-        warp_wait(&landed[i % C::kRing], (i / C::kRing) & 1u, p, 53, kDrainNs);
+    for (; taken < sent; ++taken)  // copies in flight after a time-out land before the CTA exits
+        warp_wait(&landed[taken % C::kRing], (taken / C::kRing) & 1u, p, 53, kDrainNs);
 }
 
 // How a score follows from q.k: by a positive scale, capped after a positive
@@ -398,7 +409,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 8 + withheld(p)), mbar_init(&p_ready[h][1], 8), mbar_init(&o_full[h], 1);
         mbar_init(&drain, 1);
         if (kQ8) {
-            for (int i = 0; i < C::kStages; ++i) mbar_init(&conv[i], kConvertWarps);
+            for (int i = 0; i < C::kStages; ++i) mbar_init(&conv[i], kKeys / kPieceRows);
             for (int i = 0; i < kConvertWarps * C::kRing; ++i) mbar_init(&landed[i], 1);
         }
         prefetch_map(&tp.mq);
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     __syncthreads();
 
     if (kQ8 && warp >= kConvertWarp) {
-        convert_tiles<T, D>(tp, run, next, smem, landed, empty, conv);
+        convert_tiles<T, D>(tp, kMode == kScaled ? p.scale_log2 : 1.f, run, next, smem, landed, empty, conv);
     } else if (warp >= kCopyWarp && warp < kCopyWarp + (kQ8 ? 1 : kCopyWarps)) {
         // ---- Q of each segment and its K tiles, or its V tiles
         const int me = warp - kCopyWarp;
@@ -735,9 +746,10 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                         : kMode == kAny && capped ? __all_sync(0xffffffffu, most * fabsf(p.cap_y) < kTanhNear)
                                                   : false;
                     if (mt != -CUDART_INF_F)
-                        mt = kMode == kCapped ? capped_far(mt, p)
-                             : capped         ? score<true>(mt * sign, p)
-                                              : score<false>(mt * sign, p);
+                        mt = kMode == kCapped            ? capped_far(mt, p)
+                             : capped                    ? score<true>(mt * sign, p)
+                             : kQ8 && kMode == kScaled   ? mt
+                                                         : score<false>(mt * sign, p);
                     uint32_t ref_up = ref;  // with this tile's scales
                     if (kRef) {
                         const float4 x = *reinterpret_cast<const float4 *>(vs - 64 * ch + 4 * lane);
@@ -782,10 +794,13 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     auto take = [&](auto is_plain, int c, const float (&raw)[16]) {
                         constexpr bool kPlain = decltype(is_plain)::value;
                         uint32_t w[8];
+                        constexpr bool kFused = kQ8 && kMode == kScaled;  // the scale is a factor of K's scales
                         float u[16];
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
-                            if (kQ8) {
+                            float4 ksc = make_float4(1.f, 1.f, 1.f, 1.f);
+                            if (kFused) ksc = *reinterpret_cast<const float4 *>(ks + 16 * c + i);
+                            if (kQ8 && !kFused) {
                                 scaled(raw + i, ks + 16 * c + i, u + i);
                             } else {
 #pragma unroll
@@ -835,8 +850,8 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                                 e2[0] = fma2(r2, d2[1], kPlain ? base2 : fma2(x2[0], hide2, base2));
                                 e2[1] = fma2(r2, d2[0], kPlain ? base2 : fma2(x2[1], hide2, base2));
                             } else {
-                                e2[0] = fma2(e2[0], scale2, base2);
-                                e2[1] = fma2(e2[1], scale2, base2);
+                                e2[0] = fma2(e2[0], kFused ? pack2(ksc.x, ksc.y) : scale2, base2);
+                                e2[1] = fma2(e2[1], kFused ? pack2(ksc.z, ksc.w) : scale2, base2);
                             }
                             // codes: the values' scales join the weights
                             float4 vsc = make_float4(1.f, 1.f, 1.f, 1.f);
@@ -1012,7 +1027,7 @@ cudaError_t launch_form(const AttnArgs &a, const Params &p, int num_sms, cudaStr
     tp.p.tt = 2 * tp.tth;
     tp.p.tt_magic = 0xffffffffu / unsigned(tp.p.tt) + 1;
     tp.p.extra = kExtra;
-    tp.box_rows = std::min(a.b.page, kForm == kCodes ? kConvertRows : kKeys);
+    tp.box_rows = std::min(a.b.page, kForm == kCodes ? kPieceRows : kKeys);
     const uint32_t fmt = a.type == MOE_BF16 ? (1u << 7) | (1u << 10) : 0u;  // A and B bf16
     tp.idesc_qk = tc::idesc_f16_f32(kHalf, kKeys) | fmt;
     tp.idesc_pv = tc::idesc_f16_f32(kHalf, a.b.D) | fmt | (1u << 16);       // B: N contiguous
