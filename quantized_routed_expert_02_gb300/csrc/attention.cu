@@ -423,7 +423,7 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     // 57.5 and 58.3; 8 over 93 of one 5.5 and 9.7).
     if (long(max_new) * G > kMaxRows)
         return (form == 0 ? launch_tc : form == 1 ? launch_tc_masks : launch_tc_codes)(a, base, num_sms, s);
-    if (form == 2) return launch_stream_codes(a, base, num_sms, s);
+    if (form == 2) return launch_stream_codes(a, base, max_new, num_sms, s);
     StreamParams sp = {};
     sp.p = base;
     sp.p.tt = kMaxRows / G;

@@ -2,33 +2,54 @@
 // (moe_attention_cache with scales, up to 16 rows): the streaming kernel for half the bytes.
 //
 // A key is k_scale * code, so a score is k_scale * (q . code), the product by
-// mma.sync m16n8k16 on codes made 16-bit operands in registers (exact), the scale in
-// fp32 behind it; a weight takes its value's scale before it is rounded for the product with V.
+// mma.sync m16n8k16 on codes made fp16 operands in registers (exact), the scale in fp32
+// behind it; a weight takes its value's scale before it is rounded for the product with V.
+// bf16 queries become fp16 ones, each row by a power of two that puts its largest
+// element below 2^15: a bf16 element within 2^-28 of that is exact, the others are off by less
+// than 2^-39 of it, and fp16 codes cost 5 instructions for 4, bf16 ones 8.
 //
-// Bytes bound as the 16-bit kernel is, at twice the keys per byte, so a piece is 32
-// keys and what is done once a piece (maxima, rescales, waits) costs as much per byte as
-// there.  The fragments need no shuffles: ldmatrix gives a lane four channels in a row of a
-// key's codes, which as two pairs are an operand of the instruction for some order of the
-// channels, and the queries are read in the same order; transposed it gives two channels of
-// two keys, whose even and odd channels are two tiles of the output.
+// Bytes bound as the 16-bit kernel is, at twice the keys per byte, so what counts is the
+// instructions per key.  The products are transposed, S^T = K Q^T and O^T = V^T P^T: keys, and
+// channels, fill the instruction's 16 rows and the query rows its 8 columns, once or
+// twice, so that up to 8 rows (a token of a group of 8) pay for no padding.  The fragments need no
+// shuffles: ldmatrix gives a lane four channels in a row of a key's codes, which as two
+// pairs are an operand of the instruction for some order of the channels, and the queries
+// are read in the same order; transposed it gives two channels of two keys, an operand
+// whose rows are the even and the odd channels.  The weights turn in registers (movmatrix).
 #include <cuda.h>
 #include <type_traits>
 
 #include "attention_stream.cuh"
 #include "codes.cuh"
+#include "tcgen05.cuh"
 
 namespace moeq4k {
 namespace attn {
 
 constexpr int kCodePiece = 32;                      // keys of a piece
+constexpr float kGrowth = 8.f;                      // log2 growth of a maximum that moves the reference
 constexpr int kCodeTile = kWarps * kCodePiece;      // keys of a tile: as many bytes as the 16-bit kernel's
 
 struct CodesParams {
-    CUtensorMap mk, mv, mks, mvs;
+    CUtensorMap mk, mv;
     Params p;
     int boxes;         // of a piece: 1, or 2 where pages have 16 rows
     bool join_launch;  // split items are joined by a second launch
 };
+
+// An 8 x 8 matrix of 16-bit values, a row's two in a lane, transposed.
+__device__ __forceinline__ uint32_t turned(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// Two queries as the fp16 operand: a bf16 pair times its row's factor.
+__device__ __forceinline__ uint32_t query_pair(__half, uint32_t w, float) { return w; }
+__device__ __forceinline__ uint32_t query_pair(__nv_bfloat16, uint32_t w, float f) {
+    const float2 x = Pair<__nv_bfloat16>::load(w);
+    return Pair<__half>::make(x.x * f, x.y * f);
+}
 
 __device__ __forceinline__ void tma_codes(void *dst, const CUtensorMap *map, int row, int z, uint64_t *bar) {
     asm volatile(
@@ -37,31 +58,24 @@ __device__ __forceinline__ void tma_codes(void *dst, const CUtensorMap *map, int
         "l"(map), "r"(0), "r"(row), "r"(z), "r"(smem_addr(bar))
         : "memory");
 }
-__device__ __forceinline__ void tma_scales(void *dst, const CUtensorMap *map, int row, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-        "{%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(row), "r"(z), "r"(smem_addr(bar))
-        : "memory");
-}
-
 // Byte of 16-byte chunk c of row r as the copy's swizzle places it.
 template <int D>
 __device__ __forceinline__ int code_chunk(int r, int c) {
     return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <typename T, int D, bool kCap>
+// kN: tiles of 8 query rows.
+template <typename T, int D, bool kCap, int kN>
 __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __grid_constant__ CodesParams sp) {
     constexpr int kPiece = kCodePiece, kTile = kCodeTile;
     constexpr int kBytes = kPiece * D;                   // of a piece's keys, or values
     constexpr int kStages = kRing / (2 * kBytes);
+    constexpr bool kScaleQ = std::is_same_v<T, __nv_bfloat16>;
     constexpr int kOS = row_floats(D);
     static_assert(kMaxRows * kOS * 4 <= kRing, "a warp's sums fit its ring");
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[kWarps][kStages];
-    // of keys, of values; a box's begin on 128 bytes, as a copy's place has to
-    __shared__ __align__(128) float scales[kWarps][kStages][2][2 * kPiece];
+    __shared__ __align__(16) float scales[kWarps][kStages][2][kPiece];  // of keys, of values
     __shared__ float sm_m[kWarps][kMaxRows], sm_l[kWarps][kMaxRows];
     __shared__ unsigned failed;
     __shared__ bool joins;
@@ -71,17 +85,14 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
     const int gid = lane >> 2, tig = lane & 3;
     const int G = p.b.Hq / p.b.Hkv;
     const int nb = sp.boxes, box_rows = kPiece / nb;
-    const int gap = nb == 2 ? 16 : 0;  // in the scales' places, ahead of a piece's key 16
     uint8_t *ring = smem + warp * kRing;
     if (tid == 0) {
         failed = 0;
         prefetch_map(&sp.mk);
         prefetch_map(&sp.mv);
-        prefetch_map(&sp.mks);
-        prefetch_map(&sp.mvs);
     }
     if (lane == 0)
-        for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1 + withheld(p));
+        for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1 + 32 + withheld(p));
     __syncwarp();
     fence_mbar_init();
     pdl_enter();
@@ -118,21 +129,44 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
             return pg < 0 ? p.b.num_pages : pg;
         };
         int pages = page_at(lane), pages_next = n * nb > 32 ? page_at(32 + lane) : 0;
-        Sight sight[2];  // of this thread's rows: gid, gid + 8
-        uint32_t qa[D / 16][4];
+        // the queries: row 8 x + gid, four channels in a row as the codes come
+        uint32_t qb[kN][D / 16][2];
+        float unit[kN][2];  // what the scores of this thread's rows (8 x + 2 tig, + 1) take back
+        Sight sight[kN][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = 8 * h + gid;
-            const int tok = r / G;
+        for (int x = 0; x < kN; ++x) {
+            const int r = 8 * x + gid, tok = r / G;
             const bool live = tok < it.nt;
-            sight[h] = row_sight(p, run.seq, live, it.row0 + tok, it.qt * p.tt + tok);
             const T *row = static_cast<const T *>(p.q) +
                            (size_t(it.row0 + (live ? tok : 0)) * p.b.Hq + it.kh * G + r % G) * D;
+            float factor = 1.f;
+            uint2 w[D / 16];
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {  // four channels in a row, as the codes come
-                const uint2 w = *reinterpret_cast<const uint2 *>(row + 16 * k + 4 * tig);
-                qa[k][h] = live ? w.x : 0u;
-                qa[k][2 + h] = live ? w.y : 0u;
+            for (int k = 0; k < D / 16; ++k)
+                w[k] = live ? *reinterpret_cast<const uint2 *>(row + 16 * k + 4 * tig) : make_uint2(0u, 0u);
+            if (kScaleQ) {
+                float most = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const float2 a = Pair<T>::load(w[k].x), b = Pair<T>::load(w[k].y);
+                    most = fmaxf(fmaxf(most, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+                }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                // 2^14 over the largest's power of two, at most 2^126
+                factor = __uint_as_float(min(268u - (__float_as_uint(most) >> 23), 253u) << 23);
+            }
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                qb[x][k][0] = query_pair(T(), w[k].x, factor);
+                qb[x][k][1] = query_pair(T(), w[k].y, factor);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int mine = 8 * x + 2 * tig + c, t = mine / G;
+                unit[x][c] = kScaleQ ? 1.f / __shfl_sync(0xffffffffu, factor, 8 * tig + 4 * c) : 1.f;
+                sight[x][c] = row_sight(p, run.seq, t < it.nt, it.row0 + t, it.qt * p.tt + t);
+                __syncwarp();
             }
         }
         __syncwarp();
@@ -143,19 +177,32 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
                 pages_next = page_at(sent * nb + 32 + lane);
                 __syncwarp();
             }
-            const int box = lane >> 2;  // lanes 0 .. 4 nb - 1: box, and keys, values, scales of either
-            const int z = __shfl_sync(0xffffffffu, pages, (sent * nb + box) & 31) * p.b.Hkv + it.kh;
             const uint32_t st = issued % kStages;
             uint64_t *bar = &full[warp][st];
-            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kBytes + 2 * kPiece * 4);
-            __syncwarp();
-            if (box < nb) {
-                const int row = (key_of(sent) + box * box_rows) & (p.b.page - 1);
-                uint8_t *dst = ring + st * (2 * kBytes) + box * box_rows * D;
-                if ((lane & 3) == 0) tma_codes(dst, &sp.mk, row, z, bar);
-                else if ((lane & 3) == 1) tma_codes(dst + kBytes, &sp.mv, row, z, bar);
-                else if ((lane & 3) == 2) tma_scales(&scales[warp][st][0][box * kPiece], &sp.mks, row, z, bar);
-                else tma_scales(&scales[warp][st][1][box * kPiece], &sp.mvs, row, z, bar);
+            const int row0 = key_of(sent) & (p.b.page - 1);
+            // the scales, four keys a lane, by copies of the lanes' own: a copy of the copying unit for each
+            // kind in the way of the codes' took 48 ragged sequences from 36 to 43 us
+            const int kind = (lane >> 3) & 1, key = 4 * (lane & 7), box = key / box_rows;
+            const int pg = __shfl_sync(0xffffffffu, pages, (sent * nb + box) & 31);
+            if (lane < 16) {
+                const bool there = pg < p.b.num_pages;
+                // (boxes of a piece are of different pages, and begin at their first row)
+                const size_t at = (size_t(there ? pg : 0) * p.b.Hkv + it.kh) * p.b.page +
+                                  ((row0 + box * box_rows) & (p.b.page - 1)) + key % box_rows;
+                tc::cp_async_16_zfill(&scales[warp][st][kind][key], (kind == 0 ? p.ks : p.vs) + at, there);
+            }
+            cp_async_arrive_noinc(bar);
+            if (lane == 0) {
+                uint8_t *dst = ring + st * (2 * kBytes);
+                mbar_arrive_expect_tx(bar, 2 * kBytes);
+                tma_codes(dst, &sp.mk, row0, pg * p.b.Hkv + it.kh, bar);
+                tma_codes(dst + kBytes, &sp.mv, row0, pg * p.b.Hkv + it.kh, bar);
+            }
+            if (nb == 2 && lane == 4) {  // (whose keys are the second box's)
+                uint8_t *dst = ring + st * (2 * kBytes) + box_rows * D;
+                const int row = (row0 + box_rows) & (p.b.page - 1);
+                tma_codes(dst, &sp.mk, row, pg * p.b.Hkv + it.kh, bar);
+                tma_codes(dst + kBytes, &sp.mv, row, pg * p.b.Hkv + it.kh, bar);
             }
             __syncwarp();
             ++sent;
@@ -163,13 +210,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
         };
         for (int i = 0; i < kStages && i < n; ++i) issue();
 
-        // sums of channels 16 c + 4 tig + 2 x (tile 2 c) and one after each (tile 2 c + 1)
-        float o[D / 8][4], mx[2], l[2];
+        // sums of channels 16 c + 2 gid (o[][c][0 .. 1]) and the one after (o[][c][2 .. 3]) of this thread's rows
+        float o[kN][D / 16][4], mx[kN][2], l[kN][2];
         uint32_t ref = kRefLeast;
-        mx[0] = mx[1] = -CUDART_INF_F;
-        l[0] = l[1] = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        for (int x = 0; x < kN; ++x) {
+            mx[x][0] = mx[x][1] = -CUDART_INF_F;
+            l[x][0] = l[x][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
+        }
 
         bool ok = true;
         for (int i = 0; i < n; ++i) {
@@ -181,46 +231,41 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
             const int key0 = key_of(i);
             const uint32_t kb = smem_addr(ring + st * (2 * kBytes)), vb = kb + kBytes;
             const float *ks = scales[warp][st][0], *vs = scales[warp][st][1];
-            float s[4][4];
+            // S^T: matrices of keys 8 j .. 8 j + 7, the same 16 channels of each; s[][t]: keys 16 t + gid, + 8
+            float s[kN][2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-            // S: matrices of keys 8 j .. 8 j + 7, the same 16 channels of each
+            for (int x = 0; x < kN; ++x)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) s[x][t][0] = s[x][t][1] = s[x][t][2] = s[x][t][3] = 0.f;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint32_t b[4];
                 ldsm4(b, kb + code_chunk<D>(lane, k));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const CodePair<T> c(b[j]);
-                    mma16816<T>(s[j], qa[k], c.template take<0, 1>(), c.template take<2, 3>());
+                for (int t = 0; t < 2; ++t) {
+                    const CodePair<__half> lo(b[2 * t]), hi(b[2 * t + 1]);
+                    const uint32_t a[4] = {lo.template take<0, 1>(), hi.template take<0, 1>(), lo.template take<2, 3>(),
+                                           hi.template take<2, 3>()};
+#pragma unroll
+                    for (int x = 0; x < kN; ++x) mma16816<__half>(s[x][t], a, qb[x][k][0], qb[x][k][1]);
                 }
             }
             // keys that some row does not see
             const int all = p.tree != nullptr ? run.seq.len - run.seq.n - 1 : it.pos0;
             const bool edge = key0 + kPiece - 1 > all ||
                               (p.window > 0 && key0 <= last - p.window && key0 + kPiece > p.sinks);
-            uint32_t sees[2] = {0u, 0u};
-            if (edge) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) sees[h] = sight32(p, run.seq, sight[h], key0) >> (2 * tig);
-                __syncwarp();
-            }
-            // the values' scales; those past the sequence's end hold anything, and a weight of 0 takes them
+            // the scales of keys 8 j + gid; the values' past the sequence's end hold anything, and a weight of 0
+            // takes them
             const bool tail = key0 + kPiece > it.len;
-            float w[4][2];
+            float kf[4], vf[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 v = *reinterpret_cast<const float2 *>(vs + 8 * j + (j >> 1) * gap + 2 * tig);
-                w[j][0] = v.x;
-                w[j][1] = v.y;
-                if (tail) {
-                    if (key0 + 8 * j + 2 * tig >= it.len) w[j][0] = 0.f;
-                    if (key0 + 8 * j + 2 * tig + 1 >= it.len) w[j][1] = 0.f;
-                }
+                kf[j] = ks[8 * j + gid];
+                vf[j] = tail && key0 + 8 * j + gid >= it.len ? 0.f : vs[8 * j + gid];
             }
             float grown = 1.f;  // of the sums, where the scales' reference has grown
-            if (ScaleRef<T>::kUsed) {
-                const float mine = tail && key0 + lane >= it.len ? 0.f : vs[lane + (lane >> 4) * gap];
+            {
+                const float mine = tail && key0 + lane >= it.len ? 0.f : vs[lane];
                 const uint32_t top = ref_bits(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
                 if (top > ref) {
                     grown = __uint_as_float(ref) * over_ref(top);
@@ -228,57 +273,70 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
                 }
                 const float over = over_ref(ref);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j][0] *= over, w[j][1] *= over;
+                for (int j = 0; j < 4; ++j) vf[j] *= over;
             }
+            // The rows' reference maxima, and with them the sums, follow the scores only where one has grown by
+            // more than 2^kGrowth since (weights up to that are as exact in 16 bits as those up to 1, and
+            // the sums are fp32): in a short range new maxima are frequent.
+            float v[kN][2];
+            bool grows = grown != 1.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 k = *reinterpret_cast<const float2 *>(ks + 8 * j + (j >> 1) * gap + 2 * tig);
+            for (int x = 0; x < kN; ++x)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    s[j][c] = score<kCap>(s[j][c] * ((c & 1) != 0 ? k.y : k.x), p);
-                    if (edge && (sees[c >> 1] >> (8 * j + (c & 1)) & 1u) == 0u) s[j][c] = -CUDART_INF_F;
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t sees = 0xffffffffu;
+                    if (edge) sees = sight32(p, run.seq, sight[x][c], key0) >> gid;
+                    float top = -CUDART_INF_F;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float &z = s[x][j >> 1][2 * (j & 1) + c];
+                        z = score<kCap>(z * (kScaleQ ? kf[j] * unit[x][c] : kf[j]), p);
+                        if (edge && (sees >> (8 * j) & 1u) == 0u) z = -CUDART_INF_F;
+                        top = fmaxf(top, z);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                    v[x][c] = top;
+                    grows = grows || top > mx[x][c] + kGrowth;
+                }
+            if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                for (int x = 0; x < kN; ++x) {
+                    float cor[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float up = fmaxf(mx[x][c], v[x][c]);
+                        cor[c] = exp2_approx(mx[x][c] - (up == -CUDART_INF_F ? 0.f : up));  // -inf: nothing seen yet
+                        mx[x][c] = up;
+                        l[x][c] *= cor[c];
+                        cor[c] *= grown;
+                    }
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[x][j][0] *= cor[0], o[x][j][1] *= cor[1];
+                        o[x][j][2] *= cor[0], o[x][j][3] *= cor[1];
+                    }
                 }
             }
-            float cor[2];
+            // the weights times the values' scales, rounded to fp16 for the product (its two operands have one
+            // type); the sum l keeps the weights whole
+            uint32_t pb[kN][2][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float v = mx[h];
+            for (int x = 0; x < kN; ++x) {
+                float base[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v = fmaxf(v, fmaxf(s[j][2 * h], s[j][2 * h + 1]));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                const float base = v == -CUDART_INF_F ? 0.f : v;  // nothing seen yet
-                cor[h] = exp2_approx(mx[h] - base);
-                mx[h] = v;
-                float sum = 0.f;
+                for (int c = 0; c < 2; ++c) base[c] = mx[x][c] == -CUDART_INF_F ? 0.f : mx[x][c];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        s[j][2 * h + c] = exp2_approx(s[j][2 * h + c] - base);
-                    sum += s[j][2 * h] + s[j][2 * h + 1];
-                }
-                l[h] = l[h] * cor[h] + sum;
-                cor[h] *= grown;
-            }
-            // the weights times the values' scales, rounded to the 16-bit type for the product (its two
-            // operands have one type); the sum l keeps the weights whole
-            uint32_t pa[2][4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int j = 2 * t + (x >> 1), h = x & 1;
-                    pa[t][x] = Pair<T>::make(s[j][2 * h] * w[j][0], s[j][2 * h + 1] * w[j][1]);
-                }
-            if (__any_sync(0xffffffffu, cor[0] != 1.f || cor[1] != 1.f)) {
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[j][0] *= cor[0], o[j][1] *= cor[0];
-                    o[j][2] *= cor[1], o[j][3] *= cor[1];
+                    const float a = exp2_approx(s[x][j >> 1][2 * (j & 1)] - base[0]);
+                    const float b = exp2_approx(s[x][j >> 1][2 * (j & 1) + 1] - base[1]);
+                    l[x][0] += a;
+                    l[x][1] += b;
+                    pb[x][j >> 1][j & 1] = turned(Pair<__half>::make(a * vf[j], b * vf[j]));
                 }
             }
-            // O: matrices (keys 0-7 and 8-15 of 16, channel chunk c), then of chunk c + 1, transposed
+            // O^T: matrices (keys 0-7 and 8-15 of 16, channel chunk c), then of chunk c + 1, transposed
             const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -287,10 +345,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
                     uint32_t b[4];
                     ldsm4_trans(b, vb + code_chunk<D>(16 * t + vrow, c + vc));
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const CodePair<T> lo(b[2 * x]), hi(b[2 * x + 1]);
-                        mma16816<T>(o[2 * (c + x)], pa[t], lo.template take<0, 2>(), hi.template take<0, 2>());
-                        mma16816<T>(o[2 * (c + x) + 1], pa[t], lo.template take<1, 3>(), hi.template take<1, 3>());
+                    for (int y = 0; y < 2; ++y) {
+                        const CodePair<__half> lo(b[2 * y]), hi(b[2 * y + 1]);
+                        const uint32_t a[4] = {lo.template take<0, 2>(), lo.template take<1, 3>(),
+                                               hi.template take<0, 2>(), hi.template take<1, 3>()};
+#pragma unroll
+                        for (int x = 0; x < kN; ++x) mma16816<__half>(o[x][c + y], a, pb[x][t][0], pb[x][t][1]);
                     }
                 }
             ++done;
@@ -309,25 +369,26 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
 
         // the warps' sums into their rings, the rows' statistics beside them
         float *so = reinterpret_cast<float *>(ring);
-        const float unit = ScaleRef<T>::kUsed ? __uint_as_float(ref) : 1.f;
+        const float back = __uint_as_float(ref);
         __syncwarp();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v = l[h];
-            v += __shfl_xor_sync(0xffffffffu, v, 1);
-            v += __shfl_xor_sync(0xffffffffu, v, 2);
-            const int r = 8 * h + gid;
-            if (tig == 0) {
-                sm_m[warp][r] = mx[h];
-                sm_l[warp][r] = v;
-            }
-            __syncwarp();
+        for (int x = 0; x < kN; ++x)
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c)
-                *reinterpret_cast<float4 *>(so + r * kOS + 16 * c + 4 * tig) =
-                    make_float4(o[2 * c][2 * h] * unit, o[2 * c + 1][2 * h] * unit, o[2 * c][2 * h + 1] * unit,
-                                o[2 * c + 1][2 * h + 1] * unit);
-        }
+            for (int c = 0; c < 2; ++c) {
+                float sum = l[x][c];
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+                const int r = 8 * x + 2 * tig + c;
+                if (gid == 0) {
+                    sm_m[warp][r] = mx[x][c];
+                    sm_l[warp][r] = sum;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                    *reinterpret_cast<float2 *>(so + r * kOS + 16 * j + 2 * gid) =
+                        make_float2(o[x][j][c] * back, o[x][j][2 + c] * back);
+            }
         __syncthreads();
         __syncwarp();
         if (failed != 0) return;
@@ -342,46 +403,56 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
 
 constexpr int kCodesSmem = kWarps * kRing;
 
+// f on every form of the kernel for a type.
+template <typename T, typename F>
+void each_codes(F f) {
+    f(attention_codes_kernel<T, 64, false, 1>);
+    f(attention_codes_kernel<T, 64, false, 2>);
+    f(attention_codes_kernel<T, 64, true, 1>);
+    f(attention_codes_kernel<T, 64, true, 2>);
+    f(attention_codes_kernel<T, 128, false, 1>);
+    f(attention_codes_kernel<T, 128, false, 2>);
+    f(attention_codes_kernel<T, 128, true, 1>);
+    f(attention_codes_kernel<T, 128, true, 2>);
+}
+
 cudaError_t init_stream_codes() {
     cudaError_t e = cudaSuccess;
-    auto of = [&](auto kernel) {
+    auto set = [&](auto kernel) {
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCodesSmem);
     };
-    auto with = [&](auto type) {
-        using T = decltype(type);
-        of(attention_codes_kernel<T, 64, false>);
-        of(attention_codes_kernel<T, 64, true>);
-        of(attention_codes_kernel<T, 128, false>);
-        of(attention_codes_kernel<T, 128, true>);
-    };
-    with(__half());
-    with(__nv_bfloat16());
+    each_codes<__half>(set);
+    each_codes<__nv_bfloat16>(set);
     return e;
 }
 
-cudaError_t launch_stream_codes(const AttnArgs &a, Params p, int num_sms, cudaStream_t s) {
+cudaError_t launch_stream_codes(const AttnArgs &a, Params p, int max_new, int num_sms, cudaStream_t s) {
     CodesParams sp = {};
-    p.tt = kMaxRows / (a.b.Hq / a.b.Hkv);
+    const int G = a.b.Hq / a.b.Hkv, tiles = long(max_new) * G <= 8 ? 1 : 2;
+    p.tt = 8 * tiles / G;
     p.tt_magic = 0xffffffffu / unsigned(p.tt) + 1;
     p.extra = kExtra;
     sp.p = p;
     sp.boxes = a.b.page < kCodePiece ? 2 : 1;
     const int box_rows = kCodePiece / sp.boxes;
-    if (!encode_codes_map(&sp.mk, a.k, a.b, box_rows, false) || !encode_codes_map(&sp.mv, a.v, a.b, box_rows, false) ||
-        !encode_scales_map(&sp.mks, a.ks, a.b, box_rows) || !encode_scales_map(&sp.mvs, a.vs, a.b, box_rows))
+    if (!encode_codes_map(&sp.mk, a.k, a.b, box_rows, false) || !encode_codes_map(&sp.mv, a.v, a.b, box_rows, false))
         return cudaErrorInvalidValue;
     const int grid = std::min(2 * num_sms, kMaxCtas);
     sp.join_launch = joins_by_launch(a.b, grid, kCodeTile);
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(kCodesSmem), s, sp);
     };
-    auto of = [&](auto type, auto cap) {
+    auto of = [&](auto type, auto cap, auto n) {
         using T = decltype(type);
         constexpr bool kCap = decltype(cap)::value;
-        return a.b.D == 64 ? go(attention_codes_kernel<T, 64, kCap>) : go(attention_codes_kernel<T, 128, kCap>);
+        constexpr int kN = decltype(n)::value;
+        return a.b.D == 64 ? go(attention_codes_kernel<T, 64, kCap, kN>) : go(attention_codes_kernel<T, 128, kCap, kN>);
     };
-    auto with = [&](auto type) { return p.cap_in != 0.f ? of(type, std::true_type()) : of(type, std::false_type()); };
+    auto rows = [&](auto type, auto cap) {
+        return tiles == 1 ? of(type, cap, std::integral_constant<int, 1>()) : of(type, cap, std::integral_constant<int, 2>());
+    };
+    auto with = [&](auto type) { return p.cap_in != 0.f ? rows(type, std::true_type()) : rows(type, std::false_type()); };
     const cudaError_t e = a.type == MOE_F16 ? with(__half()) : with(__nv_bfloat16());
     if (e != cudaSuccess || !sp.join_launch) return e;
     return launch_join(p, a.type, grid, kPartRows, kPartRows, p.tt, s);

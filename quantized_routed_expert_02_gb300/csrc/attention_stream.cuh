@@ -159,7 +159,7 @@ inline bool joins_by_launch(const PagedBatch &b, int grid, int tile) {
 
 // The same over a cache of 8-bit codes (any masks).
 cudaError_t init_stream_codes();
-cudaError_t launch_stream_codes(const AttnArgs &a, Params p, int num_sms, cudaStream_t s);
+cudaError_t launch_stream_codes(const AttnArgs &a, Params p, int max_new, int num_sms, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace moeq4k

@@ -391,7 +391,7 @@ constexpr float kCapNear = 64.f;
 template <typename T, int D, int kMode, int kForm>
 __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(const __grid_constant__ TcParams tp) {
     using C = Cfg<D, kForm>;
-    constexpr bool kMasks = kForm != kPaged, kQ8 = kForm == kCodes, kRef = kQ8 && ScaleRef<T>::kUsed;
+    constexpr bool kMasks = kForm != kPaged, kQ8 = kForm == kCodes, kRef = kQ8 && std::is_same_v<T, __half>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2][2],
         o_full[2], drain, conv[kQ8 ? C::kStages : 1], landed[kQ8 ? kConvertWarps * C::kRing : 1];

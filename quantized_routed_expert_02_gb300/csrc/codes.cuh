@@ -43,17 +43,8 @@ struct CodePair<__nv_bfloat16> {
 };
 
 // fp16 weights times the values' scales would leave the type's range: they are taken
-// over a power of two near the largest scale so far (kept in what is enough for any
-// value that fits the type), which the sums are multiplied by at the end.  bf16 has the range.
-template <typename T>
-struct ScaleRef {
-    static constexpr bool kUsed = false;
-};
-template <>
-struct ScaleRef<__half> {
-    static constexpr bool kUsed = true;
-};
-constexpr uint32_t kRefLeast = 0x0d800000u, kRefMost = 0x71800000u;  // 2^-100, 2^100
+// over a power of two near the largest scale so far, which the sums are multiplied by at the end.
+constexpr uint32_t kRefLeast = 0x00800000u, kRefMost = 0x7e800000u;  // 2^-126, 2^126
 // The power of two at or below a scale (its bits), in that range.
 __device__ __forceinline__ uint32_t ref_bits(uint32_t scale_bits) {
     return min(max(scale_bits & 0x7f800000u, kRefLeast), kRefMost);
