@@ -71,7 +71,6 @@ constexpr int form_threads(int form) { return form == kCodes ? kCodesThreads : k
 
 struct TcParams {
     CUtensorMap mq, mk, mv;
-    CUtensorMap mks, mvs;  // the scales of codes
     Params p;          // p.tt: tokens of an item (both halves)
     int tth;           // tokens of a half
     int box_rows;      // rows of a K/V box
@@ -84,24 +83,21 @@ struct Cfg {
     static constexpr int kSlab = 128 * 128;            // bytes of a 128-row slab
     static constexpr int kTileB = kCh * kSlab;         // a tile of K, of V, or of a half's Q
     static constexpr bool kQ8 = kForm == kCodes;
-    static constexpr int kStages = kQ8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
+    static constexpr int kStages = kQ8 ? (D == 128 ? 4 : 6) : (D == 128 ? 4 : 8);
     static constexpr int kQAt = kStages * kTileB;
     // Results on their way out, 32 rows x 32 channels of each softmax warp (over codes, whose form has
     // no room for them, only what two warps exchange).
     static constexpr int kStageOut = kQ8 ? 256 : 32 * 64;
     static constexpr int kOutAt = kQAt + 2 * kTileB;
-    // Codes: each converting warp's ring of pieces and their scales, and the scales as the softmax reads
-    // them, K's and V's of a tile.  Those are written when the tile kStages before has been used: for
-    // the keys' then the softmax is done with the tile kScaleTiles before.
-    static constexpr int kRing = 2;
+    // Codes: each converting warp's next piece and its scales, and the scales as the softmax reads them,
+    // K's and V's of a tile.  Those are written when the tile kStages before has been used: for the
+    // keys' that says that the softmax is done with the tile kScaleTiles before.
     static constexpr int kPiece = kPieceRows * D;
     static constexpr int kCodesAt = kOutAt + kSoftmaxWarps * kStageOut;
-    static constexpr int kCodeScalesAt = kCodesAt + (kQ8 ? kConvertWarps * kRing * kPiece : 0);
-    static constexpr int kScalesAt = kCodeScalesAt + (kQ8 ? kConvertWarps * kRing * 256 : 0);
-    static constexpr int kScaleTiles = D == 128 ? 2 : 4;
+    static constexpr int kCodeScalesAt = kCodesAt + (kQ8 ? kConvertWarps * kPiece : 0);
+    static constexpr int kScalesAt = kCodeScalesAt + (kQ8 ? kConvertWarps * kPieceRows * 4 : 0);
+    static constexpr int kScaleTiles = kStages / 2 + 1;
     static constexpr int kSmem = kScalesAt + (kQ8 ? kScaleTiles * 2 * kKeys * 4 : 0);
-    // A converting warp waits for each release of the stages that it uses, in turn.
-    static_assert(!kQ8 || kStages * (kKeys / kPieceRows) % kConvertWarps == 0, "the warps' pieces repeat with the ring");
 };
 
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
@@ -110,14 +106,6 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, i
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
         "{%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_box2(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-        "{%2, %3}], [%4];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
 }
 
@@ -253,12 +241,15 @@ __device__ __forceinline__ Run &run_place(Run &found, Run &mine) {
 }
 
 // A converting warp of the form over codes.  The pieces of the tiles (K, V, K, ..), 32 rows each,
-// go round the warps.  A warp copies its pieces (and their scales) ahead into a ring of its
-// own, spreads them to the 16-bit tile that the products read (8-row groups of 1024
-// bytes, 128 a row, swizzled) once that place is free, and puts the scales where the
-// softmax reads them (K's times `k_unit`).  A thread has 16 codes of a row at a time: the
-// two chunks that they become are stored in an order that keeps the eight lanes of a row
-// on different banks.
+// go round the warps.  A warp copies its next piece (and its scales) while it spreads one
+// to the 16-bit tile that the products read (8-row groups of 1024 bytes, 128 a row,
+// swizzled), once that place is free, and puts the scales where the softmax reads them
+// (K's times `k_unit`).  A thread has 16 codes of a row at a time: the two chunks that they
+// become are stored in an order that keeps the eight lanes of a row on different banks.
+//
+// A place's release is waited for by its parity, although a warp has pieces in two of three
+// tiles only: releases come in order, and that of the tile kStages before its last piece's, two
+// tiles back at most, is behind it.
 template <typename T, int D, typename F>
 __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, const Run &run, F next, uint8_t *smem,
                                               uint64_t *landed, uint64_t *empty, uint64_t *conv) {
@@ -268,10 +259,10 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
     const Params &p = tp.p;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
     const int c = lane % kLanes, odd = (c ^ (c >> 2)) & 1;
-    const int nb = kPieceRows / tp.box_rows, gap = nb == 2 ? (lane >> 4) * 16 : 0;  // boxes of a piece: 2 where pages have 16 rows
-    uint8_t *codes = smem + C::kCodesAt + warp * C::kRing * C::kPiece;
-    uint8_t *code_scales = smem + C::kCodeScalesAt + warp * C::kRing * 256;
-    landed += warp * C::kRing;
+    const int nb = kPieceRows / tp.box_rows;  // boxes of a piece: 1, or 2 where pages have 16 rows
+    uint8_t *codes = smem + C::kCodesAt + warp * C::kPiece;
+    float *code_scales = reinterpret_cast<float *>(smem + C::kCodeScalesAt) + warp * kPieceRows;
+    landed += warp;
     uint32_t g0 = 0;               // tiles of the segments before
     uint32_t taken = 0, sent = 0;  // pieces of this warp, over all segments
     bool ok = true;
@@ -307,53 +298,51 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
                 pages_next = page_at(i_sent * nb + 32 + lane);
                 __syncwarp();
             }
-            const int box = lane >> 1;  // lanes 0 .. 2 nb - 1: a box's codes, its scales
-            const int z = __shfl_sync(0xffffffffu, pages, (i_sent * nb + box) & 31) * p.b.Hkv + it.kh;
             const bool value = ((first + i_sent * kConvertWarps) / kTilePieces & 1) != 0;
-            const uint32_t slot = sent % C::kRing;
-            uint64_t *bar = &landed[slot];
-            if (lane == 0) mbar_arrive_expect_tx(bar, C::kPiece + kPieceRows * 4);
-            __syncwarp();
-            if (box < nb) {
-                const int row = (key_of(i_sent) + box * tp.box_rows) & (p.b.page - 1);
-                if ((lane & 1) == 0)
-                    tma_box3(smem_addr(codes + slot * C::kPiece + box * tp.box_rows * D), value ? &tp.mv : &tp.mk, 0,
-                             row, z, bar);
-                else
-                    tma_box2(smem_addr(code_scales + slot * 256 + box * 128), value ? &tp.mvs : &tp.mks, row, z, bar);
+            const int row0 = key_of(i_sent) & (p.b.page - 1), key = 4 * (lane & 7), box = key / tp.box_rows;
+            const int pg = __shfl_sync(0xffffffffu, pages, (i_sent * nb + box) & 31);
+            const int row = (row0 + box * tp.box_rows) & (p.b.page - 1);
+            if (lane < 8) {  // the scales, four keys a lane
+                const bool there = pg < p.b.num_pages;
+                const size_t at = (size_t(there ? pg : 0) * p.b.Hkv + it.kh) * p.b.page + row + key % tp.box_rows;
+                tc::cp_async_16_zfill(code_scales + key, (value ? p.vs : p.ks) + at, there);
             }
+            cp_async_arrive_noinc(landed);
+            if (lane == 0) mbar_arrive_expect_tx(landed, C::kPiece);
+            if (lane == 0 || (nb == 2 && lane == 4))  // (a lane of the box's)
+                tma_box3(smem_addr(codes + box * tp.box_rows * D), value ? &tp.mv : &tp.mk, 0, row,
+                         pg * p.b.Hkv + it.kh, landed);
             __syncwarp();
             ++i_sent;
             ++sent;
         };
-        for (int i = 0; i < C::kRing && i < mine; ++i) issue();
+        if (mine > 0) issue();
         for (int i = 0; i < mine; ++i) {
             const int at = first + i * kConvertWarps, quarter = at % kTilePieces;
-            const uint32_t g = g0 + uint32_t(at / kTilePieces), st = g % C::kStages, slot = taken % C::kRing;
-            if (!(ok = warp_wait(&landed[slot], (taken / C::kRing) & 1u, p, 67))) break;
+            const uint32_t g = g0 + uint32_t(at / kTilePieces), st = g % C::kStages;
+            if (!(ok = warp_wait(landed, taken & 1u, p, 67))) break;
             ++taken;
+            uint4 x[kSteps];
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) x[k] = *reinterpret_cast<const uint4 *>(codes + (k * 32 + lane) * 16);
+            const float f = code_scales[lane];
+            fence_proxy_async_smem();  // these reads before the next copy into their place
+            __syncwarp();
+            if (i_sent < mine) issue();
             if (g >= uint32_t(C::kStages) && !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 68))) break;
-            const uint8_t *from = codes + slot * C::kPiece;
             uint8_t *tile = smem + st * C::kTileB + quarter * kPieceRows * 128;
-            const float f = reinterpret_cast<const float *>(code_scales + slot * 256)[lane + gap];
 #pragma unroll
-            for (int k0 = 0; k0 < kSteps; k0 += 4) {
-                uint4 x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const uint4 *>(from + ((k0 + k) * 32 + lane) * 16);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = (k0 + k) * kRowsAtOnce + lane / kLanes;
-                    const CodePair<T> a(x[k].x), b(x[k].y), d(x[k].z), e(x[k].w);
-                    const uint4 lo = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(),
-                                                b.template take<0, 1>(), b.template take<2, 3>());
-                    const uint4 hi = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(),
-                                                e.template take<0, 1>(), e.template take<2, 3>());
-                    uint8_t *row = tile + (c >> 2) * C::kSlab + r * 128;
-                    const int chunk = 2 * (c & 3) + odd;
-                    *reinterpret_cast<uint4 *>(row + ((chunk ^ (r & 7)) << 4)) = odd != 0 ? hi : lo;
-                    *reinterpret_cast<uint4 *>(row + ((chunk ^ 1 ^ (r & 7)) << 4)) = odd != 0 ? lo : hi;
-                }
+            for (int k = 0; k < kSteps; ++k) {
+                const int r = k * kRowsAtOnce + lane / kLanes;
+                const CodePair<T> a(x[k].x), b(x[k].y), d(x[k].z), e(x[k].w);
+                const uint4 lo = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(),
+                                            b.template take<0, 1>(), b.template take<2, 3>());
+                const uint4 hi = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(),
+                                            e.template take<0, 1>(), e.template take<2, 3>());
+                uint8_t *row = tile + (c >> 2) * C::kSlab + r * 128;
+                const int chunk = 2 * (c & 3) + odd;
+                *reinterpret_cast<uint4 *>(row + ((chunk ^ (r & 7)) << 4)) = odd != 0 ? hi : lo;
+                *reinterpret_cast<uint4 *>(row + ((chunk ^ 1 ^ (r & 7)) << 4)) = odd != 0 ? lo : hi;
             }
             // past the sequence's end the scales may be anything.  A key's is above 0: a hidden score is an
             // infinity, which 0 would make a NaN (the codes of a scale of 0 are 0 themselves).
@@ -364,18 +353,16 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
                 value  ? (past ? 0.f : f)
                 : past ? 1.f
                        : (kf <= 1.17549435e-38f ? 1.17549435e-38f : kf);
-            // these stores before the products' reads of them, the reads before the copy into their place
-            fence_proxy_async_smem();
+            fence_proxy_async_smem();  // these stores before the products' reads of them
             __syncwarp();
             if (lane == 0) mbar_arrive(&conv[st]);
             __syncwarp();
-            if (i_sent < mine) issue();
         }
         g0 += 2 * n;
         next();
     }
-    for (; taken < sent; ++taken)  // copies in flight after a time-out land before the CTA exits
-        warp_wait(&landed[taken % C::kRing], (taken / C::kRing) & 1u, p, 53, kDrainNs);
+    // copies in flight after a time-out land before the CTA exits
+    if (taken < sent) warp_wait(landed, taken & 1u, p, 53, kDrainNs);
 }
 
 // How a score follows from q.k: by a positive scale, capped after a positive
@@ -394,7 +381,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     constexpr bool kMasks = kForm != kPaged, kQ8 = kForm == kCodes, kRef = kQ8 && std::is_same_v<T, __half>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2][2],
-        o_full[2], drain, conv[kQ8 ? C::kStages : 1], landed[kQ8 ? kConvertWarps * C::kRing : 1];
+        o_full[2], drain, conv[kQ8 ? C::kStages : 1], landed[kQ8 ? kConvertWarps : 1];
     __shared__ uint32_t tmem_base;
     __shared__ Run run_sh;
     __shared__ Run run_of[kQ8 ? kCodesThreads / 32 : 1];  // each warp's own, where registers are few
@@ -410,12 +397,11 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         mbar_init(&drain, 1);
         if (kQ8) {
             for (int i = 0; i < C::kStages; ++i) mbar_init(&conv[i], kKeys / kPieceRows);
-            for (int i = 0; i < kConvertWarps * C::kRing; ++i) mbar_init(&landed[i], 1);
+            for (int i = 0; i < kConvertWarps; ++i) mbar_init(&landed[i], 1 + 32);
         }
         prefetch_map(&tp.mq);
         prefetch_map(&tp.mk);
         prefetch_map(&tp.mv);
-        if (kQ8) prefetch_map(&tp.mks), prefetch_map(&tp.mvs);
     }
     __syncwarp();
     fence_mbar_init();
@@ -1036,9 +1022,6 @@ cudaError_t launch_form(const AttnArgs &a, const Params &p, int num_sms, cudaStr
                                : encode_pages_map(map, base, a.b, a.type, tp.box_rows);
     };
     if (!pages(&tp.mk, a.k) || !pages(&tp.mv, a.v) || !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
-        return cudaErrorInvalidValue;
-    if (kForm == kCodes && (!encode_scales_map(&tp.mks, a.ks, a.b, tp.box_rows) ||
-                            !encode_scales_map(&tp.mvs, a.vs, a.b, tp.box_rows)))
         return cudaErrorInvalidValue;
     const int grid = std::min(num_sms, kMaxGrid);
     const bool near_cap = a.softcap <= kCapNear && p.cap_in > 1e-30f;  // kCapped: kTanhMinusOne / cap_in is finite
