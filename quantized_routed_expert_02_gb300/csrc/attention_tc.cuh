@@ -46,8 +46,7 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kCopyWarps = 2;               // K tiles, V tiles
 constexpr int kMmaWarp = kSoftmaxWarps, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + kCopyWarps);
-// Over 8-bit codes: a copying warp for the queries, and six that copy the keys' and values' codes
-// and spread them, a piece of a tile each in turn.
+// Over 8-bit codes: a copying warp, and six that spread the codes, a piece of a tile each in turn.
 constexpr int kConvertWarp = kCopyWarp + 1, kConvertWarps = 6;
 constexpr int kPieceRows = 32;
 constexpr int kCodesThreads = 32 * (kConvertWarp + kConvertWarps);
@@ -71,6 +70,7 @@ constexpr int form_threads(int form) { return form == kCodes ? kCodesThreads : k
 
 struct TcParams {
     CUtensorMap mq, mk, mv;
+    CUtensorMap mks, mvs;  // the scales of codes
     Params p;          // p.tt: tokens of an item (both halves)
     int tth;           // tokens of a half
     int box_rows;      // rows of a K/V box
@@ -83,21 +83,24 @@ struct Cfg {
     static constexpr int kSlab = 128 * 128;            // bytes of a 128-row slab
     static constexpr int kTileB = kCh * kSlab;         // a tile of K, of V, or of a half's Q
     static constexpr bool kQ8 = kForm == kCodes;
-    static constexpr int kStages = kQ8 ? (D == 128 ? 4 : 6) : (D == 128 ? 4 : 8);
+    static constexpr int kStages = kQ8 ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 8);
     static constexpr int kQAt = kStages * kTileB;
     // Results on their way out, 32 rows x 32 channels of each softmax warp (over codes, whose form has
     // no room for them, only what two warps exchange).
     static constexpr int kStageOut = kQ8 ? 256 : 32 * 64;
     static constexpr int kOutAt = kQAt + 2 * kTileB;
-    // Codes: each converting warp's next piece and its scales, and the scales as the softmax reads them,
-    // K's and V's of a tile.  Those are written when the tile kStages before has been used: for the
-    // keys' that says that the softmax is done with the tile kScaleTiles before.
-    static constexpr int kPiece = kPieceRows * D;
+    // Codes: the ring of tiles as they are copied, their scales (of each box on 128 bytes), and the scales as
+    // the softmax reads them, K's and V's of a tile.  Those are written when the tile kStages before has
+    // been used: for the keys' that says that the softmax is done with the tile kScaleTiles before.
+    static constexpr int kSlots = 3;
     static constexpr int kCodesAt = kOutAt + kSoftmaxWarps * kStageOut;
-    static constexpr int kCodeScalesAt = kCodesAt + (kQ8 ? kConvertWarps * kPiece : 0);
-    static constexpr int kScalesAt = kCodeScalesAt + (kQ8 ? kConvertWarps * kPieceRows * 4 : 0);
-    static constexpr int kScaleTiles = kStages / 2 + 1;
+    static constexpr int kCodeScalesAt = kCodesAt + (kQ8 ? kSlots * kKeys * D : 0);
+    static constexpr int kScalesAt = kCodeScalesAt + (kQ8 ? kSlots * 1024 : 0);
+    static constexpr int kScaleTiles = D == 128 ? 2 : 4;
     static constexpr int kSmem = kScalesAt + (kQ8 ? kScaleTiles * 2 * kKeys * 4 : 0);
+    // A converting warp sees every use of the slots and places that it uses.
+    static_assert(!kQ8 || (kStages * (kKeys / kPieceRows) % kConvertWarps == 0 &&
+                           kSlots * (kKeys / kPieceRows) % kConvertWarps == 0), "the warps' pieces repeat with the rings");
 };
 
 __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
@@ -106,6 +109,14 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap *map, i
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
         "{%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_box2(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
         : "memory");
 }
 
@@ -240,116 +251,122 @@ __device__ __forceinline__ Run &run_place(Run &found, Run &mine) {
     return mine;
 }
 
-// A converting warp of the form over codes.  The pieces of the tiles (K, V, K, ..), 32 rows each,
-// go round the warps.  A warp copies its next piece (and its scales) while it spreads one
-// to the 16-bit tile that the products read (8-row groups of 1024 bytes, 128 a row,
-// swizzled), once that place is free, and puts the scales where the softmax reads them
-// (K's times `k_unit`).  A thread has 16 codes of a row at a time: the two chunks that they
-// become are stored in an order that keeps the eight lanes of a row on different banks.
+// The copies of a segment's tiles in the form over codes, by one warp: a lane for each box's codes
+// and one for its scales.  `g`: tiles (K, V, K, ..) of the segments before.
+template <int D>
+__device__ __forceinline__ bool copy_codes(const TcParams &tp, const Item &it, int s0, int n, uint32_t &g, uint8_t *smem,
+                                           uint64_t *landed, uint64_t *taken) {
+    using C = Cfg<D, kCodes>;
+    const Params &p = tp.p;
+    const int lane = threadIdx.x & 31, box = lane >> 1, rows = tp.box_rows, boxes = kKeys / rows;
+    auto page_z = [&](int j) {  // page-head of this lane's box of tile j
+        if (j >= n || box >= boxes) return 0;
+        // past the tensor, read as zeros: a box past the end, one between the sinks and every row's
+        // window (its page may be gone already) and a bad page
+        const int key = tile_key<kKeys, true>(it, s0 + j) + box * rows;
+        const int pg = key >= it.len || (key + rows <= it.seen && key >= p.sinks) ? -1 : page_of(p.b, it.b, key, p.hdr);
+        return (pg < 0 ? p.b.num_pages : pg) * p.b.Hkv + it.kh;
+    };
+    int z_next = page_z(0);
+    for (int j = 0; j < n; ++j) {
+        const int z = z_next, row = (tile_key<kKeys, true>(it, s0 + j) + box * rows) & (p.b.page - 1);
+        z_next = page_z(j + 1);
+        for (int kv = 0; kv < 2; ++kv, ++g) {
+            const uint32_t slot = g % C::kSlots;
+            if (g >= uint32_t(C::kSlots) && !warp_wait(&taken[slot], (g / C::kSlots - 1) & 1u, p, 51 + kv)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&landed[slot], kKeys * D + kKeys * 4);
+            __syncwarp();
+            if (box < boxes) {
+                if ((lane & 1) == 0)
+                    tma_box3(smem_addr(smem) + C::kCodesAt + slot * (kKeys * D) + box * rows * D,
+                             kv == 0 ? &tp.mk : &tp.mv, 0, row, z, &landed[slot]);
+                else
+                    tma_box2(smem_addr(smem) + C::kCodeScalesAt + slot * 1024 + box * max(rows * 4, 128),
+                             kv == 0 ? &tp.mks : &tp.mvs, row, z, &landed[slot]);
+            }
+            __syncwarp();
+        }
+    }
+    return true;
+}
+
+// A converting warp of the form over codes.  The pieces of the tiles, 32 rows each, go round the
+// warps.  A warp spreads its piece to the 16-bit tile that the products read (8-row groups
+// of 1024 bytes, 128 a row, swizzled), once that place is free, and puts the scales where
+// the softmax reads them (K's times `k_unit`).  A thread has 16 codes of a row at a time:
+// the two chunks that they become are stored in an order that keeps the eight lanes of a row
+// on different banks.
 //
-// A place's release is waited for by its parity, although a warp has pieces in two of three
-// tiles only: releases come in order, and that of the tile kStages before its last piece's, two
-// tiles back at most, is behind it.
+// The products wait for the place's release and then for these warps, so what can be done
+// ahead of the release is: the codes are in registers, half of them as operands.  (Where these
+// warps also made the copies, a piece took them 3900 cycles, a third of it in the copies'
+// issue.)
 template <typename T, int D, typename F>
 __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, const Run &run, F next, uint8_t *smem,
-                                              uint64_t *landed, uint64_t *empty, uint64_t *conv) {
+                                              uint64_t *landed, uint64_t *taken, uint64_t *empty, uint64_t *conv) {
     using C = Cfg<D, kCodes>;
     constexpr int kLanes = D / 16, kRowsAtOnce = 32 / kLanes, kSteps = kPieceRows / kRowsAtOnce;  // of a row; of a piece
-    constexpr int kTilePieces = kKeys / kPieceRows;
+    constexpr int kAhead = kSteps / 2, kTilePieces = kKeys / kPieceRows;
     const Params &p = tp.p;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
     const int c = lane % kLanes, odd = (c ^ (c >> 2)) & 1;
-    const int nb = kPieceRows / tp.box_rows;  // boxes of a piece: 1, or 2 where pages have 16 rows
-    uint8_t *codes = smem + C::kCodesAt + warp * C::kPiece;
-    float *code_scales = reinterpret_cast<float *>(smem + C::kCodeScalesAt) + warp * kPieceRows;
-    landed += warp;
-    uint32_t g0 = 0;               // tiles of the segments before
-    uint32_t taken = 0, sent = 0;  // pieces of this warp, over all segments
+    uint32_t piece = warp, g0 = 0;  // of all pieces; tiles of the segments before
     bool ok = true;
     while (ok && run.u < run.end) {
         int s0, s1;
         if (!run_segment(p, run, s0, s1)) break;
-        const Item &it = run.item;
-        const int n = s1 - s0;
-        // the segment's pieces first, first + kConvertWarps, ..: tile i / kTilePieces (K and V in turn)
-        const int first = int((warp + kConvertWarps - (g0 * kTilePieces) % kConvertWarps) % kConvertWarps);
-        const int all = 2 * n * kTilePieces, mine = first < all ? (all - 1 - first) / kConvertWarps + 1 : 0;
-        auto key_of = [&](int i) {  // of this warp's i-th piece
-            const int at = first + i * kConvertWarps;
-            return tile_key<kKeys, true>(it, s0 + at / (2 * kTilePieces)) + at % kTilePieces * kPieceRows;
-        };
-        // the pages of 32 boxes at a time, and of the 32 after them
-        auto page_at = [&](int i) {
-            const int piece = nb == 2 ? i >> 1 : i;
-            if (piece >= mine) return 0;
-            // past the tensor, read as zeros: a box past the end, one between the sinks and every row's
-            // window (its page may be gone already) and a bad page
-            const int key = key_of(piece) + (nb == 2 ? (i & 1) * tp.box_rows : 0);
-            const int pg = key >= it.len || (key + tp.box_rows <= it.seen && key >= p.sinks)
-                               ? -1
-                               : page_of(p.b, it.b, key, p.hdr);
-            return pg < 0 ? p.b.num_pages : pg;
-        };
-        int pages = page_at(lane), pages_next = mine * nb > 32 ? page_at(32 + lane) : 0;
-        int i_sent = 0;
-        auto issue = [&]() {
-            if (i_sent > 0 && ((i_sent * nb) & 31) == 0) {
-                pages = pages_next;
-                pages_next = page_at(i_sent * nb + 32 + lane);
-                __syncwarp();
-            }
-            const bool value = ((first + i_sent * kConvertWarps) / kTilePieces & 1) != 0;
-            const int row0 = key_of(i_sent) & (p.b.page - 1), key = 4 * (lane & 7), box = key / tp.box_rows;
-            const int pg = __shfl_sync(0xffffffffu, pages, (i_sent * nb + box) & 31);
-            const int row = (row0 + box * tp.box_rows) & (p.b.page - 1);
-            if (lane < 8) {  // the scales, four keys a lane
-                const bool there = pg < p.b.num_pages;
-                const size_t at = (size_t(there ? pg : 0) * p.b.Hkv + it.kh) * p.b.page + row + key % tp.box_rows;
-                tc::cp_async_16_zfill(code_scales + key, (value ? p.vs : p.ks) + at, there);
-            }
-            cp_async_arrive_noinc(landed);
-            if (lane == 0) mbar_arrive_expect_tx(landed, C::kPiece);
-            if (lane == 0 || (nb == 2 && lane == 4))  // (a lane of the box's)
-                tma_box3(smem_addr(codes + box * tp.box_rows * D), value ? &tp.mv : &tp.mk, 0, row,
-                         pg * p.b.Hkv + it.kh, landed);
-            __syncwarp();
-            ++i_sent;
-            ++sent;
-        };
-        if (mine > 0) issue();
-        for (int i = 0; i < mine; ++i) {
-            const int at = first + i * kConvertWarps, quarter = at % kTilePieces;
-            const uint32_t g = g0 + uint32_t(at / kTilePieces), st = g % C::kStages;
-            if (!(ok = warp_wait(landed, taken & 1u, p, 67))) break;
-            ++taken;
+        const uint32_t end = g0 + 2 * (s1 - s0);
+        const int len = run.item.len, ts = run.item.ts, t0 = run.item.t0;
+        for (; piece / kTilePieces < end; piece += kConvertWarps) {
+            const uint32_t g = piece / kTilePieces, quarter = piece % kTilePieces, st = g % C::kStages, slot = g % C::kSlots;
+            const bool value = (g & 1) != 0;
+            if (!(ok = warp_wait(&landed[slot], (g / C::kSlots) & 1u, p, 67))) break;
+            const uint8_t *codes = smem + C::kCodesAt + slot * (kKeys * D) + quarter * kPieceRows * D + lane * 16;
             uint4 x[kSteps];
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) x[k] = *reinterpret_cast<const uint4 *>(codes + (k * 32 + lane) * 16);
-            const float f = code_scales[lane];
+            for (int k = 0; k < kSteps; ++k) x[k] = *reinterpret_cast<const uint4 *>(codes + k * 512);
+            const int key_in = quarter * kPieceRows + lane;
+            const int spread = tp.box_rows == 16 ? (key_in >> 4) * 32 + (key_in & 15) : key_in;
+            const float f = reinterpret_cast<const float *>(smem + C::kCodeScalesAt + slot * 1024)[spread];
             fence_proxy_async_smem();  // these reads before the next copy into their place
             __syncwarp();
-            if (i_sent < mine) issue();
-            if (g >= uint32_t(C::kStages) && !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 68))) break;
-            uint8_t *tile = smem + st * C::kTileB + quarter * kPieceRows * 128;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const int r = k * kRowsAtOnce + lane / kLanes;
-                const CodePair<T> a(x[k].x), b(x[k].y), d(x[k].z), e(x[k].w);
+            if (lane == 0) mbar_arrive(&taken[slot]);
+            __syncwarp();
+            auto wide = [&](const uint4 &v, uint4 &first, uint4 &second) {  // as they are stored
+                const CodePair<T> a(v.x), b(v.y), d(v.z), e(v.w);
                 const uint4 lo = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(),
                                             b.template take<0, 1>(), b.template take<2, 3>());
                 const uint4 hi = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(),
                                             e.template take<0, 1>(), e.template take<2, 3>());
-                uint8_t *row = tile + (c >> 2) * C::kSlab + r * 128;
-                const int chunk = 2 * (c & 3) + odd;
-                *reinterpret_cast<uint4 *>(row + ((chunk ^ (r & 7)) << 4)) = odd != 0 ? hi : lo;
-                *reinterpret_cast<uint4 *>(row + ((chunk ^ 1 ^ (r & 7)) << 4)) = odd != 0 ? lo : hi;
+                first = odd != 0 ? hi : lo;
+                second = odd != 0 ? lo : hi;
+            };
+            uint4 w[kAhead][2];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) wide(x[k], w[k][0], w[k][1]);
+            if (g >= uint32_t(C::kStages) && !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 68))) break;
+            uint8_t *tile = smem + st * C::kTileB + quarter * kPieceRows * 128 + (c >> 2) * C::kSlab + lane / kLanes * 128;
+            auto store = [&](int k, const uint4 &first, const uint4 &second) {
+                const int r = k * kRowsAtOnce + lane / kLanes, chunk = 2 * (c & 3) + odd;
+                uint8_t *row = tile + k * kRowsAtOnce * 128;
+                *reinterpret_cast<uint4 *>(row + ((chunk ^ (r & 7)) << 4)) = first;
+                *reinterpret_cast<uint4 *>(row + ((chunk ^ 1 ^ (r & 7)) << 4)) = second;
+            };
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) store(k, w[k][0], w[k][1]);
+#pragma unroll
+            for (int k = kAhead; k < kSteps; ++k) {
+                uint4 first, second;
+                wide(x[k], first, second);
+                store(k, first, second);
             }
             // past the sequence's end the scales may be anything.  A key's is above 0: a hidden score is an
             // infinity, which 0 would make a NaN (the codes of a scale of 0 are 0 themselves).
-            const bool past = key_of(i) + lane >= it.len, value = (at / kTilePieces & 1) != 0;
+            const int i = s0 + int((g - g0) >> 1);
+            const bool past = (i < ts ? i : t0 - ts + i) * kKeys + key_in >= len;
             const float kf = f * k_unit;
             reinterpret_cast<float *>(smem + C::kScalesAt)[((g >> 1) % C::kScaleTiles) * (2 * kKeys) +
-                                                           (value ? kKeys : 0) + quarter * kPieceRows + lane] =
+                                                           (value ? kKeys : 0) + key_in] =
                 value  ? (past ? 0.f : f)
                 : past ? 1.f
                        : (kf <= 1.17549435e-38f ? 1.17549435e-38f : kf);
@@ -358,11 +375,9 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
             if (lane == 0) mbar_arrive(&conv[st]);
             __syncwarp();
         }
-        g0 += 2 * n;
+        g0 = end;
         next();
     }
-    // copies in flight after a time-out land before the CTA exits
-    if (taken < sent) warp_wait(landed, taken & 1u, p, 53, kDrainNs);
 }
 
 // How a score follows from q.k: by a positive scale, capped after a positive
@@ -381,7 +396,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     constexpr bool kMasks = kForm != kPaged, kQ8 = kForm == kCodes, kRef = kQ8 && std::is_same_v<T, __half>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2][2],
-        o_full[2], drain, conv[kQ8 ? C::kStages : 1], landed[kQ8 ? kConvertWarps : 1];
+        o_full[2], drain, conv[kQ8 ? C::kStages : 1], landed[C::kSlots], taken[C::kSlots];
     __shared__ uint32_t tmem_base;
     __shared__ Run run_sh;
     __shared__ Run run_of[kQ8 ? kCodesThreads / 32 : 1];  // each warp's own, where registers are few
@@ -397,11 +412,12 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         mbar_init(&drain, 1);
         if (kQ8) {
             for (int i = 0; i < C::kStages; ++i) mbar_init(&conv[i], kKeys / kPieceRows);
-            for (int i = 0; i < kConvertWarps; ++i) mbar_init(&landed[i], 1 + 32);
+            for (int i = 0; i < C::kSlots; ++i) mbar_init(&landed[i], 1), mbar_init(&taken[i], kKeys / kPieceRows);
         }
         prefetch_map(&tp.mq);
         prefetch_map(&tp.mk);
         prefetch_map(&tp.mv);
+        if (kQ8) prefetch_map(&tp.mks), prefetch_map(&tp.mvs);
     }
     __syncwarp();
     fence_mbar_init();
@@ -432,7 +448,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     __syncthreads();
 
     if (kQ8 && warp >= kConvertWarp) {
-        convert_tiles<T, D>(tp, kMode == kScaled ? p.scale_log2 : 1.f, run, next, smem, landed, empty, conv);
+        convert_tiles<T, D>(tp, kMode == kScaled ? p.scale_log2 : 1.f, run, next, smem, landed, taken, empty, conv);
     } else if (warp >= kCopyWarp && warp < kCopyWarp + (kQ8 ? 1 : kCopyWarps)) {
         // ---- Q of each segment and its K tiles, or its V tiles
         const int me = warp - kCopyWarp;
@@ -455,7 +471,8 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
             ++seg;
             if (me == 0 && lane == 0 && s0 == 0 && s1 < it.tiles) p.desc[blockIdx.x] = join_desc(p, run);
             __syncwarp();
-            if (kQ8) {
+            if constexpr (kQ8) {
+                ok = copy_codes<D>(tp, it, s0, s1 - s0, g, smem, landed, taken);
                 next();
                 continue;
             }
@@ -498,7 +515,10 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         }
         // this warp's last copies land before the CTA exits, whoever else gave up on what: the MMA
         // warp may have left by a time-out of its own and not waited for them
-        for (uint32_t i = 0; i < uint32_t(C::kStages) && i < g; ++i) {
+        if (kQ8)
+            for (uint32_t i = 0; i < uint32_t(C::kSlots) && i < g; ++i)
+                warp_wait(&landed[(g - 1 - i) % C::kSlots], ((g - 1 - i) / C::kSlots) & 1u, p, 53, kDrainNs);
+        for (uint32_t i = 0; !kQ8 && i < uint32_t(C::kStages) && i < g; ++i) {
             const uint32_t gg = g - 1 - i;
             if (int(gg % 2) == me) warp_wait(&full[gg % C::kStages], (gg / C::kStages) & 1u, p, 53, kDrainNs);
         }
@@ -1013,7 +1033,7 @@ cudaError_t launch_form(const AttnArgs &a, const Params &p, int num_sms, cudaStr
     tp.p.tt = 2 * tp.tth;
     tp.p.tt_magic = 0xffffffffu / unsigned(tp.p.tt) + 1;
     tp.p.extra = kExtra;
-    tp.box_rows = std::min(a.b.page, kForm == kCodes ? kPieceRows : kKeys);
+    tp.box_rows = std::min(a.b.page, kKeys);
     const uint32_t fmt = a.type == MOE_BF16 ? (1u << 7) | (1u << 10) : 0u;  // A and B bf16
     tp.idesc_qk = tc::idesc_f16_f32(kHalf, kKeys) | fmt;
     tp.idesc_pv = tc::idesc_f16_f32(kHalf, a.b.D) | fmt | (1u << 16);       // B: N contiguous
@@ -1022,6 +1042,9 @@ cudaError_t launch_form(const AttnArgs &a, const Params &p, int num_sms, cudaStr
                                : encode_pages_map(map, base, a.b, a.type, tp.box_rows);
     };
     if (!pages(&tp.mk, a.k) || !pages(&tp.mv, a.v) || !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
+        return cudaErrorInvalidValue;
+    if (kForm == kCodes &&
+        (!encode_scales_map(&tp.mks, a.ks, a.b, tp.box_rows) || !encode_scales_map(&tp.mvs, a.vs, a.b, tp.box_rows)))
         return cudaErrorInvalidValue;
     const int grid = std::min(num_sms, kMaxGrid);
     const bool near_cap = a.softcap <= kCapNear && p.cap_in > 1e-30f;  // kCapped: kTanhMinusOne / cap_in is finite

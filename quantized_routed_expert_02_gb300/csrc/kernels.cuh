@@ -188,8 +188,9 @@ struct AttnArgs {
 bool encode_pages_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
                       int box_rows);
 // Pages of 8-bit codes in the same way, boxes of box_rows whole rows, swizzled over a row's
-// length or (`flat`) row after row.
+// length or (`flat`) row after row; and their scales [num_pages * Hkv][page], boxes of box_rows.
 bool encode_codes_map(CUtensorMap *map, const void *base, const PagedBatch &b, int box_rows, bool flat);
+bool encode_scales_map(CUtensorMap *map, const float *base, const PagedBatch &b, int box_rows);
 // Query rows [N][Hq][D] as a 3-D map: boxes of 64 channels x one group's heads
 // x `tokens` rows.
 bool encode_rows_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,

@@ -871,6 +871,15 @@ bool encode_codes_map(CUtensorMap *map, const void *base, const PagedBatch &b, i
                                 : CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+bool encode_scales_map(CUtensorMap *map, const float *base, const PagedBatch &b, int box_rows) {
+    if (g_encode == nullptr) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(b.page), cuuint64_t(b.num_pages) * b.Hkv};
+    const cuuint64_t strides[1] = {cuuint64_t(b.page) * 4};
+    const cuuint32_t box[2] = {cuuint32_t(box_rows), 1}, estr[2] = {1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool encode_rows_map(CUtensorMap *map, const void *base, const PagedBatch &b, moe_dtype type,
                      int tokens) {
     return encode_16bit_3d(map, base, type, b.D, b.Hq, b.N, b.Hq / b.Hkv, tokens);
