@@ -86,13 +86,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
 constexpr float kTanhNear = 0.55f;
 constexpr float kTanh1 = -0.33333331f, kTanh2 = 0.13333113f, kTanh3 = -0.053909428f, kTanh4 = 0.021309389f,
                 kTanh5 = -0.0066102277f;  // of y^2, y^4, ...
-__device__ __forceinline__ float capped_far(float s, const Params &p) {
-    return fmaf(__fdividef(-2.f, 1.f + exp2_approx(s * p.cap_in)), p.cap_log2, p.cap_log2);
+__device__ __forceinline__ float capped_far(float s, float cap_in, const Params &p) {
+    return fmaf(__fdividef(-2.f, 1.f + exp2_approx(s * cap_in)), p.cap_log2, p.cap_log2);
 }
 template <bool kCap>
 __device__ __forceinline__ float score(float s, const Params &p) {
     if (!kCap) return s * p.scale_log2;
-    const float far = capped_far(s, p);  // always: a branch costs more (48 tokens over 1500 35.4 us, so 31.8)
+    const float far = capped_far(s, p.cap_in, p);  // always: a branch costs more (48 tokens over 1500 35.4 us, so 31.8)
     const float y = s * p.cap_y, t = y * y;
     float r = fmaf(t, kTanh5, kTanh4);
     r = fmaf(t, r, kTanh3);

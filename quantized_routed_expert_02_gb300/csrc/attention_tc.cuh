@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     __syncthreads();
 
     if (kQ8 && warp >= kConvertWarp) {
-        convert_tiles<T, D>(tp, kMode == kScaled ? p.scale_log2 : 1.f, run, next, smem, landed, taken, empty, conv);
+        convert_tiles<T, D>(tp, kMode == kScaled ? p.scale_log2 : kMode == kCapped ? p.cap_in : 1.f, run, next, smem, landed, taken, empty, conv);
     } else if (warp >= kCopyWarp && warp < kCopyWarp + (kQ8 ? 1 : kCopyWarps)) {
         // ---- Q of each segment and its K tiles, or its V tiles
         const int me = warp - kCopyWarp;
@@ -627,7 +627,9 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         // The q.k of a key that a row does not see, and the least (by sign) of one that it does: what
         // is less, an infinity too, has the same capped score, and is not taken for hidden
         const float hidden = -CUDART_INF_F * sign;
-        const float lowest = kMode == kCapped ? kTanhMinusOne / p.cap_in : -CUDART_MAX_NORMAL_F;
+        constexpr bool kInCap = kQ8 && kMode == kCapped;  // the scores come over the cap: a factor of K's scales
+        const float cap_in = kInCap ? 1.f : p.cap_in;
+        const float lowest = kMode == kCapped ? kTanhMinusOne / cap_in : -CUDART_MAX_NORMAL_F;
         uint32_t ns = 0, no = 0, nx = 0;  // S tiles and O results taken, exchanges
         uint32_t gt = 0;                  // tiles of all segments (kQ8)
         bool ok = true;  // after a time-out: no more waits, but every barrier still met
@@ -748,11 +750,11 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     // kCapped: a tile that every row sees whole and whose tangents stay off 1; kAny: one
                     // whose scores all are far below the cap (a hidden score's magnitude is infinite)
                     const bool plain =
-                        kMode == kCapped ? !edge && !__any_sync(0xffffffffu, mt * p.cap_in > kTanhOne)
+                        kMode == kCapped ? !edge && !__any_sync(0xffffffffu, mt * cap_in > kTanhOne)
                         : kMode == kAny && capped ? __all_sync(0xffffffffu, most * fabsf(p.cap_y) < kTanhNear)
                                                   : false;
                     if (mt != -CUDART_INF_F)
-                        mt = kMode == kCapped            ? capped_far(mt, p)
+                        mt = kMode == kCapped            ? capped_far(mt, cap_in, p)
                              : capped                    ? score<true>(mt * sign, p)
                              : kQ8 && kMode == kScaled   ? mt
                                                          : score<false>(mt * sign, p);
@@ -839,7 +841,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     float x, y;
-                                    unpack2(mul2(e2[k], scale2), x, y);
+                                    unpack2(kInCap ? e2[k] : mul2(e2[k], scale2), x, y);
                                     if (!kPlain) {
                                         x = min_nan(max_nan(x, from), kTanhOne);
                                         y = min_nan(max_nan(y, from), kTanhOne);
