@@ -473,9 +473,10 @@ MOE_API moe_status moe_rope_append_q8(const void *qkv_dev, const int32_t *pos_de
  * moe_attention_cache: moe_attention_paged over either cache and with more masks.
  *  Codes: with k_scales_dev and v_scales_dev (both or neither) k_pages_dev and
  *  v_pages_dev are the int8 codes above; dtype is that of q and out.  The codes are
- *  exact in dtype: q . code and its scale are taken in fp32 (q . code has to stay in
- *  its range, with a cap too), and a weight times its value's scale is rounded to
- *  dtype once.  Scales below kv_lens are finite and not negative.
+ *  exact in either 16-bit type: q . code and its scale are taken in fp32 (q . code
+ *  has to stay in its range, with a cap too), and a weight times its value's scale is
+ *  rounded once, to dtype or to fp16.  Scales below kv_lens are finite and not
+ *  negative; a code 0 with any of them is 0.
  *  Sinks: with window > 0 a row at cache index t sees the keys j <= t with
  *  j > t - window or j < sinks (sinks >= 0; without a window they change nothing).
  *  Table entries of pages between the two that no new token sees are not read.

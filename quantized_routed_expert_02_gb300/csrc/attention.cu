@@ -20,6 +20,10 @@
 // ragged batch some 7 us) and, with many parts, 4 us for the joining launch: one
 // token over 131071 53 us, over 2000 9.1.  A cap's polynomial costs batches that the
 // bytes do not fill 1.5 us (48 tokens over 1500 30.1 -> 31.8) and the others nothing.
+//
+// kMasks: the form for trees and sinks (moe_attention_cache); pieces that some row does not see
+// whole take a bit a key from the rows' masks: 32 sequences with a window of 2048 and 4 sinks
+// 34.8 us, a tree of 12 over 700 9.8.
 #include <algorithm>
 #include <type_traits>
 

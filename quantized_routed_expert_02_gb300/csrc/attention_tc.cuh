@@ -3,7 +3,7 @@
 // memory and S, P, O in tensor memory.
 //
 // An item is two halves of 128 query rows (tokens x the group's heads) that
-// share every key tile of 128 keys.  Nineteen warps: for each half eight
+// share every key tile of 128 keys.  Nineteen warps (24 over codes): for each half eight
 // softmax warps (two threads per row, half the keys each), a warp that issues the
 // MMAs, and two that copy (K tiles with the queries, V tiles; TMA boxes of
 // one page at most).  The two halves take turns on the tensor pipe: while one
@@ -24,6 +24,18 @@
 // time): a prompt of 4096, 117 us = 1.18 PFLOP/s.  One thread per row
 // (four warps a half) was slower by the latency of its chain: the capped chunk 613
 // against 465 us, the prompt 2 us faster.
+//
+// Three forms are built of it.  kPaged: chains in a window.  kMasked: trees and sinks too; a
+// tile that some row does not see whole takes a bit a key from its row's mask, the others are
+// as before (16 trees of 48 to 64 nodes over 900 to 8100 keys, 64/4 heads: 104 us = 1.02
+// PFLOP/s).  kCodes: the same over 8-bit codes.  Their copies land in a ring of their own, six
+// more warps spread them to the 16-bit tiles that the products read (every code is exact
+// there), and the scales come in the softmax: K's as a factor of the scores, in fp32, V's as
+// one of the weights before those are rounded.  80 registers a thread are left for that, so
+// each warp's run lies in shared memory.  The chunk of 2048 over 16384 takes 528 us = 0.97
+// PFLOP/s, with a cap 694: the memory's bytes are half, but the issue slots (62 % used) and the path to
+// shared memory (57 %, beside the products' own reads) now carry the codes' conversion and 768 loads of
+// scales a tile; without the conversion it would take 465 us, without the softmax's scales 493.
 #pragma once
 
 #include <algorithm>

@@ -17,6 +17,9 @@
 // start (3 us) and the latency of 16 warps an SM at 128 registers; weights folded into
 // the sines (fewer operations, more registers) took 33.4 us, a ring of bulk
 // copies and more warps with fewer chunks in flight no less than this.
+//
+// kCodes (moe_rope_append_q8): a key's or value's lanes share its largest magnitude and store 16
+// codes each; queries are as before.  4100 rows of 64/4 heads 33.3 us, one row 3.4 us.
 #include <algorithm>
 #include <type_traits>
 

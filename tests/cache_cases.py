@@ -2,8 +2,9 @@
 chains: 8-bit codes, trees of drafted tokens, sinks beside a window.
 
 Error bounds count the roundings that the operators' statements allow, as in
-block_cases; over codes also one fp32 product for each scale, and for fp16
-weights half of the type's smallest step beside the largest value of the cache.
+block_cases; over codes also one fp32 product for each scale, and, as the weights may
+be fp16 there whatever the type, half of that type's smallest step beside the largest
+value of the cache.
 """
 from __future__ import annotations
 
@@ -112,7 +113,8 @@ def cache_ref(case, scale, window=0, softcap=0.0, sinks=0, trees=None, words=0):
     lse_tol = torch.full_like(lse, nan)
     t = case.q.dtype
     G, u = case.Hq // case.Hkv, half_step(t)
-    tiny = 2.0 ** -25 if t is torch.float16 else 0.0
+    # half a step of fp16 below 2^-14; over codes bf16 queries' weights are fp16 as well (up to 16 rows a head)
+    tiny = 2.0 ** -25 if codes or t is torch.float16 else 0.0
     row0 = 0
     for b, (n, L) in enumerate(zip(case.new, case.lens_list)):
         if n == 0:
