@@ -436,7 +436,7 @@ cudaError_t launch_attention(const AttnArgs &a, int max_new, int num_sms, cudaSt
     if (!encode_pages_map(&sp.mk, a.k, a.b, a.type, kPiece) || !encode_pages_map(&sp.mv, a.v, a.b, a.type, kPiece))
         return cudaErrorInvalidValue;
     const int grid = std::min(2 * num_sms, kMaxCtas);
-    sp.join_launch = joins_by_launch(a.b, grid, kTile);
+    sp.join_launch = joins_by_launch(a.b, grid, kTile, kJoinInside);
     cudaError_t e;
     if (a.type == MOE_F16)
         e = a.b.D == 64 ? launch_stream<__half, 64>(sp, form == 1, grid, s) : launch_stream<__half, 128>(sp, form == 1, grid, s);

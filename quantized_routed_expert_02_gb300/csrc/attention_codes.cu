@@ -17,8 +17,10 @@
 // are read in the same order; transposed it gives two channels of two keys, an operand
 // whose rows are the even and the odd channels.  The weights turn in registers (movmatrix).
 //
-// Measured (32/4 heads of 128): 48 sequences of 150 to 12000 tokens 38.4 us (16-bit values 57.9), 128
-// of 4000 97.8 us = 5.5 TB/s, one over 93 6.2, one over 100000 30.5.  With the rows where the keys
+// The first copies are under way before anything waits for the queries (48 of 2000 31.0 -> 29.2 us).
+//
+// Measured (32/4 heads of 128): 48 sequences of 150 to 12000 tokens 38.3 us (16-bit values 57.9), 128
+// of 4000 97.8 us = 5.5 TB/s, one over 93 6.1, one over 100000 30.5.  With the rows where the keys
 // are now (16 of them, half padding) and a rescale for every new maximum these took 42.9,
 // 110.7, 6.5 and 33.7; without any arithmetic the copies take 33 and 89.  Beside those, three CTAs an SM
 // with smaller rings (46.7 and 116), and the next piece's scores computed among a piece's softmax
@@ -34,6 +36,10 @@ namespace moeq4k {
 namespace attn {
 
 constexpr int kCodePiece = 32;                      // keys of a piece
+constexpr long kCodeJoinInside = 10;                // parts that the last CTA joins (6, 10: 700 tokens of one 17.0, 12.7 us)
+// What parting items costs, in key tiles (2, 5, 9: 200 tokens of one sequence 8.7, 7.4, 7.3 us, 700
+// 10.4, 10.4, 12.7; 600 of 48 18.3, 14.3, 14.3; 2000 of 48 30.8, 30.8, 32.0).
+constexpr int kCodeSplit = 5;
 constexpr float kGrowth = 8.f;                      // log2 growth of a maximum that moves the reference
 constexpr int kCodeTile = kWarps * kCodePiece;      // keys of a tile: as many bytes as the 16-bit kernel's
 
@@ -109,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
     const bool looks = !sp.join_launch && blockIdx.x == 0 && tid == 0;
     const unsigned long long tags = looks ? p.hdr->cta_calls : 0ull;
     Run run;
-    const bool work = run_begin<kTile, true>(p, kLeast, kSplit, reinterpret_cast<long *>(smem), &run_sh, run);
+    const bool work = run_begin<kTile, true>(p, kLeast, kCodeSplit, reinterpret_cast<long *>(smem), &run_sh, run);
     if (tags != 0) record_status(p.hdr, MOE_ERR_WORKSPACE, 0);
     if (!work) return;
     fence_proxy_async_smem();  // the prefix sums (generic) before the copies into the ring
@@ -137,44 +143,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
         };
         int pages = page_at(lane), pages_next = n * nb > 32 ? page_at(32 + lane) : 0;
         // the queries: row 8 x + gid, four channels in a row as the codes come
-        uint32_t qb[kN][D / 16][2];
-        float unit[kN][2];  // what the scores of this thread's rows (8 x + 2 tig, + 1) take back
-        Sight sight[kN][2];
+        uint2 w[kN][D / 16];
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
             const int r = 8 * x + gid, tok = r / G;
             const bool live = tok < it.nt;
             const T *row = static_cast<const T *>(p.q) +
                            (size_t(it.row0 + (live ? tok : 0)) * p.b.Hq + it.kh * G + r % G) * D;
-            float factor = 1.f;
-            uint2 w[D / 16];
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                w[k] = live ? *reinterpret_cast<const uint2 *>(row + 16 * k + 4 * tig) : make_uint2(0u, 0u);
-            if (kScaleQ) {
-                float most = 0.f;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const float2 a = Pair<T>::load(w[k].x), b = Pair<T>::load(w[k].y);
-                    most = fmaxf(fmaxf(most, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
-                }
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                // 2^14 over the largest's power of two, at most 2^126
-                factor = __uint_as_float(min(268u - (__float_as_uint(most) >> 23), 253u) << 23);
-            }
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                qb[x][k][0] = query_pair(T(), w[k].x, factor);
-                qb[x][k][1] = query_pair(T(), w[k].y, factor);
-            }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int mine = 8 * x + 2 * tig + c, t = mine / G;
-                unit[x][c] = kScaleQ ? 1.f / __shfl_sync(0xffffffffu, factor, 8 * tig + 4 * c) : 1.f;
-                sight[x][c] = row_sight(p, run.seq, t < it.nt, it.row0 + t, it.qt * p.tt + t);
-                __syncwarp();
-            }
+                w[x][k] = live ? *reinterpret_cast<const uint2 *>(row + 16 * k + 4 * tig) : make_uint2(0u, 0u);
         }
         __syncwarp();
         int sent = 0;  // pieces of this segment issued
@@ -214,7 +192,41 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
             ++sent;
             ++issued;
         };
-        for (int i = 0; i < kStages && i < n; ++i) issue();
+        for (int i = 0; i < kStages && i < n; ++i) issue();  // ahead of what has to wait for the queries
+
+        uint32_t qb[kN][D / 16][2];
+        float unit[kN][2];  // what the scores of this thread's rows (8 x + 2 tig, + 1) take back
+        Sight sight[kN][2];
+#pragma unroll
+        for (int x = 0; x < kN; ++x) {
+            float factor = 1.f;
+            if (kScaleQ) {
+                float most = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const float2 a = Pair<T>::load(w[x][k].x), b = Pair<T>::load(w[x][k].y);
+                    most = fmaxf(fmaxf(most, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+                }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                // 2^14 over the largest's power of two, at most 2^126
+                factor = __uint_as_float(min(268u - (__float_as_uint(most) >> 23), 253u) << 23);
+            }
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                qb[x][k][0] = query_pair(T(), w[x][k].x, factor);
+                qb[x][k][1] = query_pair(T(), w[x][k].y, factor);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int t = (8 * x + 2 * tig + c) / G;
+                // (over a power of two: the exponent's complement)
+                const float f = __shfl_sync(0xffffffffu, factor, 8 * tig + 4 * c);
+                unit[x][c] = kScaleQ ? __uint_as_float(0x7f000000u - __float_as_uint(f)) : 1.f;
+                sight[x][c] = row_sight(p, run.seq, t < it.nt, it.row0 + t, it.qt * p.tt + t);
+                __syncwarp();
+            }
+        }
 
         // sums of channels 16 c + 2 gid (o[][c][0 .. 1]) and the one after (o[][c][2 .. 3]) of this thread's rows
         float o[kN][D / 16][4], mx[kN][2], l[kN][2];
@@ -445,7 +457,7 @@ cudaError_t launch_stream_codes(const AttnArgs &a, Params p, int max_new, int nu
     if (!encode_codes_map(&sp.mk, a.k, a.b, box_rows, false) || !encode_codes_map(&sp.mv, a.v, a.b, box_rows, false))
         return cudaErrorInvalidValue;
     const int grid = std::min(2 * num_sms, kMaxCtas);
-    sp.join_launch = joins_by_launch(a.b, grid, kCodeTile);
+    sp.join_launch = joins_by_launch(a.b, grid, kCodeTile, kCodeJoinInside);
     auto go = [&](auto kernel) {
         return launch_pdl(kernel, dim3(grid), dim3(kThreads), size_t(kCodesSmem), s, sp);
     };

@@ -150,11 +150,11 @@ Params make_params(const AttnArgs &a);
 // token over 93: 9.6 us with the launch, 5.9 without); more take it longer than a second
 // launch that spreads them over the GPU (one token over 600, 10 parts and more: 8.8 us with
 // the launch, 9.4 without; over 131071, 76 parts: 52 and 56).
-inline bool joins_by_launch(const PagedBatch &b, int grid, int tile) {
-    constexpr long kJoinInside = 10;
+constexpr long kJoinInside = 10;
+inline bool joins_by_launch(const PagedBatch &b, int grid, int tile, long inside) {
     const long items = long(b.B) * b.Hkv;
     const long tiles = (long(b.max_pages) * b.page + tile - 1) / tile + kExtra;  // of an item, at most
-    return std::min(grid / items, tiles / kLeast) + 1 > kJoinInside;
+    return std::min(grid / items, tiles / kLeast) + 1 > inside;
 }
 
 // The same over a cache of 8-bit codes (any masks).
