@@ -305,9 +305,10 @@ __device__ __forceinline__ bool copy_codes(const TcParams &tp, const Item &it, i
 // A converting warp of the form over codes.  The pieces of the tiles, 32 rows each, go round the
 // warps.  A warp spreads its piece to the 16-bit tile that the products read (8-row groups
 // of 1024 bytes, 128 a row, swizzled), once that place is free, and puts the scales where
-// the softmax reads them (K's times `k_unit`).  A thread has 16 codes of a row at a time:
-// the two chunks that they become are stored in an order that keeps the eight lanes of a row
-// on different banks.
+// the softmax reads them (K's times `k_unit`).  A thread has 16 codes of a row at a time, which
+// become two chunks of 16 bytes.  Eight lanes have four chunks of one row and the same four
+// of another, of the other parity (r and r ^ 5 where rows are 128 bytes of codes, which the copy
+// swizzles by the row), so that their loads and their stores go to different banks.
 //
 // The products wait for the place's release and then for these warps, so what can be done
 // ahead of the release is: the codes are in registers, half of them as operands.  (Where these
@@ -317,11 +318,17 @@ template <typename T, int D, typename F>
 __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, const Run &run, F next, uint8_t *smem,
                                               uint64_t *landed, uint64_t *taken, uint64_t *empty, uint64_t *conv) {
     using C = Cfg<D, kCodes>;
-    constexpr int kLanes = D / 16, kRowsAtOnce = 32 / kLanes, kSteps = kPieceRows / kRowsAtOnce;  // of a row; of a piece
+    constexpr int kRowsAtOnce = 512 / D, kSteps = kPieceRows / kRowsAtOnce;  // of a piece
     constexpr int kAhead = kSteps / 2, kTilePieces = kKeys / kPieceRows;
     const Params &p = tp.p;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kConvertWarp;
-    const int c = lane % kLanes, odd = (c ^ (c >> 2)) & 1;
+    // this thread's chunk of its row, and its row of step k
+    const int c = D == 128 ? (lane & 3) + ((lane >> 3) & 1) * 4 : lane & 3;
+    auto row_of = [&](int k) {
+        if (D == 64) return k * kRowsAtOnce + (lane >> 2);
+        const int r = (k & 1) * 2 + (lane >> 4);
+        return k / 2 * 8 + ((lane & 4) != 0 ? r ^ 5 : r);
+    };
     uint32_t piece = warp, g0 = 0;  // of all pieces; tiles of the segments before
     bool ok = true;
     while (ok && run.u < run.end) {
@@ -333,10 +340,13 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
             const uint32_t g = piece / kTilePieces, quarter = piece % kTilePieces, st = g % C::kStages, slot = g % C::kSlots;
             const bool value = (g & 1) != 0;
             if (!(ok = warp_wait(&landed[slot], (g / C::kSlots) & 1u, p, 67))) break;
-            const uint8_t *codes = smem + C::kCodesAt + slot * (kKeys * D) + quarter * kPieceRows * D + lane * 16;
+            const uint8_t *codes = smem + C::kCodesAt + slot * (kKeys * D) + quarter * kPieceRows * D;
             uint4 x[kSteps];
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) x[k] = *reinterpret_cast<const uint4 *>(codes + k * 512);
+            for (int k = 0; k < kSteps; ++k) {
+                const int r = row_of(k);
+                x[k] = *reinterpret_cast<const uint4 *>(codes + r * D + ((D == 128 ? c ^ (r & 7) : c) << 4));
+            }
             const int key_in = quarter * kPieceRows + lane;
             const int spread = tp.box_rows == 16 ? (key_in >> 4) * 32 + (key_in & 15) : key_in;
             const float f = reinterpret_cast<const float *>(smem + C::kCodeScalesAt + slot * 1024)[spread];
@@ -344,25 +354,22 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
             __syncwarp();
             if (lane == 0) mbar_arrive(&taken[slot]);
             __syncwarp();
-            auto wide = [&](const uint4 &v, uint4 &first, uint4 &second) {  // as they are stored
+            auto wide = [&](const uint4 &v, uint4 &first, uint4 &second) {
                 const CodePair<T> a(v.x), b(v.y), d(v.z), e(v.w);
-                const uint4 lo = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(),
-                                            b.template take<0, 1>(), b.template take<2, 3>());
-                const uint4 hi = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(),
-                                            e.template take<0, 1>(), e.template take<2, 3>());
-                first = odd != 0 ? hi : lo;
-                second = odd != 0 ? lo : hi;
+                first = make_uint4(a.template take<0, 1>(), a.template take<2, 3>(), b.template take<0, 1>(),
+                                   b.template take<2, 3>());
+                second = make_uint4(d.template take<0, 1>(), d.template take<2, 3>(), e.template take<0, 1>(),
+                                    e.template take<2, 3>());
             };
             uint4 w[kAhead][2];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) wide(x[k], w[k][0], w[k][1]);
             if (g >= uint32_t(C::kStages) && !(ok = warp_wait(&empty[st], (g / C::kStages - 1) & 1u, p, 68))) break;
-            uint8_t *tile = smem + st * C::kTileB + quarter * kPieceRows * 128 + (c >> 2) * C::kSlab + lane / kLanes * 128;
+            uint8_t *tile = smem + st * C::kTileB + quarter * kPieceRows * 128 + (c >> 2) * C::kSlab;
             auto store = [&](int k, const uint4 &first, const uint4 &second) {
-                const int r = k * kRowsAtOnce + lane / kLanes, chunk = 2 * (c & 3) + odd;
-                uint8_t *row = tile + k * kRowsAtOnce * 128;
-                *reinterpret_cast<uint4 *>(row + ((chunk ^ (r & 7)) << 4)) = first;
-                *reinterpret_cast<uint4 *>(row + ((chunk ^ 1 ^ (r & 7)) << 4)) = second;
+                const int r = row_of(k), chunk = 2 * (c & 3);
+                *reinterpret_cast<uint4 *>(tile + r * 128 + ((chunk ^ (r & 7)) << 4)) = first;
+                *reinterpret_cast<uint4 *>(tile + r * 128 + (((chunk + 1) ^ (r & 7)) << 4)) = second;
             };
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) store(k, w[k][0], w[k][1]);
@@ -1052,7 +1059,7 @@ cudaError_t launch_form(const AttnArgs &a, const Params &p, int num_sms, cudaStr
     tp.idesc_qk = tc::idesc_f16_f32(kHalf, kKeys) | fmt;
     tp.idesc_pv = tc::idesc_f16_f32(kHalf, a.b.D) | fmt | (1u << 16);       // B: N contiguous
     auto pages = [&](CUtensorMap *map, const void *base) {
-        return kForm == kCodes ? encode_codes_map(map, base, a.b, tp.box_rows, true)
+        return kForm == kCodes ? encode_codes_map(map, base, a.b, tp.box_rows, a.b.D == 64)
                                : encode_pages_map(map, base, a.b, a.type, tp.box_rows);
     };
     if (!pages(&tp.mk, a.k) || !pages(&tp.mv, a.v) || !encode_rows_map(&tp.mq, a.q, a.b, a.type, tp.tth))
