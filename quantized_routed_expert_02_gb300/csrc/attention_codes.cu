@@ -20,7 +20,7 @@
 // The first copies are under way before anything waits for the queries (48 of 2000 31.0 -> 29.2 us).
 //
 // Measured (32/4 heads of 128): 48 sequences of 150 to 12000 tokens 38.3 us (16-bit values 57.9), 128
-// of 4000 97.8 us = 5.5 TB/s, one over 93 6.1, one over 100000 30.5.  With the rows where the keys
+// of 4000 97.8 us = 5.5 TB/s, one over 93 6.1, one over 100000 30.4.  With the rows where the keys
 // are now (16 of them, half padding) and a rescale for every new maximum these took 42.9,
 // 110.7, 6.5 and 33.7; without any arithmetic the copies take 33 and 89.  Beside those, three CTAs an SM
 // with smaller rings (46.7 and 116), and the next piece's scores computed among a piece's softmax

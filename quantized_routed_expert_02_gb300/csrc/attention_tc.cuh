@@ -32,10 +32,10 @@
 // more warps spread them to the 16-bit tiles that the products read (every code is exact
 // there), and the scales come in the softmax: K's as a factor of the scores, in fp32, V's as
 // one of the weights before those are rounded.  80 registers a thread are left for that, so
-// each warp's run lies in shared memory.  The chunk of 2048 over 16384 takes 528 us = 0.97
-// PFLOP/s, with a cap 694: the memory's bytes are half, but the issue slots (62 % used) and the path to
+// each warp's run lies in shared memory.  The chunk of 2048 over 16384 takes 518 us = 0.99
+// PFLOP/s, with a cap 689: the memory's bytes are half, but the issue slots (62 % used) and the path to
 // shared memory (57 %, beside the products' own reads) now carry the codes' conversion and 768 loads of
-// scales a tile; without the conversion it would take 465 us, without the softmax's scales 493.
+// scales a tile; without the conversion it took 465 of 583 us, without the softmax's scales 493 of 529.
 #pragma once
 
 #include <algorithm>
