@@ -337,7 +337,8 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
         const uint32_t end = g0 + 2 * (s1 - s0);
         const int len = run.item.len, ts = run.item.ts, t0 = run.item.t0;
         for (; piece / kTilePieces < end; piece += kConvertWarps) {
-            const uint32_t g = piece / kTilePieces, quarter = piece % kTilePieces, st = g % C::kStages, slot = g % C::kSlots;
+            const uint32_t g = piece / kTilePieces, quarter = piece % kTilePieces;
+            const uint32_t st = g % C::kStages, slot = g % C::kSlots;
             const bool value = (g & 1) != 0;
             if (!(ok = warp_wait(&landed[slot], (g / C::kSlots) & 1u, p, 67))) break;
             const uint8_t *codes = smem + C::kCodesAt + slot * (kKeys * D) + quarter * kPieceRows * D;
@@ -427,7 +428,10 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
         for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
-        for (int h = 0; h < 2; ++h) mbar_init(&s_full[h], 1), mbar_init(&p_ready[h][0], 8 + withheld(p)), mbar_init(&p_ready[h][1], 8), mbar_init(&o_full[h], 1);
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(&s_full[h], 1), mbar_init(&o_full[h], 1);
+            mbar_init(&p_ready[h][0], 8 + withheld(p)), mbar_init(&p_ready[h][1], 8);
+        }
         mbar_init(&drain, 1);
         if (kQ8) {
             for (int i = 0; i < C::kStages; ++i) mbar_init(&conv[i], kKeys / kPieceRows);
@@ -467,7 +471,8 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     __syncthreads();
 
     if (kQ8 && warp >= kConvertWarp) {
-        convert_tiles<T, D>(tp, kMode == kScaled ? p.scale_log2 : kMode == kCapped ? p.cap_in : 1.f, run, next, smem, landed, taken, empty, conv);
+        const float k_unit = kMode == kScaled ? p.scale_log2 : kMode == kCapped ? p.cap_in : 1.f;
+        convert_tiles<T, D>(tp, k_unit, run, next, smem, landed, taken, empty, conv);
     } else if (warp >= kCopyWarp && warp < kCopyWarp + (kQ8 ? 1 : kCopyWarps)) {
         // ---- Q of each segment and its K tiles, or its V tiles
         const int me = warp - kCopyWarp;
@@ -500,7 +505,9 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                 if (j >= s1 - s0 || lane >= nbox || key >= it.len) return 0;
                 // past the tensor, read as zeros: a box before every row's window (its page may be
                 // gone already) and a bad page
-                const int pg = key + tp.box_rows <= it.seen && (!kMasks || key >= p.sinks) ? -1 : page_of(p.b, it.b, key, p.hdr);
+                const int pg = key + tp.box_rows <= it.seen && (!kMasks || key >= p.sinks)
+                                   ? -1
+                                   : page_of(p.b, it.b, key, p.hdr);
                 return (pg < 0 ? p.b.num_pages : pg) * p.b.Hkv + it.kh;
             };
             int z_next = page_z(0);
