@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
             float grown = 1.f;  // of the sums, where the scales' reference has grown
             {
                 const float mine = tail && key0 + lane >= it.len ? 0.f : vs[lane];
-                const uint32_t top = ref_bits(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
+                const uint32_t top = ref_bits(__reduce_max_sync(0xffffffffu, scale_bits(mine)));
                 if (top > ref) {
                     grown = __uint_as_float(ref) * over_ref(top);
                     ref = top;

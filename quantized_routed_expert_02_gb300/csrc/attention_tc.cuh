@@ -788,8 +788,8 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     if (kRef) {
                         const float4 x = *reinterpret_cast<const float4 *>(vs - 64 * ch + 4 * lane);
                         ref_up = max(ref, ref_bits(__reduce_max_sync(0xffffffffu,
-                                                                     max(max(__float_as_uint(x.x), __float_as_uint(x.y)),
-                                                                         max(__float_as_uint(x.z), __float_as_uint(x.w))))));
+                                                                     max(max(scale_bits(x.x), scale_bits(x.y)),
+                                                                         max(scale_bits(x.z), scale_bits(x.w))))));
                     }
                     if (j == 0) {
                         top = mt;

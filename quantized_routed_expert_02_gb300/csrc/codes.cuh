@@ -45,6 +45,8 @@ struct CodePair<__nv_bfloat16> {
 // fp16 weights times the values' scales would leave the type's range: they are taken
 // over a power of two near the largest scale so far, which the sums are multiplied by at the end.
 constexpr uint32_t kRefLeast = 0x00800000u, kRefMost = 0x7e800000u;  // 2^-126, 2^126
+// The bits of a scale, which rise with it: those of -0.0, the largest otherwise, are 0's.
+__device__ __forceinline__ uint32_t scale_bits(float scale) { return __float_as_uint(scale) & 0x7fffffffu; }
 // The power of two at or below a scale (its bits), in that range.
 __device__ __forceinline__ uint32_t ref_bits(uint32_t scale_bits) {
     return min(max(scale_bits & 0x7f800000u, kRefLeast), kRefMost);
