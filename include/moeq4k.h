@@ -475,8 +475,10 @@ MOE_API moe_status moe_rope_append_q8(const void *qkv_dev, const int32_t *pos_de
  *  v_pages_dev are the int8 codes above; dtype is that of q and out.  The codes are
  *  exact in either 16-bit type: q . code and its scale are taken in fp32 (q . code
  *  has to stay in its range, with a cap too), and a weight times its value's scale is
- *  rounded once, to dtype or to fp16.  Scales below kv_lens are finite and not
- *  negative; a code 0 with any of them is 0.
+ *  rounded once, to dtype or (max_new Hq / Hkv up to 16) to fp16: by half a step, in
+ *  fp16 by at most 2^-24 of the largest such product of what the row sees, whatever
+ *  the scales of other tokens.  Scales below kv_lens are finite and not negative
+ *  (-0.0 is 0), values' scales below 2^100; a code 0 with any of them is 0.
  *  Sinks: with window > 0 a row at cache index t sees the keys j <= t with
  *  j > t - window or j < sinks (sinks >= 0; without a window they change nothing).
  *  Table entries of pages between the two that no new token sees are not read.

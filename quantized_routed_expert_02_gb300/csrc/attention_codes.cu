@@ -19,8 +19,8 @@
 //
 // The first copies are under way before anything waits for the queries (48 of 2000 31.0 -> 29.2 us).
 //
-// Measured (32/4 heads of 128): 48 sequences of 150 to 12000 tokens 38.3 us (16-bit values 57.9), 128
-// of 4000 97.8 us = 5.5 TB/s, one over 93 6.1, one over 100000 30.4.  With the rows where the keys
+// Measured (32/4 heads of 128): 48 sequences of 150 to 12000 tokens 38.5 us (16-bit values 57.9), 128
+// of 4000 98.7 us = 5.5 TB/s, one over 93 6.3, one over 100000 30.5.  With the rows where the keys
 // are now (16 of them, half padding) and a rescale for every new maximum these took 42.9,
 // 110.7, 6.5 and 33.7; without any arithmetic the copies take 33 and 89.  Beside those, three CTAs an SM
 // with smaller rings (46.7 and 116), and the next piece's scores computed among a piece's softmax
@@ -30,6 +30,7 @@
 
 #include "attention_stream.cuh"
 #include "codes.cuh"
+#include "f32x2.cuh"
 #include "tcgen05.cuh"
 
 namespace moeq4k {
@@ -230,14 +231,23 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
 
         // sums of channels 16 c + 2 gid (o[][c][0 .. 1]) and the one after (o[][c][2 .. 3]) of this thread's rows
         float o[kN][D / 16][4], mx[kN][2], l[kN][2];
-        uint32_t ref = kRefLeast;
+        float re[kN][2], rf[kN][2];  // the rows' e, and 2^(kLift - e)
+        float enough[kN][2];         // scores up to here move no reference
+        // the scales that the pieces so far had, from `range` (their bits) to kSpread above it, and the logarithm
+        // of a power of two above those
+        uint32_t range = 0x80000000u;  // none
+        float range_log2 = 0.f;
 #pragma unroll
         for (int x = 0; x < kN; ++x) {
             mx[x][0] = mx[x][1] = -CUDART_INF_F;
             l[x][0] = l[x][1] = 0.f;
+            re[x][0] = re[x][1] = 0.f;
+            rf[x][0] = rf[x][1] = 1.f;
+            enough[x][0] = enough[x][1] = -CUDART_INF_F;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
         }
+        auto bounded = [&](int x, int c) { enough[x][c] = mx[x][c] + fminf(kGrowth, re[x][c] + kGrowth - range_log2); };
 
         bool ok = true;
         for (int i = 0; i < n; ++i) {
@@ -281,23 +291,26 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
                 kf[j] = ks[8 * j + gid];
                 vf[j] = tail && key0 + 8 * j + gid >= it.len ? 0.f : vs[8 * j + gid];
             }
-            float grown = 1.f;  // of the sums, where the scales' reference has grown
-            {
-                const float mine = tail && key0 + lane >= it.len ? 0.f : vs[lane];
-                const uint32_t top = ref_bits(__reduce_max_sync(0xffffffffu, scale_bits(mine)));
-                if (top > ref) {
-                    grown = __uint_as_float(ref) * over_ref(top);
-                    ref = top;
-                }
-                const float over = over_ref(ref);
+            bool apart = false;  // the piece's scales are: the rows' products are looked for key by key
+            const uint32_t mine = scale_bits(vs[lane]);
+            if (!__all_sync(0xffffffffu, mine - range <= kSpread)) {
+                // (of keys that some row may see)
+                const bool none = edge && (key0 + lane >= it.len || (key0 + lane >= p.sinks && key0 + lane < it.seen));
+                const uint32_t hi = __reduce_max_sync(0xffffffffu, none ? 0u : mine);
+                const uint32_t lo = min(hi, __reduce_min_sync(0xffffffffu, none ? 0xffffffffu : mine));
+                apart = hi - lo > kSpread;
+                if (!apart && (lo < range || hi - range > kSpread)) {
+                    range = lo - min(lo, (kSpread - (hi - lo)) / 2);
+                    range_log2 = scale_log2(range + kSpread);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) vf[j] *= over;
+                    for (int x = 0; x < kN; ++x) bounded(x, 0), bounded(x, 1);
+                }
             }
             // The rows' reference maxima, and with them the sums, follow the scores only where one has grown by
             // more than 2^kGrowth since (weights up to that are as exact in 16 bits as those up to 1, and
-            // the sums are fp32): in a short range new maxima are frequent.
-            float v[kN][2];
-            bool grows = grown != 1.f;
+            // the sums are fp32): in a short range new maxima are frequent.  So do the references of the products.
+            float v[kN][2];  // the rows' largest scores
+            bool grows = apart;
 #pragma unroll
             for (int x = 0; x < kN; ++x)
 #pragma unroll
@@ -316,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
                     v[x][c] = top;
-                    grows = grows || top > mx[x][c] + kGrowth;
+                    grows = grows || top > enough[x][c];
                 }
             if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
@@ -324,11 +337,24 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
                     float cor[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float up = fmaxf(mx[x][c], v[x][c]);
-                        cor[c] = exp2_approx(mx[x][c] - (up == -CUDART_INF_F ? 0.f : up));  // -inf: nothing seen yet
+                        const float up = fmaxf(mx[x][c], v[x][c]), base = up == -CUDART_INF_F ? 0.f : up;
+                        float product = v[x][c] + range_log2;  // the row's largest of the piece (log2)
+                        if (apart) {
+                            product = -CUDART_INF_F;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                product = fmaxf(product, s[x][j >> 1][2 * (j & 1) + c] + scale_log2(scale_bits(vf[j])));
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1)
+                                product = fmaxf(product, __shfl_xor_sync(0xffffffffu, product, w));
+                        }
+                        const float e = ref_exponent(fmaxf(mx[x][c] + re[x][c], product), base);
+                        l[x][c] *= exp2_approx(mx[x][c] - base);  // -inf: nothing seen yet
+                        cor[c] = exp2_approx((mx[x][c] - base) + (re[x][c] - e));
                         mx[x][c] = up;
-                        l[x][c] *= cor[c];
-                        cor[c] *= grown;
+                        re[x][c] = e;
+                        rf[x][c] = power_of_2(kLift - e);
+                        bounded(x, c);
                     }
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
@@ -342,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
             uint32_t pb[kN][2][2];
 #pragma unroll
             for (int x = 0; x < kN; ++x) {
+                const unsigned long long rf2 = pack2(rf[x][0], rf[x][1]);
                 float base[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) base[c] = mx[x][c] == -CUDART_INF_F ? 0.f : mx[x][c];
@@ -351,7 +378,9 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
                     const float b = exp2_approx(s[x][j >> 1][2 * (j & 1) + 1] - base[1]);
                     l[x][0] += a;
                     l[x][1] += b;
-                    pb[x][j >> 1][j & 1] = turned(Pair<__half>::make(a * vf[j], b * vf[j]));
+                    float wa, wb;
+                    unpack2(mul2(mul2(pack2(a, b), rf2), pack2(vf[j], vf[j])), wa, wb);
+                    pb[x][j >> 1][j & 1] = turned(Pair<__half>::make(wa, wb));
                 }
             }
             // O^T: matrices (keys 0-7 and 8-15 of 16, channel chunk c), then of chunk c + 1, transposed
@@ -387,7 +416,6 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
 
         // the warps' sums into their rings, the rows' statistics beside them
         float *so = reinterpret_cast<float *>(ring);
-        const float back = __uint_as_float(ref);
         __syncwarp();
 #pragma unroll
         for (int x = 0; x < kN; ++x)
@@ -397,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
 #pragma unroll
                 for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
                 const int r = 8 * x + 2 * tig + c;
+                const float back = power_of_2(re[x][c] - kLift);
                 if (gid == 0) {
                     sm_m[warp][r] = mx[x][c];
                     sm_l[warp][r] = sum;

@@ -33,7 +33,7 @@
 // there), and the scales come in the softmax: K's as a factor of the scores, in fp32, V's as
 // one of the weights before those are rounded.  80 registers a thread are left for that, so
 // each warp's run lies in shared memory.  The chunk of 2048 over 16384 takes 518 us = 0.99
-// PFLOP/s, with a cap 689: the memory's bytes are half, but the issue slots (62 % used) and the path to
+// PFLOP/s (fp16, whose rows have references of their own for V's scales: 538), with a cap 689: the memory's bytes are half, but the issue slots (62 % used) and the path to
 // shared memory (57 %, beside the products' own reads) now carry the codes' conversion and 768 loads of
 // scales a tile; without the conversion it took 465 of 583 us, without the softmax's scales 493 of 529.
 #pragma once
@@ -335,7 +335,7 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
         int s0, s1;
         if (!run_segment(p, run, s0, s1)) break;
         const uint32_t end = g0 + 2 * (s1 - s0);
-        const int len = run.item.len, ts = run.item.ts, t0 = run.item.t0;
+        const int len = run.item.len, ts = run.item.ts, t0 = run.item.t0, seen = run.item.seen;
         for (; piece / kTilePieces < end; piece += kConvertWarps) {
             const uint32_t g = piece / kTilePieces, quarter = piece % kTilePieces;
             const uint32_t st = g % C::kStages, slot = g % C::kSlots;
@@ -382,12 +382,13 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
             }
             // past the sequence's end the scales may be anything.  A key's is above 0: a hidden score is an
             // infinity, which 0 would make a NaN (the codes of a scale of 0 are 0 themselves).
-            const int i = s0 + int((g - g0) >> 1);
-            const bool past = (i < ts ? i : t0 - ts + i) * kKeys + key_in >= len;
+            // A value's of a key that no row sees is -0.0, all others' are positive or 0.
+            const int i = s0 + int((g - g0) >> 1), key = (i < ts ? i : t0 - ts + i) * kKeys + key_in;
+            const bool past = key >= len;
             const float kf = f * k_unit;
             reinterpret_cast<float *>(smem + C::kScalesAt)[((g >> 1) % C::kScaleTiles) * (2 * kKeys) +
                                                            (value ? kKeys : 0) + key_in] =
-                value  ? (past ? 0.f : f)
+                value  ? (past || (key >= p.sinks && key < seen) ? -0.f : fabsf(f))
                 : past ? 1.f
                        : (kf <= 1.17549435e-38f ? 1.17549435e-38f : kf);
             fence_proxy_async_smem();  // these stores before the products' reads of them
@@ -688,7 +689,9 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                 const bool tree = kMasks && p.tree != nullptr;
                 const int all = tree ? run.seq.len - run.seq.n - 1 : first, late = tree ? it.len - 1 : first + nth - 1;
                 float top = -CUDART_INF_F, sum = 0.f;  // reference maximum (log2), sum of weights
-                uint32_t ref = kRefLeast;              // of the values' scales
+                // kRef: the row's e; the scales that the tiles so far had, as in the streaming kernel
+                float re = 0.f;
+                uint32_t range = 0x80000000u;
                 for (int j = 0; j < s1 - s0; ++j) {
                     ok = ok && warp_wait(&s_full[h], ns & 1u, p, 61 + h);
                     ++ns;
@@ -784,26 +787,58 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                              : capped                    ? score<true>(mt * sign, p)
                              : kQ8 && kMode == kScaled   ? mt
                                                          : score<false>(mt * sign, p);
-                    uint32_t ref_up = ref;  // with this tile's scales
+                    float product = -CUDART_INF_F;  // the row's largest of the tile (log2)
                     if (kRef) {
-                        const float4 x = *reinterpret_cast<const float4 *>(vs - 64 * ch + 4 * lane);
-                        ref_up = max(ref, ref_bits(__reduce_max_sync(0xffffffffu,
-                                                                     max(max(scale_bits(x.x), scale_bits(x.y)),
-                                                                         max(scale_bits(x.z), scale_bits(x.w))))));
+                        // the tile's scales, four a lane (-0.0 is the least as a signed number, and above all others as
+                        // an unsigned one)
+                        const uint4 x = *reinterpret_cast<const uint4 *>(vs - 64 * ch + 4 * lane);
+                        const int hi = max(max(int(x.x), int(x.y)), max(int(x.z), int(x.w)));
+                        const uint32_t lo = min(min(x.x, x.y), min(x.z, x.w));
+                        bool apart = false;
+                        if (!__all_sync(0xffffffffu, lo >= range && hi <= int(range + kSpread))) {
+                            const uint32_t hi_all = max(__reduce_max_sync(0xffffffffu, hi), 0);
+                            const uint32_t lo_all = min(__reduce_min_sync(0xffffffffu, lo), hi_all);
+                            apart = hi_all - lo_all > kSpread;
+                            if (!apart) {
+                                range = lo_all - min(lo_all, (kSpread - (hi_all - lo_all)) / 2);
+                            }
+                        }
+                        if (apart) {
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                float u[16];
+                                tmem_ld16(ts + 16 * c, u);
+                                wait_ld16(u);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float x = u[i] * ks[16 * c + i];
+                                    const float z = kMode == kCapped            ? capped_far(fmaxf(x, lowest), cap_in, p)
+                                                    : capped                    ? score<true>(x, p)
+                                                    : kMode == kScaled          ? x
+                                                                                : score<false>(x, p);
+                                    if (x != hidden) product = fmaxf(product, z + scale_log2(scale_bits(vs[16 * c + i])));
+                                }
+                            }
+                            product = fmaxf(product, exchange(product));
+                        } else {
+                            product = mt + scale_log2(range + kSpread);
+                        }
+                        if (!live) product = -CUDART_INF_F;
                     }
                     if (j == 0) {
                         top = mt;
-                        ref = ref_up;
-                    } else if (__any_sync(0xffffffffu, mt - top > kGrowth) || ref_up != ref) {
+                        if (kRef) re = ref_exponent(product, top == -CUDART_INF_F ? 0.f : top);
+                    } else if (__any_sync(0xffffffffu, mt - top > kGrowth || (kRef && product - top - re > kGrowth))) {
                         // this half's P V of the tile before is complete: its S came after it
-                        const float up = fmaxf(top, mt);
-                        float f = exp2_approx(top - (up == -CUDART_INF_F ? 0.f : up));
+                        const float up = fmaxf(top, mt), base = up == -CUDART_INF_F ? 0.f : up;
+                        float f = exp2_approx(top - base);
                         sum *= f;
-                        top = up;
                         if (kRef) {
-                            f *= __uint_as_float(ref) * over_ref(ref_up);
-                            ref = ref_up;
+                            const float e = ref_exponent(fmaxf(top + re, product), base);
+                            f = exp2_approx((top - base) + (re - e));
+                            re = e;
                         }
+                        top = up;
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
                             float o[16];
@@ -823,7 +858,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     const unsigned long long scale2 = pack2(scale, scale), base2 = pack2(b, b);
                     const unsigned long long one2 = pack2(1.f, 1.f), near2 = pack2(p.cap_y, p.cap_y);
                     const float from = edge ? -CUDART_INF_F : kTanhMinusOne;
-                    const float per_ref = kRef ? over_ref(ref) : 1.f;
+                    const float rf = kRef ? power_of_2(kLift - re) : 1.f;
                     const unsigned long long hide2 = pack2(0x1p-100f, 0x1p-100f);
                     auto take = [&](auto is_plain, int c, const float (&raw)[16]) {
                         constexpr bool kPlain = decltype(is_plain)::value;
@@ -904,9 +939,9 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                                 // rounded for the product, whose operands have one type (V's values were
                                 // rounded to it by the same half step); the sum keeps the weight whole
                                 if (kQ8) {
-                                    unsigned long long v2 = k == 0 ? pack2(vsc.x, vsc.y) : pack2(vsc.z, vsc.w);
-                                    if (kRef) v2 = mul2(v2, pack2(per_ref, per_ref));
-                                    unpack2(mul2(pack2(x, y), v2), x, y);
+                                    unsigned long long w2 = pack2(x, y);
+                                    if (kRef) w2 = mul2(w2, pack2(rf, rf));
+                                    unpack2(mul2(w2, k == 0 ? pack2(vsc.x, vsc.y) : pack2(vsc.z, vsc.w)), x, y);
                                 }
                                 w[i / 2 + k] = Pair<T>::make(x, y);
                             }
@@ -952,7 +987,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                 const int out_row = live ? (it.row0 + h * tp.tth + tok_h) * p.b.Hq + it.kh * G + head : -1;
                 float *mine = p.part + size_t(part_slot(blockIdx.x, s0 == 0)) * part_floats(2 * kHalf, D);
                 const int prow = h * kHalf + row;
-                const float unit = kRef ? __uint_as_float(ref) : 1.f, inv = over_sum(sum) * unit;
+                const float unit = kRef ? power_of_2(re - kLift) : 1.f, inv = over_sum(sum) * unit;
 #pragma unroll 1
                 for (int c = 0; ok && c < D / 64; ++c) {
                     const int ch0 = D / 2 * ch + 32 * c;  // first of 32 channels

@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <math_constants.h>
 
 #include <stdint.h>
 
@@ -42,15 +43,29 @@ struct CodePair<__nv_bfloat16> {
     }
 };
 
-// fp16 weights times the values' scales would leave the type's range: they are taken
-// over a power of two near the largest scale so far, which the sums are multiplied by at the end.
-constexpr uint32_t kRefLeast = 0x00800000u, kRefMost = 0x7e800000u;  // 2^-126, 2^126
+// Weights times the values' scales, the product's operands, would leave fp16's range.  Each row
+// takes them over 2^(e - kLift) of its own, which its sums are multiplied by at the end: 2^e is at or above the
+// largest of them (over the row's reference maximum) that the row has seen, so that neither a scale that it does
+// not see nor one without weight costs it anything.  As the maximum does, e follows only growth past 2^kGrowth: an
+// operand is at most 2^(kLift + 8) = 2^14.
+//
+// The largest product of a tile is bounded by the largest weight times the largest scale where the scales are
+// within 2^4 of one another, and else looked for key by key.  With the roundings up to powers of two e is at most
+// 6.1 above it, so what an operand loses below 2^-14, half a step of 2^-24, is at most 2^-24 of the row's largest.
+constexpr float kLift = 6.f;
+constexpr float kRefLeast = -112.f, kRefMost = 126.f;  // of e: the factors stay normal
+constexpr uint32_t kSpread = 4u << 23;                 // as a difference of scales' bits
 // The bits of a scale, which rise with it: those of -0.0, the largest otherwise, are 0's.
 __device__ __forceinline__ uint32_t scale_bits(float scale) { return __float_as_uint(scale) & 0x7fffffffu; }
-// The power of two at or below a scale (its bits), in that range.
-__device__ __forceinline__ uint32_t ref_bits(uint32_t scale_bits) {
-    return min(max(scale_bits & 0x7f800000u, kRefLeast), kRefMost);
+// The exponent of the power of two above a scale (its bits), -inf for 0.
+__device__ __forceinline__ float scale_log2(uint32_t bits) {
+    return bits == 0u ? -CUDART_INF_F : float(int(bits >> 23) - 126);
 }
-__device__ __forceinline__ float over_ref(uint32_t bits) { return __uint_as_float(0x7f000000u - bits); }
+// e of a row whose largest product and reference maximum have these logarithms.
+__device__ __forceinline__ float ref_exponent(float product, float base) {
+    return fminf(fmaxf(ceilf(product - base), kRefLeast), kRefMost);
+}
+// 2^e of an integer e from -126 to 127.
+__device__ __forceinline__ float power_of_2(float e) { return __int_as_float((int(e) + 127) << 23); }
 
 }  // namespace moeq4k
