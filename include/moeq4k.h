@@ -477,8 +477,10 @@ MOE_API moe_status moe_rope_append_q8(const void *qkv_dev, const int32_t *pos_de
  *  has to stay in its range, with a cap too), and a weight times its value's scale is
  *  rounded once, to dtype or (max_new Hq / Hkv up to 16) to fp16: by half a step, in
  *  fp16 by at most 2^-24 of the largest such product of what the row sees, whatever
- *  the scales of other tokens.  Scales below kv_lens are finite and not negative
- *  (-0.0 is 0), values' scales below 2^100; a code 0 with any of them is 0.
+ *  the scales of other tokens.  Scales below kv_lens are not negative (-0.0 is 0),
+ *  values' scales below 2^100; a code 0 with any of them is 0.  A scale that is not
+ *  finite, its head's codes 0 (as the append stores it), makes the rows that see it NaN, out and
+ *  lse, and no others.
  *  Sinks: with window > 0 a row at cache index t sees the keys j <= t with
  *  j > t - window or j < sinks (sinks >= 0; without a window they change nothing).
  *  Table entries of pages between the two that no new token sees are not read.

@@ -295,12 +295,27 @@ __global__ void __launch_bounds__(kThreads, 2) attention_codes_kernel(const __gr
             const uint32_t mine = scale_bits(vs[lane]);
             if (!__all_sync(0xffffffffu, mine - range <= kSpread)) {
                 // (of keys that some row may see)
-                const bool none = edge && (key0 + lane >= it.len || (key0 + lane >= p.sinks && key0 + lane < it.seen));
+                bool none = edge && (key0 + lane >= it.len || (key0 + lane >= p.sinks && key0 + lane < it.seen));
+                const uint32_t odd = __ballot_sync(0xffffffffu, mine >= kInfinity);
+                if (odd != 0u) {
+                    // values that are not finite make the rows that see them NaN; the others' weights are 0, and
+                    // so must those be
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (scale_bits(vf[j]) >= kInfinity) vf[j] = 0.f;
+#pragma unroll
+                    for (int x = 0; x < kN; ++x)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if ((sight32(p, run.seq, sight[x][c], key0) & odd) != 0u) l[x][c] = CUDART_NAN_F;
+                    none = none || mine >= kInfinity;
+                    __syncwarp();
+                }
                 const uint32_t hi = __reduce_max_sync(0xffffffffu, none ? 0u : mine);
                 const uint32_t lo = min(hi, __reduce_min_sync(0xffffffffu, none ? 0xffffffffu : mine));
                 apart = hi - lo > kSpread;
                 if (!apart && (lo < range || hi - range > kSpread)) {
-                    range = lo - min(lo, (kSpread - (hi - lo)) / 2);
+                    range = min(lo - min(lo, (kSpread - (hi - lo)) / 2), kInfinity - 1 - kSpread);
                     range_log2 = scale_log2(range + kSpread);
 #pragma unroll
                     for (int x = 0; x < kN; ++x) bounded(x, 0), bounded(x, 1);

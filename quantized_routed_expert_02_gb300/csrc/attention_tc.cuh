@@ -32,8 +32,8 @@
 // more warps spread them to the 16-bit tiles that the products read (every code is exact
 // there), and the scales come in the softmax: K's as a factor of the scores, in fp32, V's as
 // one of the weights before those are rounded.  80 registers a thread are left for that, so
-// each warp's run lies in shared memory.  The chunk of 2048 over 16384 takes 518 us = 0.99
-// PFLOP/s (fp16, whose rows have references of their own for V's scales: 538), with a cap 689: the memory's bytes are half, but the issue slots (62 % used) and the path to
+// each warp's run lies in shared memory.  The chunk of 2048 over 16384 takes 529 us = 0.97
+// PFLOP/s (fp16, whose rows have references of their own for V's scales: 536), with a cap 697: the memory's bytes are half, but the issue slots (62 % used) and the path to
 // shared memory (57 %, beside the products' own reads) now carry the codes' conversion and 768 loads of
 // scales a tile; without the conversion it took 465 of 583 us, without the softmax's scales 493 of 529.
 #pragma once
@@ -316,7 +316,8 @@ __device__ __forceinline__ bool copy_codes(const TcParams &tp, const Item &it, i
 // issue.)
 template <typename T, int D, typename F>
 __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, const Run &run, F next, uint8_t *smem,
-                                              uint64_t *landed, uint64_t *taken, uint64_t *empty, uint64_t *conv) {
+                                              uint64_t *landed, uint64_t *taken, uint64_t *empty, uint64_t *conv,
+                                              volatile int *odd) {
     using C = Cfg<D, kCodes>;
     constexpr int kRowsAtOnce = 512 / D, kSteps = kPieceRows / kRowsAtOnce;  // of a piece
     constexpr int kAhead = kSteps / 2, kTilePieces = kKeys / kPieceRows;
@@ -381,14 +382,21 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
                 store(k, first, second);
             }
             // past the sequence's end the scales may be anything.  A key's is above 0: a hidden score is an
-            // infinity, which 0 would make a NaN (the codes of a scale of 0 are 0 themselves).
-            // A value's of a key that no row sees is -0.0, all others' are positive or 0.
+            // infinity, which 0 would make a NaN (the codes of a scale of 0 are 0 themselves).  For the same reason one
+            // that is not finite becomes an infinity: times the codes 0 it gives NaN to the rows that see it.
+            // A value's of a key that no row sees is -0.0, and so is one that is not finite: what it makes NaN is found
+            // at the segment's end, where `odd` says that there is any.  All others are positive or 0.
             const int i = s0 + int((g - g0) >> 1), key = (i < ts ? i : t0 - ts + i) * kKeys + key_in;
             const bool past = key >= len;
-            const float kf = f * k_unit;
+            const float kf = fminf(f, CUDART_INF_F) * k_unit;  // (of a NaN an infinity)
+            float vf = past || (key >= p.sinks && key < seen) ? -0.f : fabsf(f);
+            if (value && scale_bits(vf) >= kInfinity) {
+                vf = -0.f;
+                *odd = 1;
+            }
             reinterpret_cast<float *>(smem + C::kScalesAt)[((g >> 1) % C::kScaleTiles) * (2 * kKeys) +
                                                            (value ? kKeys : 0) + key_in] =
-                value  ? (past || (key >= p.sinks && key < seen) ? -0.f : fabsf(f))
+                value  ? vf
                 : past ? 1.f
                        : (kf <= 1.17549435e-38f ? 1.17549435e-38f : kf);
             fence_proxy_async_smem();  // these stores before the products' reads of them
@@ -399,6 +407,26 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
         g0 = end;
         next();
     }
+}
+
+// Whether the row sees one of a segment's keys whose value's scale is not finite, in 64 keys of each tile from
+// `at` on; the whole warp calls it.
+static __device__ __noinline__ bool sees_odd(const Params &p, const SeqView &s, const Item &it, const Sight &sight, int s0, int s1,
+                                      int at) {
+    const int lane = threadIdx.x & 31;
+    bool sees = false;
+    for (int i = 2 * s0; i < 2 * s1; ++i) {
+        const int key0 = tile_key<kKeys, true>(it, i >> 1) + at + 32 * (i & 1), key = key0 + lane;
+        bool is = false;
+        if (key < it.len && (key < p.sinks || key >= it.seen)) {
+            const int pg = page_of(p.b, it.b, key, p.hdr);
+            is = pg >= 0 && scale_bits(p.vs[(size_t(pg) * p.b.Hkv + it.kh) * p.b.page + key % p.b.page]) >= kInfinity;
+        }
+        const uint32_t odd = __ballot_sync(0xffffffffu, is);
+        sees = sees || (odd != 0u && (sight32(p, s, sight, key0) & odd) != 0u);
+        __syncwarp();
+    }
+    return sees;
 }
 
 // How a score follows from q.k: by a positive scale, capped after a positive
@@ -418,6 +446,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[C::kStages], empty[C::kStages], q_full, q_empty, s_full[2], p_ready[2][2],
         o_full[2], drain, conv[kQ8 ? C::kStages : 1], landed[C::kSlots], taken[C::kSlots];
+    __shared__ int odd;  // values that are not finite have been met
     __shared__ uint32_t tmem_base;
     __shared__ Run run_sh;
     __shared__ Run run_of[kQ8 ? kCodesThreads / 32 : 1];  // each warp's own, where registers are few
@@ -438,6 +467,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
             for (int i = 0; i < C::kStages; ++i) mbar_init(&conv[i], kKeys / kPieceRows);
             for (int i = 0; i < C::kSlots; ++i) mbar_init(&landed[i], 1), mbar_init(&taken[i], kKeys / kPieceRows);
         }
+        odd = 0;
         prefetch_map(&tp.mq);
         prefetch_map(&tp.mk);
         prefetch_map(&tp.mv);
@@ -473,7 +503,7 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
 
     if (kQ8 && warp >= kConvertWarp) {
         const float k_unit = kMode == kScaled ? p.scale_log2 : kMode == kCapped ? p.cap_in : 1.f;
-        convert_tiles<T, D>(tp, k_unit, run, next, smem, landed, taken, empty, conv);
+        convert_tiles<T, D>(tp, k_unit, run, next, smem, landed, taken, empty, conv, &odd);
     } else if (warp >= kCopyWarp && warp < kCopyWarp + (kQ8 ? 1 : kCopyWarps)) {
         // ---- Q of each segment and its K tiles, or its V tiles
         const int me = warp - kCopyWarp;
@@ -977,6 +1007,9 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                     unpack2(add2(s2[0], s2[1]), sa, sb);
                     sum += sa + sb;
                 }
+                if (kQ8 && *static_cast<volatile int *>(&odd) != 0 && sees_odd(p, run.seq, it, sight, s0, s1, 64 * ch))
+                    sum = CUDART_NAN_F;
+                __syncwarp();
                 // ---- the half's result: this warp's channels
                 sum += exchange(sum);
                 meet();  // both have read: the space is free for the results

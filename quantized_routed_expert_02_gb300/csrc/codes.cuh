@@ -57,6 +57,7 @@ constexpr float kRefLeast = -112.f, kRefMost = 126.f;  // of e: the factors stay
 constexpr uint32_t kSpread = 4u << 23;                 // as a difference of scales' bits
 // The bits of a scale, which rise with it: those of -0.0, the largest otherwise, are 0's.
 __device__ __forceinline__ uint32_t scale_bits(float scale) { return __float_as_uint(scale) & 0x7fffffffu; }
+constexpr uint32_t kInfinity = 0x7f800000u;  // bits of scales from there on are of an infinity or a NaN
 // The exponent of the power of two above a scale (its bits), -inf for 0.
 __device__ __forceinline__ float scale_log2(uint32_t bits) {
     return bits == 0u ? -CUDART_INF_F : float(int(bits >> 23) - 126);

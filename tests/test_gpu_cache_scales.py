@@ -161,3 +161,94 @@ def test_large_scales_that_come_and_go(m, new, dtype):
         case.vs = torch.where(case.vs.isnan(), math.nan, size)
         run_row_ref(m, case)
         run_row_ref(m, case, window=100, sinks=3, trees=random_trees([new]))
+
+
+SPOILED = pytest.mark.parametrize("which", ["k", "v", "both"])
+
+
+def spoil(case, b, tokens, value, which):
+    """Heads as the append stores them where they hold an infinity or a NaN: that as the scale, codes 0."""
+    for j in tokens:
+        pg, row = at(case, b, j)
+        for n in "kv" if which == "both" else which:
+            getattr(case, n)[pg, :, row] = 0
+            getattr(case, n + "s")[pg, :, row] = value
+
+
+def check_spoiled(m, case, b, tokens, value, which, window=0, softcap=0.0, sinks=0, trees=None, scale=None):
+    """The rows that see one of the tokens are NaN (and say so in lse), all others as if it were finite."""
+    words = 0 if trees is None else -(-case.most // 32)
+    scale = case.D ** -0.5 if scale is None else scale
+    o, e, tol, lse_tol = cache_ref(case, scale, window, softcap, sinks, trees, words)
+    spoil(case, b, tokens, value, which)
+    out, lse, code, detail = run_attn(m, case, window, softcap, sinks,
+                                      None if trees is None else tree_tensor(trees, case.N, words), scale=scale)
+    assert code == 0, (m.status_str(code), detail)
+    first, n = sum(case.new[:b]), case.new[b]
+    seen = visible(n, case.lens_list[b], window, sinks, None if trees is None else trees[first:first + n], words)
+    hit = torch.zeros(case.N, dtype=torch.bool)
+    hit[first:first + n] = seen[:, list(tokens)].any(1)
+    assert bool(out[hit].isnan().all()) and bool(lse[hit].isnan().all())
+    within(out[~hit], o[~hit], tol[~hit], "out")
+    within(lse[~hit], e[~hit], lse_tol[~hit], "lse")
+    return int(hit.sum())
+
+
+MODES = pytest.mark.parametrize("softcap,scale", [(0.0, None), (20.0, None), (100.0, None), (0.0, -0.1), (30.0, -0.1)],
+                                ids=["plain", "cap", "farcap", "negative", "negativecap"])
+
+
+@SPOILED
+@TYPES
+@MODES
+@pytest.mark.parametrize("new", [2, 6, 60, 150])
+def test_scales_that_are_not_finite_in_other_branches(m, new, softcap, scale, dtype, which):
+    """A drafted token whose head holds an infinity or a NaN: its own row and its descendants' are NaN, no others."""
+    for value in (math.inf, math.nan):
+        case = Batch8([new, 1], [new + 200, 70], 8, 4, 64, 16, dtype, seed=new)
+        evens = sum(1 << i for i in range(0, new, 2))
+        trees = [evens & ((2 << i) - 1) | 1 << i for i in range(new)] + [1]
+        assert check_spoiled(m, case, 0, [200 + new // 4 * 2 + 1], value, which, softcap=softcap, scale=scale, trees=trees) == 1
+
+
+@SPOILED
+@TYPES
+@pytest.mark.parametrize("new", [1, 4, 40, 300])
+def test_scales_that_are_not_finite_out_of_sight(m, new, dtype, which):
+    """Between the sinks and the window, at both ends of that, and in a chunk's last tokens."""
+    window, sinks, L = 150, 5, new + 700
+    for value in (math.inf, math.nan):
+        hidden = [sinks, sinks + 1, 100, L - new - window - 5, L - new - window]
+        case = Batch8([new], [L], 8, 4, 128, 16, dtype, seed=2)
+        assert check_spoiled(m, case, 0, hidden, value, which, window=window, sinks=sinks) == 0
+        case = Batch8([new], [new + 30], 8, 4, 128, 32, dtype, seed=1)
+        assert check_spoiled(m, case, 0, [new + 29], value, which) == 1
+        case = Batch8([new], [L], 8, 4, 128, 32, dtype, seed=1)
+        assert check_spoiled(m, case, 0, [sinks - 1, 333], value, which, window=window, sinks=sinks) == new
+        assert check_spoiled(m, Batch8([new], [L], 8, 4, 128, 32, dtype, seed=1), 0, [333], value, which) == new
+
+
+@TYPES
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_spoiled_row_from_append_to_attention(m, new, dtype):
+    """A projected row that holds a NaN: the append stores it, and the rows that do not see it are as without."""
+    from tests.test_gpu_cache import run_rope8
+    case = Batch8([new + 2], [new + 202], 8, 2, 128, 16, dtype, seed=5)
+    rows = torch.randn(case.N, 12 * 128, generator=torch.Generator().manual_seed(1)).to(dtype)
+    rows[new + 1, 8 * 128:] = math.nan
+    r = run_rope8(m, case, torch.arange(200, new + 202, dtype=torch.int32)[None], 128, qkv=rows)
+    for n in ("k", "v", "ks", "vs"):
+        setattr(case, n, r[n])
+    case.q = r["q_out"]
+    trees = [(1 << i) - 1 | 1 << i for i in range(new + 1)] + [2 << new]
+    words = -(-case.most // 32)
+    clean = Batch8([new + 2], [new + 202], 8, 2, 128, 16, dtype, seed=5)
+    for n in ("k", "v", "ks", "vs", "q"):
+        setattr(clean, n, getattr(case, n).clone())
+    pg, row = at(clean, 0, new + 201)
+    clean.ks[pg, :, row] = clean.vs[pg, :, row] = 0.0
+    o, e, tol, lse_tol = cache_ref(clean, 128 ** -0.5, trees=trees, words=words)
+    out, lse, code, _ = run_attn(m, case, tree=tree_tensor(trees, case.N, words))
+    assert code == 0 and bool(out[new + 1].isnan().all()) and bool(lse[new + 1].isnan().all())
+    within(out[:new + 1], o[:new + 1], tol[:new + 1], "out")
+    within(lse[:new + 1], e[:new + 1], lse_tol[:new + 1], "lse")
