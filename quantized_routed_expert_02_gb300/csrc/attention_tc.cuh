@@ -398,7 +398,7 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
                                                            (value ? kKeys : 0) + key_in] =
                 value  ? vf
                 : past ? 1.f
-                       : (kf <= 1.17549435e-38f ? 1.17549435e-38f : kf);
+                       : (kf <= 1.4e-45f ? 1.4e-45f : kf);
             fence_proxy_async_smem();  // these stores before the products' reads of them
             __syncwarp();
             if (lane == 0) mbar_arrive(&conv[st]);

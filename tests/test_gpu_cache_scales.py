@@ -252,3 +252,13 @@ def test_a_spoiled_row_from_append_to_attention(m, new, dtype):
     assert code == 0 and bool(out[new + 1].isnan().all()) and bool(lse[new + 1].isnan().all())
     within(out[:new + 1], o[:new + 1], tol[:new + 1], "out")
     within(lse[:new + 1], e[:new + 1], lse_tol[:new + 1], "lse")
+
+
+@pytest.mark.parametrize("softcap", [0.0, 20.0, 100.0])
+@pytest.mark.parametrize("new", [1, 60])
+def test_tiny_key_scales_under_large_queries(m, new, softcap):
+    """Keys' scales at and below the smallest normal fp32, whose products with large queries are scores of some size."""
+    case = Batch8([new], [new + 300], 8, 4, 64, 16, BF16, seed=7)
+    case.q.mul_(2.0 ** 114)  # q . code up to some 2^126
+    case.ks.mul_(2.0 ** -123)  # about 2^-129
+    check_attn(m, case, scale=0.25, softcap=softcap)
