@@ -528,16 +528,18 @@ MOE_API moe_status moe_cache_keep(void *k_pages_dev, void *v_pages_dev, float *k
 
 /*
  * Test hooks for the bounded device-side waits (not for production use).
- * moe_debug_set_wait_limit: upper bound, in ns, of every device-side wait
- * of later calls (0 restores the default of 1 s).  moe_debug_withhold_arrivals:
+ * moe_debug_set_wait_limit: upper bound, in ns, of the device-side waits
+ * of later calls (0 restores the default of 1 s).  Two kinds may last longer: the
+ * router's CTAs wait for one another up to twice that, and attention's wait up to 1 s, whatever
+ * the limit, for copies and products of their own.  moe_debug_withhold_arrivals:
  * n != 0 makes CTA 0 of later single-token calls publish none of its router
  * logits and h values, so the other CTAs' waits for them run out; such a
  * call records MOE_ERR_TIMEOUT in the workspace status and writes no output.
  * On the tensor-core batch path, CTA 0 of the gate/up GEMM then counts none
  * of its finished h rows, so the down GEMM's waits for those experts run
  * out: MOE_ERR_TIMEOUT again, and y holds no valid output.  CTA 0 of
- * moe_attention_paged's kernels then waits for an arrival that nobody makes:
- * MOE_ERR_TIMEOUT, no valid output.
+ * moe_attention_paged's and moe_attention_cache's kernels then waits for an arrival
+ * that nobody makes: MOE_ERR_TIMEOUT, no valid output.
  * Re-initialise the workspace (moe_workspace_init) afterwards to clear the
  * sticky status.
  */

@@ -407,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm_kernel(const __grid_
     constexpr int nmat = 2;  // two A operands per item: gate and up, or two 128-row halves
     const int S = p.K / kBK;  // MMA stages per item
     const int SR = S / kSub;  // raw stages per item
-    // The waits within the CTA follow from the wait for another launch's rows: they run out later, so that
-    // the place that is recorded is the cause.
-    const uint64_t ready_deadline = global_timer_ns() + p.wait_ns, deadline = ready_deadline + p.wait_ns / 8;
+    // The waits within the CTA follow from the wait for another launch's rows: that runs out an eighth of the
+    // limit ahead of them, so that the place that is recorded is the cause.
+    const uint64_t deadline = global_timer_ns() + p.wait_ns, ready_deadline = deadline - p.wait_ns / 8;
     const uint32_t tcols = 512u;  // two 256-column accumulators (buffers, or M halves)
     const uint32_t nbuf = p.mh == 2 ? 1u : 2u;  // accumulator buffers (item li uses li % nbuf)
 
