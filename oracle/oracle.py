@@ -69,8 +69,11 @@ def lib():
 
 
 def load_variant(path: str):
-    """Load another build of the oracle source (used by the mutation tests)."""
-    return _load(path)
+    """Load another build of the oracle source (used by the mutation tests).  Its indices may be
+    wrong, so an ``Oracle`` over it hands it copies of the weights with as much again before and after them."""
+    handle = _load(path)
+    handle.roomy = True
+    return handle
 
 
 def _p(a: np.ndarray):
@@ -86,6 +89,14 @@ class Oracle:
 
     def __init__(self, handle=None):
         self.L = handle if handle is not None else lib()
+
+    def _weights(self, blob):
+        blob = _c(blob, np.uint8).reshape(-1)
+        if not getattr(self.L, "roomy", False):
+            return blob
+        room = np.zeros(3 * blob.size, dtype=np.uint8)
+        room[blob.size:2 * blob.size] = blob
+        return room[blob.size:2 * blob.size]
 
     def set_threads(self, n: int):
         self.L.moq_set_threads(int(n))
@@ -125,8 +136,8 @@ class Oracle:
         xv = _c(xv, np.float64)
         h = np.empty(I, dtype=np.float64)
         o = np.empty(H, dtype=np.float64)
-        self.L.moq_expert(_p(xv), _p(_c(gate_e, np.uint8)), _p(_c(up_e, np.uint8)),
-                          _p(_c(down_e, np.uint8)), H, I, _p(h), _p(o))
+        gate_e, up_e, down_e = (self._weights(b) for b in (gate_e, up_e, down_e))
+        self.L.moq_expert(_p(xv), _p(gate_e), _p(up_e), _p(down_e), H, I, _p(h), _p(o))
         return h, o
 
     def ffn(self, x, idx, w, gate, up, down, E, I, tokens=None):
@@ -138,8 +149,8 @@ class Oracle:
         w = _c(w, np.float64)
         y = np.full((T, H), np.nan, dtype=np.float64)
         tok = None if tokens is None else _c(tokens, np.int32)
-        skipped = self.L.moq_ffn(_p(x), _p(idx), _p(w), _p(_c(gate, np.uint8)),
-                                 _p(_c(up, np.uint8)), _p(_c(down, np.uint8)),
+        gate, up, down = (self._weights(b) for b in (gate, up, down))
+        skipped = self.L.moq_ffn(_p(x), _p(idx), _p(w), _p(gate), _p(up), _p(down),
                                  T, H, E, k, I, None if tok is None else _p(tok),
                                  0 if tok is None else tok.size, _p(y))
         return y, int(skipped)
@@ -178,7 +189,8 @@ class Oracle:
 
     def row_dot_q8k(self, row, ncols, q, d, sums):
         """fp64 dot of one Q4_K row (bytes) with one Q8_K vector."""
-        return float(self.L.moq_row_dot_q8k(_p(_c(row, np.uint8)), ncols // 256,
+        row = self._weights(row)
+        return float(self.L.moq_row_dot_q8k(_p(row), ncols // 256,
                                             _p(_c(q, np.int8)), _p(_c(d, np.float32)),
                                             _p(_c(sums, np.int32))))
 
@@ -192,8 +204,8 @@ class Oracle:
         w = _c(w, np.float64)
         y = np.full((T, H), np.nan, dtype=np.float64)
         tok = None if tokens is None else _c(tokens, np.int32)
-        skipped = self.L.moq_ffn_q8k(_p(x), _p(idx), _p(w), _p(_c(gate, np.uint8)),
-                                     _p(_c(up, np.uint8)), _p(_c(down, np.uint8)),
+        gate, up, down = (self._weights(b) for b in (gate, up, down))
+        skipped = self.L.moq_ffn_q8k(_p(x), _p(idx), _p(w), _p(gate), _p(up), _p(down),
                                      T, H, E, k, I, None if tok is None else _p(tok),
                                      0 if tok is None else tok.size, _p(y))
         return y, int(skipped)
