@@ -33,7 +33,7 @@
 // there), and the scales come in the softmax: K's as a factor of the scores, in fp32, V's as
 // one of the weights before those are rounded.  80 registers a thread are left for that, so
 // each warp's run lies in shared memory.  The chunk of 2048 over 16384 takes 529 us = 0.97
-// PFLOP/s (fp16, whose rows have references of their own for V's scales: 536), with a cap 697: the memory's bytes are half, but the issue slots (62 % used) and the path to
+// PFLOP/s (fp16, whose rows have references of their own for V's scales: 545), with a cap 697: the memory's bytes are half, but the issue slots (62 % used) and the path to
 // shared memory (57 %, beside the products' own reads) now carry the codes' conversion and 768 loads of
 // scales a tile; without the conversion it took 465 of 583 us, without the softmax's scales 493 of 529.
 #pragma once
@@ -801,7 +801,15 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                         if (kMode == kAny && capped) most = max3(fmaxf(a4[0], a4[1]), a4[2], a4[3]);
                     }
                     tmem_ld16(ts, v[0]);  // for the second pass
-                    mt = fmaxf(mt, exchange(mt));
+                    if (kRef) {
+                        // Where a wait has run out for one of the two warps, both know from here on: what follows meets
+                        // only where the scales say so, and only while both have seen the same ones.
+                        const float other = exchange(ok ? mt : CUDART_NAN_F);
+                        ok = ok && other == other;
+                        mt = fmaxf(mt, other);
+                    } else {
+                        mt = fmaxf(mt, exchange(mt));
+                    }
                     if (capped && !edge) mt = fmaxf(mt, lowest);
                     // a row of no token holds what was in shared memory, or another sequence's query:
                     // it has no say in the warp's choices below, which show in the live rows' roundings
@@ -829,11 +837,9 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
                             const uint32_t hi_all = max(__reduce_max_sync(0xffffffffu, hi), 0);
                             const uint32_t lo_all = min(__reduce_min_sync(0xffffffffu, lo), hi_all);
                             apart = hi_all - lo_all > kSpread;
-                            if (!apart) {
-                                range = lo_all - min(lo_all, (kSpread - (hi_all - lo_all)) / 2);
-                            }
+                            if (!apart) range = lo_all - min(lo_all, (kSpread - (hi_all - lo_all)) / 2);
                         }
-                        if (apart) {
+                        if (apart && ok) {
 #pragma unroll 1
                             for (int c = 0; c < 4; ++c) {
                                 float u[16];

@@ -262,3 +262,22 @@ def test_tiny_key_scales_under_large_queries(m, new, softcap):
     case.q.mul_(2.0 ** 114)  # q . code up to some 2^126
     case.ks.mul_(2.0 ** -123)  # about 2^-129
     check_attn(m, case, scale=0.25, softcap=softcap)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,lens", [([60], [100]), ([300] * 8, [900] * 8), ([900], [2500]), ([4] * 20, [3000] * 20)])
+def test_waits_that_run_out_over_scales_far_apart(m, new, lens, D):
+    """Whatever a warp reads after a wait has run out, the call ends, and the workspace serves again."""
+    case = Batch8(new, lens, 16, 2, D, 16, F16, seed=11)
+    g = torch.Generator().manual_seed(3)
+    case.vs *= 2.0 ** torch.randint(-40, 3, case.vs.shape, generator=g)
+    ws = m.alloc_attention_workspace(16, 2, D, device=DEV)
+    try:
+        m.moe_debug_set_wait_limit(20_000_000)      # 20 ms
+        m.moe_debug_withhold_arrivals(1)
+        assert m.status_str(run_attn(m, case, ws=ws)[2]) == "MOE_ERR_TIMEOUT"
+    finally:
+        m.moe_debug_withhold_arrivals(0)
+        m.moe_debug_set_wait_limit(0)
+    m.moe_workspace_init(ws)
+    check_attn(m, case, ws=ws)
