@@ -424,7 +424,8 @@ MOE_API moe_status moe_rope_append(const void *qkv_dev, const int32_t *pos_dev,
  *  lse -inf.  q_dev, out_dev [N, Hq, D] of dtype, not overlapping; scale
  *  finite, and scale / softcap.
  *  max_new >= 1: the most new tokens of any sequence, as far as the caller
- *  knows; it picks the kernel and may be wrong (only speed depends on it).
+ *  knows; it picks the kernel and may be wrong (speed depends on it, and which of
+ *  the roundings named here results have).
  *  Scores, softmax statistics and sums are fp32; without a cap q . k has to stay
  *  in its range, with one a score is within 2^-20 of itself or (softcap up to 64)
  *  2^-21 of the cap.  The weights are rounded to dtype for their product with
