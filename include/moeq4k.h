@@ -540,7 +540,9 @@ MOE_API moe_status moe_cache_keep(void *k_pages_dev, void *v_pages_dev, float *k
  * of its finished h rows, so the down GEMM's waits for those experts run
  * out: MOE_ERR_TIMEOUT again, and y holds no valid output.  CTA 0 of
  * moe_attention_paged's and moe_attention_cache's kernels then waits for an arrival
- * that nobody makes: MOE_ERR_TIMEOUT, no valid output.
+ * that nobody makes: MOE_ERR_TIMEOUT, no valid output.  With n = 2 the warps of
+ * CTA 0 of their tensor-core kernel instead take the lengths of a call of several items for
+ * changed under it: MOE_ERR_CACHE_RANGE, no valid output.
  * Re-initialise the workspace (moe_workspace_init) afterwards to clear the
  * sticky status.
  */

@@ -64,8 +64,12 @@ struct Params {
     int withhold;       // test hook: CTA 0's waits run out
 };
 
-// The arrivals that CTA 0's barriers expect and never get (moe_debug_withhold_arrivals).
-__device__ __forceinline__ int withheld(const Params &p) { return p.withhold != 0 && blockIdx.x == 0 ? 1 : 0; }
+// The arrivals that CTA 0's barriers expect and never get (moe_debug_withhold_arrivals), or, with this
+// value, CTA 0's pairs of warps count their tiles differently.
+constexpr int kCountApart = 2;
+__device__ __forceinline__ int withheld(const Params &p) {
+    return p.withhold != 0 && p.withhold != kCountApart && blockIdx.x == 0 ? 1 : 0;
+}
 
 // Bring a tensor map (a kernel parameter) into the cache of such descriptors.
 __device__ __forceinline__ void prefetch_map(const void *map) {

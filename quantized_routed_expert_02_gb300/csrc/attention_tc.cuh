@@ -1087,6 +1087,14 @@ __global__ void __launch_bounds__(form_threads(kForm), 1) attention_tc_kernel(co
             }
             gt += s1 - s0;
             next();
+            // Each warp reads the lengths for itself.  Should they change under the call (a missing stream order), the
+            // two of a row could count their tiles differently, and a barrier has no limit: they go on only together.
+            const unsigned turn = unsigned(run.item.tiles) * 512u + unsigned(run.item.nt) +
+                                  (p.withhold == kCountApart && blockIdx.x == 0 ? ch : 0);
+            if (run.u < run.end && __float_as_uint(exchange(__uint_as_float(turn))) != turn) {
+                record_status(p.hdr, MOE_ERR_CACHE_RANGE, run.seq.len);
+                break;
+            }
         }
     }
     tc::fence_before_sync();
