@@ -476,12 +476,12 @@ MOE_API moe_status moe_rope_append_q8(const void *qkv_dev, const int32_t *pos_de
  *  v_pages_dev are the int8 codes above; dtype is that of q and out.  The codes are
  *  exact in either 16-bit type: q . code and its scale are taken in fp32 (q . code
  *  has to stay in its range, with a cap too), and a weight times its value's scale is
- *  rounded once, to dtype or (max_new Hq / Hkv up to 16) to fp16: by half a step, in
- *  fp16 by at most 2^-24 of the largest such product of what the row sees, whatever
- *  the scales of other tokens.  Scales below kv_lens are not negative (-0.0 is 0),
- *  values' scales below 2^100; a code 0 with any of them is 0.  A scale that is not
- *  finite, its head's codes 0 (as the append stores it), makes the rows that see it NaN, out and
- *  lse, and no others.
+ *  rounded once, to dtype or (max_new Hq / Hkv up to 16) to fp16: by at most half a
+ *  step or, in fp16 and where that is more, 2^-24 of the largest such product of what
+ *  the row sees, whatever the scales of other tokens.  Scales below kv_lens are not
+ *  negative (-0.0 is 0), values' scales below 2^100; a code 0 with any of them is 0.
+ *  A scale that is not finite, its head's codes 0 (as the append stores it), makes the
+ *  rows that see it NaN, out and lse, and no others.
  *  Sinks: with window > 0 a row at cache index t sees the keys j <= t with
  *  j > t - window or j < sinks (sinks >= 0; without a window they change nothing).
  *  Table entries of pages between the two that no new token sees are not read.
@@ -531,8 +531,8 @@ MOE_API moe_status moe_cache_keep(void *k_pages_dev, void *v_pages_dev, float *k
  * Test hooks for the bounded device-side waits (not for production use).
  * moe_debug_set_wait_limit: upper bound, in ns, of the device-side waits
  * of later calls (0 restores the default of 1 s).  Two kinds may last longer: the
- * router's CTAs wait for one another up to twice that, and attention's wait up to 1 s, whatever
- * the limit, for copies and products of their own.  moe_debug_withhold_arrivals:
+ * router's CTAs wait for one another up to twice that, and attention's wait up to
+ * 1 s for copies and products of their own.  moe_debug_withhold_arrivals:
  * n != 0 makes CTA 0 of later single-token calls publish none of its router
  * logits and h values, so the other CTAs' waits for them run out; such a
  * call records MOE_ERR_TIMEOUT in the workspace status and writes no output.

@@ -33,9 +33,11 @@
 // there), and the scales come in the softmax: K's as a factor of the scores, in fp32, V's as
 // one of the weights before those are rounded.  80 registers a thread are left for that, so
 // each warp's run lies in shared memory.  The chunk of 2048 over 16384 takes 529 us = 0.97
-// PFLOP/s (fp16, whose rows have references of their own for V's scales: 545), with a cap 697: the memory's bytes are half, but the issue slots (62 % used) and the path to
-// shared memory (57 %, beside the products' own reads) now carry the codes' conversion and 768 loads of
-// scales a tile; without the conversion it took 465 of 583 us, without the softmax's scales 493 of 529.
+// PFLOP/s (fp16, whose rows have references of their own for V's scales: 545), with a cap 697:
+// the memory's bytes are half, but the issue slots (62 % used) and the path to shared memory
+// (57 %, beside the products' own reads) now carry the codes' conversion and 768 loads of scales a
+// tile; when it took 583 us it took 465 without the conversion, when 529 (an earlier form) 493
+// without the softmax's scales.
 #pragma once
 
 #include <algorithm>
@@ -411,8 +413,8 @@ __device__ __forceinline__ void convert_tiles(const TcParams &tp, float k_unit, 
 
 // Whether the row sees one of a segment's keys whose value's scale is not finite, in 64 keys of each tile from
 // `at` on; the whole warp calls it.
-static __device__ __noinline__ bool sees_odd(const Params &p, const SeqView &s, const Item &it, const Sight &sight, int s0, int s1,
-                                      int at) {
+static __device__ __noinline__ bool sees_odd(const Params &p, const SeqView &s, const Item &it, const Sight &sight,
+                                             int s0, int s1, int at) {
     const int lane = threadIdx.x & 31;
     bool sees = false;
     for (int i = 2 * s0; i < 2 * s1; ++i) {
