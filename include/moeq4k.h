@@ -474,8 +474,8 @@ MOE_API moe_status moe_rope_append_q8(const void *qkv_dev, const int32_t *pos_de
  * moe_attention_cache: moe_attention_paged over either cache and with more masks.
  *  Codes: with k_scales_dev and v_scales_dev (both or neither) k_pages_dev and
  *  v_pages_dev are the int8 codes above; dtype is that of q and out.  The codes are
- *  exact in either 16-bit type: q . code and its scale are taken in fp32 (q . code
- *  has to stay in its range, with a cap too), and a weight times its value's scale is
+ *  exact in either 16-bit type: q . code and its scale are taken in fp32 (both products
+ *  have to stay in its range, with a cap too), and a weight times its value's scale is
  *  rounded once, to dtype or (max_new Hq / Hkv up to 16) to fp16: by at most half a
  *  step or, in fp16 and where that is more, 2^-24 of the largest such product of what
  *  the row sees, whatever the scales of other tokens.  Scales below kv_lens are not
